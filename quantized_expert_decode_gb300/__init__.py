@@ -1,4 +1,4 @@
-"""Python binding of libcolimoe (include/colimoe.h): argument marshalling only.
+"""Python binding of libcolimoe (include/colimoe.h, include/colilayer.h): argument marshalling only.
 
 Every function here has the name of the C entry point it calls and passes device pointers
 (ints, or torch tensors whose data_ptr() is taken) and a CUDA stream handle straight through.
@@ -32,6 +32,15 @@ EXPORTS = ("coli_moe_workspace_bytes", "coli_moe_route", "coli_moe_forward", "co
 
 COLI_MOE_NOALLOC_SCRATCH_BYTES = 32 << 20
 
+# include/colilayer.h: the operators around the block
+COLI_ACT_F32, COLI_ACT_BF16, COLI_ACT_F16 = 0, 1, 2
+COLI_KV_BF16, COLI_KV_F16, COLI_KV_E4M3 = 1, 2, 3
+COLI_GATE_NONE, COLI_GATE_CHANNEL, COLI_GATE_ROW, COLI_GATE_ELEMENT = 0, 1, 2, 3
+COLI_LAYER_BAD_PAGE, COLI_LAYER_BAD_POSITION, COLI_LAYER_BAD_SEQUENCE = 1, 2, 4
+
+# every symbol include/colilayer.h declares
+LAYER_EXPORTS = ("coli_kv_append", "coli_attn_workspace_bytes", "coli_attn_decode", "coli_block_norms")
+
 
 class coli_moe_desc(ctypes.Structure):
     _fields_ = [("T", ctypes.c_int32), ("H", ctypes.c_int32), ("I", ctypes.c_int32),
@@ -45,6 +54,37 @@ class coli_moe_desc(ctypes.Structure):
 class coli_moe_expert(ctypes.Structure):
     _fields_ = [("gate_w", ctypes.c_void_p), ("up_w", ctypes.c_void_p), ("down_w", ctypes.c_void_p),
                 ("gate_s", ctypes.c_void_p), ("up_s", ctypes.c_void_p), ("down_s", ctypes.c_void_p)]
+
+
+class coli_kv_cache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("fmt", ctypes.c_int32), ("pages", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("heads", ctypes.c_int32), ("dim", ctypes.c_int32),
+                ("reserved", ctypes.c_int32), ("page_stride", ctypes.c_int64),
+                ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
+
+
+class coli_append_desc(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int32), ("q_heads", ctypes.c_int32), ("seqs", ctypes.c_int32),
+                ("table_width", ctypes.c_int32), ("act", ctypes.c_int32), ("rotary", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32), ("reserved", ctypes.c_int32),
+                ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64),
+                ("v_stride", ctypes.c_int64), ("q_out_stride", ctypes.c_int64)]
+
+
+class coli_attn_desc(ctypes.Structure):
+    _fields_ = [("seqs", ctypes.c_int32), ("q_heads", ctypes.c_int32), ("table_width", ctypes.c_int32),
+                ("act", ctypes.c_int32), ("window", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("q_stride", ctypes.c_int64), ("out_stride", ctypes.c_int64)]
+
+
+class coli_norms_desc(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int32), ("width", ctypes.c_int32), ("act", ctypes.c_int32),
+                ("gate", ctypes.c_int32), ("post_eps", ctypes.c_float), ("pre_eps", ctypes.c_float),
+                ("resid_scale", ctypes.c_float), ("reserved", ctypes.c_int32),
+                ("y_stride", ctypes.c_int64), ("resid_stride", ctypes.c_int64),
+                ("gate_stride", ctypes.c_int64), ("resid_out_stride", ctypes.c_int64),
+                ("xn_stride", ctypes.c_int64)]
 
 
 class ColiMoeError(RuntimeError):
@@ -89,6 +129,15 @@ def _load():
     lib.coli_moe_rmsnorm.restype = ctypes.c_int
     lib.coli_moe_noalloc_check.argtypes = [P]
     lib.coli_moe_noalloc_check.restype = ctypes.c_int
+    C = ctypes.POINTER(coli_kv_cache)
+    lib.coli_kv_append.argtypes = [ctypes.POINTER(coli_append_desc), C, P, P, P, P, P, P, P, P, P, P]
+    lib.coli_kv_append.restype = ctypes.c_int
+    lib.coli_attn_workspace_bytes.argtypes = [ctypes.POINTER(coli_attn_desc), C]
+    lib.coli_attn_workspace_bytes.restype = SZ
+    lib.coli_attn_decode.argtypes = [ctypes.POINTER(coli_attn_desc), C, P, P, P, P, P, P, P, SZ, P]
+    lib.coli_attn_decode.restype = ctypes.c_int
+    lib.coli_block_norms.argtypes = [ctypes.POINTER(coli_norms_desc), P, P, P, P, P, P, P, P]
+    lib.coli_block_norms.restype = ctypes.c_int
     lib.coli_moe_last_cuda_error.argtypes = []
     lib.coli_moe_last_cuda_error.restype = ctypes.c_int
     return lib
@@ -227,3 +276,54 @@ def coli_moe_noalloc_check(stream=None, raise_on_error=True):
     the stream)."""
     rc = _lib.coli_moe_noalloc_check(_stream(stream))
     return _check(rc, "coli_moe_noalloc_check", raise_on_error)
+
+
+# ---------------------------------------------------------------- the operators around the block
+def make_kv_cache(k, v, fmt, pages, page_size, heads, dim, page_stride=None, token_stride=None,
+                  head_stride=None, k_scale=None, v_scale=None):
+    """Description of a paged cache. Strides (elements) default to [pages][heads][page_size][dim]."""
+    return coli_kv_cache(_ptr(k), _ptr(v), _ptr(k_scale), _ptr(v_scale), fmt, pages, page_size, heads, dim, 0,
+                         heads * page_size * dim if page_stride is None else page_stride,
+                         dim if token_stride is None else token_stride,
+                         page_size * dim if head_stride is None else head_stride)
+
+
+def make_append_desc(tokens, q_heads, seqs, table_width, act=COLI_ACT_F32, rotary=0, interleaved=False,
+                     q_stride=0, k_stride=0, v_stride=0, q_out_stride=0):
+    return coli_append_desc(tokens, q_heads, seqs, table_width, act, rotary, int(interleaved), 0, q_stride,
+                            k_stride, v_stride, q_out_stride)
+
+
+def make_attn_desc(seqs, q_heads, table_width, act, scale, window=0, q_stride=0, out_stride=0):
+    return coli_attn_desc(seqs, q_heads, table_width, act, window, scale, q_stride, out_stride)
+
+
+def make_norms_desc(rows, width, act=COLI_ACT_F32, gate=COLI_GATE_NONE, post_eps=0.0, pre_eps=0.0,
+                    resid_scale=1.0, y_stride=0, resid_stride=0, gate_stride=0, resid_out_stride=0,
+                    xn_stride=0):
+    return coli_norms_desc(rows, width, act, gate, post_eps, pre_eps, resid_scale, 0, y_stride, resid_stride,
+                           gate_stride, resid_out_stride, xn_stride)
+
+
+def coli_kv_append(desc, cache, q, k, v, inv_freq, seq, pos, table, q_out, err=None, stream=None,
+                   raise_on_error=True):
+    rc = _lib.coli_kv_append(ctypes.byref(desc), ctypes.byref(cache), _ptr(q), _ptr(k), _ptr(v), _ptr(inv_freq),
+                             _ptr(seq), _ptr(pos), _ptr(table), _ptr(q_out), _ptr(err), _stream(stream))
+    return _check(rc, "coli_kv_append", raise_on_error)
+
+
+def coli_attn_workspace_bytes(desc, cache) -> int:
+    return int(_lib.coli_attn_workspace_bytes(ctypes.byref(desc), ctypes.byref(cache)))
+
+
+def coli_attn_decode(desc, cache, q, table, lens, out, lse=None, err=None, ws=None, ws_bytes=0, stream=None,
+                     raise_on_error=True):
+    rc = _lib.coli_attn_decode(ctypes.byref(desc), ctypes.byref(cache), _ptr(q), _ptr(table), _ptr(lens), _ptr(out),
+                               _ptr(lse), _ptr(err), _ptr(ws), ws_bytes, _stream(stream))
+    return _check(rc, "coli_attn_decode", raise_on_error)
+
+
+def coli_block_norms(desc, y, resid, post_w, gate, pre_w, resid_out, xn, stream=None, raise_on_error=True):
+    rc = _lib.coli_block_norms(ctypes.byref(desc), _ptr(y), _ptr(resid), _ptr(post_w), _ptr(gate), _ptr(pre_w),
+                               _ptr(resid_out), _ptr(xn), _stream(stream))
+    return _check(rc, "coli_block_norms", raise_on_error)

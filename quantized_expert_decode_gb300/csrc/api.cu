@@ -11,6 +11,7 @@
 #include <chrono>
 #include <random>
 
+#include "host.h"
 #include "kernels.h"
 
 using namespace colimoe;
@@ -19,12 +20,14 @@ namespace {
 
 thread_local int g_last_cuda = 0;
 
+}  // namespace
+
+namespace colimoe {
+
 int cuda_fail(cudaError_t e) {
     g_last_cuda = (int)e;
     return COLI_MOE_ECUDA;
 }
-
-bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 int check_device() {
     static int cache[64];  // 0 unknown, 1 ok, 2 wrong device
@@ -40,6 +43,21 @@ int check_device() {
     if (dev >= 0 && dev < 64) cache[dev] = ok ? 1 : 2;
     return ok ? COLI_MOE_OK : COLI_MOE_EDEVICE;
 }
+
+int num_sms() {
+    static int cache[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 152;
+    if (dev >= 0 && dev < 64 && cache[dev]) return cache[dev];
+    int n = 0;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1) n = 152;
+    if (dev >= 0 && dev < 64) cache[dev] = n;
+    return n;
+}
+
+}  // namespace colimoe
+
+namespace {
 
 int check_fmt(int fmt) {
     if (fmt == COLI_FMT_INT8 || fmt == COLI_FMT_INT4 || fmt == COLI_FMT_INT2 || fmt == COLI_FMT_INT4G)
@@ -129,17 +147,6 @@ int record(void *const *events, int i, cudaStream_t st) {
     if (!events) return COLI_MOE_OK;
     cudaError_t e = cudaEventRecord(static_cast<cudaEvent_t>(events[i]), st);
     return e == cudaSuccess ? COLI_MOE_OK : cuda_fail(e);
-}
-
-int num_sms() {
-    static int cache[64];
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return 152;
-    if (dev >= 0 && dev < 64 && cache[dev]) return cache[dev];
-    int n = 0;
-    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1) n = 152;
-    if (dev >= 0 && dev < 64) cache[dev] = n;
-    return n;
 }
 
 // Call ids of the single-token kernel: a random 64-bit base per process (so that ids left in a

@@ -1,0 +1,223 @@
+// kv_append.cu — new tokens' queries and keys rotated by their positions, keys and values written
+// to the paged cache, in one launch.
+//
+// Mathematics. Pair i of a head turns by p * inv_freq[i]. In units of a full turn that is
+// p * (inv_freq[i] / 2 pi), and only its fraction counts. fp32 has no fraction left at far
+// positions, so inv_freq / 2 pi is taken as a 64-bit fixed-point fraction of a turn (the 24-bit
+// mantissa times 64 bits of 1 / 2 pi) and the product with the integer p wraps modulo one turn by
+// itself: off by p * 2^-64 turns. sincospi then takes the fraction as a float.
+//
+// What bounds it: bytes, each read and written once. A CTA owns a few tokens; its threads compute
+// the tokens' cosines and sines once into shared memory and then walk all heads of q, k and v of
+// those tokens, so that the angle work is shared by the heads.
+#include "act.cuh"
+#include "layer.h"
+
+namespace colimoe {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kMaxTokens = 8;                // tokens of a CTA
+constexpr int kMaxPairs = 128;               // rotary / 2 at most (dim <= 256)
+
+// f / 2 pi as a fraction of a turn in units of 2^-64, modulo one turn
+__device__ __forceinline__ unsigned long long turns_per_step(float f) {
+    constexpr unsigned long long kR = 0xa2f9836e4e441529ull;  // 2^66 / 2 pi
+    const unsigned bits = __float_as_uint(f), e = (bits >> 23) & 0xff;
+    const unsigned long long m = e ? (bits & 0x7fffff) | 0x800000 : 0;  // f = m * 2^(e - 150); below 2^-126: 0
+    const unsigned long long hi = __umul64hi(m, kR), lo = m * kR;
+    const int s = 152 - (int)e;
+    unsigned long long c;
+    if (s >= 128) c = 0;
+    else if (s >= 64) c = hi >> (s - 64);
+    else if (s > 0) c = (hi << (64 - s)) | (lo >> s);
+    else c = s > -64 ? lo << -s : 0;
+    return (bits >> 31) ? 0ull - c : c;
+}
+
+__device__ __forceinline__ float2 turn(int p, float f) {
+    const long long t = (long long)((unsigned long long)(long long)p * turns_per_step(f));
+    float s, c;
+    sincospif((float)t * 1.0842021724855044e-19f, &s, &c);  // 2^-63: half turns
+    if (!isfinite(f)) s = c = __int_as_float(0x7fffffff);
+    return make_float2(c, s);
+}
+
+template <typename C>
+__device__ __forceinline__ C to_cache(float x, float scale) {
+    return from_f32<C>(x);
+}
+template <>
+__device__ __forceinline__ __nv_fp8_e4m3 to_cache<__nv_fp8_e4m3>(float x, float scale) {
+    return from_f32<__nv_fp8_e4m3>(x / scale);
+}
+
+// One item: 2 * V elements of one head of one token. Items below rotary / (2 V) rotate V pairs: V
+// elements at i * V and V at rotary / 2 + i * V, or, interleaved, 2 V elements at i * 2 V. The rest
+// copy 2 V elements.
+template <typename A, typename C, int V>
+__global__ void __launch_bounds__(kThreads) kv_append_kernel(const AppendParams P, int tokens_per_cta,
+                                                             int heads_per_cta) {
+    __shared__ float2 cs[kMaxTokens * kMaxPairs];
+    __shared__ long long row_k[kMaxTokens];  // offset of the token's row of kv head 0, or -1
+    const int n0 = blockIdx.x * tokens_per_cta;
+    const int nt = min(tokens_per_cta, P.tokens - n0);
+    const int half = P.rotary / 2;
+    if (threadIdx.x < nt) {
+        const int n = n0 + threadIdx.x;
+        const int b = P.seq ? P.seq[n] : n;
+        const int p = P.pos[n];
+        long long off = -1;
+        int flag = 0;
+        if (b >= 0 && b < P.seqs) {
+            int why;
+            off = kv_row(P.cache, P.table + (int64_t)b * P.table_width, P.table_width, p, 0, why);
+            flag = why == kKvBadPage ? COLI_LAYER_BAD_PAGE : why == kKvBadPosition ? COLI_LAYER_BAD_POSITION : 0;
+        } else if (b != -1) {
+            flag = COLI_LAYER_BAD_SEQUENCE;
+        }
+        row_k[threadIdx.x] = off;
+        if (flag && P.err) atomicOr(P.err, flag);
+    }
+    for (int i = threadIdx.x; i < nt * half; i += kThreads) {
+        const int t = i / half, j = i - t * half;
+        cs[t * half + j] = turn(P.pos[n0 + t], P.inv_freq[j]);
+    }
+    __syncthreads();
+    const int per_row = P.dim / (2 * V), turned = half / V;
+    const int h0 = blockIdx.y * heads_per_cta;
+    const int heads = min(heads_per_cta, P.q_heads + 2 * P.kv_heads - h0);
+    const int items = nt * heads * per_row;
+#pragma unroll 2
+    for (int it = threadIdx.x; it < items; it += kThreads) {
+        const int r = it / per_row, c = it - r * per_row;
+        const int t = r / heads;
+        int h = h0 + (r - t * heads);
+        const int n = n0 + t;
+        const bool is_q = h < P.q_heads, is_k = !is_q && h < P.q_heads + P.kv_heads;
+        const A *src;
+        if (is_q) {
+            src = (const A *)P.q + n * P.q_stride + (int64_t)h * P.dim;
+        } else if (is_k) {
+            h -= P.q_heads;
+            src = (const A *)P.k + n * P.k_stride + (int64_t)h * P.dim;
+        } else {
+            h -= P.q_heads + P.kv_heads;
+            src = (const A *)P.v + n * P.v_stride + (int64_t)h * P.dim;
+        }
+        const bool rot = (is_q || is_k) && c < turned;
+        // two runs of V elements at o0, o1; adjacent unless the item rotates halves
+        const bool split = rot && !P.interleaved;
+        const int o0 = split ? c * V : c * 2 * V, o1 = split ? half + c * V : c * 2 * V + V;
+        Run<A, V> a, b;
+        a.load(src + o0);
+        b.load(src + o1);
+        float x[V], y[V];
+#pragma unroll
+        for (int j = 0; j < V; j++) {
+            x[j] = to_f32(a.e[j]);
+            y[j] = to_f32(b.e[j]);
+        }
+        if (rot) {
+            const float2 *w = cs + t * half + c * V;
+            if (split) {
+#pragma unroll
+                for (int j = 0; j < V; j++) {
+                    const float2 e = w[j];
+                    const float u = x[j], v = y[j];
+                    x[j] = fmaf(u, e.x, -(v * e.y));
+                    y[j] = fmaf(v, e.x, u * e.y);
+                }
+            } else {
+                // the 2 V elements x, y hold V adjacent pairs
+                float z[2 * V];
+#pragma unroll
+                for (int j = 0; j < V; j++) {
+                    z[j] = x[j];
+                    z[V + j] = y[j];
+                }
+#pragma unroll
+                for (int j = 0; j < V; j++) {
+                    const float2 e = w[j];
+                    const float u = z[2 * j], v = z[2 * j + 1];
+                    z[2 * j] = fmaf(u, e.x, -(v * e.y));
+                    z[2 * j + 1] = fmaf(v, e.x, u * e.y);
+                }
+#pragma unroll
+                for (int j = 0; j < V; j++) {
+                    x[j] = z[j];
+                    y[j] = z[V + j];
+                }
+            }
+        }
+        if (is_q) {
+            A *dst = (A *)P.q_out + n * P.q_out_stride + (int64_t)h * P.dim;
+#pragma unroll
+            for (int j = 0; j < V; j++) {
+                a.e[j] = from_f32<A>(x[j]);
+                b.e[j] = from_f32<A>(y[j]);
+            }
+            a.store(dst + o0);
+            b.store(dst + o1);
+        } else if (row_k[t] >= 0) {
+            const float *sc = is_k ? P.k_scale : P.v_scale;
+            const float s = sc ? sc[h] : 1.f;
+            C *dst = (C *)(is_k ? P.k_cache : P.v_cache) + row_k[t] + (int64_t)h * P.cache.head_stride;
+            Run<C, V> ca, cb;
+#pragma unroll
+            for (int j = 0; j < V; j++) {
+                ca.e[j] = to_cache<C>(x[j], s);
+                cb.e[j] = to_cache<C>(y[j], s);
+            }
+            ca.store(dst + o0);
+            cb.store(dst + o1);
+        }
+    }
+}
+
+bool multiple(const void *p, int64_t stride, int act_bytes, int run) {
+    const int64_t bytes = (int64_t)run * act_bytes;
+    const int64_t a = bytes % 16 == 0 ? 16 : bytes;
+    return reinterpret_cast<uintptr_t>(p) % a == 0 && (stride * act_bytes) % a == 0;
+}
+
+template <typename A, typename C>
+cudaError_t launch_typed(const AppendParams &P, cudaStream_t s) {
+    // widest run that the rotated part, the rest, and the rows' alignment allow (the cache's rows
+    // are 16-byte aligned with strides of 16 bytes, which the entry point has checked)
+    const int half = P.rotary / 2, rest = P.dim - P.rotary;
+    auto fits = [&](int v) {
+        const int sz = (int)sizeof(A);
+        return half % v == 0 && rest % (2 * v) == 0 && (!P.q_heads || (multiple(P.q, P.q_stride, sz, v) && multiple(P.q_out, P.q_out_stride, sz, v))) &&
+               multiple(P.k, P.k_stride, sz, v) && multiple(P.v, P.v_stride, sz, v);
+    };
+    const int rows = P.q_heads + 2 * P.kv_heads;
+    const int tp = P.tokens >= 4096 ? 4 : 1;
+    const int hp = P.tokens >= 512 ? rows : 16;
+    dim3 grid((P.tokens + tp - 1) / tp, (rows + hp - 1) / hp);
+    if (fits(8)) kv_append_kernel<A, C, 8><<<grid, kThreads, 0, s>>>(P, tp, hp);
+    else if (fits(4)) kv_append_kernel<A, C, 4><<<grid, kThreads, 0, s>>>(P, tp, hp);
+    else kv_append_kernel<A, C, 1><<<grid, kThreads, 0, s>>>(P, tp, hp);
+    return cudaGetLastError();
+}
+
+template <typename A>
+cudaError_t launch_act(const AppendParams &P, cudaStream_t s) {
+    switch (P.fmt) {
+    case COLI_KV_BF16: return launch_typed<A, __nv_bfloat16>(P, s);
+    case COLI_KV_F16: return launch_typed<A, __half>(P, s);
+    default: return launch_typed<A, __nv_fp8_e4m3>(P, s);
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_kv_append(const AppendParams &P, cudaStream_t s) {
+    switch (P.act) {
+    case COLI_ACT_F32: return launch_act<float>(P, s);
+    case COLI_ACT_BF16: return launch_act<__nv_bfloat16>(P, s);
+    default: return launch_act<__half>(P, s);
+    }
+}
+
+}  // namespace colimoe

@@ -1,0 +1,54 @@
+// kv_index.h — where a token's row lies in a paged cache. Plain C++ with no CUDA header, so that
+// the index arithmetic is the same on the device and in the host tests. Internal to libcolimoe.
+#pragma once
+
+#include <cstdint>
+
+#ifdef __CUDACC__
+#define COLI_HD __host__ __device__ __forceinline__
+#else
+#define COLI_HD inline
+#endif
+
+namespace colimoe {
+
+struct KvShape {
+    int64_t page_stride, token_stride, head_stride;  // elements
+    int32_t pages, page_size;
+};
+
+enum KvWhy : int { kKvOk = 0, kKvBadPage = 1, kKvBadPosition = 2 };
+
+// Element offset of token t's row of kv head h, where row[0..width) are the sequence's pages; -1
+// (and why) if there is none. Products are 64-bit: a pool may hold more than 2^31 elements.
+COLI_HD int64_t kv_row(const KvShape &c, const int32_t *row, int32_t width, int32_t t, int32_t h, int &why) {
+    why = kKvOk;
+    if (t < 0) {
+        why = kKvBadPosition;
+        return -1;
+    }
+    const uint32_t i = (uint32_t)t / (uint32_t)c.page_size;
+    if (i >= (uint32_t)width) {
+        why = kKvBadPosition;
+        return -1;
+    }
+    const int32_t page = row[i];
+    if ((uint32_t)page >= (uint32_t)c.pages) {
+        why = kKvBadPage;
+        return -1;
+    }
+    const int32_t slot = (int32_t)((uint32_t)t - i * (uint32_t)c.page_size);
+    return (int64_t)page * c.page_stride + (int64_t)slot * c.token_stride + (int64_t)h * c.head_stride;
+}
+
+// The tokens [first, end) of a sequence of n cached tokens that the new token sees; n is clamped to
+// what the table can name (and flagged).
+COLI_HD void kv_span(int32_t n, int32_t width, int32_t page_size, int32_t window, int32_t &first, int32_t &end,
+                     int &why) {
+    const int64_t most = (int64_t)width * page_size;
+    why = (n < 0 || n > most) ? kKvBadPosition : kKvOk;
+    end = n < 0 ? 0 : n > most ? (int32_t)most : n;
+    first = (window > 0 && end > window) ? end - window : 0;
+}
+
+}  // namespace colimoe

@@ -1,0 +1,206 @@
+"""Host-side checks of include/colilayer.h: the binding declares what the header does, bad arguments
+are refused with the documented codes before the GPU is touched, and the page arithmetic the kernels
+share (csrc/kv_index.h) is right at its borders, on bad pages and behind 2^31 elements."""
+import ctypes
+import os
+import re
+import subprocess
+
+import pytest
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+FAKE = 1 << 40  # a 256-byte aligned address never dereferenced: validation fails first
+
+
+@pytest.fixture(scope="module")
+def q():
+    import __graft_entry__
+    __graft_entry__._builder().build()
+    import quantized_expert_decode_gb300 as q
+    return q
+
+
+def test_header_and_binding_agree(q):
+    with open(os.path.join(ROOT, "include", "colilayer.h")) as f:
+        text = f.read()
+    names = sorted(re.findall(r"^(?:int|size_t)\s+(coli_[a-z_]+)\s*\(", text, re.M))
+    assert names == sorted(q.LAYER_EXPORTS)
+    lib = ctypes.CDLL(q.LIB_PATH)
+    for n in names:
+        getattr(lib, n)
+    for name, value in re.findall(r"^#define (COLI_(?:ACT|KV|GATE|LAYER)_\w+) (\d+)", text, re.M):
+        assert getattr(q, name) == int(value), name
+
+
+def test_struct_layouts_match_the_header(q, tmp_path):
+    # sizes and the last field's offset as a C compiler sees them
+    src = tmp_path / "l.c"
+    names = {"coli_kv_cache": "head_stride", "coli_append_desc": "q_out_stride", "coli_attn_desc": "out_stride",
+             "coli_norms_desc": "xn_stride"}
+    body = "".join(f'printf("%zu %zu\\n", sizeof({n}), offsetof({n}, {f}));' for n, f in names.items())
+    src.write_text('#include <stdio.h>\n#include "colilayer.h"\nint main(void){' + body + "return 0;}")
+    exe = tmp_path / "l"
+    subprocess.run(["gcc", "-I", os.path.join(ROOT, "include"), str(src), "-o", str(exe)], check=True)
+    got = [tuple(map(int, l.split())) for l in subprocess.run([str(exe)], capture_output=True, text=True,
+                                                              check=True).stdout.splitlines()]
+    want = [(ctypes.sizeof(getattr(q, n)), getattr(getattr(q, n), f).offset) for n, f in names.items()]
+    assert got == want
+
+
+def cache(q, **over):
+    d = dict(k=FAKE, v=FAKE, fmt=1, pages=10, page_size=16, heads=4, dim=128)
+    d.update(over)
+    return q.make_kv_cache(**d)
+
+
+BAD_CACHES = [(dict(k=None), "EINVAL"), (dict(v=None), "EINVAL"), (dict(fmt=0), "EINVAL"), (dict(fmt=4), "EINVAL"),
+              (dict(pages=0), "EINVAL"), (dict(page_size=0), "EINVAL"), (dict(heads=0), "EINVAL"),
+              (dict(heads=2000), "EINVAL"), (dict(dim=0), "EINVAL"), (dict(dim=100), "ENOTSUP"),
+              (dict(dim=264), "ENOTSUP"), (dict(fmt=3, dim=72), "ENOTSUP"), (dict(k=FAKE + 8), "EALIGN"),
+              (dict(v=FAKE + 2), "EALIGN"), (dict(token_stride=64), "EINVAL"), (dict(head_stride=-128), "EINVAL"),
+              (dict(page_stride=0), "EINVAL"), (dict(token_stride=132), "EALIGN"), (dict(k_scale=FAKE + 1), "EALIGN")]
+
+
+def append(lib, c=None, **over):
+    d = dict(tokens=3, q_heads=8, seqs=3, table_width=5, act=0, rotary=64)
+    a = dict(q=FAKE, k=FAKE, v=FAKE, inv_freq=FAKE, seq=FAKE, pos=FAKE, table=FAKE, q_out=FAKE, err=None)
+    for k, v in over.items():
+        (d if k not in a else a)[k] = v
+    return lib.coli_kv_append(lib.make_append_desc(**d), c or cache(lib), raise_on_error=False, **a)
+
+
+@pytest.mark.parametrize("over,code", BAD_CACHES)
+def test_bad_caches_are_refused_everywhere(q, over, code):
+    want = getattr(q, "COLI_MOE_" + code)
+    c = cache(q, **over)
+    assert append(q, c) == want
+    d = q.make_attn_desc(2, 8, 5, 0, 0.1)
+    assert q.coli_attn_workspace_bytes(d, c) == 0
+    assert q.coli_attn_decode(d, c, FAKE, FAKE, FAKE, FAKE, ws=FAKE, ws_bytes=1 << 40, raise_on_error=False) == want
+
+
+@pytest.mark.parametrize("over,code", [
+    (dict(tokens=0), "EINVAL"), (dict(q_heads=-1), "EINVAL"), (dict(q_heads=2000), "EINVAL"), (dict(seqs=0), "EINVAL"),
+    (dict(table_width=0), "EINVAL"), (dict(table_width=1 << 28), "EINVAL"), (dict(act=3), "EINVAL"),
+    (dict(rotary=-2), "EINVAL"), (dict(rotary=63), "EINVAL"), (dict(rotary=130), "EINVAL"), (dict(interleaved=2), "EINVAL"),
+    (dict(k=None), "EINVAL"), (dict(v=None), "EINVAL"), (dict(pos=None), "EINVAL"), (dict(table=None), "EINVAL"),
+    (dict(inv_freq=None), "EINVAL"), (dict(q=None), "EINVAL"), (dict(q_out=None), "EINVAL"), (dict(q_heads=0), "EINVAL"),
+    (dict(seq=None, tokens=4), "EINVAL"), (dict(q_stride=1000), "EINVAL"), (dict(k_stride=511), "EINVAL"),
+    (dict(v_stride=-1), "EINVAL"), (dict(q_stride=1100), "EINVAL"), (dict(q=FAKE + 2), "EALIGN"),
+    (dict(k=FAKE + 1), "EALIGN"), (dict(err=FAKE + 2), "EALIGN"), (dict(pos=FAKE + 1), "EALIGN")])
+def test_append_refusals(q, over, code):
+    # q and q_out are the same rows here, so unequal strides are refused too
+    assert append(q, **over) == getattr(q, "COLI_MOE_" + code)
+
+
+@pytest.mark.parametrize("desc,args,code", [
+    (dict(seqs=0), {}, "EINVAL"), (dict(seqs=5000), {}, "EINVAL"), (dict(q_heads=0), {}, "EINVAL"),
+    (dict(q_heads=6), {}, "EINVAL"), (dict(q_heads=2048), {}, "EINVAL"), (dict(table_width=0), {}, "EINVAL"),
+    (dict(table_width=1 << 27), {}, "EINVAL"), (dict(act=-1), {}, "EINVAL"), (dict(window=-1), {}, "EINVAL"),
+    (dict(scale=float("nan")), {}, "EINVAL"), (dict(scale=float("inf")), {}, "EINVAL"), (dict(q_stride=8), {}, "EINVAL"),
+    (dict(out_stride=-8), {}, "EINVAL"), ({}, dict(q=None), "EINVAL"), ({}, dict(out=None), "EINVAL"),
+    ({}, dict(table=None), "EINVAL"), ({}, dict(lens=None), "EINVAL"), ({}, dict(q=FAKE + 1), "EALIGN"),
+    ({}, dict(lens=FAKE + 2), "EALIGN"), ({}, dict(lse=FAKE + 2), "EALIGN"), ({}, dict(ws=None), "EWORKSPACE"),
+    ({}, dict(ws=FAKE + 16), "EWORKSPACE"), ({}, dict(ws_bytes=0), "EWORKSPACE")])
+def test_attention_refusals(q, desc, args, code):
+    d = dict(seqs=2, q_heads=8, table_width=5, act=0, scale=0.1)
+    d.update(desc)
+    a = dict(q=FAKE, table=FAKE, lens=FAKE, out=FAKE, ws=FAKE, ws_bytes=1 << 40)
+    a.update(args)
+    assert q.coli_attn_decode(q.make_attn_desc(**d), cache(q), raise_on_error=False, **a) == getattr(q, "COLI_MOE_" + code)
+    if desc:
+        assert q.coli_attn_workspace_bytes(q.make_attn_desc(**d), cache(q)) == 0
+
+
+def test_attention_workspace(q):
+    d = q.make_attn_desc(2, 8, 5, 0, 0.1)
+    n = q.coli_attn_workspace_bytes(d, cache(q))
+    assert n > 0 and n % 256 == 0
+    assert q.coli_attn_decode(d, cache(q), FAKE, FAKE, FAKE, FAKE, ws=FAKE, ws_bytes=n - 1,
+                              raise_on_error=False) == q.COLI_MOE_EWORKSPACE
+
+
+@pytest.mark.parametrize("desc,args,code", [
+    (dict(rows=0), {}, "EINVAL"), (dict(width=0), {}, "EINVAL"), (dict(width=65537), {}, "EINVAL"),
+    (dict(act=5), {}, "EINVAL"), (dict(gate=4), {}, "EINVAL"), (dict(gate=1), {}, "EINVAL"),
+    (dict(post_eps=-1.0), {}, "EINVAL"), (dict(pre_eps=float("nan")), {}, "EINVAL"),
+    (dict(resid_scale=float("inf")), {}, "EINVAL"), (dict(y_stride=63), {}, "EINVAL"), (dict(xn_stride=-1), {}, "EINVAL"),
+    ({}, dict(y=None), "EINVAL"), ({}, dict(resid=None), "EINVAL"), ({}, dict(resid_out=None), "EINVAL"),
+    ({}, dict(gate=FAKE), "EINVAL"), ({}, dict(xn=None), "EINVAL"), ({}, dict(xn=2 * FAKE), "EINVAL"),
+    (dict(resid_stride=80), dict(resid_out=3 * FAKE), "EINVAL"), ({}, dict(y=FAKE + 2), "EALIGN"),
+    ({}, dict(post_w=FAKE + 2), "EALIGN")])
+def test_norms_refusals(q, desc, args, code):
+    d = dict(rows=2, width=64)
+    d.update(desc)
+    a = dict(y=FAKE, resid=3 * FAKE, post_w=FAKE, gate=None, pre_w=FAKE, resid_out=2 * FAKE, xn=4 * FAKE)
+    a.update(args)
+    assert q.coli_block_norms(q.make_norms_desc(**d), raise_on_error=False, **a) == getattr(q, "COLI_MOE_" + code)
+
+
+# ---------------------------------------------------------------------- page arithmetic
+@pytest.fixture(scope="module")
+def index(tmp_path_factory):
+    d = tmp_path_factory.mktemp("kv")
+    src = d / "kv.cc"
+    src.write_text('''
+#include "kv_index.h"
+using namespace colimoe;
+extern "C" long long row(long long ps_, long long ts, long long hs, int pages, int page_size, const int *t, int width,
+                         int tok, int h, int *why) {
+    KvShape c{ps_, ts, hs, pages, page_size};
+    return kv_row(c, t, width, tok, h, *why);
+}
+extern "C" void span(int n, int width, int page_size, int window, int *out) {
+    kv_span(n, width, page_size, window, out[0], out[1], out[2]);
+}
+''')
+    so = d / "libkv.so"
+    inc = os.path.join(ROOT, "quantized_expert_decode_gb300", "csrc")
+    subprocess.run(["g++", "-std=c++17", "-shared", "-fPIC", "-I", inc, str(src), "-o", str(so)], check=True)
+    lib = ctypes.CDLL(str(so))
+    lib.row.restype = ctypes.c_longlong
+    lib.row.argtypes = [ctypes.c_longlong] * 3 + [ctypes.c_int] * 2 + [ctypes.c_void_p] + [ctypes.c_int] * 3 + [ctypes.c_void_p]
+    return lib
+
+
+def row(lib, table, tok, head=0, pages=1 << 20, ps=16, strides=(8192, 128, 2048)):
+    arr = (ctypes.c_int * len(table))(*table)
+    why = ctypes.c_int(-1)
+    return lib.row(*strides, pages, ps, arr, len(table), tok, head, ctypes.byref(why)), why.value
+
+
+def test_rows_follow_the_table(index):
+    table = [7, 2, 900000]
+    for tok in (0, 1, 15, 16, 31, 32, 47):
+        for head in (0, 3):
+            want = table[tok // 16] * 8192 + tok % 16 * 128 + head * 2048
+            assert row(index, table, tok, head) == (want, 0)
+    assert row(index, table, 32)[0] > 1 << 31  # 64-bit products
+
+
+@pytest.mark.parametrize("ps", [1, 3, 24])
+def test_rows_of_odd_pages(index, ps):
+    table = list(range(50, 40, -1))
+    for tok in range(10 * ps):
+        assert row(index, table, tok, 1, ps=ps, strides=(1000, 16, 400))[0] == table[tok // ps] * 1000 + tok % ps * 16 + 400
+
+
+def test_bad_pages_and_positions_have_no_row(index):
+    assert row(index, [-1, 2], 3) == (-1, 1)
+    assert row(index, [5, 2], 3, pages=5) == (-1, 1)
+    assert row(index, [4, 2], 3, pages=5) == (4 * 8192 + 3 * 128, 0)
+    assert row(index, [2 ** 31 - 1, 2], 3) == (-1, 1)
+    assert row(index, [-2 ** 31, 2], 3) == (-1, 1)
+    assert row(index, [1, 2], 32) == (-1, 2)
+    assert row(index, [1, 2], -1) == (-1, 2)
+    assert row(index, [1, 2], 2 ** 31 - 1) == (-1, 2)
+
+
+@pytest.mark.parametrize("n,width,ps,window,want", [
+    (0, 4, 16, 0, (0, 0, 0)), (1, 4, 16, 0, (0, 1, 0)), (64, 4, 16, 0, (0, 64, 0)), (65, 4, 16, 0, (0, 64, 2)),
+    (-1, 4, 16, 0, (0, 0, 2)), (-2 ** 31, 4, 16, 5, (0, 0, 2)), (60, 4, 16, 10, (50, 60, 0)), (10, 4, 16, 10, (0, 10, 0)),
+    (11, 4, 16, 10, (1, 11, 0)), (2 ** 31 - 1, 4, 16, 1, (63, 64, 2)), (5, 4, 16, 2 ** 31 - 1, (0, 5, 0))])
+def test_spans(index, n, width, ps, window, want):
+    out = (ctypes.c_int * 3)()
+    index.span(n, width, ps, window, out)
+    assert tuple(out) == want
