@@ -93,7 +93,7 @@ int coli_kv_append(const coli_append_desc *desc, const coli_kv_cache *cache, con
 
 /* Attention of one new token per sequence. */
 typedef struct {
-    int32_t seqs;        /* 1..4096 */
+    int32_t seqs;        /* 1..2048 */
     int32_t q_heads;     /* a multiple of cache->heads, <= 1024; head h reads kv head h / (q_heads / heads) */
     int32_t table_width; /* entries per row of the page table; table_width * page_size < 2^31 */
     int32_t act;         /* COLI_ACT_* of q and out */

@@ -1,96 +1,137 @@
-// attn_decode.cu — attention of one new token per sequence over a paged cache.
-//
-// Mathematics: s_t = scale * q . k_t, p = softmax(s), out = sum_t p_t v_t, with a running maximum m
-// and sum l: a later score above m scales what is summed so far by exp(m - m').
-//
-// One CTA per (sequence, query head); each warp takes every fourth token, its lanes share the
-// head's elements, and the four warps' (m, l, sum) are joined in shared memory.
-#include "act.cuh"
-#include "layer.h"
+// attn_decode.cu — coli_attn_decode: how a call is laid out, and the join of the items that a run's
+// border cut (attn_kernel.cuh has the streaming kernel).
+#include "attn.h"
+#include "host.h"
 
 namespace colimoe {
 namespace {
 
-constexpr int kWarps = 4;
+constexpr int kJoinThreads = 256;
 
-template <typename A, typename C>
-__global__ void __launch_bounds__(kWarps * 32) attn_decode_kernel(const AttnParams P) {
-    const int h = blockIdx.x, b = blockIdx.y, w = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const int kh = h / (P.q_heads / P.kv_heads);
-    int first, end, why;
-    kv_span(P.lens[b], P.table_width, P.cache.page_size, P.window, first, end, why);
-    if (why && threadIdx.x == 0 && P.err) atomicOr(P.err, COLI_LAYER_BAD_POSITION);
-    float q[8], o[8];
-    const float ks = P.scale * (P.k_scale ? P.k_scale[kh] : 1.f);
-#pragma unroll
-    for (int j = 0; j < 8; j++) {
-        const int d = lane + 32 * j;
-        q[j] = d < P.dim ? to_f32(((const A *)P.q)[b * P.q_stride + (int64_t)h * P.dim + d]) : 0.f;
-        o[j] = 0.f;
+// One block per (border between runs, head of the group): the block of an item's first border adds up
+// the partial sums of all runs that hold units of the item, in the order of the runs. Everything is
+// scaled to the largest m, by exact powers of two.
+template <int DP>
+__global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnParams P, const AttnWork W, int grid, int shift) {
+    constexpr int kWarps = kJoinThreads / 32, kPer = DP / 32;
+    __shared__ float red[kWarps][DP];
+    __shared__ float2 red_ml[kWarps];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int heads = 8 * W.nt;
+    const int64_t total = (int64_t)W.prefix[P.seqs] * W.groups;
+    const int64_t n = min((int64_t)grid, total), c = (int64_t)blockIdx.x + 1;
+    if (c >= n) return;
+    const int64_t x = attn_run_start(c, total, n);
+    int lo = 0, hi = P.seqs;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if ((int64_t)W.prefix[mid] * W.groups <= x) lo = mid;
+        else hi = mid;
     }
-    float m = -INFINITY, l = 0.f;
-    for (int t = first + w; t < end; t += kWarps) {
-        const int64_t off = kv_row(P.cache, P.table + (int64_t)b * P.table_width, P.table_width, t, kh, why);
-        if (off < 0) {
-            if (lane == 0 && P.err) atomicOr(P.err, COLI_LAYER_BAD_PAGE);
-            continue;
-        }
-        const C *k = (const C *)P.k_cache + off, *v = (const C *)P.v_cache + off;
-        float s = 0.f;
+    const int b = lo, units = W.prefix[lo + 1] - W.prefix[lo];
+    const int64_t base = (int64_t)W.prefix[lo] * W.groups;
+    const int hv = (int)((x - base) / units);
+    const int64_t i0 = base + (int64_t)hv * units, i1 = i0 + units;
+    // this border cuts the item, and is the first that does
+    if (i0 == x || attn_run_start(c - 1, total, n) > i0) return;
+    const int64_t c0 = c - 1, c1 = attn_run_of(i1 - 1, total, n);
+    const int kh = hv / W.chunks, group = P.q_heads / P.kv_heads, h0 = (hv - kh * W.chunks) * heads, h = blockIdx.y;
+    if (h0 + h >= group) return;
+    const int w = threadIdx.x / 32, lane = threadIdx.x % 32;
+    auto slot = [&](int64_t r) { return (2 * r + (r == c0 ? 1 : 0)) * heads + h; };
+    float top = -INFINITY;
+    for (int64_t r = c0 + lane; r <= c1; r += 32) top = fmaxf(top, W.part_ml[slot(r)].x);
 #pragma unroll
-        for (int j = 0; j < 8; j++)
-            if (lane + 32 * j < P.dim) s = fmaf(q[j], to_f32(k[lane + 32 * j]), s);
+    for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+    const float ref = top == -INFINITY ? 0.f : top;
+    float o[kPer], l = 0.f;
 #pragma unroll
-        for (int i = 16; i; i >>= 1) s += __shfl_xor_sync(0xffffffffu, s, i);
-        s *= ks;
-        const float n = fmaxf(m, s), f = n == -INFINITY ? 0.f : expf(m - n), p = n == -INFINITY ? 0.f : expf(s - n);
-        m = n;
-        l = fmaf(l, f, p);
+    for (int j = 0; j < kPer; j++) o[j] = 0.f;
+#pragma unroll 4
+    for (int64_t r = c0 + w; r <= c1; r += kWarps) {
+        const int64_t s = slot(r);
+        const float2 e = W.part_ml[s];
+        Run<float, kPer> v;
+        v.load(W.part_o + s * DP + lane * kPer);
+        const float f = exp2f(e.x - ref);
+        l = fmaf(e.y, f, l);
 #pragma unroll
-        for (int j = 0; j < 8; j++)
-            if (lane + 32 * j < P.dim) o[j] = fmaf(o[j], f, p * to_f32(v[lane + 32 * j]));
+        for (int j = 0; j < kPer; j++) o[j] = fmaf(v.e[j], f, o[j]);
     }
-    __shared__ float sm[kWarps], sl[kWarps], so[kWarps][256];
-    if (lane == 0) {
-        sm[w] = m;
-        sl[w] = l;
-    }
 #pragma unroll
-    for (int j = 0; j < 8; j++) so[w][lane + 32 * j] = o[j];
+    for (int j = 0; j < kPer; j++) red[w][lane * kPer + j] = o[j];
+    if (lane == 0) red_ml[w].y = l;
     __syncthreads();
-    float top = -INFINITY, sum = 0.f;
-    for (int i = 0; i < kWarps; i++) top = fmaxf(top, sm[i]);
-    for (int i = 0; i < kWarps; i++) sum += sm[i] == -INFINITY ? 0.f : sl[i] * expf(sm[i] - top);
+    float sum = 0.f;
+#pragma unroll
+    for (int k = 0; k < kWarps; k++) sum += red_ml[k].y;
     const float vs = P.v_scale ? P.v_scale[kh] : 1.f;
-    for (int d = threadIdx.x; d < P.dim; d += kWarps * 32) {
-        float x = 0.f;
-        for (int i = 0; i < kWarps; i++) x += sm[i] == -INFINITY ? 0.f : so[i][d] * expf(sm[i] - top);
-        ((A *)P.out)[b * P.out_stride + (int64_t)h * P.dim + d] = from_f32<A>(sum == 0.f ? 0.f : x / sum * vs);
+    const int qh = kh * group + h0 + h;
+    for (int d = threadIdx.x; d < P.dim; d += kJoinThreads) {
+        float v = 0.f;
+#pragma unroll
+        for (int k = 0; k < kWarps; k++) v += red[k][d];
+        store_act(P.out, b * P.out_stride + (int64_t)qh * P.dim + d, sum == 0.f ? 0.f : v / sum * vs, P.act);
     }
-    if (threadIdx.x == 0 && P.lse) P.lse[(int64_t)b * P.q_heads + h] = sum == 0.f ? -INFINITY : top + logf(sum);
+    if (threadIdx.x == 0 && P.lse) P.lse[(int64_t)b * P.q_heads + qh] = attn_lse(ref, sum, shift);
 }
 
-template <typename A>
-void launch_act(const AttnParams &P, cudaStream_t s) {
-    const dim3 grid(P.q_heads, P.seqs);
-    switch (P.fmt) {
-    case COLI_KV_BF16: attn_decode_kernel<A, __nv_bfloat16><<<grid, kWarps * 32, 0, s>>>(P); break;
-    case COLI_KV_F16: attn_decode_kernel<A, __half><<<grid, kWarps * 32, 0, s>>>(P); break;
-    default: attn_decode_kernel<A, __nv_fp8_e4m3><<<grid, kWarps * 32, 0, s>>>(P); break;
-    }
+struct Layout {
+    AttnWork w;
+    int grid;
+    size_t ml, o, total;
+};
+
+Layout layout_of(const AttnParams &P) {
+    Layout L{};
+    const int group = P.q_heads / P.kv_heads;
+    L.w.dim = P.dim <= 64 ? 64 : P.dim <= 128 ? 128 : 256;
+    L.w.nt = group <= 8 ? 1 : 2;
+    // q in one part where the cache's type (f16 for e4m3, scaled) holds it
+    L.w.wide = P.act == COLI_ACT_F32 || (P.act == COLI_ACT_F16 && P.fmt == COLI_KV_BF16);
+    L.w.chunks = (group + 8 * L.w.nt - 1) / (8 * L.w.nt);
+    L.w.groups = P.kv_heads * L.w.chunks;
+    L.w.unit = attn_unit(P.fmt, L.w.dim);
+    // no more CTAs than units that the page tables can name
+    const int64_t seen = P.window > 0 ? P.window : (int64_t)P.table_width * P.cache.page_size;
+    const int64_t most = ((seen + L.w.unit - 1) / L.w.unit) * P.seqs * L.w.groups;
+    const int64_t ctas = (int64_t)num_sms() * attn_ctas_per_sm(L.w.dim);
+    L.grid = (int)(most < ctas ? most : ctas);
+    auto up = [](size_t n) { return (n + 255) / 256 * 256; };
+    L.ml = up((size_t)(P.seqs + 1) * 4);
+    L.o = L.ml + up((size_t)2 * L.grid * 8 * L.w.nt * sizeof(float2));
+    L.total = L.o + up((size_t)2 * L.grid * 8 * L.w.nt * L.w.dim * 4);
+    return L;
 }
 
 }  // namespace
 
-size_t attn_workspace_bytes(const AttnParams &P) { return 256; }
+size_t attn_workspace_bytes(const AttnParams &P) { return layout_of(P).total; }
 
 cudaError_t launch_attn_decode(const AttnParams &P, cudaStream_t s) {
-    switch (P.act) {
-    case COLI_ACT_F32: launch_act<float>(P, s); break;
-    case COLI_ACT_BF16: launch_act<__nv_bfloat16>(P, s); break;
-    default: launch_act<__half>(P, s); break;
-    }
-    return cudaGetLastError();
+    Layout L = layout_of(P);
+    char *ws = (char *)P.ws;
+    L.w.prefix = (int32_t *)ws;
+    L.w.part_ml = (float2 *)(ws + L.ml);
+    L.w.part_o = (float *)(ws + L.o);
+    const cudaError_t e = P.fmt == COLI_KV_BF16  ? launch_attn_bf16(P, L.w, L.grid, s)
+                          : P.fmt == COLI_KV_F16 ? launch_attn_f16(P, L.w, L.grid, s)
+                                                 : launch_attn_e4m3(P, L.w, L.grid, s);
+    if (e != cudaSuccess || L.grid == 1) return e;  // one run: no borders
+    // the join's blocks start while the streaming kernel runs and wait for its end
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(L.grid - 1, 8 * L.w.nt);
+    cfg.blockDim = dim3(kJoinThreads);
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    const int shift = P.fmt == COLI_KV_BF16 ? 0 : 14;
+    return L.w.dim == 64    ? cudaLaunchKernelEx(&cfg, attn_join_kernel<64>, P, L.w, L.grid, shift)
+           : L.w.dim == 128 ? cudaLaunchKernelEx(&cfg, attn_join_kernel<128>, P, L.w, L.grid, shift)
+                            : cudaLaunchKernelEx(&cfg, attn_join_kernel<256>, P, L.w, L.grid, shift);
 }
 
 }  // namespace colimoe

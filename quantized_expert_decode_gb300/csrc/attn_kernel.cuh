@@ -1,0 +1,614 @@
+// attn_kernel.cuh — the streaming kernel of coli_attn_decode. Internal to libcolimoe; instantiated
+// per cache type by attn_bf16.cu, attn_f16.cu and attn_e4m3.cu.
+//
+// Mathematics. With x_t = scale * log2(e) * q . k_t a running integer m >= max x_t is kept (the
+// maximum rounded up), l = sum 2^(x_t - m) and o = sum 2^(x_t - m) v_t. A later, larger m' scales l
+// and o by 2^(m - m'), which is exact because both are integers; so is every later join of parts.
+//
+// What bounds it: the bytes of K and V, read once for all query heads of a kv head (4 * heads
+// operations per 2 * dim-element pair: far below the tensor cores' rate up to 16 heads).
+//
+// Work. The cached tokens of every (sequence, kv head, group of query heads) are cut into units of
+// kWarps tiles of kTile tokens. All units of the call form one line that is cut into equal runs, one
+// per CTA, so a CTA's share does not depend on how the lengths are spread; an item that a run's
+// border cuts leaves partial sums in the workspace, which the join kernel adds up in a fixed order.
+// Within a unit each warp owns one tile: it copies the tile's K and V rows to its own ring of kStages
+// stages with 16-byte asynchronous copies (two tiles in flight while one is computed), and no warp
+// waits for another until the item ends.
+//
+// Products. Tokens are the rows of the matrix instruction and the query heads its 8 columns, so a
+// group of up to 8 heads fills it: S^T [16 tokens x 8 heads] = K q^T, then O^T [16 dims x 8 heads] +=
+// V^T P^T, where P^T comes from S^T's registers by an 8x8 transposition. K and V enter in the cache's
+// own type (e4m3 widened to f16, exactly). q and p are sums of parts in that type: a bf16 or f16 q
+// that the type holds is one part; an fp32 q is three bf16 parts or two f16 parts (scaled by a power of
+// two per head); p is two parts, or three in bf16 beside an fp32 q. Each tile's O is summed from zero
+// and added in fp32, so that the matrix unit's truncating accumulation never runs over more than a tile.
+#pragma once
+
+#include <atomic>
+
+#include "act.cuh"
+#include "attn.h"
+
+namespace colimoe {
+
+namespace attn {
+
+__device__ __forceinline__ uint32_t smem_addr(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
+
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool valid) {
+    const int n = valid ? 16 : 0;  // 0: the 16 bytes are zeroed and src is not read
+    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+__device__ __forceinline__ void ldm4(uint32_t (&r)[4], uint32_t a) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
+}
+__device__ __forceinline__ void ldm4t(uint32_t (&r)[4], uint32_t a) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
+}
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+__device__ __forceinline__ float exp2_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+template <int FMT>
+__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    if (FMT == COLI_KV_BF16)
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    else
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// two e4m3 values to two f16 values (exact; NaN stays NaN)
+__device__ __forceinline__ uint32_t widen(uint32_t two_bytes) {
+    uint32_t y;
+    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}" : "=r"(y) : "r"(two_bytes));
+    return y;
+}
+__device__ __forceinline__ uint32_t widen_hi(uint32_t four_bytes) {
+    uint32_t y;
+    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, hi;\n\t}" : "=r"(y) : "r"(four_bytes));
+    return y;
+}
+
+// the leading part of (a, b) in the matrix type as two packed 16-bit values; a, b keep the rest
+template <int FMT>
+__device__ __forceinline__ uint32_t take_part(float &a, float &b) {
+    uint32_t r;
+    if (FMT == COLI_KV_BF16) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+        a -= __low2float(h);
+        b -= __high2float(h);
+        r = *reinterpret_cast<const uint32_t *>(&h);
+    } else {
+        const __half2 h = __floats2half2_rn(a, b);
+        a -= __low2float(h);
+        b -= __high2float(h);
+        r = *reinterpret_cast<const uint32_t *>(&h);
+    }
+    return r;
+}
+
+__device__ __forceinline__ float load_act(const void *p, int64_t i, int act) {
+    return act == COLI_ACT_F32 ? ((const float *)p)[i]
+           : act == COLI_ACT_BF16 ? to_f32(((const __nv_bfloat16 *)p)[i])
+                                  : to_f32(((const __half *)p)[i]);
+}
+
+// a place on the line of units
+struct Cursor {
+    int b, hv, u, units;  // sequence, head group, unit of the item, units of the item
+};
+
+}  // namespace attn
+
+// FMT the cache type, DP the head size rounded up to 64, 128 or 256, NT groups of 8 query heads per CTA,
+// WIDE: q (and p in bf16) in more parts
+template <int FMT, int DP, int NT, bool WIDE>
+struct AttnTraits {
+    static constexpr int kFmt = FMT, kDim = DP, kNT = NT;
+    static constexpr int kSize = FMT == COLI_KV_E4M3 ? 1 : 2;
+    static constexpr int kRow = DP * kSize;                       // bytes of a row in shared memory
+    static constexpr int kTile = 32 / kSize;                      // tokens of a warp's tile
+    static constexpr int kMT = kTile / 16;
+    static constexpr int kWarps = attn_warps(DP);
+    static constexpr int kStages = kAttnStages;
+    static constexpr int kStageBytes = 2 * kTile * kRow;          // K and V
+    static constexpr int kHeads = 8 * NT;
+    static constexpr int kQParts = !WIDE ? 1 : FMT == COLI_KV_BF16 ? 3 : 2;
+    static constexpr int kPParts = WIDE && FMT == COLI_KV_BF16 ? 3 : 2;
+    static constexpr int kKS = DP / 16;                           // products of 16 along the head
+    static constexpr int kQWords = kQParts * NT * kKS * 32;       // uint2
+    // p is kept times 2^kShift, so that the second f16 part of a small p is still above f16's smallest step
+    static constexpr int kShift = FMT == COLI_KV_BF16 ? 0 : 14;
+    static_assert(kWarps * kStages * kStageBytes + kQWords * 8 + kWarps * kHeads * 8 + kHeads * 4 + kWarps * kStages * 4 +
+                          (kAttnMaxSeqs + 1) * 4 + 64 <=
+                      (227 << 10) / attn_ctas_per_sm(DP) - 1024,
+                  "shared memory of an SM");
+    static_assert(kHeads * DP * 4 <= kStageBytes, "a warp's sums fit its free stage");
+    static_assert(kWarps * kTile == attn_unit(FMT, DP), "unit");
+    static constexpr size_t smem(int seqs) {
+        return (size_t)kWarps * kStages * kStageBytes + (size_t)kQWords * 8 + kWarps * kHeads * 8 + kHeads * 4 +
+               kWarps * kStages * 4 + ((size_t)seqs + 1) * 4 + 64;
+    }
+};
+
+template <typename T>
+__global__ void __launch_bounds__(T::kWarps * 32, attn_ctas_per_sm(T::kDim)) attn_stream_kernel(const AttnParams P, const AttnWork W) {
+    using namespace attn;
+    constexpr int DP = T::kDim, NT = T::kNT, kThreads = T::kWarps * 32, FMT = T::kFmt;
+    extern __shared__ __align__(128) unsigned char sm[];
+    unsigned char *ring = sm;
+    uint2 *qf = reinterpret_cast<uint2 *>(ring + T::kWarps * T::kStages * T::kStageBytes);
+    float2 *ml = reinterpret_cast<float2 *>(qf + T::kQWords);          // [warp][head] (m, l)
+    float *qs = reinterpret_cast<float *>(ml + T::kWarps * T::kHeads);  // [head] factor of the products
+    uint32_t *seen = reinterpret_cast<uint32_t *>(qs + T::kHeads);     // [warp][stage] rows that hold a token
+    int *pre = reinterpret_cast<int *>(seen + T::kWarps * T::kStages);  // [seqs + 1] units before a sequence
+    int *scan = pre + P.seqs + 1;                                      // [16]
+    const int tid = threadIdx.x, w = tid / 32, lane = tid % 32, g = lane >> 2, c = lane & 3;
+
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+    // ---- units before each sequence (per head group)
+    auto units_of = [&](int b) {
+        int first, end, why;
+        kv_span(P.lens[b], P.table_width, P.cache.page_size, P.window, first, end, why);
+        if (why && blockIdx.x == 0 && P.err) atomicOr(P.err, COLI_LAYER_BAD_POSITION);
+        return (end - first + W.unit - 1) / W.unit;
+    };
+    const int per = (P.seqs + kThreads - 1) / kThreads;
+    const int b0 = min(tid * per, P.seqs), b1 = min(b0 + per, P.seqs);
+    int mine = 0;
+    for (int b = b0; b < b1; b++) {
+        const int u = units_of(b);
+        pre[b + 1] = u;
+        mine += u;
+    }
+    int run = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, run, o);
+        if (lane >= o) run += v;
+    }
+    if (lane == 31) scan[w] = run;
+    __syncthreads();
+    int before = run - mine;
+    for (int i = 0; i < w; i++) before += scan[i];
+    for (int b = b0; b < b1; b++) {
+        const int u = pre[b + 1];
+        before += u;
+        pre[b + 1] = before;
+    }
+    if (tid == 0) pre[0] = 0;
+    __syncthreads();
+    const int64_t total = (int64_t)pre[P.seqs] * W.groups;
+    const int ctas = (int)min((int64_t)gridDim.x, total);
+    if (blockIdx.x == 0)
+        for (int b = tid; b <= P.seqs; b += kThreads) W.prefix[b] = pre[b];
+
+    // ---- sequences with nothing to see
+    for (int b = blockIdx.x; b < P.seqs; b += gridDim.x) {
+        if (pre[b + 1] != pre[b]) continue;
+        for (int i = tid; i < P.q_heads * P.dim; i += kThreads)
+            store_act(P.out, b * P.out_stride + i, 0.f, P.act);
+        if (P.lse)
+            for (int i = tid; i < P.q_heads; i += kThreads) P.lse[(int64_t)b * P.q_heads + i] = -INFINITY;
+    }
+    if ((int)blockIdx.x >= ctas) return;
+
+    // ---- this CTA's run of units
+    const int64_t x0 = attn_run_start(blockIdx.x, total, ctas), x1 = attn_run_start(blockIdx.x + 1, total, ctas);
+    Cursor at;
+    {
+        // the last sequence whose units begin at or before x0
+        int lo = 0, hi = P.seqs;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) / 2;
+            if ((int64_t)pre[mid] * W.groups <= x0) lo = mid;
+            else hi = mid;
+        }
+        at.b = lo;
+        at.units = pre[lo + 1] - pre[lo];
+        const int64_t r = x0 - (int64_t)pre[lo] * W.groups;
+        at.hv = (int)(r / at.units);
+        at.u = (int)(r - (int64_t)at.hv * at.units);
+    }
+    const int n_units = (int)(x1 - x0);
+    auto advance = [&](Cursor &k) {
+        if (++k.u < k.units) return;
+        k.u = 0;
+        if (++k.hv < W.groups) return;
+        k.hv = 0;
+        do {
+            k.b++;
+        } while (k.b < P.seqs && pre[k.b + 1] == pre[k.b]);
+        if (k.b < P.seqs) k.units = pre[k.b + 1] - pre[k.b];
+    };
+
+    // ---- copies: lane r looks up row r of the tile one tile ahead of its copy
+    unsigned char *my_ring = ring + w * T::kStages * T::kStageBytes;
+    const uint32_t my_ring_a = smem_addr(my_ring);
+    Cursor ld = at;
+    int ld_left = n_units;
+    long long off = -1;  // of the tile that is copied next
+    auto look_up = [&]() {
+        off = -1;
+        if (ld_left <= 0) return;
+        int first, end, why;
+        kv_span(P.lens[ld.b], P.table_width, P.cache.page_size, P.window, first, end, why);
+        const int t = first + (ld.u * T::kWarps + w) * T::kTile + lane;
+        if (lane < T::kTile && t < end) {
+            off = kv_row(P.cache, P.table + (int64_t)ld.b * P.table_width, P.table_width, t, ld.hv / W.chunks, why);
+            if (off < 0 && P.err) atomicOr(P.err, COLI_LAYER_BAD_PAGE);
+        }
+        advance(ld);
+        ld_left--;
+    };
+    const char *kbase = (const char *)P.k_cache, *vbase = (const char *)P.v_cache;
+    constexpr int kChunks = T::kRow / 16, kRowsPer = 32 / kChunks;
+    const int ch = lane % kChunks, sub = lane / kChunks;
+    const bool in_row = ch * 16 < P.dim * T::kSize;
+    auto place = [](int row, int chunk) -> uint32_t {
+        // 16-byte chunks of a row are exchanged so that 8 rows' same chunk lie in 8 bank groups
+        if (T::kRow >= 128) return row * T::kRow + ((chunk ^ (row & 7)) << 4);
+        const int line = row >> 1;
+        return line * 128 + (((((row & 1) << 2) | chunk) ^ (line & 3)) << 4);
+    };
+    auto copy_tile = [&](int stage) {
+        const unsigned rows = __ballot_sync(0xffffffffu, off >= 0);
+        if (lane == 0) seen[w * T::kStages + stage] = rows;
+        if (rows) {
+            const uint32_t dst = my_ring_a + stage * T::kStageBytes;
+#pragma unroll
+            for (int i = 0; i < T::kTile / kRowsPer; i++) {
+                const int row = i * kRowsPer + sub;
+                const long long o = __shfl_sync(0xffffffffu, off, row);
+                const bool ok = o >= 0 && in_row;
+                const long long byte = ok ? o * T::kSize + ch * 16 : 0;
+                const uint32_t d = dst + place(row, ch);
+                copy16(d, kbase + byte, ok);
+                copy16(d + T::kTile * T::kRow, vbase + byte, ok);
+            }
+        }
+        copy_commit();
+        look_up();
+    };
+
+    look_up();
+#pragma unroll
+    for (int i = 0; i < T::kStages; i++) copy_tile(i);
+
+    float o[T::kKS][NT][4], m[NT][2], l[NT][2], sc[NT][2];
+    int stage = 0;
+    bool fresh = true;
+    int seg0 = 0;  // first unit of the current segment
+    for (int it = 0; it < n_units; it++) {
+        if (fresh) {
+            // ---- q of the item: parts in the order the matrix instruction takes them
+            fresh = false;
+            seg0 = at.u;
+            const int kh = at.hv / W.chunks, h0 = (at.hv - kh * W.chunks) * T::kHeads;
+            const int group = P.q_heads / P.kv_heads;
+            const float ks = P.scale * 1.4426950408889634f * (P.k_scale ? P.k_scale[kh] : 1.f);
+            for (int h = w; h < T::kHeads; h += T::kWarps) {
+                const bool real = h0 + h < group;
+                const int64_t src = at.b * P.q_stride + (int64_t)(kh * group + h0 + h) * P.dim;
+                float x[DP / 32];  // pairs: 2 * lane + 64 * i (+ 1)
+                float top = 0.f;
+#pragma unroll
+                for (int i = 0; i < DP / 64; i++)
+#pragma unroll
+                    for (int j = 0; j < 2; j++) {
+                        const int d = 64 * i + 2 * lane + j;
+                        x[2 * i + j] = real && d < P.dim ? load_act(P.q, src + d, P.act) : 0.f;
+                        top = fmaxf(top, fabsf(x[2 * i + j]));
+                    }
+                float up = 1.f, down = 1.f;
+                if (FMT != COLI_KV_BF16) {
+                    // the largest element of the head at 2^14..2^15
+#pragma unroll
+                    for (int s = 16; s; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
+                    int e = (int)((__float_as_uint(top) >> 23) & 0xff) - 127;
+                    e = max(e, -100);
+                    if (top > 0.f && e < 128) {
+                        up = __uint_as_float((unsigned)(127 + 14 - e) << 23);
+                        down = __uint_as_float((unsigned)(127 - 14 + e) << 23);
+                    }
+                }
+                if (lane == 0) qs[h] = ks * down;
+#pragma unroll
+                for (int i = 0; i < DP / 64; i++) {
+                    float a = x[2 * i] * up, b = x[2 * i + 1] * up;
+                    const int d = 64 * i + 2 * lane;  // even
+                    // which 16-product, lane of the group and register of the fragment hold (d, d + 1)
+                    const int k = d & 15;
+                    const int cc = FMT == COLI_KV_E4M3 ? k >> 2 : (k & 7) >> 1;
+                    const int rr = FMT == COLI_KV_E4M3 ? (k >> 1) & 1 : k >> 3;
+#pragma unroll
+                    for (int p = 0; p < T::kQParts; p++) {
+                        const uint32_t v = take_part<FMT>(a, b);
+                        uint32_t *to = reinterpret_cast<uint32_t *>(
+                            qf + ((p * NT + h / 8) * T::kKS + (d >> 4)) * 32 + (h & 7) * 4 + cc);
+                        to[rr] = v;
+                    }
+                }
+            }
+            __syncthreads();
+#pragma unroll
+            for (int n = 0; n < NT; n++) {
+#pragma unroll
+                for (int j = 0; j < 2; j++) {
+                    m[n][j] = -INFINITY;
+                    l[n][j] = 0.f;
+                    sc[n][j] = qs[n * 8 + 2 * c + j];
+                }
+#pragma unroll
+                for (int i = 0; i < T::kKS; i++)
+#pragma unroll
+                    for (int j = 0; j < 4; j++) o[i][n][j] = 0.f;
+            }
+        }
+
+        copy_wait<T::kStages - 1>();
+        __syncwarp();
+        const unsigned rows = seen[w * T::kStages + stage];
+        if (rows) {
+            const uint32_t kt = my_ring_a + stage * T::kStageBytes, vt = kt + T::kTile * T::kRow;
+            float s[T::kMT][NT][4];
+#pragma unroll
+            for (int i = 0; i < T::kMT; i++)
+#pragma unroll
+                for (int n = 0; n < NT; n++)
+#pragma unroll
+                    for (int j = 0; j < 4; j++) s[i][n][j] = 0.f;
+            const int lr = lane & 7, li = lane >> 3;
+            // ---- S^T = K q^T
+            if (FMT != COLI_KV_E4M3) {
+                const int row = lr + (li & 1) * 8;
+#pragma unroll
+                for (int ks = 0; ks < T::kKS; ks++) {
+                    uint32_t a[4];
+                    ldm4(a, kt + place(row, 2 * ks + (li >> 1)));
+#pragma unroll
+                    for (int p = 0; p < T::kQParts; p++)
+#pragma unroll
+                        for (int n = 0; n < NT; n++) {
+                            const uint2 q = qf[((p * NT + n) * T::kKS + ks) * 32 + lane];
+                            mma<FMT>(s[0][n], a, q.x, q.y);
+                        }
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < T::kMT; i++) {
+                    const int row = i * 16 + lr + (li & 1) * 8;
+#pragma unroll
+                    for (int k2 = 0; k2 < T::kKS / 2; k2++) {
+                        uint32_t raw[4];
+                        ldm4(raw, kt + place(row, 2 * k2 + (li >> 1)));
+#pragma unroll
+                        for (int hf = 0; hf < 2; hf++) {
+                            const uint32_t a[4] = {widen(raw[2 * hf]), widen(raw[2 * hf + 1]), widen_hi(raw[2 * hf]),
+                                                   widen_hi(raw[2 * hf + 1])};
+#pragma unroll
+                            for (int p = 0; p < T::kQParts; p++)
+#pragma unroll
+                                for (int n = 0; n < NT; n++) {
+                                    const uint2 q = qf[((p * NT + n) * T::kKS + 2 * k2 + hf) * 32 + lane];
+                                    mma<FMT>(s[i][n], a, q.x, q.y);
+                                }
+                        }
+                    }
+                }
+            }
+            // ---- softmax over the tile's tokens, head by head
+            uint32_t pf[T::kPParts][T::kMT][NT][2];
+            float f[NT][2];
+            const bool all = rows == (T::kTile == 32 ? 0xffffffffu : 0xffffu);
+#pragma unroll
+            for (int n = 0; n < NT; n++) {
+#pragma unroll
+                for (int j = 0; j < 2; j++) {
+                    float top = -INFINITY;
+#pragma unroll
+                    for (int i = 0; i < T::kMT; i++)
+#pragma unroll
+                        for (int r = 0; r < 2; r++) {
+                            float x = s[i][n][2 * r + j] * sc[n][j];
+                            if (!all && !((rows >> (i * 16 + r * 8 + g)) & 1)) x = -INFINITY;
+                            s[i][n][2 * r + j] = x;
+                            top = fmaxf(top, x);
+                        }
+#pragma unroll
+                    for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+                    const float mn = fmaxf(m[n][j], ceilf(top));
+                    const float ref = mn == -INFINITY ? 0.f : mn;
+                    f[n][j] = exp2_fast(m[n][j] - ref);  // exact: an integer power; 0 from -inf
+                    m[n][j] = mn;
+                    float sum = 0.f;
+#pragma unroll
+                    for (int i = 0; i < T::kMT; i++)
+#pragma unroll
+                        for (int r = 0; r < 2; r++) {
+                            const float p = exp2_fast(s[i][n][2 * r + j] - ref + (float)T::kShift);
+                            s[i][n][2 * r + j] = p;
+                            sum += p;
+                        }
+                    l[n][j] = fmaf(l[n][j], f[n][j], sum);
+                }
+#pragma unroll
+                for (int i = 0; i < T::kMT; i++)
+#pragma unroll
+                    for (int r = 0; r < 2; r++) {
+                        float a = s[i][n][2 * r], b = s[i][n][2 * r + 1];
+#pragma unroll
+                        for (int p = 0; p < T::kPParts; p++) pf[p][i][n][r] = transpose8(take_part<FMT>(a, b));
+                    }
+            }
+            // ---- O^T += V^T P^T
+            if (FMT != COLI_KV_E4M3) {
+                const int row = lr + (li >> 1) * 8;
+#pragma unroll
+                for (int d = 0; d < T::kKS; d++) {
+                    uint32_t a[4];
+                    ldm4t(a, vt + place(row, 2 * d + (li & 1)));
+#pragma unroll
+                    for (int n = 0; n < NT; n++) {
+                        float t[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                        for (int p = T::kPParts - 1; p >= 0; p--) mma<FMT>(t, a, pf[p][0][n][0], pf[p][0][n][1]);
+#pragma unroll
+                        for (int j = 0; j < 4; j++) o[d][n][j] = fmaf(o[d][n][j], f[n][j & 1], t[j]);
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int d2 = 0; d2 < T::kKS / 2; d2++) {
+                    float t[2][NT][4];
+#pragma unroll
+                    for (int hf = 0; hf < 2; hf++)
+#pragma unroll
+                        for (int n = 0; n < NT; n++)
+#pragma unroll
+                            for (int j = 0; j < 4; j++) t[hf][n][j] = 0.f;
+#pragma unroll
+                    for (int i = 0; i < T::kMT; i++) {
+                        uint32_t raw[4];
+                        ldm4t(raw, vt + place(i * 16 + lr + (li & 1) * 8, 2 * d2 + (li >> 1)));
+#pragma unroll
+                        for (int hf = 0; hf < 2; hf++) {
+                            // bytes (token, dim): 00 01 10 11 -> even dim's two tokens, odd dim's two tokens
+                            const uint32_t x = __byte_perm(raw[2 * hf], 0, 0x3120), y = __byte_perm(raw[2 * hf + 1], 0, 0x3120);
+                            const uint32_t a[4] = {widen(x), widen_hi(x), widen(y), widen_hi(y)};
+#pragma unroll
+                            for (int n = 0; n < NT; n++)
+#pragma unroll
+                                for (int p = T::kPParts - 1; p >= 0; p--)
+                                    mma<FMT>(t[hf][n], a, pf[p][i][n][0], pf[p][i][n][1]);
+                        }
+                    }
+#pragma unroll
+                    for (int hf = 0; hf < 2; hf++)
+#pragma unroll
+                        for (int n = 0; n < NT; n++)
+#pragma unroll
+                            for (int j = 0; j < 4; j++)
+                                o[2 * d2 + hf][n][j] = fmaf(o[2 * d2 + hf][n][j], f[n][j & 1], t[hf][n][j]);
+                }
+            }
+            __syncwarp();
+        }
+
+        if (at.u + 1 == at.units || it + 1 == n_units) {
+            // ---- the segment ends: the warps' sums through their free stages
+            float *mo = reinterpret_cast<float *>(my_ring + stage * T::kStageBytes);
+#pragma unroll
+            for (int n = 0; n < NT; n++) {
+#pragma unroll
+                for (int j = 0; j < 2; j++) {
+                    float x = l[n][j];
+#pragma unroll
+                    for (int d = 4; d < 32; d <<= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
+                    if (g == 0) ml[w * T::kHeads + n * 8 + 2 * c + j] = make_float2(m[n][j], x);
+                }
+#pragma unroll
+                for (int i = 0; i < T::kKS; i++)
+#pragma unroll
+                    for (int j = 0; j < 4; j++) {
+                        const int head = n * 8 + 2 * c + (j & 1);
+                        const int d = 16 * i + (FMT == COLI_KV_E4M3 ? 2 * g + (j >> 1) : g + 8 * (j >> 1));
+                        mo[head * DP + (d ^ (c << 3))] = o[i][n][j];
+                    }
+            }
+            __syncthreads();
+            const int kh = at.hv / W.chunks, h0 = (at.hv - kh * W.chunks) * T::kHeads;
+            const int group = P.q_heads / P.kv_heads;
+            const bool whole = seg0 == 0 && at.u + 1 == at.units;
+            const int slot = 2 * blockIdx.x + (seg0 == 0 ? 1 : 0);
+            const float vs = P.v_scale ? P.v_scale[kh] : 1.f;
+            for (int i = tid; i < T::kHeads * DP; i += kThreads) {
+                const int h = i / DP, d = i % DP;
+                if (h0 + h >= group) break;
+                float top = -INFINITY;
+#pragma unroll
+                for (int k = 0; k < T::kWarps; k++) top = fmaxf(top, ml[k * T::kHeads + h].x);
+                const float ref = top == -INFINITY ? 0.f : top;
+                float x = 0.f, sum = 0.f;
+#pragma unroll
+                for (int k = 0; k < T::kWarps; k++) {
+                    const float2 e = ml[k * T::kHeads + h];
+                    const float e2 = exp2_fast(e.x - ref);
+                    const float *src = reinterpret_cast<const float *>(ring + (k * T::kStages + stage) * T::kStageBytes);
+                    x = fmaf(src[h * DP + (d ^ (((h & 7) >> 1) << 3))], e2, x);
+                    sum = fmaf(e.y, e2, sum);
+                }
+                const int qh = kh * group + h0 + h;
+                if (whole) {
+                    if (d < P.dim)
+                        store_act(P.out, at.b * P.out_stride + (int64_t)qh * P.dim + d, sum == 0.f ? 0.f : x / sum * vs, P.act);
+                    if (d == 0 && P.lse)
+                        P.lse[(int64_t)at.b * P.q_heads + qh] = attn_lse(ref, sum, T::kShift);
+                } else {
+                    W.part_o[((int64_t)slot * T::kHeads + h) * DP + d] = x;
+                    if (d == 0) W.part_ml[(int64_t)slot * T::kHeads + h] = make_float2(top, sum);
+                }
+            }
+            __syncthreads();
+            fresh = true;
+        }
+        copy_tile(stage);
+        stage = stage + 1 == T::kStages ? 0 : stage + 1;
+        advance(at);
+    }
+    copy_wait<0>();
+}
+
+template <typename T>
+cudaError_t launch_stream(const AttnParams &P, const AttnWork &W, int grid, cudaStream_t s) {
+    static std::atomic<uint64_t> ready{0};  // devices whose limit is raised
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+    if (!bit || !(ready.load(std::memory_order_relaxed) & bit)) {
+        e = cudaFuncSetAttribute(attn_stream_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)T::smem(kAttnMaxSeqs));
+        if (e != cudaSuccess) return e;
+        ready.fetch_or(bit, std::memory_order_relaxed);
+    }
+    attn_stream_kernel<T><<<grid, T::kWarps * 32, T::smem(P.seqs), s>>>(P, W);
+    return cudaGetLastError();
+}
+
+template <int FMT, int DP, int NT>
+cudaError_t launch_wide(const AttnParams &P, const AttnWork &W, int grid, cudaStream_t s) {
+    return W.wide ? launch_stream<AttnTraits<FMT, DP, NT, true>>(P, W, grid, s)
+                  : launch_stream<AttnTraits<FMT, DP, NT, false>>(P, W, grid, s);
+}
+
+template <int FMT, int DP>
+cudaError_t launch_heads(const AttnParams &P, const AttnWork &W, int grid, cudaStream_t s) {
+    return W.nt == 1 ? launch_wide<FMT, DP, 1>(P, W, grid, s) : launch_wide<FMT, DP, 2>(P, W, grid, s);
+}
+
+template <int FMT>
+cudaError_t launch_dims(const AttnParams &P, const AttnWork &W, int grid, cudaStream_t s) {
+    return W.dim == 64    ? launch_heads<FMT, 64>(P, W, grid, s)
+           : W.dim == 128 ? launch_heads<FMT, 128>(P, W, grid, s)
+                          : launch_heads<FMT, 256>(P, W, grid, s);
+}
+
+}  // namespace colimoe

@@ -2,15 +2,14 @@
 // launches. No allocation, no synchronisation.
 #include <cmath>
 
+#include "attn.h"
 #include "host.h"
-#include "layer.h"
 
 using namespace colimoe;
 
 namespace {
 
 constexpr int kMaxHeads = 1024;
-constexpr int kMaxSeqs = 4096;
 constexpr int kMaxHeadDim = 256;
 constexpr int64_t kMaxStride = (int64_t)1 << 40;  // keeps row * stride in 64 bits
 
@@ -54,7 +53,7 @@ int stride_of(int64_t given, int64_t row, int64_t &out) {
 int check_attn(const coli_attn_desc *d, const coli_kv_cache *c) {
     if (!d) return COLI_MOE_EINVAL;
     if (int rc = check_cache(c)) return rc;
-    if (d->seqs < 1 || d->seqs > kMaxSeqs || d->q_heads < 1 || d->q_heads > kMaxHeads || d->q_heads % c->heads ||
+    if (d->seqs < 1 || d->seqs > kAttnMaxSeqs || d->q_heads < 1 || d->q_heads > kMaxHeads || d->q_heads % c->heads ||
         d->table_width < 1 || (int64_t)d->table_width * c->page_size > INT32_MAX || !act_ok(d->act) || d->window < 0 ||
         !std::isfinite(d->scale))
         return COLI_MOE_EINVAL;

@@ -398,7 +398,7 @@ def test_attention_many_sequences(q):
 
 
 def test_attention_most_sequences(q):
-    check_attend(q, 20, [i % 3 for i in range(4096)], (2, 1), 16, page=2)
+    check_attend(q, 20, [i % 3 for i in range(2048)], (2, 1), 16, page=2)
 
 
 def test_attention_peaked_and_flat_scores(q):

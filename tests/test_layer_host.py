@@ -94,7 +94,7 @@ def test_append_refusals(q, over, code):
 
 
 @pytest.mark.parametrize("desc,args,code", [
-    (dict(seqs=0), {}, "EINVAL"), (dict(seqs=5000), {}, "EINVAL"), (dict(q_heads=0), {}, "EINVAL"),
+    (dict(seqs=0), {}, "EINVAL"), (dict(seqs=2049), {}, "EINVAL"), (dict(q_heads=0), {}, "EINVAL"),
     (dict(q_heads=6), {}, "EINVAL"), (dict(q_heads=2048), {}, "EINVAL"), (dict(table_width=0), {}, "EINVAL"),
     (dict(table_width=1 << 27), {}, "EINVAL"), (dict(act=-1), {}, "EINVAL"), (dict(window=-1), {}, "EINVAL"),
     (dict(scale=float("nan")), {}, "EINVAL"), (dict(scale=float("inf")), {}, "EINVAL"), (dict(q_stride=8), {}, "EINVAL"),
