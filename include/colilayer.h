@@ -40,6 +40,7 @@ extern "C" {
 #define COLI_LAYER_BAD_PAGE 1     /* a page number outside [0, pages) */
 #define COLI_LAYER_BAD_POSITION 2 /* a position or length beyond table_width * page_size, or below 0 */
 #define COLI_LAYER_BAD_SEQUENCE 4 /* a sequence number outside [0, seqs) */
+#define COLI_LAYER_TIMEOUT 8      /* a copy of cached rows did not arrive within its bounded wait */
 
 /* A paged cache: `pages` pages of `page_size` tokens, for keys and (with the same strides) for
  * values. The row of `dim` contiguous elements of page p, slot s, kv head h starts

@@ -1,6 +1,8 @@
 // attn.h — what the streaming and the join kernel of coli_attn_decode share. Internal to libcolimoe.
 #pragma once
 
+#include <cuda.h>
+
 #include "act.cuh"
 #include "layer.h"
 
@@ -24,6 +26,10 @@ struct AttnWork {
     int32_t chunks;  // head groups per kv head
     int32_t groups;  // head groups per sequence
     int32_t unit;    // tokens of a unit
+    int32_t box_rows;    // K and V come as boxes of so many tokens through tensor maps; 0: row by row
+    int32_t whole_rows;  // a box holds whole rows, not one span of 128 bytes
+    KvDivide divide;     // by the page size
+    int32_t mask;        // tiles begin at tokens that are 0 under it
     int32_t *prefix; // [seqs + 1] units (per head group) before each sequence
     float2 *part_ml; // [2 * CTAs][8 * nt] (m, l) of a run's first and last cut item
     float *part_o;   // [2 * CTAs][8 * nt][dim]
@@ -45,8 +51,13 @@ __device__ __forceinline__ float attn_lse(float m, float l, int shift) {
     return l == 0.f ? -INFINITY : (m - (float)shift + log2f(l)) * 0.6931471805599453f;
 }
 
-cudaError_t launch_attn_bf16(const AttnParams &P, const AttnWork &W, int grid, cudaStream_t s);
-cudaError_t launch_attn_f16(const AttnParams &P, const AttnWork &W, int grid, cudaStream_t s);
-cudaError_t launch_attn_e4m3(const AttnParams &P, const AttnWork &W, int grid, cudaStream_t s);
+// tensor maps of K and V: (element of a span, slot, span, head, page)
+struct AttnMaps {
+    CUtensorMap k, v;
+};
+
+cudaError_t launch_attn_bf16(const AttnParams &P, const AttnWork &W, const AttnMaps &M, int grid, cudaStream_t s);
+cudaError_t launch_attn_f16(const AttnParams &P, const AttnWork &W, const AttnMaps &M, int grid, cudaStream_t s);
+cudaError_t launch_attn_e4m3(const AttnParams &P, const AttnWork &W, const AttnMaps &M, int grid, cudaStream_t s);
 
 }  // namespace colimoe

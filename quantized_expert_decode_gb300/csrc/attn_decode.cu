@@ -1,9 +1,14 @@
 // attn_decode.cu — coli_attn_decode: how a call is laid out, and the join of the items that a run's
 // border cut (attn_kernel.cuh has the streaming kernel).
+#include <cudaTypedefs.h>
+
 #include "attn.h"
 #include "host.h"
 
 namespace colimoe {
+
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();  // prefill.cu
+
 namespace {
 
 constexpr int kJoinThreads = 256;
@@ -92,9 +97,17 @@ Layout layout_of(const AttnParams &P) {
     L.w.chunks = (group + 8 * L.w.nt - 1) / (8 * L.w.nt);
     L.w.groups = P.kv_heads * L.w.chunks;
     L.w.unit = attn_unit(P.fmt, L.w.dim);
+    // the tallest box that divides a page, up to a tile
+    const int tile = P.fmt == COLI_KV_E4M3 ? 32 : 16, size = P.fmt == COLI_KV_E4M3 ? 1 : 2;
+    for (int r = tile; r >= 8 && !L.w.box_rows; r /= 2)
+        if (P.cache.page_size % r == 0) L.w.box_rows = r;
+    L.w.divide = kv_divide_by(P.cache.page_size);
+    L.w.mask = L.w.box_rows ? L.w.box_rows - 1 : 0;
+    // (a stage holds a span's rows one below the other for the whole tile)
+    L.w.whole_rows = L.w.box_rows == tile && P.dim * size % (L.w.dim * size < 128 ? L.w.dim * size : 128) == 0;
     // no more CTAs than units that the page tables can name
     const int64_t seen = P.window > 0 ? P.window : (int64_t)P.table_width * P.cache.page_size;
-    const int64_t most = ((seen + L.w.unit - 1) / L.w.unit) * P.seqs * L.w.groups;
+    const int64_t most = ((seen + L.w.mask + L.w.unit - 1) / L.w.unit) * P.seqs * L.w.groups;
     const int64_t ctas = (int64_t)num_sms() * attn_ctas_per_sm(L.w.dim);
     L.grid = (int)(most < ctas ? most : ctas);
     auto up = [](size_t n) { return (n + 255) / 256 * 256; };
@@ -102,6 +115,34 @@ Layout layout_of(const AttnParams &P) {
     L.o = L.ml + up((size_t)2 * L.grid * 8 * L.w.nt * sizeof(float2));
     L.total = L.o + up((size_t)2 * L.grid * 8 * L.w.nt * L.w.dim * 4);
     return L;
+}
+
+// Maps for boxes of W.box_rows tokens; false where the strides are none that a tensor map takes. Rows whose
+// size is whole spans of 128 bytes are a fifth axis, and a box takes them whole; other rows come span by
+// span, the last one filled up with zeros.
+bool make_maps(const AttnParams &P, const AttnWork &W, AttnMaps &M) {
+    const int size = P.fmt == COLI_KV_E4M3 ? 1 : 2;
+    const KvShape &c = P.cache;
+    PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
+    if (!encode) return false;
+    const int row = W.dim * size, span = (row < 128 ? row : 128) / size;
+    const cuuint64_t dims[5] = {(cuuint64_t)(W.whole_rows ? span : P.dim), (cuuint64_t)c.page_size,
+                                (cuuint64_t)(W.whole_rows ? P.dim / span : 1), (cuuint64_t)P.kv_heads, (cuuint64_t)c.pages};
+    cuuint64_t strides[4] = {(cuuint64_t)c.token_stride * size, (cuuint64_t)span * size, (cuuint64_t)c.head_stride * size,
+                             (cuuint64_t)c.page_stride * size};
+    for (int i = 0; i < 4; i++) {
+        if (strides[i] >> 40) return false;
+        if (strides[i] == 0) strides[i] = 16;  // an axis of one entry
+    }
+    const cuuint32_t box[5] = {(cuuint32_t)span, (cuuint32_t)W.box_rows, (cuuint32_t)(W.whole_rows ? W.dim / span : 1), 1, 1};
+    const cuuint32_t one[5] = {1, 1, 1, 1, 1};
+    const CUtensorMapDataType type = size == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16;
+    auto map = [&](CUtensorMap *m, const void *base) {
+        return encode(m, type, 5, const_cast<void *>(base), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                      span * size == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                      CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    };
+    return map(&M.k, P.k_cache) && map(&M.v, P.v_cache);
 }
 
 }  // namespace
@@ -114,9 +155,11 @@ cudaError_t launch_attn_decode(const AttnParams &P, cudaStream_t s) {
     L.w.prefix = (int32_t *)ws;
     L.w.part_ml = (float2 *)(ws + L.ml);
     L.w.part_o = (float *)(ws + L.o);
-    const cudaError_t e = P.fmt == COLI_KV_BF16  ? launch_attn_bf16(P, L.w, L.grid, s)
-                          : P.fmt == COLI_KV_F16 ? launch_attn_f16(P, L.w, L.grid, s)
-                                                 : launch_attn_e4m3(P, L.w, L.grid, s);
+    AttnMaps M{};
+    if (L.w.box_rows && !make_maps(P, L.w, M)) L.w.box_rows = 0;
+    const cudaError_t e = P.fmt == COLI_KV_BF16  ? launch_attn_bf16(P, L.w, M, L.grid, s)
+                          : P.fmt == COLI_KV_F16 ? launch_attn_f16(P, L.w, M, L.grid, s)
+                                                 : launch_attn_e4m3(P, L.w, M, L.grid, s);
     if (e != cudaSuccess || L.grid == 1) return e;  // one run: no borders
     // the join's blocks start while the streaming kernel runs and wait for its end
     cudaLaunchConfig_t cfg{};

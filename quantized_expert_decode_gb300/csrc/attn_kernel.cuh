@@ -13,8 +13,9 @@
 // per CTA, so a CTA's share does not depend on how the lengths are spread; an item that a run's
 // border cuts leaves partial sums in the workspace, which the join kernel adds up in a fixed order.
 // Within a unit each warp owns one tile: it copies the tile's K and V rows to its own ring of kStages
-// stages with 16-byte asynchronous copies (two tiles in flight while one is computed), and no warp
-// waits for another until the item ends.
+// stages (two tiles in flight while one is computed), and no warp waits for another until the item
+// ends. Where pages hold whole groups of 8 tokens or more the rows come as boxes through tensor maps,
+// one lane per box; else as 16-byte asynchronous copies, one row address per token.
 //
 // Products. Tokens are the rows of the matrix instruction and the query heads its 8 columns, so a
 // group of up to 8 heads fills it: S^T [16 tokens x 8 heads] = K q^T, then O^T [16 dims x 8 heads] +=
@@ -29,12 +30,11 @@
 
 #include "act.cuh"
 #include "attn.h"
+#include "ptx.cuh"
 
 namespace colimoe {
 
 namespace attn {
-
-__device__ __forceinline__ uint32_t smem_addr(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
 
 __device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool valid) {
     const int n = valid ? 16 : 0;  // 0: the 16 bytes are zeroed and src is not read
@@ -42,6 +42,24 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool valid
 }
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N> __device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// box at (element x, slot, span 0, head, page) of a cache
+__device__ __forceinline__ void copy_box(uint32_t dst, const CUtensorMap *map, int x, int slot, int head, int page, uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
+        "l"(map), "r"(x), "r"(slot), "r"(0), "r"(head), "r"(page), "r"(smem_u32(bar))
+        : "memory");
+}
+__device__ __forceinline__ void expect_bytes(uint64_t *bar, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
+}
+// a copy that takes more tries than this (seconds) is given up
+constexpr int kMaxTries = 1 << 18;
+__device__ __forceinline__ bool wait_bytes(uint64_t *bar, uint32_t parity) {
+    for (int i = 0; i < kMaxTries; i++)
+        if (mbar_try_wait(bar, parity)) return true;
+    return false;
+}
 
 __device__ __forceinline__ void ldm4(uint32_t (&r)[4], uint32_t a) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -134,9 +152,12 @@ struct AttnTraits {
     static constexpr int kPParts = WIDE && FMT == COLI_KV_BF16 ? 3 : 2;
     static constexpr int kKS = DP / 16;                           // products of 16 along the head
     static constexpr int kQWords = kQParts * NT * kKS * 32;       // uint2
+    static constexpr int kSpan = kRow < 128 ? kRow : 128;         // bytes of a row in one box
+    static constexpr int kSpans = kRow / kSpan;                   // boxes side by side
+    static_assert(2 * (kTile / 8) * kSpans <= 32, "a lane per box");
     // p is kept times 2^kShift, so that the second f16 part of a small p is still above f16's smallest step
     static constexpr int kShift = FMT == COLI_KV_BF16 ? 0 : 14;
-    static_assert(kWarps * kStages * kStageBytes + kQWords * 8 + kWarps * kHeads * 8 + kHeads * 4 + kWarps * kStages * 4 +
+    static_assert(kWarps * kStages * kStageBytes + kQWords * 8 + kWarps * kHeads * 8 + kHeads * 4 + kWarps * kStages * 12 +
                           (kAttnMaxSeqs + 1) * 4 + 64 <=
                       (227 << 10) / attn_ctas_per_sm(DP) - 1024,
                   "shared memory of an SM");
@@ -144,19 +165,20 @@ struct AttnTraits {
     static_assert(kWarps * kTile == attn_unit(FMT, DP), "unit");
     static constexpr size_t smem(int seqs) {
         return (size_t)kWarps * kStages * kStageBytes + (size_t)kQWords * 8 + kWarps * kHeads * 8 + kHeads * 4 +
-               kWarps * kStages * 4 + ((size_t)seqs + 1) * 4 + 64;
+               kWarps * kStages * 12 + ((size_t)seqs + 1) * 4 + 64;
     }
 };
 
 template <typename T>
-__global__ void __launch_bounds__(T::kWarps * 32, attn_ctas_per_sm(T::kDim)) attn_stream_kernel(const AttnParams P, const AttnWork W) {
+__global__ void __launch_bounds__(T::kWarps * 32, attn_ctas_per_sm(T::kDim)) attn_stream_kernel(const AttnParams P, const AttnWork W, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
     using namespace attn;
     constexpr int DP = T::kDim, NT = T::kNT, kThreads = T::kWarps * 32, FMT = T::kFmt;
-    extern __shared__ __align__(128) unsigned char sm[];
+    extern __shared__ __align__(1024) unsigned char sm[];
     unsigned char *ring = sm;
     uint2 *qf = reinterpret_cast<uint2 *>(ring + T::kWarps * T::kStages * T::kStageBytes);
     float2 *ml = reinterpret_cast<float2 *>(qf + T::kQWords);          // [warp][head] (m, l)
-    float *qs = reinterpret_cast<float *>(ml + T::kWarps * T::kHeads);  // [head] factor of the products
+    uint64_t *bars = reinterpret_cast<uint64_t *>(ml + T::kWarps * T::kHeads);  // [warp][stage]
+    float *qs = reinterpret_cast<float *>(bars + T::kWarps * T::kStages);  // [head] factor of the products
     uint32_t *seen = reinterpret_cast<uint32_t *>(qs + T::kHeads);     // [warp][stage] rows that hold a token
     int *pre = reinterpret_cast<int *>(seen + T::kWarps * T::kStages);  // [seqs + 1] units before a sequence
     int *scan = pre + P.seqs + 1;                                      // [16]
@@ -169,7 +191,7 @@ __global__ void __launch_bounds__(T::kWarps * 32, attn_ctas_per_sm(T::kDim)) att
         int first, end, why;
         kv_span(P.lens[b], P.table_width, P.cache.page_size, P.window, first, end, why);
         if (why && blockIdx.x == 0 && P.err) atomicOr(P.err, COLI_LAYER_BAD_POSITION);
-        return (end - first + W.unit - 1) / W.unit;
+        return (end - (first & ~W.mask) + W.unit - 1) / W.unit;  // tiles begin at a box's first token
     };
     const int per = (P.seqs + kThreads - 1) / kThreads;
     const int b0 = min(tid * per, P.seqs), b1 = min(b0 + per, P.seqs);
@@ -240,55 +262,114 @@ __global__ void __launch_bounds__(T::kWarps * 32, attn_ctas_per_sm(T::kDim)) att
         if (k.b < P.seqs) k.units = pre[k.b + 1] - pre[k.b];
     };
 
-    // ---- copies: lane r looks up row r of the tile one tile ahead of its copy
+    // ---- copies: rows or boxes are looked up in the page table one tile ahead of their copy
     unsigned char *my_ring = ring + w * T::kStages * T::kStageBytes;
-    const uint32_t my_ring_a = smem_addr(my_ring);
+    const uint32_t my_ring_a = smem_u32(my_ring);
+    uint64_t *my_bars = bars + w * T::kStages;
+    if (lane == 0) {
+        for (int i = 0; i < T::kStages; i++) mbar_init(my_bars + i, 1);
+        fence_mbar_init();
+    }
+    __syncwarp();
+    // 16-byte chunks of a 128-byte span are exchanged so that 8 rows' same chunk lie in 8 bank groups (the
+    // 128-byte swizzle of a tensor copy; its 64-byte one for rows of 64 bytes)
+    auto place = [](int row, int chunk) -> uint32_t {
+        if (T::kRow >= 128) return (chunk >> 3) * (T::kTile * 128) + row * 128 + (((chunk & 7) ^ (row & 7)) << 4);
+        const int line = row >> 1;
+        return line * 128 + (((((row & 1) << 2) | chunk) ^ (line & 3)) << 4);
+    };
     Cursor ld = at;
     int ld_left = n_units;
-    long long off = -1;  // of the tile that is copied next
+    // Of the tile that is copied next, its page numbers not yet looked at, so that their load is not waited
+    // for. Rows: lane r has row r. Boxes: lane i has box i = ((K or V) * groups + group of rows) * spans + span,
+    // and the group's rows that hold a token the query sees.
+    int32_t raw_page = -1, slot = 0;
+    bool real = false;  // the lane has a row or a box
+    unsigned box_rows = 0;
+    int ld_first = 0, ld_end = 0, ld_head = 0;
+    const int32_t *ld_pages = P.table;
+    auto enter = [&]() {  // an item
+        int why;
+        kv_span(P.lens[ld.b], P.table_width, P.cache.page_size, P.window, ld_first, ld_end, why);
+        ld_pages = P.table + (int64_t)ld.b * P.table_width;
+        ld_head = ld.hv / W.chunks;
+    };
+    bool lost = false;  // a copy did not arrive: nothing more is copied
+    const int spans = W.whole_rows ? 1 : T::kSpans, groups = W.box_rows ? T::kTile / W.box_rows : 1, half_boxes = groups * spans;
+    const int box_span = lane % spans, box_group = (lane / spans) % groups;
+    const unsigned group_rows = W.box_rows == 32 ? 0xffffffffu : (1u << W.box_rows) - 1u;
+    const unsigned box_bytes = W.box_rows * (W.whole_rows ? T::kRow : T::kSpan);
+    const bool my_box = W.box_rows ? lane < 2 * half_boxes : lane < T::kTile;
+    const int my_t = w * T::kTile + (W.box_rows ? box_group * W.box_rows : lane);
     auto look_up = [&]() {
-        off = -1;
-        if (ld_left <= 0) return;
-        int first, end, why;
-        kv_span(P.lens[ld.b], P.table_width, P.cache.page_size, P.window, first, end, why);
-        const int t = first + (ld.u * T::kWarps + w) * T::kTile + lane;
-        if (lane < T::kTile && t < end) {
-            off = kv_row(P.cache, P.table + (int64_t)ld.b * P.table_width, P.table_width, t, ld.hv / W.chunks, why);
-            if (off < 0 && P.err) atomicOr(P.err, COLI_LAYER_BAD_PAGE);
+        real = false;
+        if (ld_left <= 0 || lost) return;
+        const int t = (ld_first & ~W.mask) + ld.u * W.unit + my_t;
+        real = my_box && t < ld_end && (W.box_rows || t >= ld_first);
+        if (real) {
+            const int i = kv_quotient(W.divide, t);
+            slot = t - i * P.cache.page_size;
+            raw_page = ld_pages[i];
+            if (W.box_rows)
+                box_rows = (ld_end - t >= W.box_rows ? group_rows : (1u << (ld_end - t)) - 1u) &
+                           (ld_first > t ? group_rows << (ld_first - t) : group_rows);
         }
-        advance(ld);
         ld_left--;
     };
     const char *kbase = (const char *)P.k_cache, *vbase = (const char *)P.v_cache;
     constexpr int kChunks = T::kRow / 16, kRowsPer = 32 / kChunks;
     const int ch = lane % kChunks, sub = lane / kChunks;
     const bool in_row = ch * 16 < P.dim * T::kSize;
-    auto place = [](int row, int chunk) -> uint32_t {
-        // 16-byte chunks of a row are exchanged so that 8 rows' same chunk lie in 8 bank groups
-        if (T::kRow >= 128) return row * T::kRow + ((chunk ^ (row & 7)) << 4);
-        const int line = row >> 1;
-        return line * 128 + (((((row & 1) << 2) | chunk) ^ (line & 3)) << 4);
-    };
+    unsigned phase = 0, pending = 0;  // per stage: parity awaited next; boxes on their way
     auto copy_tile = [&](int stage) {
-        const unsigned rows = __ballot_sync(0xffffffffu, off >= 0);
-        if (lane == 0) seen[w * T::kStages + stage] = rows;
-        if (rows) {
-            const uint32_t dst = my_ring_a + stage * T::kStageBytes;
-#pragma unroll
-            for (int i = 0; i < T::kTile / kRowsPer; i++) {
-                const int row = i * kRowsPer + sub;
-                const long long o = __shfl_sync(0xffffffffu, off, row);
-                const bool ok = o >= 0 && in_row;
-                const long long byte = ok ? o * T::kSize + ch * 16 : 0;
-                const uint32_t d = dst + place(row, ch);
-                copy16(d, kbase + byte, ok);
-                copy16(d + T::kTile * T::kRow, vbase + byte, ok);
-            }
+        const uint32_t dst = my_ring_a + stage * T::kStageBytes;
+        if (real && (uint32_t)raw_page >= (uint32_t)P.cache.pages) {
+            real = false;
+            if (P.err) atomicOr(P.err, COLI_LAYER_BAD_PAGE);
         }
-        copy_commit();
+        if (W.box_rows) {
+            const unsigned rows = __reduce_or_sync(0xffffffffu, real && lane < half_boxes ? (box_rows & group_rows) << (W.box_rows * box_group) : 0u);
+            const int boxes = __popc(__ballot_sync(0xffffffffu, real));
+            if (lane == 0) {
+                seen[w * T::kStages + stage] = rows;
+                if (boxes) expect_bytes(my_bars + stage, boxes * box_bytes);
+            }
+            __syncwarp();
+            if (boxes) pending |= 1u << stage;
+            if (real) {
+                const bool is_v = lane >= half_boxes;
+                copy_box(dst + (is_v ? T::kTile * T::kRow : 0) + box_span * (T::kTile * 128) + box_group * W.box_rows * T::kSpan,
+                         is_v ? &vmap : &kmap, box_span * (128 / T::kSize), slot, ld_head, raw_page, my_bars + stage);
+            }
+        } else {
+            const unsigned rows = __ballot_sync(0xffffffffu, real);
+            if (lane == 0) seen[w * T::kStages + stage] = rows;
+            if (rows) {
+                const long long off = real ? (raw_page * P.cache.page_stride + slot * P.cache.token_stride +
+                                              ld_head * P.cache.head_stride) * T::kSize
+                                           : -1;
+#pragma unroll
+                for (int i = 0; i < T::kTile / kRowsPer; i++) {
+                    const int row = i * kRowsPer + sub;
+                    const long long o = __shfl_sync(0xffffffffu, off, row);
+                    const bool ok = o >= 0 && in_row;
+                    const long long byte = ok ? o + ch * 16 : 0;
+                    const uint32_t d = dst + place(row, ch);
+                    copy16(d, kbase + byte, ok);
+                    copy16(d + T::kTile * T::kRow, vbase + byte, ok);
+                }
+            }
+            copy_commit();
+        }
+        // the cursor moves on behind the copy: the item's head is still needed for it
+        if (ld_left > 0) {
+            advance(ld);
+            if (ld.u == 0) enter();
+        }
         look_up();
     };
 
+    enter();
     look_up();
 #pragma unroll
     for (int i = 0; i < T::kStages; i++) copy_tile(i);
@@ -364,38 +445,72 @@ __global__ void __launch_bounds__(T::kWarps * 32, attn_ctas_per_sm(T::kDim)) att
             }
         }
 
-        copy_wait<T::kStages - 1>();
-        __syncwarp();
-        const unsigned rows = seen[w * T::kStages + stage];
+        unsigned rows;
+        bool written = false;  // by ordinary stores, which the next copy into the stage has to follow
+        constexpr unsigned kAll = T::kTile == 32 ? 0xffffffffu : 0xffffu;
+        const uint32_t kt = my_ring_a + stage * T::kStageBytes, vt = kt + T::kTile * T::kRow;
+        if (W.box_rows) {
+            __syncwarp();
+            rows = seen[w * T::kStages + stage];
+            if (rows && !lost) {
+                if (wait_bytes(my_bars + stage, (phase >> stage) & 1)) {
+                    phase ^= 1u << stage;
+                    pending &= ~(1u << stage);
+                    if (rows != kAll) {
+                        // rows without a token: p is 0 there, so v must be finite
+#pragma unroll
+                        for (int i = 0; i < T::kTile / kRowsPer; i++) {
+                            const int row = i * kRowsPer + sub;
+                            if (!((rows >> row) & 1))
+                                asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(vt + place(row, ch)), "r"(0) : "memory");
+                        }
+                        written = true;
+                        __syncwarp();
+                    }
+                } else {
+                    lost = true;
+                    if (lane == 0 && P.err) atomicOr(P.err, COLI_LAYER_TIMEOUT);
+                }
+                lost = __any_sync(0xffffffffu, lost);
+            }
+            if (lost) rows = 0;
+        } else {
+            copy_wait<T::kStages - 1>();
+            __syncwarp();
+            rows = seen[w * T::kStages + stage];
+        }
         if (rows) {
-            const uint32_t kt = my_ring_a + stage * T::kStageBytes, vt = kt + T::kTile * T::kRow;
             float s[T::kMT][NT][4];
-#pragma unroll
-            for (int i = 0; i < T::kMT; i++)
-#pragma unroll
-                for (int n = 0; n < NT; n++)
-#pragma unroll
-                    for (int j = 0; j < 4; j++) s[i][n][j] = 0.f;
             const int lr = lane & 7, li = lane >> 3;
-            // ---- S^T = K q^T
-            if (FMT != COLI_KV_E4M3) {
-                const int row = lr + (li & 1) * 8;
+            // ---- S^T = K q^T; the leading parts in two chains, the others in one, added at the end
 #pragma unroll
-                for (int ks = 0; ks < T::kKS; ks++) {
-                    uint32_t a[4];
-                    ldm4(a, kt + place(row, 2 * ks + (li >> 1)));
+            for (int i = 0; i < T::kMT; i++) {
+                constexpr int kChains = T::kQParts > 1 ? 3 : 2;
+                float acc[kChains][NT][4];
+#pragma unroll
+                for (int k = 0; k < kChains; k++)
+#pragma unroll
+                    for (int n = 0; n < NT; n++)
+#pragma unroll
+                        for (int j = 0; j < 4; j++) acc[k][n][j] = 0.f;
+                const int row = i * 16 + lr + (li & 1) * 8;
+                auto product = [&](const uint32_t (&a)[4], int ks) {
 #pragma unroll
                     for (int p = 0; p < T::kQParts; p++)
 #pragma unroll
                         for (int n = 0; n < NT; n++) {
                             const uint2 q = qf[((p * NT + n) * T::kKS + ks) * 32 + lane];
-                            mma<FMT>(s[0][n], a, q.x, q.y);
+                            mma<FMT>(acc[p ? kChains - 1 : ks & 1][n], a, q.x, q.y);
                         }
-                }
-            } else {
+                };
+                if (FMT != COLI_KV_E4M3) {
 #pragma unroll
-                for (int i = 0; i < T::kMT; i++) {
-                    const int row = i * 16 + lr + (li & 1) * 8;
+                    for (int ks = 0; ks < T::kKS; ks++) {
+                        uint32_t a[4];
+                        ldm4(a, kt + place(row, 2 * ks + (li >> 1)));
+                        product(a, ks);
+                    }
+                } else {
 #pragma unroll
                     for (int k2 = 0; k2 < T::kKS / 2; k2++) {
                         uint32_t raw[4];
@@ -404,21 +519,20 @@ __global__ void __launch_bounds__(T::kWarps * 32, attn_ctas_per_sm(T::kDim)) att
                         for (int hf = 0; hf < 2; hf++) {
                             const uint32_t a[4] = {widen(raw[2 * hf]), widen(raw[2 * hf + 1]), widen_hi(raw[2 * hf]),
                                                    widen_hi(raw[2 * hf + 1])};
-#pragma unroll
-                            for (int p = 0; p < T::kQParts; p++)
-#pragma unroll
-                                for (int n = 0; n < NT; n++) {
-                                    const uint2 q = qf[((p * NT + n) * T::kKS + 2 * k2 + hf) * 32 + lane];
-                                    mma<FMT>(s[i][n], a, q.x, q.y);
-                                }
+                            product(a, 2 * k2 + hf);
                         }
                     }
                 }
+#pragma unroll
+                for (int n = 0; n < NT; n++)
+#pragma unroll
+                    for (int j = 0; j < 4; j++)
+                        s[i][n][j] = acc[0][n][j] + (acc[1][n][j] + (kChains > 2 ? acc[kChains - 1][n][j] : 0.f));
             }
             // ---- softmax over the tile's tokens, head by head
             uint32_t pf[T::kPParts][T::kMT][NT][2];
             float f[NT][2];
-            const bool all = rows == (T::kTile == 32 ? 0xffffffffu : 0xffffu);
+            const bool all = rows == kAll;
 #pragma unroll
             for (int n = 0; n < NT; n++) {
 #pragma unroll
@@ -428,10 +542,8 @@ __global__ void __launch_bounds__(T::kWarps * 32, attn_ctas_per_sm(T::kDim)) att
                     for (int i = 0; i < T::kMT; i++)
 #pragma unroll
                         for (int r = 0; r < 2; r++) {
-                            float x = s[i][n][2 * r + j] * sc[n][j];
-                            if (!all && !((rows >> (i * 16 + r * 8 + g)) & 1)) x = -INFINITY;
-                            s[i][n][2 * r + j] = x;
-                            top = fmaxf(top, x);
+                            const float x = s[i][n][2 * r + j] * sc[n][j];
+                            top = all || ((rows >> (i * 16 + r * 8 + g)) & 1) ? fmaxf(top, x) : top;
                         }
 #pragma unroll
                     for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
@@ -444,7 +556,9 @@ __global__ void __launch_bounds__(T::kWarps * 32, attn_ctas_per_sm(T::kDim)) att
                     for (int i = 0; i < T::kMT; i++)
 #pragma unroll
                         for (int r = 0; r < 2; r++) {
-                            const float p = exp2_fast(s[i][n][2 * r + j] - ref + (float)T::kShift);
+                            // one rounding for the exponent, small where p is large
+                            float p = exp2_fast(fmaf(s[i][n][2 * r + j], sc[n][j], (float)T::kShift - ref));
+                            p = all || ((rows >> (i * 16 + r * 8 + g)) & 1) ? p : 0.f;
                             s[i][n][2 * r + j] = p;
                             sum += p;
                         }
@@ -569,16 +683,24 @@ __global__ void __launch_bounds__(T::kWarps * 32, attn_ctas_per_sm(T::kDim)) att
             }
             __syncthreads();
             fresh = true;
+            written = true;
+        }
+        if (W.box_rows) {
+            if (written) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
         }
         copy_tile(stage);
         stage = stage + 1 == T::kStages ? 0 : stage + 1;
         advance(at);
     }
     copy_wait<0>();
+    // after a lost copy: the others on their way still write to this CTA's memory
+    for (int i = 0; lost && i < T::kStages; i++)
+        if ((pending >> i) & 1) wait_bytes(my_bars + i, (phase >> i) & 1);
 }
 
 template <typename T>
-cudaError_t launch_stream(const AttnParams &P, const AttnWork &W, int grid, cudaStream_t s) {
+cudaError_t launch_stream(const AttnParams &P, const AttnWork &W, const AttnMaps &M, int grid, cudaStream_t s) {
     static std::atomic<uint64_t> ready{0};  // devices whose limit is raised
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -589,26 +711,26 @@ cudaError_t launch_stream(const AttnParams &P, const AttnWork &W, int grid, cuda
         if (e != cudaSuccess) return e;
         ready.fetch_or(bit, std::memory_order_relaxed);
     }
-    attn_stream_kernel<T><<<grid, T::kWarps * 32, T::smem(P.seqs), s>>>(P, W);
+    attn_stream_kernel<T><<<grid, T::kWarps * 32, T::smem(P.seqs), s>>>(P, W, M.k, M.v);
     return cudaGetLastError();
 }
 
 template <int FMT, int DP, int NT>
-cudaError_t launch_wide(const AttnParams &P, const AttnWork &W, int grid, cudaStream_t s) {
-    return W.wide ? launch_stream<AttnTraits<FMT, DP, NT, true>>(P, W, grid, s)
-                  : launch_stream<AttnTraits<FMT, DP, NT, false>>(P, W, grid, s);
+cudaError_t launch_wide(const AttnParams &P, const AttnWork &W, const AttnMaps &M, int grid, cudaStream_t s) {
+    return W.wide ? launch_stream<AttnTraits<FMT, DP, NT, true>>(P, W, M, grid, s)
+                  : launch_stream<AttnTraits<FMT, DP, NT, false>>(P, W, M, grid, s);
 }
 
 template <int FMT, int DP>
-cudaError_t launch_heads(const AttnParams &P, const AttnWork &W, int grid, cudaStream_t s) {
-    return W.nt == 1 ? launch_wide<FMT, DP, 1>(P, W, grid, s) : launch_wide<FMT, DP, 2>(P, W, grid, s);
+cudaError_t launch_heads(const AttnParams &P, const AttnWork &W, const AttnMaps &M, int grid, cudaStream_t s) {
+    return W.nt == 1 ? launch_wide<FMT, DP, 1>(P, W, M, grid, s) : launch_wide<FMT, DP, 2>(P, W, M, grid, s);
 }
 
 template <int FMT>
-cudaError_t launch_dims(const AttnParams &P, const AttnWork &W, int grid, cudaStream_t s) {
-    return W.dim == 64    ? launch_heads<FMT, 64>(P, W, grid, s)
-           : W.dim == 128 ? launch_heads<FMT, 128>(P, W, grid, s)
-                          : launch_heads<FMT, 256>(P, W, grid, s);
+cudaError_t launch_dims(const AttnParams &P, const AttnWork &W, const AttnMaps &M, int grid, cudaStream_t s) {
+    return W.dim == 64    ? launch_heads<FMT, 64>(P, W, M, grid, s)
+           : W.dim == 128 ? launch_heads<FMT, 128>(P, W, M, grid, s)
+                          : launch_heads<FMT, 256>(P, W, M, grid, s);
 }
 
 }  // namespace colimoe

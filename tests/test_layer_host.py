@@ -153,6 +153,7 @@ extern "C" long long row(long long ps_, long long ts, long long hs, int pages, i
 extern "C" void span(int n, int width, int page_size, int window, int *out) {
     kv_span(n, width, page_size, window, out[0], out[1], out[2]);
 }
+extern "C" int quotient(int size, int t) { return kv_quotient(kv_divide_by(size), t); }
 ''')
     so = d / "libkv.so"
     inc = os.path.join(ROOT, "quantized_expert_decode_gb300", "csrc")
@@ -204,3 +205,11 @@ def test_spans(index, n, width, ps, window, want):
     out = (ctypes.c_int * 3)()
     index.span(n, width, ps, window, out)
     assert tuple(out) == want
+
+
+@pytest.mark.parametrize("size", [1, 2, 3, 5, 7, 8, 16, 24, 48, 100, 333, 1000, 65535, 65536, 65537, 2 ** 30 - 1, 2 ** 30, 2 ** 31 - 1])
+def test_page_quotients(index, size):
+    for m in [0, 1, 2, 3, 1000, (2 ** 31 - 1) // size - 1, (2 ** 31 - 1) // size]:
+        for t in (m * size - 1, m * size, m * size + 1, m * size + size - 1):
+            if 0 <= t < 2 ** 31:
+                assert index.quotient(size, t) == t // size, (size, t)
