@@ -40,14 +40,15 @@ extern "C" {
 #define COLI_LAYER_BAD_PAGE 1     /* a page number outside [0, pages) */
 #define COLI_LAYER_BAD_POSITION 2 /* a position or length beyond table_width * page_size, or below 0 */
 #define COLI_LAYER_BAD_SEQUENCE 4 /* a sequence number outside [0, seqs) */
-#define COLI_LAYER_TIMEOUT 8      /* a copy of cached rows did not arrive within its bounded wait */
 
 /* A paged cache: `pages` pages of `page_size` tokens, for keys and (with the same strides) for
  * values. The row of `dim` contiguous elements of page p, slot s, kv head h starts
  * p * page_stride + s * token_stride + h * head_stride elements behind k (or v). Any order of the
  * three axes is taken; offsets are computed in 64 bits. Strides are multiples of 16 bytes and k, v
  * 16-byte aligned (COLI_MOE_EALIGN). dim: a multiple of 16 bytes of elements, at most 256
- * (COLI_MOE_ENOTSUP). COLI_KV_E4M3 stores value / scale[head], saturated to +-448 (NaN stays NaN);
+ * (COLI_MOE_ENOTSUP). The attention reaches rows by 32-bit multiples of the strides' largest common power of
+ * two, which is at least 16 bytes: 64 GB of keys at that least, 1 TB at rows of 256 bytes; beyond, it
+ * answers COLI_MOE_ENOTSUP. COLI_KV_E4M3 stores value / scale[head], saturated to +-448 (NaN stays NaN);
  * a NULL scale stands for 1. The scales are ignored for the other types. */
 typedef struct {
     void *k, *v;

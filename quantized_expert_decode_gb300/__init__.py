@@ -36,7 +36,7 @@ COLI_MOE_NOALLOC_SCRATCH_BYTES = 32 << 20
 COLI_ACT_F32, COLI_ACT_BF16, COLI_ACT_F16 = 0, 1, 2
 COLI_KV_BF16, COLI_KV_F16, COLI_KV_E4M3 = 1, 2, 3
 COLI_GATE_NONE, COLI_GATE_CHANNEL, COLI_GATE_ROW, COLI_GATE_ELEMENT = 0, 1, 2, 3
-COLI_LAYER_BAD_PAGE, COLI_LAYER_BAD_POSITION, COLI_LAYER_BAD_SEQUENCE, COLI_LAYER_TIMEOUT = 1, 2, 4, 8
+COLI_LAYER_BAD_PAGE, COLI_LAYER_BAD_POSITION, COLI_LAYER_BAD_SEQUENCE = 1, 2, 4
 
 # every symbol include/colilayer.h declares
 LAYER_EXPORTS = ("coli_kv_append", "coli_attn_workspace_bytes", "coli_attn_decode", "coli_block_norms")

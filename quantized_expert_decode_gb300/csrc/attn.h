@@ -1,8 +1,6 @@
 // attn.h — what the streaming and the join kernel of coli_attn_decode share. Internal to libcolimoe.
 #pragma once
 
-#include <cuda.h>
-
 #include "act.cuh"
 #include "layer.h"
 
@@ -11,12 +9,25 @@ namespace colimoe {
 constexpr int kAttnMaxSeqs = 2048;
 constexpr int kAttnStages = 3;
 
-// A stage is 64 bytes per head element and warp (K and V, 16 tokens of 2 bytes or 32 of 1), so three
-// stages of eight warps fill the SM's shared memory at 128 elements; two such CTAs fit at 64, four
-// warps at 256.
-constexpr int attn_warps(int dim) { return dim == 256 ? 4 : 8; }
-constexpr int attn_ctas_per_sm(int dim) { return dim == 64 ? 2 : 1; }
-constexpr int attn_unit(int fmt, int dim) { return attn_warps(dim) * (fmt == COLI_KV_E4M3 ? 32 : 16); }
+// A slot (K or V of a tile: 16 tokens of 2 bytes or 32 of 1) is 32 bytes per head element and warp. Two CTAs
+// share an SM, each with three slots per warp at 128 elements, except where the sums of 16 heads take the
+// registers of one, or the three parts of q at 256 elements too much shared memory: that one has the
+// slots of both.
+constexpr bool attn_alone(int fmt, int dim, int nt, bool wide) {
+    return (nt == 2 && dim != 64) || (dim == 256 && wide && fmt == COLI_KV_BF16);
+}
+constexpr int attn_warps(int dim, int nt) { return dim == 256 && nt == 1 ? 4 : 8; }
+constexpr int attn_ctas_per_sm(int fmt, int dim, int nt, bool wide) { return attn_alone(fmt, dim, nt, wide) ? 1 : 2; }
+constexpr int attn_slots(int fmt, int dim, int nt, bool wide) {
+    return dim == 64 || (attn_alone(fmt, dim, nt, wide) && !(dim == 256 && nt == 2)) ? 6 : 3;
+}
+constexpr int attn_unit(int fmt, int dim, int nt) { return attn_warps(dim, nt) * (fmt == COLI_KV_E4M3 ? 32 : 16); }
+
+// The item whose units a border between two runs cuts, told for its first cut only (b < 0: none): its
+// sequence, head group and last run. The first entry tells how many runs there are.
+struct AttnCut {
+    int32_t b, hv, last, runs;
+};
 
 // How the launch is laid out, and the workspace
 struct AttnWork {
@@ -26,11 +37,10 @@ struct AttnWork {
     int32_t chunks;  // head groups per kv head
     int32_t groups;  // head groups per sequence
     int32_t unit;    // tokens of a unit
-    int32_t box_rows;    // K and V come as boxes of so many tokens through tensor maps; 0: row by row
-    int32_t whole_rows;  // a box holds whole rows, not one span of 128 bytes
-    KvDivide divide;     // by the page size
-    int32_t mask;        // tiles begin at tokens that are 0 under it
-    int32_t *prefix; // [seqs + 1] units (per head group) before each sequence
+    KvDivide divide;  // by the page size
+    // the cache's strides in steps of 2^off_shift bytes, which divides them all
+    uint32_t page_step, token_step, head_step, off_shift;
+    AttnCut *cuts;   // [CTAs] at the border before a run
     float2 *part_ml; // [2 * CTAs][8 * nt] (m, l) of a run's first and last cut item
     float *part_o;   // [2 * CTAs][8 * nt][dim]
 };
@@ -51,13 +61,12 @@ __device__ __forceinline__ float attn_lse(float m, float l, int shift) {
     return l == 0.f ? -INFINITY : (m - (float)shift + log2f(l)) * 0.6931471805599453f;
 }
 
-// tensor maps of K and V: (element of a span, slot, span, head, page)
-struct AttnMaps {
-    CUtensorMap k, v;
-};
+cudaError_t launch_attn_bf16(const AttnParams &P, const AttnWork &W, int grid, cudaStream_t s);
+cudaError_t launch_attn_f16(const AttnParams &P, const AttnWork &W, int grid, cudaStream_t s);
+cudaError_t launch_attn_e4m3(const AttnParams &P, const AttnWork &W, int grid, cudaStream_t s);
 
-cudaError_t launch_attn_bf16(const AttnParams &P, const AttnWork &W, const AttnMaps &M, int grid, cudaStream_t s);
-cudaError_t launch_attn_f16(const AttnParams &P, const AttnWork &W, const AttnMaps &M, int grid, cudaStream_t s);
-cudaError_t launch_attn_e4m3(const AttnParams &P, const AttnWork &W, const AttnMaps &M, int grid, cudaStream_t s);
+// Whether 32 bits reach every row of the pool in steps of the strides' largest common power of two; then
+// that step's shift.
+bool attn_steps(const KvShape &c, int heads, int elem_bytes, uint32_t &shift);
 
 }  // namespace colimoe

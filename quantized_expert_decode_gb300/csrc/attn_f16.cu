@@ -3,8 +3,8 @@
 
 namespace colimoe {
 
-cudaError_t launch_attn_f16(const AttnParams &P, const AttnWork &W, const AttnMaps &M, int grid, cudaStream_t s) {
-    return launch_dims<COLI_KV_F16>(P, W, M, grid, s);
+cudaError_t launch_attn_f16(const AttnParams &P, const AttnWork &W, int grid, cudaStream_t s) {
+    return launch_dims<COLI_KV_F16>(P, W, grid, s);
 }
 
 }  // namespace colimoe

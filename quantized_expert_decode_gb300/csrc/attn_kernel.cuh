@@ -12,10 +12,10 @@
 // kWarps tiles of kTile tokens. All units of the call form one line that is cut into equal runs, one
 // per CTA, so a CTA's share does not depend on how the lengths are spread; an item that a run's
 // border cuts leaves partial sums in the workspace, which the join kernel adds up in a fixed order.
-// Within a unit each warp owns one tile: it copies the tile's K and V rows to its own ring of kStages
-// stages (two tiles in flight while one is computed), and no warp waits for another until the item
-// ends. Where pages hold whole groups of 8 tokens or more the rows come as boxes through tensor maps,
-// one lane per box; else as 16-byte asynchronous copies, one row address per token.
+// Within a unit each warp owns one tile: it copies the tile's K rows and V rows to its own ring of kSlots
+// slots with 16-byte asynchronous copies, K and V of a tile apart, so that a slot is copied into as
+// soon as its half is used up, and no warp waits for another until the item ends. Page numbers are
+// loaded one tile ahead of the copies that need them.
 //
 // Products. Tokens are the rows of the matrix instruction and the query heads its 8 columns, so a
 // group of up to 8 heads fills it: S^T [16 tokens x 8 heads] = K q^T, then O^T [16 dims x 8 heads] +=
@@ -30,7 +30,7 @@
 
 #include "act.cuh"
 #include "attn.h"
-#include "ptx.cuh"
+#include "ptx.cuh"  // smem_u32
 
 namespace colimoe {
 
@@ -42,24 +42,6 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool valid
 }
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N> __device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
-
-// box at (element x, slot, span 0, head, page) of a cache
-__device__ __forceinline__ void copy_box(uint32_t dst, const CUtensorMap *map, int x, int slot, int head, int page, uint64_t *bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
-        "l"(map), "r"(x), "r"(slot), "r"(0), "r"(head), "r"(page), "r"(smem_u32(bar))
-        : "memory");
-}
-__device__ __forceinline__ void expect_bytes(uint64_t *bar, uint32_t bytes) {
-    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
-}
-// a copy that takes more tries than this (seconds) is given up
-constexpr int kMaxTries = 1 << 18;
-__device__ __forceinline__ bool wait_bytes(uint64_t *bar, uint32_t parity) {
-    for (int i = 0; i < kMaxTries; i++)
-        if (mbar_try_wait(bar, parity)) return true;
-    return false;
-}
 
 __device__ __forceinline__ void ldm4(uint32_t (&r)[4], uint32_t a) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -144,43 +126,39 @@ struct AttnTraits {
     static constexpr int kRow = DP * kSize;                       // bytes of a row in shared memory
     static constexpr int kTile = 32 / kSize;                      // tokens of a warp's tile
     static constexpr int kMT = kTile / 16;
-    static constexpr int kWarps = attn_warps(DP);
-    static constexpr int kStages = kAttnStages;
-    static constexpr int kStageBytes = 2 * kTile * kRow;          // K and V
+    static constexpr int kWarps = attn_warps(DP, NT);
+    static constexpr int kCtas = attn_ctas_per_sm(FMT, DP, NT, WIDE), kSlots = attn_slots(FMT, DP, NT, WIDE);
+    static constexpr int kSlotBytes = kTile * kRow;               // K or V of a tile
     static constexpr int kHeads = 8 * NT;
     static constexpr int kQParts = !WIDE ? 1 : FMT == COLI_KV_BF16 ? 3 : 2;
     static constexpr int kPParts = WIDE && FMT == COLI_KV_BF16 ? 3 : 2;
     static constexpr int kKS = DP / 16;                           // products of 16 along the head
-    static constexpr int kQWords = kQParts * NT * kKS * 32;       // uint2
-    static constexpr int kSpan = kRow < 128 ? kRow : 128;         // bytes of a row in one box
-    static constexpr int kSpans = kRow / kSpan;                   // boxes side by side
-    static_assert(2 * (kTile / 8) * kSpans <= 32, "a lane per box");
+    static constexpr int kQWords = kQParts * NT * kKS / 2 * 32;   // uint4
     // p is kept times 2^kShift, so that the second f16 part of a small p is still above f16's smallest step
     static constexpr int kShift = FMT == COLI_KV_BF16 ? 0 : 14;
-    static_assert(kWarps * kStages * kStageBytes + kQWords * 8 + kWarps * kHeads * 8 + kHeads * 4 + kWarps * kStages * 12 +
-                          (kAttnMaxSeqs + 1) * 4 + 64 <=
-                      (227 << 10) / attn_ctas_per_sm(DP) - 1024,
-                  "shared memory of an SM");
-    static_assert(kHeads * DP * 4 <= kStageBytes, "a warp's sums fit its free stage");
-    static_assert(kWarps * kTile == attn_unit(FMT, DP), "unit");
+    static_assert(8 * DP * 4 == kSlotBytes, "a warp's sums of 8 heads fill its free slot");
+    static_assert(kWarps * kTile == attn_unit(FMT, DP, NT), "unit");
     static constexpr size_t smem(int seqs) {
-        return (size_t)kWarps * kStages * kStageBytes + (size_t)kQWords * 8 + kWarps * kHeads * 8 + kHeads * 4 +
-               kWarps * kStages * 12 + ((size_t)seqs + 1) * 4 + 64;
+        return (size_t)kWarps * kSlots * kSlotBytes + (size_t)kQWords * 16 + kWarps * kHeads * 8 + kHeads * 4 +
+               kWarps * 4 * 4 + ((size_t)seqs + 1) * 4 + 64;
     }
+    static_assert(kWarps * kSlots * kSlotBytes + kQWords * 16 + kWarps * kHeads * 8 + kHeads * 4 + kWarps * 16 +
+                          (kAttnMaxSeqs + 1) * 4 + 64 <=
+                      (227 << 10) / kCtas - 1024,
+                  "shared memory of an SM");
 };
 
 template <typename T>
-__global__ void __launch_bounds__(T::kWarps * 32, attn_ctas_per_sm(T::kDim)) attn_stream_kernel(const AttnParams P, const AttnWork W, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
+__global__ void __launch_bounds__(T::kWarps * 32, T::kCtas) attn_stream_kernel(const AttnParams P, const AttnWork W) {
     using namespace attn;
     constexpr int DP = T::kDim, NT = T::kNT, kThreads = T::kWarps * 32, FMT = T::kFmt;
     extern __shared__ __align__(1024) unsigned char sm[];
     unsigned char *ring = sm;
-    uint2 *qf = reinterpret_cast<uint2 *>(ring + T::kWarps * T::kStages * T::kStageBytes);
+    uint4 *qf = reinterpret_cast<uint4 *>(ring + T::kWarps * T::kSlots * T::kSlotBytes);
     float2 *ml = reinterpret_cast<float2 *>(qf + T::kQWords);          // [warp][head] (m, l)
-    uint64_t *bars = reinterpret_cast<uint64_t *>(ml + T::kWarps * T::kHeads);  // [warp][stage]
-    float *qs = reinterpret_cast<float *>(bars + T::kWarps * T::kStages);  // [head] factor of the products
-    uint32_t *seen = reinterpret_cast<uint32_t *>(qs + T::kHeads);     // [warp][stage] rows that hold a token
-    int *pre = reinterpret_cast<int *>(seen + T::kWarps * T::kStages);  // [seqs + 1] units before a sequence
+    float *qs = reinterpret_cast<float *>(ml + T::kWarps * T::kHeads);  // [head] factor of the products
+    uint32_t *seen = reinterpret_cast<uint32_t *>(qs + T::kHeads);     // [warp][tile % 4] rows that hold a token
+    int *pre = reinterpret_cast<int *>(seen + T::kWarps * 4);          // [seqs + 1] units before a sequence
     int *scan = pre + P.seqs + 1;                                      // [16]
     const int tid = threadIdx.x, w = tid / 32, lane = tid % 32, g = lane >> 2, c = lane & 3;
 
@@ -191,7 +169,7 @@ __global__ void __launch_bounds__(T::kWarps * 32, attn_ctas_per_sm(T::kDim)) att
         int first, end, why;
         kv_span(P.lens[b], P.table_width, P.cache.page_size, P.window, first, end, why);
         if (why && blockIdx.x == 0 && P.err) atomicOr(P.err, COLI_LAYER_BAD_POSITION);
-        return (end - (first & ~W.mask) + W.unit - 1) / W.unit;  // tiles begin at a box's first token
+        return (end - first + W.unit - 1) / W.unit;
     };
     const int per = (P.seqs + kThreads - 1) / kThreads;
     const int b0 = min(tid * per, P.seqs), b1 = min(b0 + per, P.seqs);
@@ -220,8 +198,7 @@ __global__ void __launch_bounds__(T::kWarps * 32, attn_ctas_per_sm(T::kDim)) att
     __syncthreads();
     const int64_t total = (int64_t)pre[P.seqs] * W.groups;
     const int ctas = (int)min((int64_t)gridDim.x, total);
-    if (blockIdx.x == 0)
-        for (int b = tid; b <= P.seqs; b += kThreads) W.prefix[b] = pre[b];
+    if (blockIdx.x == 0 && tid == 0) W.cuts[0].runs = ctas;
 
     // ---- sequences with nothing to see
     for (int b = blockIdx.x; b < P.seqs; b += gridDim.x) {
@@ -262,30 +239,31 @@ __global__ void __launch_bounds__(T::kWarps * 32, attn_ctas_per_sm(T::kDim)) att
         if (k.b < P.seqs) k.units = pre[k.b + 1] - pre[k.b];
     };
 
-    // ---- copies: rows or boxes are looked up in the page table one tile ahead of their copy
-    unsigned char *my_ring = ring + w * T::kStages * T::kStageBytes;
-    const uint32_t my_ring_a = smem_u32(my_ring);
-    uint64_t *my_bars = bars + w * T::kStages;
-    if (lane == 0) {
-        for (int i = 0; i < T::kStages; i++) mbar_init(my_bars + i, 1);
-        fence_mbar_init();
+    // ---- for the join: the item that this run's first border cuts, told by the run behind its first cut
+    if (blockIdx.x > 0 && tid == 0) {
+        AttnCut cut{-1, 0, 0, 0};
+        const int64_t i0 = x0 - at.u;
+        if (at.u > 0 && attn_run_start(blockIdx.x - 1, total, ctas) <= i0)
+            cut = AttnCut{at.b, at.hv, (int)attn_run_of(i0 + at.units - 1, total, ctas), 0};
+        W.cuts[blockIdx.x] = cut;
     }
-    __syncwarp();
-    // 16-byte chunks of a 128-byte span are exchanged so that 8 rows' same chunk lie in 8 bank groups (the
-    // 128-byte swizzle of a tensor copy; its 64-byte one for rows of 64 bytes)
+
+    // ---- copies
+    unsigned char *my_ring = ring + w * T::kSlots * T::kSlotBytes;
+    const uint32_t my_ring_a = smem_u32(my_ring);
+    // 16-byte chunks of a 128-byte line are exchanged so that 8 rows' same chunk lie in 8 bank groups
     auto place = [](int row, int chunk) -> uint32_t {
-        if (T::kRow >= 128) return (chunk >> 3) * (T::kTile * 128) + row * 128 + (((chunk & 7) ^ (row & 7)) << 4);
+        if (T::kRow >= 128) return row * T::kRow + ((chunk ^ (row & 7)) << 4);
         const int line = row >> 1;
         return line * 128 + (((((row & 1) << 2) | chunk) ^ (line & 3)) << 4);
     };
+    constexpr uint32_t kAll = T::kTile == 32 ? 0xffffffffu : 0xffffu;
+    constexpr int kChunks = T::kRow / 16, kRowsPer = 32 / kChunks;
+    const int ch = lane % kChunks, sub = lane / kChunks;
+    const bool in_row = ch * 16 < P.dim * T::kSize;
+    const char *kbase = (const char *)P.k_cache + (in_row ? ch * 16 : 0), *vbase = (const char *)P.v_cache + (in_row ? ch * 16 : 0);
     Cursor ld = at;
     int ld_left = n_units;
-    // Of the tile that is copied next, its page numbers not yet looked at, so that their load is not waited
-    // for. Rows: lane r has row r. Boxes: lane i has box i = ((K or V) * groups + group of rows) * spans + span,
-    // and the group's rows that hold a token the query sees.
-    int32_t raw_page = -1, slot = 0;
-    bool real = false;  // the lane has a row or a box
-    unsigned box_rows = 0;
     int ld_first = 0, ld_end = 0, ld_head = 0;
     const int32_t *ld_pages = P.table;
     auto enter = [&]() {  // an item
@@ -294,88 +272,70 @@ __global__ void __launch_bounds__(T::kWarps * 32, attn_ctas_per_sm(T::kDim)) att
         ld_pages = P.table + (int64_t)ld.b * P.table_width;
         ld_head = ld.hv / W.chunks;
     };
-    bool lost = false;  // a copy did not arrive: nothing more is copied
-    const int spans = W.whole_rows ? 1 : T::kSpans, groups = W.box_rows ? T::kTile / W.box_rows : 1, half_boxes = groups * spans;
-    const int box_span = lane % spans, box_group = (lane / spans) % groups;
-    const unsigned group_rows = W.box_rows == 32 ? 0xffffffffu : (1u << W.box_rows) - 1u;
-    const unsigned box_bytes = W.box_rows * (W.whole_rows ? T::kRow : T::kSpan);
-    const bool my_box = W.box_rows ? lane < 2 * half_boxes : lane < T::kTile;
-    const int my_t = w * T::kTile + (W.box_rows ? box_group * W.box_rows : lane);
+    // lane r has row r of the tile that is copied next; its page number is not looked at before then, so
+    // that its load is not waited for
+    int32_t raw_page = -1, slot_of = 0;
+    bool real = false;
     auto look_up = [&]() {
         real = false;
-        if (ld_left <= 0 || lost) return;
-        const int t = (ld_first & ~W.mask) + ld.u * W.unit + my_t;
-        real = my_box && t < ld_end && (W.box_rows || t >= ld_first);
+        if (ld_left <= 0) return;
+        const int t = ld_first + ld.u * W.unit + w * T::kTile + lane;
+        real = lane < T::kTile && t < ld_end;
         if (real) {
             const int i = kv_quotient(W.divide, t);
-            slot = t - i * P.cache.page_size;
+            slot_of = t - i * P.cache.page_size;
             raw_page = ld_pages[i];
-            if (W.box_rows)
-                box_rows = (ld_end - t >= W.box_rows ? group_rows : (1u << (ld_end - t)) - 1u) &
-                           (ld_first > t ? group_rows << (ld_first - t) : group_rows);
         }
         ld_left--;
     };
-    const char *kbase = (const char *)P.k_cache, *vbase = (const char *)P.v_cache;
-    constexpr int kChunks = T::kRow / 16, kRowsPer = 32 / kChunks;
-    const int ch = lane % kChunks, sub = lane / kChunks;
-    const bool in_row = ch * 16 < P.dim * T::kSize;
-    unsigned phase = 0, pending = 0;  // per stage: parity awaited next; boxes on their way
-    auto copy_tile = [&](int stage) {
-        const uint32_t dst = my_ring_a + stage * T::kStageBytes;
+    uint32_t cp_rows = 0, cp_off = 0;  // of the tile whose halves are copied
+    auto copy_rows = [&](uint32_t dst, const char *base) {
+        if (cp_rows) {
+#pragma unroll
+            for (int i = 0; i < T::kTile / kRowsPer; i++) {
+                const int row = i * kRowsPer + sub;
+                const uint32_t o = __shfl_sync(0xffffffffu, cp_off, row);
+                const bool ok = in_row && ((cp_rows >> row) & 1);
+                copy16(dst + place(row, ch), base + ((uint64_t)(ok ? o : 0) << W.off_shift), ok);
+            }
+        }
+        copy_commit();
+    };
+    int cp_tile = 0, cp_slot = 0;
+    auto next_slot = [](int &s) { s = s + 1 == T::kSlots ? 0 : s + 1; };
+    auto copy_k = [&]() {
         if (real && (uint32_t)raw_page >= (uint32_t)P.cache.pages) {
             real = false;
             if (P.err) atomicOr(P.err, COLI_LAYER_BAD_PAGE);
         }
-        if (W.box_rows) {
-            const unsigned rows = __reduce_or_sync(0xffffffffu, real && lane < half_boxes ? (box_rows & group_rows) << (W.box_rows * box_group) : 0u);
-            const int boxes = __popc(__ballot_sync(0xffffffffu, real));
-            if (lane == 0) {
-                seen[w * T::kStages + stage] = rows;
-                if (boxes) expect_bytes(my_bars + stage, boxes * box_bytes);
-            }
-            __syncwarp();
-            if (boxes) pending |= 1u << stage;
-            if (real) {
-                const bool is_v = lane >= half_boxes;
-                copy_box(dst + (is_v ? T::kTile * T::kRow : 0) + box_span * (T::kTile * 128) + box_group * W.box_rows * T::kSpan,
-                         is_v ? &vmap : &kmap, box_span * (128 / T::kSize), slot, ld_head, raw_page, my_bars + stage);
-            }
-        } else {
-            const unsigned rows = __ballot_sync(0xffffffffu, real);
-            if (lane == 0) seen[w * T::kStages + stage] = rows;
-            if (rows) {
-                const long long off = real ? (raw_page * P.cache.page_stride + slot * P.cache.token_stride +
-                                              ld_head * P.cache.head_stride) * T::kSize
-                                           : -1;
-#pragma unroll
-                for (int i = 0; i < T::kTile / kRowsPer; i++) {
-                    const int row = i * kRowsPer + sub;
-                    const long long o = __shfl_sync(0xffffffffu, off, row);
-                    const bool ok = o >= 0 && in_row;
-                    const long long byte = ok ? o + ch * 16 : 0;
-                    const uint32_t d = dst + place(row, ch);
-                    copy16(d, kbase + byte, ok);
-                    copy16(d + T::kTile * T::kRow, vbase + byte, ok);
-                }
-            }
-            copy_commit();
-        }
-        // the cursor moves on behind the copy: the item's head is still needed for it
+        cp_rows = __ballot_sync(0xffffffffu, real);
+        cp_off = raw_page * W.page_step + slot_of * W.token_step + ld_head * W.head_step;
+        if (lane == 0) seen[w * 4 + (cp_tile & 3)] = cp_rows;
+        cp_tile++;
+        copy_rows(my_ring_a + cp_slot * T::kSlotBytes, kbase);
+        next_slot(cp_slot);
+        // the next tile's page numbers
         if (ld_left > 0) {
             advance(ld);
             if (ld.u == 0) enter();
         }
         look_up();
     };
+    auto copy_v = [&]() {
+        copy_rows(my_ring_a + cp_slot * T::kSlotBytes, vbase);
+        next_slot(cp_slot);
+    };
 
     enter();
     look_up();
 #pragma unroll
-    for (int i = 0; i < T::kStages; i++) copy_tile(i);
+    for (int i = 0; i < T::kSlots; i++) {  // K and V in turn
+        if (i % 2 == 0) copy_k();
+        else copy_v();
+    }
 
     float o[T::kKS][NT][4], m[NT][2], l[NT][2], sc[NT][2];
-    int stage = 0;
+    int slot = 0;
     bool fresh = true;
     int seg0 = 0;  // first unit of the current segment
     for (int it = 0; it < n_units; it++) {
@@ -424,8 +384,8 @@ __global__ void __launch_bounds__(T::kWarps * 32, attn_ctas_per_sm(T::kDim)) att
                     for (int p = 0; p < T::kQParts; p++) {
                         const uint32_t v = take_part<FMT>(a, b);
                         uint32_t *to = reinterpret_cast<uint32_t *>(
-                            qf + ((p * NT + h / 8) * T::kKS + (d >> 4)) * 32 + (h & 7) * 4 + cc);
-                        to[rr] = v;
+                            qf + ((p * NT + h / 8) * (T::kKS / 2) + (d >> 5)) * 32 + (h & 7) * 4 + cc);
+                        to[((d >> 4) & 1) * 2 + rr] = v;
                     }
                 }
             }
@@ -445,43 +405,17 @@ __global__ void __launch_bounds__(T::kWarps * 32, attn_ctas_per_sm(T::kDim)) att
             }
         }
 
-        unsigned rows;
-        bool written = false;  // by ordinary stores, which the next copy into the stage has to follow
-        constexpr unsigned kAll = T::kTile == 32 ? 0xffffffffu : 0xffffu;
-        const uint32_t kt = my_ring_a + stage * T::kStageBytes, vt = kt + T::kTile * T::kRow;
-        if (W.box_rows) {
-            __syncwarp();
-            rows = seen[w * T::kStages + stage];
-            if (rows && !lost) {
-                if (wait_bytes(my_bars + stage, (phase >> stage) & 1)) {
-                    phase ^= 1u << stage;
-                    pending &= ~(1u << stage);
-                    if (rows != kAll) {
-                        // rows without a token: p is 0 there, so v must be finite
-#pragma unroll
-                        for (int i = 0; i < T::kTile / kRowsPer; i++) {
-                            const int row = i * kRowsPer + sub;
-                            if (!((rows >> row) & 1))
-                                asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(vt + place(row, ch)), "r"(0) : "memory");
-                        }
-                        written = true;
-                        __syncwarp();
-                    }
-                } else {
-                    lost = true;
-                    if (lane == 0 && P.err) atomicOr(P.err, COLI_LAYER_TIMEOUT);
-                }
-                lost = __any_sync(0xffffffffu, lost);
-            }
-            if (lost) rows = 0;
-        } else {
-            copy_wait<T::kStages - 1>();
-            __syncwarp();
-            rows = seen[w * T::kStages + stage];
-        }
+        copy_wait<T::kSlots - 1>();
+        __syncwarp();
+        const uint32_t rows = seen[w * 4 + (it & 3)];
+        const uint32_t kt = my_ring_a + slot * T::kSlotBytes;
+        next_slot(slot);
+        const int v_slot = slot;
+        const uint32_t vt = my_ring_a + v_slot * T::kSlotBytes;
+        next_slot(slot);
+        const int lr = lane & 7, li = lane >> 3;
+        float s[T::kMT][NT][4];
         if (rows) {
-            float s[T::kMT][NT][4];
-            const int lr = lane & 7, li = lane >> 3;
             // ---- S^T = K q^T; the leading parts in two chains, the others in one, added at the end
 #pragma unroll
             for (int i = 0; i < T::kMT; i++) {
@@ -494,33 +428,30 @@ __global__ void __launch_bounds__(T::kWarps * 32, attn_ctas_per_sm(T::kDim)) att
 #pragma unroll
                         for (int j = 0; j < 4; j++) acc[k][n][j] = 0.f;
                 const int row = i * 16 + lr + (li & 1) * 8;
-                auto product = [&](const uint32_t (&a)[4], int ks) {
+                // two products of 16 along the head
+                auto product = [&](const uint32_t (&a0)[4], const uint32_t (&a1)[4], int k2) {
 #pragma unroll
                     for (int p = 0; p < T::kQParts; p++)
 #pragma unroll
                         for (int n = 0; n < NT; n++) {
-                            const uint2 q = qf[((p * NT + n) * T::kKS + ks) * 32 + lane];
-                            mma<FMT>(acc[p ? kChains - 1 : ks & 1][n], a, q.x, q.y);
+                            const uint4 q = qf[((p * NT + n) * (T::kKS / 2) + k2) * 32 + lane];
+                            mma<FMT>(acc[p ? kChains - 1 : 0][n], a0, q.x, q.y);
+                            mma<FMT>(acc[p ? kChains - 1 : 1][n], a1, q.z, q.w);
                         }
                 };
-                if (FMT != COLI_KV_E4M3) {
 #pragma unroll
-                    for (int ks = 0; ks < T::kKS; ks++) {
-                        uint32_t a[4];
-                        ldm4(a, kt + place(row, 2 * ks + (li >> 1)));
-                        product(a, ks);
-                    }
-                } else {
-#pragma unroll
-                    for (int k2 = 0; k2 < T::kKS / 2; k2++) {
+                for (int k2 = 0; k2 < T::kKS / 2; k2++) {
+                    if (FMT != COLI_KV_E4M3) {
+                        uint32_t a0[4], a1[4];
+                        ldm4(a0, kt + place(row, 4 * k2 + (li >> 1)));
+                        ldm4(a1, kt + place(row, 4 * k2 + 2 + (li >> 1)));
+                        product(a0, a1, k2);
+                    } else {
                         uint32_t raw[4];
                         ldm4(raw, kt + place(row, 2 * k2 + (li >> 1)));
-#pragma unroll
-                        for (int hf = 0; hf < 2; hf++) {
-                            const uint32_t a[4] = {widen(raw[2 * hf]), widen(raw[2 * hf + 1]), widen_hi(raw[2 * hf]),
-                                                   widen_hi(raw[2 * hf + 1])};
-                            product(a, 2 * k2 + hf);
-                        }
+                        const uint32_t a0[4] = {widen(raw[0]), widen(raw[1]), widen_hi(raw[0]), widen_hi(raw[1])};
+                        const uint32_t a1[4] = {widen(raw[2]), widen(raw[3]), widen_hi(raw[2]), widen_hi(raw[3])};
+                        product(a0, a1, k2);
                     }
                 }
 #pragma unroll
@@ -529,6 +460,13 @@ __global__ void __launch_bounds__(T::kWarps * 32, attn_ctas_per_sm(T::kDim)) att
                     for (int j = 0; j < 4; j++)
                         s[i][n][j] = acc[0][n][j] + (acc[1][n][j] + (kChains > 2 ? acc[kChains - 1][n][j] : 0.f));
             }
+        }
+        __syncwarp();
+        if (T::kSlots % 2) copy_v();  // the slots hold K and V in turn
+        else copy_k();
+        copy_wait<T::kSlots - 1>();
+        __syncwarp();
+        if (rows) {
             // ---- softmax over the tile's tokens, head by head
             uint32_t pf[T::kPParts][T::kMT][NT][2];
             float f[NT][2];
@@ -628,8 +566,13 @@ __global__ void __launch_bounds__(T::kWarps * 32, attn_ctas_per_sm(T::kDim)) att
         }
 
         if (at.u + 1 == at.units || it + 1 == n_units) {
-            // ---- the segment ends: the warps' sums through their free stages
-            float *mo = reinterpret_cast<float *>(my_ring + stage * T::kStageBytes);
+            // ---- the segment ends: the warps' sums through their free slots, 8 heads at a time
+            float *mo = reinterpret_cast<float *>(my_ring + v_slot * T::kSlotBytes);
+            const int kh = at.hv / W.chunks, h0 = (at.hv - kh * W.chunks) * T::kHeads;
+            const int group = P.q_heads / P.kv_heads;
+            const bool whole = seg0 == 0 && at.u + 1 == at.units;
+            const int part = 2 * blockIdx.x + (seg0 == 0 ? 1 : 0);
+            const float vs = P.v_scale ? P.v_scale[kh] : 1.f;
 #pragma unroll
             for (int n = 0; n < NT; n++) {
 #pragma unroll
@@ -643,64 +586,50 @@ __global__ void __launch_bounds__(T::kWarps * 32, attn_ctas_per_sm(T::kDim)) att
                 for (int i = 0; i < T::kKS; i++)
 #pragma unroll
                     for (int j = 0; j < 4; j++) {
-                        const int head = n * 8 + 2 * c + (j & 1);
+                        const int head = 2 * c + (j & 1);
                         const int d = 16 * i + (FMT == COLI_KV_E4M3 ? 2 * g + (j >> 1) : g + 8 * (j >> 1));
                         mo[head * DP + (d ^ (c << 3))] = o[i][n][j];
                     }
-            }
-            __syncthreads();
-            const int kh = at.hv / W.chunks, h0 = (at.hv - kh * W.chunks) * T::kHeads;
-            const int group = P.q_heads / P.kv_heads;
-            const bool whole = seg0 == 0 && at.u + 1 == at.units;
-            const int slot = 2 * blockIdx.x + (seg0 == 0 ? 1 : 0);
-            const float vs = P.v_scale ? P.v_scale[kh] : 1.f;
-            for (int i = tid; i < T::kHeads * DP; i += kThreads) {
-                const int h = i / DP, d = i % DP;
-                if (h0 + h >= group) break;
-                float top = -INFINITY;
+                __syncthreads();
+                for (int i = tid; i < 8 * DP; i += kThreads) {
+                    const int h = i / DP, d = i % DP, gh = h0 + n * 8 + h;
+                    if (gh >= group) break;
+                    float top = -INFINITY;
 #pragma unroll
-                for (int k = 0; k < T::kWarps; k++) top = fmaxf(top, ml[k * T::kHeads + h].x);
-                const float ref = top == -INFINITY ? 0.f : top;
-                float x = 0.f, sum = 0.f;
+                    for (int k = 0; k < T::kWarps; k++) top = fmaxf(top, ml[k * T::kHeads + n * 8 + h].x);
+                    const float ref = top == -INFINITY ? 0.f : top;
+                    float x = 0.f, sum = 0.f;
 #pragma unroll
-                for (int k = 0; k < T::kWarps; k++) {
-                    const float2 e = ml[k * T::kHeads + h];
-                    const float e2 = exp2_fast(e.x - ref);
-                    const float *src = reinterpret_cast<const float *>(ring + (k * T::kStages + stage) * T::kStageBytes);
-                    x = fmaf(src[h * DP + (d ^ (((h & 7) >> 1) << 3))], e2, x);
-                    sum = fmaf(e.y, e2, sum);
+                    for (int k = 0; k < T::kWarps; k++) {
+                        const float2 e = ml[k * T::kHeads + n * 8 + h];
+                        const float e2 = exp2_fast(e.x - ref);
+                        const float *src = reinterpret_cast<const float *>(ring + (k * T::kSlots + v_slot) * T::kSlotBytes);
+                        x = fmaf(src[h * DP + (d ^ ((h >> 1) << 3))], e2, x);
+                        sum = fmaf(e.y, e2, sum);
+                    }
+                    const int qh = kh * group + gh;
+                    if (whole) {
+                        if (d < P.dim)
+                            store_act(P.out, at.b * P.out_stride + (int64_t)qh * P.dim + d, sum == 0.f ? 0.f : x / sum * vs, P.act);
+                        if (d == 0 && P.lse) P.lse[(int64_t)at.b * P.q_heads + qh] = attn_lse(ref, sum, T::kShift);
+                    } else {
+                        W.part_o[((int64_t)part * T::kHeads + n * 8 + h) * DP + d] = x;
+                        if (d == 0) W.part_ml[(int64_t)part * T::kHeads + n * 8 + h] = make_float2(top, sum);
+                    }
                 }
-                const int qh = kh * group + h0 + h;
-                if (whole) {
-                    if (d < P.dim)
-                        store_act(P.out, at.b * P.out_stride + (int64_t)qh * P.dim + d, sum == 0.f ? 0.f : x / sum * vs, P.act);
-                    if (d == 0 && P.lse)
-                        P.lse[(int64_t)at.b * P.q_heads + qh] = attn_lse(ref, sum, T::kShift);
-                } else {
-                    W.part_o[((int64_t)slot * T::kHeads + h) * DP + d] = x;
-                    if (d == 0) W.part_ml[(int64_t)slot * T::kHeads + h] = make_float2(top, sum);
-                }
+                __syncthreads();
             }
-            __syncthreads();
             fresh = true;
-            written = true;
         }
-        if (W.box_rows) {
-            if (written) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            __syncwarp();
-        }
-        copy_tile(stage);
-        stage = stage + 1 == T::kStages ? 0 : stage + 1;
+        if (T::kSlots % 2) copy_k();
+        else copy_v();
         advance(at);
     }
     copy_wait<0>();
-    // after a lost copy: the others on their way still write to this CTA's memory
-    for (int i = 0; lost && i < T::kStages; i++)
-        if ((pending >> i) & 1) wait_bytes(my_bars + i, (phase >> i) & 1);
 }
 
 template <typename T>
-cudaError_t launch_stream(const AttnParams &P, const AttnWork &W, const AttnMaps &M, int grid, cudaStream_t s) {
+cudaError_t launch_stream(const AttnParams &P, const AttnWork &W, int grid, cudaStream_t s) {
     static std::atomic<uint64_t> ready{0};  // devices whose limit is raised
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -711,26 +640,26 @@ cudaError_t launch_stream(const AttnParams &P, const AttnWork &W, const AttnMaps
         if (e != cudaSuccess) return e;
         ready.fetch_or(bit, std::memory_order_relaxed);
     }
-    attn_stream_kernel<T><<<grid, T::kWarps * 32, T::smem(P.seqs), s>>>(P, W, M.k, M.v);
+    attn_stream_kernel<T><<<grid, T::kWarps * 32, T::smem(P.seqs), s>>>(P, W);
     return cudaGetLastError();
 }
 
 template <int FMT, int DP, int NT>
-cudaError_t launch_wide(const AttnParams &P, const AttnWork &W, const AttnMaps &M, int grid, cudaStream_t s) {
-    return W.wide ? launch_stream<AttnTraits<FMT, DP, NT, true>>(P, W, M, grid, s)
-                  : launch_stream<AttnTraits<FMT, DP, NT, false>>(P, W, M, grid, s);
+cudaError_t launch_wide(const AttnParams &P, const AttnWork &W, int grid, cudaStream_t s) {
+    return W.wide ? launch_stream<AttnTraits<FMT, DP, NT, true>>(P, W, grid, s)
+                  : launch_stream<AttnTraits<FMT, DP, NT, false>>(P, W, grid, s);
 }
 
 template <int FMT, int DP>
-cudaError_t launch_heads(const AttnParams &P, const AttnWork &W, const AttnMaps &M, int grid, cudaStream_t s) {
-    return W.nt == 1 ? launch_wide<FMT, DP, 1>(P, W, M, grid, s) : launch_wide<FMT, DP, 2>(P, W, M, grid, s);
+cudaError_t launch_heads(const AttnParams &P, const AttnWork &W, int grid, cudaStream_t s) {
+    return W.nt == 1 ? launch_wide<FMT, DP, 1>(P, W, grid, s) : launch_wide<FMT, DP, 2>(P, W, grid, s);
 }
 
 template <int FMT>
-cudaError_t launch_dims(const AttnParams &P, const AttnWork &W, const AttnMaps &M, int grid, cudaStream_t s) {
-    return W.dim == 64    ? launch_heads<FMT, 64>(P, W, M, grid, s)
-           : W.dim == 128 ? launch_heads<FMT, 128>(P, W, M, grid, s)
-                          : launch_heads<FMT, 256>(P, W, M, grid, s);
+cudaError_t launch_dims(const AttnParams &P, const AttnWork &W, int grid, cudaStream_t s) {
+    return W.dim == 64    ? launch_heads<FMT, 64>(P, W, grid, s)
+           : W.dim == 128 ? launch_heads<FMT, 128>(P, W, grid, s)
+                          : launch_heads<FMT, 256>(P, W, grid, s);
 }
 
 }  // namespace colimoe

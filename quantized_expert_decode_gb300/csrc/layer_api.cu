@@ -57,6 +57,8 @@ int check_attn(const coli_attn_desc *d, const coli_kv_cache *c) {
         d->table_width < 1 || (int64_t)d->table_width * c->page_size > INT32_MAX || !act_ok(d->act) || d->window < 0 ||
         !std::isfinite(d->scale))
         return COLI_MOE_EINVAL;
+    uint32_t shift;
+    if (!attn_steps(shape_of(*c), c->heads, c->fmt == COLI_KV_E4M3 ? 1 : 2, shift)) return COLI_MOE_ENOTSUP;
     int64_t s;
     const int64_t row = (int64_t)d->q_heads * c->dim;
     if (stride_of(d->q_stride, row, s) || stride_of(d->out_stride, row, s)) return COLI_MOE_EINVAL;
