@@ -305,11 +305,27 @@ def make_norms_desc(rows, width, act=COLI_ACT_F32, gate=COLI_GATE_NONE, post_eps
                            gate_stride, resid_out_stride, xn_stride)
 
 
+# the calls of a decode step: bound once, their arguments' addresses taken without the type tests of _ptr
+_kv_append, _attn_decode, _block_norms = _lib.coli_kv_append, _lib.coli_attn_decode, _lib.coli_block_norms
+_byref = ctypes.byref
+
+
+def _adr(a):
+    if a is None:
+        return None
+    try:
+        return a.data_ptr()
+    except AttributeError:
+        return _ptr(a)
+
+
 def coli_kv_append(desc, cache, q, k, v, inv_freq, seq, pos, table, q_out, err=None, stream=None,
                    raise_on_error=True):
-    rc = _lib.coli_kv_append(ctypes.byref(desc), ctypes.byref(cache), _ptr(q), _ptr(k), _ptr(v), _ptr(inv_freq),
-                             _ptr(seq), _ptr(pos), _ptr(table), _ptr(q_out), _ptr(err), _stream(stream))
-    return _check(rc, "coli_kv_append", raise_on_error)
+    rc = _kv_append(_byref(desc), _byref(cache), _adr(q), _adr(k), _adr(v), _adr(inv_freq), _adr(seq), _adr(pos),
+                    _adr(table), _adr(q_out), _adr(err), _stream(stream))
+    if rc:
+        _check(rc, "coli_kv_append", raise_on_error)
+    return rc
 
 
 def coli_attn_workspace_bytes(desc, cache) -> int:
@@ -318,12 +334,16 @@ def coli_attn_workspace_bytes(desc, cache) -> int:
 
 def coli_attn_decode(desc, cache, q, table, lens, out, lse=None, err=None, ws=None, ws_bytes=0, stream=None,
                      raise_on_error=True):
-    rc = _lib.coli_attn_decode(ctypes.byref(desc), ctypes.byref(cache), _ptr(q), _ptr(table), _ptr(lens), _ptr(out),
-                               _ptr(lse), _ptr(err), _ptr(ws), ws_bytes, _stream(stream))
-    return _check(rc, "coli_attn_decode", raise_on_error)
+    rc = _attn_decode(_byref(desc), _byref(cache), _adr(q), _adr(table), _adr(lens), _adr(out), _adr(lse), _adr(err),
+                      _adr(ws), ws_bytes, _stream(stream))
+    if rc:
+        _check(rc, "coli_attn_decode", raise_on_error)
+    return rc
 
 
 def coli_block_norms(desc, y, resid, post_w, gate, pre_w, resid_out, xn, stream=None, raise_on_error=True):
-    rc = _lib.coli_block_norms(ctypes.byref(desc), _ptr(y), _ptr(resid), _ptr(post_w), _ptr(gate), _ptr(pre_w),
-                               _ptr(resid_out), _ptr(xn), _stream(stream))
-    return _check(rc, "coli_block_norms", raise_on_error)
+    rc = _block_norms(_byref(desc), _adr(y), _adr(resid), _adr(post_w), _adr(gate), _adr(pre_w), _adr(resid_out),
+                      _adr(xn), _stream(stream))
+    if rc:
+        _check(rc, "coli_block_norms", raise_on_error)
+    return rc

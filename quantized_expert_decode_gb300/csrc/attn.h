@@ -9,19 +9,20 @@ namespace colimoe {
 constexpr int kAttnMaxSeqs = 2048;
 constexpr int kAttnStages = 3;
 
-// A slot (K or V of a tile: 16 tokens of 2 bytes or 32 of 1) is 32 bytes per head element and warp. Two CTAs
-// share an SM, each with three slots per warp at 128 elements, except where the sums of 16 heads take the
+// A slot is K or V of a tile: 16 rows of 256 bytes or more, or 32 shorter ones, 4 KB at 128 elements. Two CTAs
+// share an SM, each with three slots per warp there, except where the sums of 16 heads take the
 // registers of one, or the three parts of q at 256 elements too much shared memory: that one has the
 // slots of both.
 constexpr bool attn_alone(int fmt, int dim, int nt, bool wide) {
     return (nt == 2 && dim != 64) || (dim == 256 && wide && fmt == COLI_KV_BF16);
 }
+constexpr int attn_tile(int fmt, int dim) { return fmt == COLI_KV_E4M3 || dim == 64 ? 32 : 16; }
 constexpr int attn_warps(int dim, int nt) { return dim == 256 && nt == 1 ? 4 : 8; }
 constexpr int attn_ctas_per_sm(int fmt, int dim, int nt, bool wide) { return attn_alone(fmt, dim, nt, wide) ? 1 : 2; }
 constexpr int attn_slots(int fmt, int dim, int nt, bool wide) {
-    return dim == 64 || (attn_alone(fmt, dim, nt, wide) && !(dim == 256 && nt == 2)) ? 6 : 3;
+    return (dim == 64 && fmt == COLI_KV_E4M3) || (attn_alone(fmt, dim, nt, wide) && !(dim == 256 && nt == 2)) ? 6 : 3;
 }
-constexpr int attn_unit(int fmt, int dim, int nt) { return attn_warps(dim, nt) * (fmt == COLI_KV_E4M3 ? 32 : 16); }
+constexpr int attn_unit(int fmt, int dim, int nt) { return attn_warps(dim, nt) * attn_tile(fmt, dim); }
 
 // The item whose units a border between two runs cuts, told for its first cut only (b < 0: none): its
 // sequence, head group and last run. The first entry tells how many runs there are.

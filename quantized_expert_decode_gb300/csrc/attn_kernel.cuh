@@ -124,7 +124,7 @@ struct AttnTraits {
     static constexpr int kFmt = FMT, kDim = DP, kNT = NT;
     static constexpr int kSize = FMT == COLI_KV_E4M3 ? 1 : 2;
     static constexpr int kRow = DP * kSize;                       // bytes of a row in shared memory
-    static constexpr int kTile = 32 / kSize;                      // tokens of a warp's tile
+    static constexpr int kTile = attn_tile(FMT, DP);              // tokens of a warp's tile
     static constexpr int kMT = kTile / 16;
     static constexpr int kWarps = attn_warps(DP, NT);
     static constexpr int kCtas = attn_ctas_per_sm(FMT, DP, NT, WIDE), kSlots = attn_slots(FMT, DP, NT, WIDE);
@@ -136,7 +136,7 @@ struct AttnTraits {
     static constexpr int kQWords = kQParts * NT * kKS / 2 * 32;   // uint4
     // p is kept times 2^kShift, so that the second f16 part of a small p is still above f16's smallest step
     static constexpr int kShift = FMT == COLI_KV_BF16 ? 0 : 14;
-    static_assert(8 * DP * 4 == kSlotBytes, "a warp's sums of 8 heads fill its free slot");
+    static_assert(8 * DP * 4 <= kSlotBytes, "a warp's sums of 8 heads fit its free slot");
     static_assert(kWarps * kTile == attn_unit(FMT, DP, NT), "unit");
     static constexpr size_t smem(int seqs) {
         return (size_t)kWarps * kSlots * kSlotBytes + (size_t)kQWords * 16 + kWarps * kHeads * 8 + kHeads * 4 +
@@ -516,16 +516,24 @@ __global__ void __launch_bounds__(T::kWarps * 32, T::kCtas) attn_stream_kernel(c
                 const int row = lr + (li >> 1) * 8;
 #pragma unroll
                 for (int d = 0; d < T::kKS; d++) {
-                    uint32_t a[4];
-                    ldm4t(a, vt + place(row, 2 * d + (li & 1)));
+                    float t[NT][4];
 #pragma unroll
-                    for (int n = 0; n < NT; n++) {
-                        float t[4] = {0.f, 0.f, 0.f, 0.f};
+                    for (int n = 0; n < NT; n++)
 #pragma unroll
-                        for (int p = T::kPParts - 1; p >= 0; p--) mma<FMT>(t, a, pf[p][0][n][0], pf[p][0][n][1]);
+                        for (int j = 0; j < 4; j++) t[n][j] = 0.f;
 #pragma unroll
-                        for (int j = 0; j < 4; j++) o[d][n][j] = fmaf(o[d][n][j], f[n][j & 1], t[j]);
+                    for (int i = 0; i < T::kMT; i++) {
+                        uint32_t a[4];
+                        ldm4t(a, vt + place(i * 16 + row, 2 * d + (li & 1)));
+#pragma unroll
+                        for (int n = 0; n < NT; n++)
+#pragma unroll
+                            for (int p = T::kPParts - 1; p >= 0; p--) mma<FMT>(t[n], a, pf[p][i][n][0], pf[p][i][n][1]);
                     }
+#pragma unroll
+                    for (int n = 0; n < NT; n++)
+#pragma unroll
+                        for (int j = 0; j < 4; j++) o[d][n][j] = fmaf(o[d][n][j], f[n][j & 1], t[n][j]);
                 }
             } else {
 #pragma unroll
