@@ -7,7 +7,6 @@
 namespace colimoe {
 
 constexpr int kAttnMaxSeqs = 2048;
-constexpr int kAttnStages = 3;
 
 // A slot is K or V of a tile: 16 rows of 256 bytes or more, or 32 shorter ones, 4 KB at 128 elements. Two CTAs
 // share an SM, each with three slots per warp there, except where the sums of 16 heads take the
@@ -24,8 +23,25 @@ constexpr int attn_slots(int fmt, int dim, int nt, bool wide) {
 }
 constexpr int attn_unit(int fmt, int dim, int nt) { return attn_warps(dim, nt) * attn_tile(fmt, dim); }
 
-// The item whose units a border between two runs cuts, told for its first cut only (b < 0: none): its
-// sequence, head group and last run. The first entry tells how many runs there are.
+// The line of all units is cut into runs of equal length, the first ones one unit longer; one CTA each. (A
+// second, shorter run per share as further CTAs, to even out the 20 % by which the SMs' bandwidths differ,
+// costs as much in starts as it evens out.)
+struct AttnRuns {
+    uint32_t runs, each, more;  // `more` runs of each + 1 units
+    __device__ __forceinline__ AttnRuns(uint32_t total, uint32_t ctas) {
+        runs = total < ctas ? total : ctas;
+        each = runs ? total / runs : 0;
+        more = total - each * runs;
+    }
+    __device__ __forceinline__ uint32_t start(uint32_t r) const { return r * each + (r < more ? r : more); }
+    __device__ __forceinline__ uint32_t of(uint32_t x) const {  // the run that unit x lies in
+        const uint32_t y = more * (each + 1);
+        return x < y ? x / (each + 1) : more + (x - y) / each;
+    }
+};
+
+// The item whose units the border before a run cuts, told for its first cut only (b < 0: none): its sequence,
+// head group and last run. The first entry tells how many runs there are.
 struct AttnCut {
     int32_t b, hv, last, runs;
 };
@@ -41,15 +57,10 @@ struct AttnWork {
     KvDivide divide;  // by the page size
     // the cache's strides in steps of 2^off_shift bytes, which divides them all
     uint32_t page_step, token_step, head_step, off_shift;
-    AttnCut *cuts;   // [CTAs] at the border before a run
-    float2 *part_ml; // [2 * CTAs][8 * nt] (m, l) of a run's first and last cut item
-    float *part_o;   // [2 * CTAs][8 * nt][dim]
+    AttnCut *cuts;   // [runs] at the border before a run
+    float2 *part_ml; // [2 * runs][8 * nt] (m, l) of a run's first and last cut item
+    float *part_o;   // [2 * runs][8 * nt][dim]
 };
-
-// first unit of run c of n on a line of `total` units
-__host__ __device__ __forceinline__ int64_t attn_run_start(int64_t c, int64_t total, int64_t n) { return c * total / n; }
-// the run that unit x lies in: the last c with attn_run_start(c) <= x
-__host__ __device__ __forceinline__ int64_t attn_run_of(int64_t x, int64_t total, int64_t n) { return ((x + 1) * n - 1) / total; }
 
 __device__ __forceinline__ void store_act(void *p, int64_t i, float x, int act) {
     if (act == COLI_ACT_F32) ((float *)p)[i] = x;

@@ -67,6 +67,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnParam
 
 struct Layout {
     AttnWork w;
+    int64_t units;  // at most
     int grid;
     size_t ml, o, total;
 };
@@ -91,6 +92,7 @@ Layout layout_of(const AttnParams &P) {
     const int64_t seen = P.window > 0 ? P.window : (int64_t)P.table_width * P.cache.page_size;
     const int64_t most = ((seen + L.w.unit - 1) / L.w.unit) * P.seqs * L.w.groups;
     const int64_t ctas = (int64_t)num_sms() * attn_ctas_per_sm(P.fmt, L.w.dim, L.w.nt, L.w.wide);
+    L.units = most;
     L.grid = (int)(most < ctas ? most : ctas);
     auto up = [](size_t n) { return (n + 255) / 256 * 256; };
     L.ml = up((size_t)L.grid * sizeof(AttnCut));
@@ -114,7 +116,10 @@ bool attn_steps(const KvShape &c, int heads, int elem_bytes, uint32_t &shift) {
     return (last >> shift) >> 32 == 0;
 }
 
-size_t attn_workspace_bytes(const AttnParams &P) { return layout_of(P).total; }
+size_t attn_workspace_bytes(const AttnParams &P) {
+    const Layout L = layout_of(P);
+    return L.units > INT32_MAX ? 0 : L.total;  // units are counted in 32 bits
+}
 
 cudaError_t launch_attn_decode(const AttnParams &P, cudaStream_t s) {
     Layout L = layout_of(P);

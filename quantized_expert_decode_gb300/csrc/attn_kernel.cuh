@@ -12,6 +12,7 @@
 // kWarps tiles of kTile tokens. All units of the call form one line that is cut into equal runs, one
 // per CTA, so a CTA's share does not depend on how the lengths are spread; an item that a run's
 // border cuts leaves partial sums in the workspace, which the join kernel adds up in a fixed order.
+//
 // Within a unit each warp owns one tile: it copies the tile's K rows and V rows to its own ring of kSlots
 // slots with 16-byte asynchronous copies, K and V of a tile apart, so that a slot is copied into as
 // soon as its half is used up, and no warp waits for another until the item ends. Page numbers are
@@ -110,6 +111,13 @@ __device__ __forceinline__ float load_act(const void *p, int64_t i, int act) {
                                   : to_f32(((const __half *)p)[i]);
 }
 
+__device__ __forceinline__ void add_scaled(float4 &x, const float4 &y, float f) {
+    x.x = fmaf(y.x, f, x.x);
+    x.y = fmaf(y.y, f, x.y);
+    x.z = fmaf(y.z, f, x.z);
+    x.w = fmaf(y.w, f, x.w);
+}
+
 // a place on the line of units
 struct Cursor {
     int b, hv, u, units;  // sequence, head group, unit of the item, units of the item
@@ -159,10 +167,11 @@ __global__ void __launch_bounds__(T::kWarps * 32, T::kCtas) attn_stream_kernel(c
     float *qs = reinterpret_cast<float *>(ml + T::kWarps * T::kHeads);  // [head] factor of the products
     uint32_t *seen = reinterpret_cast<uint32_t *>(qs + T::kHeads);     // [warp][tile % 4] rows that hold a token
     int *pre = reinterpret_cast<int *>(seen + T::kWarps * 4);          // [seqs + 1] units before a sequence
-    int *scan = pre + P.seqs + 1;                                      // [16]
+    int *scan = pre + P.seqs + 1;                                      // [8]
+    static_assert(kThreads % (DP / 4) == 0, "whole heads in a round");
     const int tid = threadIdx.x, w = tid / 32, lane = tid % 32, g = lane >> 2, c = lane & 3;
 
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join's blocks may wait beside this
 
     // ---- units before each sequence (per head group)
     auto units_of = [&](int b) {
@@ -179,15 +188,15 @@ __global__ void __launch_bounds__(T::kWarps * 32, T::kCtas) attn_stream_kernel(c
         pre[b + 1] = u;
         mine += u;
     }
-    int run = mine;
+    int incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, run, o);
-        if (lane >= o) run += v;
+        const int v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += v;
     }
-    if (lane == 31) scan[w] = run;
+    if (lane == 31) scan[w] = incl;
     __syncthreads();
-    int before = run - mine;
+    int before = incl - mine;
     for (int i = 0; i < w; i++) before += scan[i];
     for (int b = b0; b < b1; b++) {
         const int u = pre[b + 1];
@@ -196,9 +205,8 @@ __global__ void __launch_bounds__(T::kWarps * 32, T::kCtas) attn_stream_kernel(c
     }
     if (tid == 0) pre[0] = 0;
     __syncthreads();
-    const int64_t total = (int64_t)pre[P.seqs] * W.groups;
-    const int ctas = (int)min((int64_t)gridDim.x, total);
-    if (blockIdx.x == 0 && tid == 0) W.cuts[0].runs = ctas;
+    const uint32_t total = (uint32_t)pre[P.seqs] * W.groups;
+    const AttnRuns R(total, gridDim.x);
 
     // ---- sequences with nothing to see
     for (int b = blockIdx.x; b < P.seqs; b += gridDim.x) {
@@ -208,24 +216,28 @@ __global__ void __launch_bounds__(T::kWarps * 32, T::kCtas) attn_stream_kernel(c
         if (P.lse)
             for (int i = tid; i < P.q_heads; i += kThreads) P.lse[(int64_t)b * P.q_heads + i] = -INFINITY;
     }
-    if ((int)blockIdx.x >= ctas) return;
 
     // ---- this CTA's run of units
-    const int64_t x0 = attn_run_start(blockIdx.x, total, ctas), x1 = attn_run_start(blockIdx.x + 1, total, ctas);
+    const uint32_t run = blockIdx.x;
+    if (run >= R.runs) {
+        if (run == 0 && tid == 0) W.cuts[0].runs = 0;
+        return;
+    }
+    const uint32_t x0 = R.start(run), x1 = R.start(run + 1);
     Cursor at;
     {
         // the last sequence whose units begin at or before x0
         int lo = 0, hi = P.seqs;
         while (hi - lo > 1) {
             const int mid = (lo + hi) / 2;
-            if ((int64_t)pre[mid] * W.groups <= x0) lo = mid;
+            if ((uint32_t)pre[mid] * W.groups <= x0) lo = mid;
             else hi = mid;
         }
         at.b = lo;
         at.units = pre[lo + 1] - pre[lo];
-        const int64_t r = x0 - (int64_t)pre[lo] * W.groups;
-        at.hv = (int)(r / at.units);
-        at.u = (int)(r - (int64_t)at.hv * at.units);
+        const uint32_t r = x0 - (uint32_t)pre[lo] * W.groups;
+        at.hv = (int)(r / (uint32_t)at.units);
+        at.u = (int)r - at.hv * at.units;
     }
     const int n_units = (int)(x1 - x0);
     auto advance = [&](Cursor &k) {
@@ -239,14 +251,25 @@ __global__ void __launch_bounds__(T::kWarps * 32, T::kCtas) attn_stream_kernel(c
         if (k.b < P.seqs) k.units = pre[k.b + 1] - pre[k.b];
     };
 
-    // ---- for the join: the item that this run's first border cuts, told by the run behind its first cut
-    if (blockIdx.x > 0 && tid == 0) {
-        AttnCut cut{-1, 0, 0, 0};
-        const int64_t i0 = x0 - at.u;
-        if (at.u > 0 && attn_run_start(blockIdx.x - 1, total, ctas) <= i0)
-            cut = AttnCut{at.b, at.hv, (int)attn_run_of(i0 + at.units - 1, total, ctas), 0};
-        W.cuts[blockIdx.x] = cut;
-    }
+    // ---- q of an item: read early, turned into parts when the item begins. A warp has the heads w, w + kWarps, ..,
+    // a lane the pairs of elements 2 * lane + 64 * i.
+    constexpr int kMyHeads = T::kHeads / T::kWarps;
+    const int group = P.q_heads / P.kv_heads;
+    float qx[kMyHeads][DP / 32];
+    auto load_q = [&](const Cursor &k) {
+        const int kh = k.hv / W.chunks, h0 = (k.hv - kh * W.chunks) * T::kHeads;
+#pragma unroll
+        for (int a = 0; a < kMyHeads; a++) {
+            const int h = h0 + w + a * T::kWarps;
+            const int64_t src = k.b * P.q_stride + (int64_t)(kh * group + h) * P.dim;
+#pragma unroll
+            for (int i = 0; i < DP / 32; i++) {
+                const int d = 64 * (i >> 1) + 2 * lane + (i & 1);
+                qx[a][i] = h < group && d < P.dim ? load_act(P.q, src + d, P.act) : 0.f;
+            }
+        }
+    };
+    load_q(at);
 
     // ---- copies
     unsigned char *my_ring = ring + w * T::kSlots * T::kSlotBytes;
@@ -272,21 +295,27 @@ __global__ void __launch_bounds__(T::kWarps * 32, T::kCtas) attn_stream_kernel(c
         ld_pages = P.table + (int64_t)ld.b * P.table_width;
         ld_head = ld.hv / W.chunks;
     };
-    // lane r has row r of the tile that is copied next; its page number is not looked at before then, so
-    // that its load is not waited for
-    int32_t raw_page = -1, slot_of = 0;
-    bool real = false;
+    // lane r has row r of a tile; the page number is not looked at before the copy, so that its load is not
+    // waited for
+    struct Look {
+        int32_t page, slot, head;
+        bool real;
+    };
     auto look_up = [&]() {
-        real = false;
-        if (ld_left <= 0) return;
+        Look k{0, 0, ld_head, false};
+        if (ld_left <= 0) return k;
         const int t = ld_first + ld.u * W.unit + w * T::kTile + lane;
-        real = lane < T::kTile && t < ld_end;
-        if (real) {
+        if (lane < T::kTile && t < ld_end) {
             const int i = kv_quotient(W.divide, t);
-            slot_of = t - i * P.cache.page_size;
-            raw_page = ld_pages[i];
+            k.slot = t - i * P.cache.page_size;
+            k.page = ld_pages[i];
+            k.real = true;
         }
-        ld_left--;
+        if (--ld_left > 0) {
+            advance(ld);
+            if (ld.u == 0) enter();
+        }
+        return k;
     };
     uint32_t cp_rows = 0, cp_off = 0;  // of the tile whose halves are copied
     auto copy_rows = [&](uint32_t dst, const char *base) {
@@ -303,23 +332,17 @@ __global__ void __launch_bounds__(T::kWarps * 32, T::kCtas) attn_stream_kernel(c
     };
     int cp_tile = 0, cp_slot = 0;
     auto next_slot = [](int &s) { s = s + 1 == T::kSlots ? 0 : s + 1; };
-    auto copy_k = [&]() {
-        if (real && (uint32_t)raw_page >= (uint32_t)P.cache.pages) {
-            real = false;
+    auto copy_k = [&](Look k) {
+        if (k.real && (uint32_t)k.page >= (uint32_t)P.cache.pages) {
+            k.real = false;
             if (P.err) atomicOr(P.err, COLI_LAYER_BAD_PAGE);
         }
-        cp_rows = __ballot_sync(0xffffffffu, real);
-        cp_off = raw_page * W.page_step + slot_of * W.token_step + ld_head * W.head_step;
+        cp_rows = __ballot_sync(0xffffffffu, k.real);
+        cp_off = k.page * W.page_step + k.slot * W.token_step + k.head * W.head_step;
         if (lane == 0) seen[w * 4 + (cp_tile & 3)] = cp_rows;
         cp_tile++;
         copy_rows(my_ring_a + cp_slot * T::kSlotBytes, kbase);
         next_slot(cp_slot);
-        // the next tile's page numbers
-        if (ld_left > 0) {
-            advance(ld);
-            if (ld.u == 0) enter();
-        }
-        look_up();
     };
     auto copy_v = [&]() {
         copy_rows(my_ring_a + cp_slot * T::kSlotBytes, vbase);
@@ -327,11 +350,30 @@ __global__ void __launch_bounds__(T::kWarps * 32, T::kCtas) attn_stream_kernel(c
     };
 
     enter();
-    look_up();
+    Look next;  // the tile whose K is copied next
+    {
+        constexpr int kFirst = (T::kSlots + 1) / 2;  // K and V in turn
+        Look k[kFirst];
 #pragma unroll
-    for (int i = 0; i < T::kSlots; i++) {  // K and V in turn
-        if (i % 2 == 0) copy_k();
-        else copy_v();
+        for (int i = 0; i < kFirst; i++) k[i] = look_up();
+        next = look_up();
+#pragma unroll
+        for (int i = 0; i < T::kSlots; i++) {
+            if (i % 2 == 0) copy_k(k[i / 2]);
+            else copy_v();
+        }
+    }
+
+    // ---- for the join: the item that this run's first border cuts, told by the run behind its first cut
+    if (tid == 0) {
+        AttnCut cut{-1, 0, 0, (int)R.runs};
+        const uint32_t i0 = x0 - at.u;
+        if (at.u > 0 && R.start(run - 1) <= i0) {
+            cut.b = at.b;
+            cut.hv = at.hv;
+            cut.last = (int)R.of(i0 + at.units - 1);
+        }
+        W.cuts[run] = cut;
     }
 
     float o[T::kKS][NT][4], m[NT][2], l[NT][2], sc[NT][2];
@@ -343,22 +385,14 @@ __global__ void __launch_bounds__(T::kWarps * 32, T::kCtas) attn_stream_kernel(c
             // ---- q of the item: parts in the order the matrix instruction takes them
             fresh = false;
             seg0 = at.u;
-            const int kh = at.hv / W.chunks, h0 = (at.hv - kh * W.chunks) * T::kHeads;
-            const int group = P.q_heads / P.kv_heads;
-            const float ks = P.scale * 1.4426950408889634f * (P.k_scale ? P.k_scale[kh] : 1.f);
-            for (int h = w; h < T::kHeads; h += T::kWarps) {
-                const bool real = h0 + h < group;
-                const int64_t src = at.b * P.q_stride + (int64_t)(kh * group + h0 + h) * P.dim;
-                float x[DP / 32];  // pairs: 2 * lane + 64 * i (+ 1)
+            const float ks = P.scale * 1.4426950408889634f * (P.k_scale ? P.k_scale[at.hv / W.chunks] : 1.f);
+#pragma unroll
+            for (int hh = 0; hh < kMyHeads; hh++) {
+                const int h = w + hh * T::kWarps;
+                float (&x)[DP / 32] = qx[hh];
                 float top = 0.f;
 #pragma unroll
-                for (int i = 0; i < DP / 64; i++)
-#pragma unroll
-                    for (int j = 0; j < 2; j++) {
-                        const int d = 64 * i + 2 * lane + j;
-                        x[2 * i + j] = real && d < P.dim ? load_act(P.q, src + d, P.act) : 0.f;
-                        top = fmaxf(top, fabsf(x[2 * i + j]));
-                    }
+                for (int i = 0; i < DP / 32; i++) top = fmaxf(top, fabsf(x[i]));
                 float up = 1.f, down = 1.f;
                 if (FMT != COLI_KV_BF16) {
                     // the largest element of the head at 2^14..2^15
@@ -463,7 +497,10 @@ __global__ void __launch_bounds__(T::kWarps * 32, T::kCtas) attn_stream_kernel(c
         }
         __syncwarp();
         if (T::kSlots % 2) copy_v();  // the slots hold K and V in turn
-        else copy_k();
+        else {
+            copy_k(next);
+            next = look_up();
+        }
         copy_wait<T::kSlots - 1>();
         __syncwarp();
         if (rows) {
@@ -575,12 +612,16 @@ __global__ void __launch_bounds__(T::kWarps * 32, T::kCtas) attn_stream_kernel(c
 
         if (at.u + 1 == at.units || it + 1 == n_units) {
             // ---- the segment ends: the warps' sums through their free slots, 8 heads at a time
+            if (it + 1 < n_units) {
+                Cursor k = at;
+                advance(k);
+                load_q(k);
+            }
             float *mo = reinterpret_cast<float *>(my_ring + v_slot * T::kSlotBytes);
             const int kh = at.hv / W.chunks, h0 = (at.hv - kh * W.chunks) * T::kHeads;
-            const int group = P.q_heads / P.kv_heads;
             const bool whole = seg0 == 0 && at.u + 1 == at.units;
-            const int part = 2 * blockIdx.x + (seg0 == 0 ? 1 : 0);
             const float vs = P.v_scale ? P.v_scale[kh] : 1.f;
+            const int64_t part = (int64_t)(2 * run + (seg0 == 0 ? 1 : 0)) * T::kHeads;
 #pragma unroll
             for (int n = 0; n < NT; n++) {
 #pragma unroll
@@ -599,38 +640,46 @@ __global__ void __launch_bounds__(T::kWarps * 32, T::kCtas) attn_stream_kernel(c
                         mo[head * DP + (d ^ (c << 3))] = o[i][n][j];
                     }
                 __syncthreads();
-                for (int i = tid; i < 8 * DP; i += kThreads) {
-                    const int h = i / DP, d = i % DP, gh = h0 + n * 8 + h;
-                    if (gh >= group) break;
+                for (int i = tid; i < 8 * DP / 4; i += kThreads) {
+                    const int h = i / (DP / 4), d = i % (DP / 4) * 4;
+                    if (h0 + n * 8 + h >= group) break;
                     float top = -INFINITY;
 #pragma unroll
                     for (int k = 0; k < T::kWarps; k++) top = fmaxf(top, ml[k * T::kHeads + n * 8 + h].x);
                     const float ref = top == -INFINITY ? 0.f : top;
-                    float x = 0.f, sum = 0.f;
+                    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+                    float sum = 0.f;
 #pragma unroll
                     for (int k = 0; k < T::kWarps; k++) {
                         const float2 e = ml[k * T::kHeads + n * 8 + h];
                         const float e2 = exp2_fast(e.x - ref);
-                        const float *src = reinterpret_cast<const float *>(ring + (k * T::kSlots + v_slot) * T::kSlotBytes);
-                        x = fmaf(src[h * DP + (d ^ ((h >> 1) << 3))], e2, x);
+                        const float4 y = *reinterpret_cast<const float4 *>(ring + (k * T::kSlots + v_slot) * T::kSlotBytes +
+                                                                           (h * DP + (d ^ ((h >> 1) << 3))) * 4);
+                        add_scaled(x, y, e2);
                         sum = fmaf(e.y, e2, sum);
                     }
-                    const int qh = kh * group + gh;
                     if (whole) {
-                        if (d < P.dim)
-                            store_act(P.out, at.b * P.out_stride + (int64_t)qh * P.dim + d, sum == 0.f ? 0.f : x / sum * vs, P.act);
+                        const int qh = kh * group + h0 + n * 8 + h;
+                        const float y[4] = {x.x, x.y, x.z, x.w}, f = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+                        for (int j = 0; j < 4; j++)
+                            if (d + j < P.dim) store_act(P.out, at.b * P.out_stride + (int64_t)qh * P.dim + d + j, y[j] * f * vs, P.act);
                         if (d == 0 && P.lse) P.lse[(int64_t)at.b * P.q_heads + qh] = attn_lse(ref, sum, T::kShift);
                     } else {
-                        W.part_o[((int64_t)part * T::kHeads + n * 8 + h) * DP + d] = x;
-                        if (d == 0) W.part_ml[(int64_t)part * T::kHeads + n * 8 + h] = make_float2(top, sum);
+                        *reinterpret_cast<float4 *>(W.part_o + (part + n * 8 + h) * DP + d) = x;
+                        if (d == 0) W.part_ml[part + n * 8 + h] = make_float2(top, sum);
                     }
                 }
                 __syncthreads();
             }
             fresh = true;
         }
-        if (T::kSlots % 2) copy_k();
-        else copy_v();
+        if (T::kSlots % 2) {
+            copy_k(next);
+            next = look_up();
+        } else {
+            copy_v();
+        }
         advance(at);
     }
     copy_wait<0>();

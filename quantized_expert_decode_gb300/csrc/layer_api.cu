@@ -157,7 +157,9 @@ int coli_attn_decode(const coli_attn_desc *d, const coli_kv_cache *c, const void
         !aligned(err, 4))
         return COLI_MOE_EALIGN;
     AttnParams p = attn_params(d, c);
-    if (!ws || !aligned(ws, 256) || ws_bytes < attn_workspace_bytes(p)) return COLI_MOE_EWORKSPACE;
+    const size_t need = attn_workspace_bytes(p);
+    if (need == 0) return COLI_MOE_ENOTSUP;
+    if (!ws || !aligned(ws, 256) || ws_bytes < need) return COLI_MOE_EWORKSPACE;
     if (int rc = check_device()) return rc;
     p.q = q;
     p.out = out;
