@@ -2,6 +2,7 @@
 // border cut (attn_kernel.cuh has the streaming kernel).
 #include "attn.h"
 #include "host.h"
+#include "pdl.cuh"
 
 namespace colimoe {
 
@@ -17,7 +18,8 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnParam
     constexpr int kWarps = kJoinThreads / 32, kPer = DP / 32;
     __shared__ float red[kWarps][DP];
     __shared__ float2 red_ml[kWarps];
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    let_next_start();
+    wait_for_previous();
     const int c = blockIdx.x + 1, runs = W.cuts[0].runs;
     const AttnCut cut = W.cuts[c];  // written if c < runs
     if (c >= runs || cut.b < 0) return;
@@ -132,19 +134,11 @@ cudaError_t launch_attn_decode(const AttnParams &P, cudaStream_t s) {
                                                  : launch_attn_e4m3(P, L.w, L.grid, s);
     if (e != cudaSuccess || L.grid == 1) return e;  // one run: no borders
     // the join's blocks start while the streaming kernel runs and wait for its end
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(L.grid - 1, 8 * L.w.nt);
-    cfg.blockDim = dim3(kJoinThreads);
-    cfg.stream = s;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
+    const dim3 grid(L.grid - 1, 8 * L.w.nt);
     const int shift = P.fmt == COLI_KV_BF16 ? 0 : 14;
-    return L.w.dim == 64    ? cudaLaunchKernelEx(&cfg, attn_join_kernel<64>, P, L.w, shift)
-           : L.w.dim == 128 ? cudaLaunchKernelEx(&cfg, attn_join_kernel<128>, P, L.w, shift)
-                            : cudaLaunchKernelEx(&cfg, attn_join_kernel<256>, P, L.w, shift);
+    return L.w.dim == 64    ? launch_overlapped(attn_join_kernel<64>, grid, kJoinThreads, 0, s, P, L.w, shift)
+           : L.w.dim == 128 ? launch_overlapped(attn_join_kernel<128>, grid, kJoinThreads, 0, s, P, L.w, shift)
+                            : launch_overlapped(attn_join_kernel<256>, grid, kJoinThreads, 0, s, P, L.w, shift);
 }
 
 }  // namespace colimoe

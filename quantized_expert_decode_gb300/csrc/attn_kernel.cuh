@@ -31,6 +31,7 @@
 
 #include "act.cuh"
 #include "attn.h"
+#include "pdl.cuh"
 #include "ptx.cuh"  // smem_u32
 
 namespace colimoe {
@@ -171,7 +172,8 @@ __global__ void __launch_bounds__(T::kWarps * 32, T::kCtas) attn_stream_kernel(c
     static_assert(kThreads % (DP / 4) == 0, "whole heads in a round");
     const int tid = threadIdx.x, w = tid / 32, lane = tid % 32, g = lane >> 2, c = lane & 3;
 
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join's blocks may wait beside this
+    wait_for_previous();
+    let_next_start();  // the join's blocks may wait beside this
 
     // ---- units before each sequence (per head group)
     auto units_of = [&](int b) {
@@ -697,8 +699,7 @@ cudaError_t launch_stream(const AttnParams &P, const AttnWork &W, int grid, cuda
         if (e != cudaSuccess) return e;
         ready.fetch_or(bit, std::memory_order_relaxed);
     }
-    attn_stream_kernel<T><<<grid, T::kWarps * 32, T::smem(P.seqs), s>>>(P, W);
-    return cudaGetLastError();
+    return launch_overlapped(attn_stream_kernel<T>, dim3(grid), T::kWarps * 32, T::smem(P.seqs), s, P, W);
 }
 
 template <int FMT, int DP, int NT>

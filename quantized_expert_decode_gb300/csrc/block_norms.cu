@@ -10,6 +10,7 @@
 
 #include "act.cuh"
 #include "layer.h"
+#include "pdl.cuh"
 
 namespace cg = cooperative_groups;
 
@@ -47,6 +48,8 @@ template <typename T, int V, int N, bool kCluster>
 __global__ void __launch_bounds__(kMaxThreads) block_norms_kernel(const NormsParams P) {
     __shared__ float part[2][32];
     __shared__ float cta[2];
+    wait_for_previous();
+    let_next_start();
     int row = blockIdx.x, rank = 0, ranks = 1;
     if (kCluster) {
         cg::cluster_group cl = cg::this_cluster();
@@ -124,10 +127,8 @@ __global__ void __launch_bounds__(kMaxThreads) block_norms_kernel(const NormsPar
 
 template <typename T, int V, int N>
 cudaError_t launch_n(const NormsParams &P, int threads, int ranks, cudaStream_t s) {
-    if (ranks == 1) {
-        block_norms_kernel<T, V, N, false><<<P.rows, threads, 0, s>>>(P);
-        return cudaGetLastError();
-    }
+    if (ranks == 1)
+        return launch_overlapped(block_norms_kernel<T, V, N, false>, dim3(P.rows), threads, 0, s, P);
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)P.rows * ranks);
     cfg.blockDim = dim3(threads);
@@ -137,7 +138,7 @@ cudaError_t launch_n(const NormsParams &P, int threads, int ranks, cudaStream_t 
     at[0].val.clusterDim.x = ranks;
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = 1;  // (not overlapped: wait_for_previous returns at once)
     return cudaLaunchKernelEx(&cfg, block_norms_kernel<T, V, N, true>, P);
 }
 

@@ -12,6 +12,7 @@
 // those tokens, so that the angle work is shared by the heads.
 #include "act.cuh"
 #include "layer.h"
+#include "pdl.cuh"
 
 namespace colimoe {
 namespace {
@@ -60,6 +61,8 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const AppendParams 
                                                              int heads_per_cta) {
     __shared__ float2 cs[kMaxTokens * kMaxPairs];
     __shared__ long long row_k[kMaxTokens];  // offset of the token's row of kv head 0, or -1
+    wait_for_previous();
+    let_next_start();
     const int n0 = blockIdx.x * tokens_per_cta;
     const int nt = min(tokens_per_cta, P.tokens - n0);
     const int half = P.rotary / 2;
@@ -195,10 +198,9 @@ cudaError_t launch_typed(const AppendParams &P, cudaStream_t s) {
     const int tp = P.tokens >= 4096 ? 4 : 1;
     const int hp = P.tokens >= 512 ? rows : 16;
     dim3 grid((P.tokens + tp - 1) / tp, (rows + hp - 1) / hp);
-    if (fits(8)) kv_append_kernel<A, C, 8><<<grid, kThreads, 0, s>>>(P, tp, hp);
-    else if (fits(4)) kv_append_kernel<A, C, 4><<<grid, kThreads, 0, s>>>(P, tp, hp);
-    else kv_append_kernel<A, C, 1><<<grid, kThreads, 0, s>>>(P, tp, hp);
-    return cudaGetLastError();
+    if (fits(8)) return launch_overlapped(kv_append_kernel<A, C, 8>, grid, kThreads, 0, s, P, tp, hp);
+    if (fits(4)) return launch_overlapped(kv_append_kernel<A, C, 4>, grid, kThreads, 0, s, P, tp, hp);
+    return launch_overlapped(kv_append_kernel<A, C, 1>, grid, kThreads, 0, s, P, tp, hp);
 }
 
 template <typename A>
