@@ -9,8 +9,10 @@
 //
 // What bounds it: bytes, each read and written once. A CTA owns a few tokens; its threads compute
 // the tokens' cosines and sines once into shared memory and then walk all heads of q, k and v of
-// those tokens, so that the angle work is shared by the heads.
+// those tokens, so that the angle work is shared by the heads. Every thread has several items' loads
+// on their way before it touches the first, the first of them before the angles are computed.
 #include "act.cuh"
+#include "host.h"
 #include "layer.h"
 #include "pdl.cuh"
 
@@ -19,6 +21,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kMaxTokens = 8;                // tokens of a CTA
+constexpr int kFewRounds = 8, kCtasPerSm = 2;
 constexpr int kMaxPairs = 128;               // rotary / 2 at most (dim <= 256)
 
 // f / 2 pi as a fraction of a turn in units of 2^-64, modulo one turn
@@ -55,10 +58,11 @@ __device__ __forceinline__ __nv_fp8_e4m3 to_cache<__nv_fp8_e4m3>(float x, float 
 
 // One item: 2 * V elements of one head of one token. Items below rotary / (2 V) rotate V pairs: V
 // elements at i * V and V at rotary / 2 + i * V, or, interleaved, 2 V elements at i * 2 V. The rest
-// copy 2 V elements.
+// copy 2 V elements. A thread keeps its item number within the rows and walks over rows, kBatch at a time.
 template <typename A, typename C, int V>
 __global__ void __launch_bounds__(kThreads) kv_append_kernel(const AppendParams P, int tokens_per_cta,
                                                              int heads_per_cta) {
+    constexpr int kBatch = V == 1 ? 2 : 32 / (V * (int)sizeof(A));  // 64 bytes
     __shared__ float2 cs[kMaxTokens * kMaxPairs];
     __shared__ long long row_k[kMaxTokens];  // offset of the token's row of kv head 0, or -1
     wait_for_previous();
@@ -66,6 +70,50 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const AppendParams 
     const int n0 = blockIdx.x * tokens_per_cta;
     const int nt = min(tokens_per_cta, P.tokens - n0);
     const int half = P.rotary / 2;
+    const int per_row = P.dim / (2 * V), turned = half / V;
+    const int h0 = blockIdx.y * heads_per_cta;
+    const int heads = min(heads_per_cta, P.q_heads + 2 * P.kv_heads - h0);
+    const int step = kThreads / per_row;  // rows that the CTA takes at once
+    const int c = threadIdx.x % per_row;
+    // two runs of V elements at o0, o1; adjacent unless the item rotates halves
+    const bool in_turn = c < turned, split = in_turn && !P.interleaved;
+    const int s0 = split ? c * V : c * 2 * V, s1 = split ? half + c * V : c * 2 * V + V;
+    const int v0 = c * 2 * V, v1 = v0 + V;  // of a value
+    // the thread's next row: token t, head h of the CTA's
+    int t = 0, h = threadIdx.x / per_row;
+    if (h >= step) t = nt;  // threads beyond whole rows
+    auto settle = [&]() {
+        while (h >= heads && t < nt) {
+            h -= heads;
+            t++;
+        }
+    };
+    settle();
+    struct Item {
+        int t, h;  // t < 0: none; h counts q heads, k heads, v heads
+        Run<A, V> a, b;
+    };
+    Item item[kBatch];
+    auto fetch = [&]() {
+#pragma unroll
+        for (int i = 0; i < kBatch; i++) {
+            Item &x = item[i];
+            x.t = t < nt ? t : -1;
+            x.h = h0 + h;
+            if (t < nt) {
+                const int64_t n = n0 + t;
+                const int kh = x.h - P.q_heads, vh = kh - P.kv_heads;
+                const A *src = kh < 0   ? (const A *)P.q + n * P.q_stride + (int64_t)x.h * P.dim
+                               : vh < 0 ? (const A *)P.k + n * P.k_stride + (int64_t)kh * P.dim
+                                        : (const A *)P.v + n * P.v_stride + (int64_t)vh * P.dim;
+                x.a.load(src + (vh < 0 ? s0 : v0));
+                x.b.load(src + (vh < 0 ? s1 : v1));
+                h += step;
+                settle();
+            }
+        }
+    };
+    fetch();
     if (threadIdx.x < nt) {
         const int n = n0 + threadIdx.x;
         const int b = P.seq ? P.seq[n] : n;
@@ -83,98 +131,80 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const AppendParams 
         if (flag && P.err) atomicOr(P.err, flag);
     }
     for (int i = threadIdx.x; i < nt * half; i += kThreads) {
-        const int t = i / half, j = i - t * half;
-        cs[t * half + j] = turn(P.pos[n0 + t], P.inv_freq[j]);
+        const int u = i / half, j = i - u * half;
+        cs[i] = turn(P.pos[n0 + u], P.inv_freq[j]);
     }
     __syncthreads();
-    const int per_row = P.dim / (2 * V), turned = half / V;
-    const int h0 = blockIdx.y * heads_per_cta;
-    const int heads = min(heads_per_cta, P.q_heads + 2 * P.kv_heads - h0);
-    const int items = nt * heads * per_row;
-#pragma unroll 2
-    for (int it = threadIdx.x; it < items; it += kThreads) {
-        const int r = it / per_row, c = it - r * per_row;
-        const int t = r / heads;
-        int h = h0 + (r - t * heads);
-        const int n = n0 + t;
-        const bool is_q = h < P.q_heads, is_k = !is_q && h < P.q_heads + P.kv_heads;
-        const A *src;
-        if (is_q) {
-            src = (const A *)P.q + n * P.q_stride + (int64_t)h * P.dim;
-        } else if (is_k) {
-            h -= P.q_heads;
-            src = (const A *)P.k + n * P.k_stride + (int64_t)h * P.dim;
-        } else {
-            h -= P.q_heads + P.kv_heads;
-            src = (const A *)P.v + n * P.v_stride + (int64_t)h * P.dim;
-        }
-        const bool rot = (is_q || is_k) && c < turned;
-        // two runs of V elements at o0, o1; adjacent unless the item rotates halves
-        const bool split = rot && !P.interleaved;
-        const int o0 = split ? c * V : c * 2 * V, o1 = split ? half + c * V : c * 2 * V + V;
-        Run<A, V> a, b;
-        a.load(src + o0);
-        b.load(src + o1);
-        float x[V], y[V];
+    while (item[0].t >= 0) {
 #pragma unroll
-        for (int j = 0; j < V; j++) {
-            x[j] = to_f32(a.e[j]);
-            y[j] = to_f32(b.e[j]);
-        }
-        if (rot) {
-            const float2 *w = cs + t * half + c * V;
-            if (split) {
-#pragma unroll
-                for (int j = 0; j < V; j++) {
-                    const float2 e = w[j];
-                    const float u = x[j], v = y[j];
-                    x[j] = fmaf(u, e.x, -(v * e.y));
-                    y[j] = fmaf(v, e.x, u * e.y);
-                }
-            } else {
-                // the 2 V elements x, y hold V adjacent pairs
-                float z[2 * V];
-#pragma unroll
-                for (int j = 0; j < V; j++) {
-                    z[j] = x[j];
-                    z[V + j] = y[j];
-                }
-#pragma unroll
-                for (int j = 0; j < V; j++) {
-                    const float2 e = w[j];
-                    const float u = z[2 * j], v = z[2 * j + 1];
-                    z[2 * j] = fmaf(u, e.x, -(v * e.y));
-                    z[2 * j + 1] = fmaf(v, e.x, u * e.y);
-                }
-#pragma unroll
-                for (int j = 0; j < V; j++) {
-                    x[j] = z[j];
-                    y[j] = z[V + j];
-                }
-            }
-        }
-        if (is_q) {
-            A *dst = (A *)P.q_out + n * P.q_out_stride + (int64_t)h * P.dim;
+        for (int i = 0; i < kBatch; i++) {
+            Item &it = item[i];
+            if (it.t < 0) continue;
+            const int kh = it.h - P.q_heads, vh = kh - P.kv_heads;
+            float x[V], y[V];
 #pragma unroll
             for (int j = 0; j < V; j++) {
-                a.e[j] = from_f32<A>(x[j]);
-                b.e[j] = from_f32<A>(y[j]);
+                x[j] = to_f32(it.a.e[j]);
+                y[j] = to_f32(it.b.e[j]);
             }
-            a.store(dst + o0);
-            b.store(dst + o1);
-        } else if (row_k[t] >= 0) {
-            const float *sc = is_k ? P.k_scale : P.v_scale;
-            const float s = sc ? sc[h] : 1.f;
-            C *dst = (C *)(is_k ? P.k_cache : P.v_cache) + row_k[t] + (int64_t)h * P.cache.head_stride;
-            Run<C, V> ca, cb;
+            if (vh < 0 && in_turn) {
+                const float2 *w = cs + it.t * half + c * V;
+                if (split) {
 #pragma unroll
-            for (int j = 0; j < V; j++) {
-                ca.e[j] = to_cache<C>(x[j], s);
-                cb.e[j] = to_cache<C>(y[j], s);
+                    for (int j = 0; j < V; j++) {
+                        const float2 e = w[j];
+                        const float u = x[j], v = y[j];
+                        x[j] = fmaf(u, e.x, -(v * e.y));
+                        y[j] = fmaf(v, e.x, u * e.y);
+                    }
+                } else {
+                    // the 2 V elements x, y hold V adjacent pairs
+                    float z[2 * V];
+#pragma unroll
+                    for (int j = 0; j < V; j++) {
+                        z[j] = x[j];
+                        z[V + j] = y[j];
+                    }
+#pragma unroll
+                    for (int j = 0; j < V; j++) {
+                        const float2 e = w[j];
+                        const float u = z[2 * j], v = z[2 * j + 1];
+                        z[2 * j] = fmaf(u, e.x, -(v * e.y));
+                        z[2 * j + 1] = fmaf(v, e.x, u * e.y);
+                    }
+#pragma unroll
+                    for (int j = 0; j < V; j++) {
+                        x[j] = z[j];
+                        y[j] = z[V + j];
+                    }
+                }
             }
-            ca.store(dst + o0);
-            cb.store(dst + o1);
+            if (kh < 0) {
+                A *dst = (A *)P.q_out + (int64_t)(n0 + it.t) * P.q_out_stride + (int64_t)it.h * P.dim;
+                Run<A, V> a, b;
+#pragma unroll
+                for (int j = 0; j < V; j++) {
+                    a.e[j] = from_f32<A>(x[j]);
+                    b.e[j] = from_f32<A>(y[j]);
+                }
+                a.store(dst + s0);
+                b.store(dst + s1);
+            } else if (row_k[it.t] >= 0) {
+                const int g = vh < 0 ? kh : vh;
+                const float *sc = vh < 0 ? P.k_scale : P.v_scale;
+                const float s = sc ? sc[g] : 1.f;
+                C *dst = (C *)(vh < 0 ? P.k_cache : P.v_cache) + row_k[it.t] + (int64_t)g * P.cache.head_stride;
+                Run<C, V> a, b;
+#pragma unroll
+                for (int j = 0; j < V; j++) {
+                    a.e[j] = to_cache<C>(x[j], s);
+                    b.e[j] = to_cache<C>(y[j], s);
+                }
+                a.store(dst + (vh < 0 ? s0 : v0));
+                b.store(dst + (vh < 0 ? s1 : v1));
+            }
         }
+        fetch();
     }
 }
 
@@ -195,11 +225,17 @@ cudaError_t launch_typed(const AppendParams &P, cudaStream_t s) {
                multiple(P.k, P.k_stride, sz, v) && multiple(P.v, P.v_stride, sz, v);
     };
     const int rows = P.q_heads + 2 * P.kv_heads;
-    const int tp = P.tokens >= 4096 ? 4 : 1;
-    const int hp = P.tokens >= 512 ? rows : 16;
-    dim3 grid((P.tokens + tp - 1) / tp, (rows + hp - 1) / hp);
-    if (fits(8)) return launch_overlapped(kv_append_kernel<A, C, 8>, grid, kThreads, 0, s, P, tp, hp);
-    if (fits(4)) return launch_overlapped(kv_append_kernel<A, C, 4>, grid, kThreads, 0, s, P, tp, hp);
+    const int v = fits(8) ? 8 : fits(4) ? 4 : 1;
+    const int step = kThreads / (P.dim / (2 * v));
+    // few rows: one round of a CTA's threads each, for latency; many: whole tokens, several per CTA where
+    // that still leaves some CTAs for every SM
+    const bool few = (int64_t)P.tokens * rows <= (int64_t)step * kFewRounds * num_sms();
+    int tp = 1;
+    while (tp < kMaxTokens && (P.tokens + 2 * tp - 1) / (2 * tp) >= kCtasPerSm * num_sms()) tp *= 2;
+    const int hp = few ? step : rows;
+    const dim3 grid((P.tokens + tp - 1) / tp, (rows + hp - 1) / hp);
+    if (v == 8) return launch_overlapped(kv_append_kernel<A, C, 8>, grid, kThreads, 0, s, P, tp, hp);
+    if (v == 4) return launch_overlapped(kv_append_kernel<A, C, 4>, grid, kThreads, 0, s, P, tp, hp);
     return launch_overlapped(kv_append_kernel<A, C, 1>, grid, kThreads, 0, s, P, tp, hp);
 }
 
