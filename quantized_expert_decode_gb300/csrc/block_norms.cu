@@ -9,6 +9,7 @@
 #include <cooperative_groups.h>
 
 #include "act.cuh"
+#include "host.h"
 #include "layer.h"
 #include "pdl.cuh"
 
@@ -17,7 +18,7 @@ namespace cg = cooperative_groups;
 namespace colimoe {
 namespace {
 
-constexpr int kMaxThreads = 1024;
+constexpr int kMaxThreads = 512;
 constexpr int kMaxElems = 16;  // elements of a row that a thread holds
 
 // Sum over the CTA, then over the cluster; every thread gets it. `part` is written once per call, so
@@ -43,9 +44,11 @@ __device__ __forceinline__ float row_sum(float v, float *part, float *cta) {
     return s;
 }
 
-// T the activation type, V elements per access, N accesses per thread
-template <typename T, int V, int N, bool kCluster>
-__global__ void __launch_bounds__(kMaxThreads) block_norms_kernel(const NormsParams P) {
+// T the activation type, V elements per access, N accesses per thread. kEarly: the factors are loaded beside the
+// row, before the first sum (one row of 6144: 3.1 us against 4.0); else where they are used, which leaves
+// registers for a second CTA on the SM (4099 rows: 60 us against 87).
+template <typename T, int V, int N, bool kCluster, bool kEarly>
+__global__ void __launch_bounds__(kMaxThreads, kEarly ? 1 : 2) block_norms_kernel(const NormsParams P) {
     __shared__ float part[2][32];
     __shared__ float cta[2];
     wait_for_previous();
@@ -70,6 +73,22 @@ __global__ void __launch_bounds__(kMaxThreads) block_norms_kernel(const NormsPar
             rv[i].load(r + (int64_t)c * V);
         }
     }
+    const bool channels = P.gate_kind == COLI_GATE_CHANNEL || P.gate_kind == COLI_GATE_ELEMENT;
+    Run<float, V> w0[N], w1[N];
+    Run<T, V> gv[N];
+    auto load_first = [&](int i, int c) {
+        if (P.post_w) w0[i].load(P.post_w + (int64_t)c * V);
+        if (channels) gv[i].load(g + (int64_t)c * V);
+    };
+    if constexpr (kEarly) {
+#pragma unroll
+        for (int i = 0; i < N; i++) {
+            const int c = first + i * step;
+            if (c >= runs) continue;
+            load_first(i, c);
+            if (P.pre_w) w1[i].load(P.pre_w + (int64_t)c * V);
+        }
+    }
     float z[N * V];
     float ss = 0.f;
 #pragma unroll
@@ -80,26 +99,22 @@ __global__ void __launch_bounds__(kMaxThreads) block_norms_kernel(const NormsPar
             z[i * V + j] = v;
             ss = fmaf(v, v, ss);
         }
-    float rs = 1.f;
-    if (P.post_w) rs = rsqrtf(row_sum<kCluster>(ss, part[0], &cta[0]) / (float)P.width + P.post_eps);
     float grow = 1.f;
     if (P.gate_kind == COLI_GATE_ROW) grow = to_f32(g[row]);
+    float rs = 1.f;
+    if (P.post_w) rs = rsqrtf(row_sum<kCluster>(ss, part[0], &cta[0]) / (float)P.width + P.post_eps);
     ss = 0.f;
 #pragma unroll
     for (int i = 0; i < N; i++) {
         const int c = first + i * step;
         if (c >= runs) continue;
-        Run<float, V> pw;
-        if (P.post_w) pw.load(P.post_w + (int64_t)c * V);
-        Run<T, V> gv;
-        if (P.gate_kind >= COLI_GATE_CHANNEL && P.gate_kind != COLI_GATE_ROW) gv.load(g + (int64_t)c * V);
+        if constexpr (!kEarly) load_first(i, c);
         Run<T, V> o;
 #pragma unroll
         for (int j = 0; j < V; j++) {
             float v = z[i * V + j];
-            if (P.post_w) v = v * rs * pw.e[j];
-            if (P.gate_kind == COLI_GATE_ROW) v *= grow;
-            else if (P.gate_kind != COLI_GATE_NONE) v *= to_f32(gv.e[j]);
+            if (P.post_w) v = v * rs * w0[i].e[j];
+            v *= channels ? to_f32(gv[i].e[j]) : grow;
             v = fmaf(P.resid_scale, to_f32(rv[i].e[j]), v);
             z[i * V + j] = v;
             ss = fmaf(v, v, ss);
@@ -113,11 +128,10 @@ __global__ void __launch_bounds__(kMaxThreads) block_norms_kernel(const NormsPar
         for (int i = 0; i < N; i++) {
             const int c = first + i * step;
             if (c >= runs) continue;
-            Run<float, V> pw;
-            pw.load(P.pre_w + (int64_t)c * V);
+            if constexpr (!kEarly) w1[i].load(P.pre_w + (int64_t)c * V);
             Run<T, V> o;
 #pragma unroll
-            for (int j = 0; j < V; j++) o.e[j] = from_f32<T>(z[i * V + j] * rs * pw.e[j]);
+            for (int j = 0; j < V; j++) o.e[j] = from_f32<T>(z[i * V + j] * rs * w1[i].e[j]);
             o.store((T *)P.xn + row * P.xn_stride + (int64_t)c * V);
         }
     }
@@ -127,8 +141,9 @@ __global__ void __launch_bounds__(kMaxThreads) block_norms_kernel(const NormsPar
 
 template <typename T, int V, int N>
 cudaError_t launch_n(const NormsParams &P, int threads, int ranks, cudaStream_t s) {
-    if (ranks == 1)
-        return launch_overlapped(block_norms_kernel<T, V, N, false>, dim3(P.rows), threads, 0, s, P);
+    if (ranks == 1)  // a row for every SM or fewer: latency
+        return P.rows <= num_sms() ? launch_overlapped(block_norms_kernel<T, V, N, false, true>, dim3(P.rows), threads, 0, s, P)
+                                   : launch_overlapped(block_norms_kernel<T, V, N, false, false>, dim3(P.rows), threads, 0, s, P);
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)P.rows * ranks);
     cfg.blockDim = dim3(threads);
@@ -139,7 +154,7 @@ cudaError_t launch_n(const NormsParams &P, int threads, int ranks, cudaStream_t 
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;  // (not overlapped: wait_for_previous returns at once)
-    return cudaLaunchKernelEx(&cfg, block_norms_kernel<T, V, N, true>, P);
+    return cudaLaunchKernelEx(&cfg, block_norms_kernel<T, V, N, true, false>, P);
 }
 
 // width over threads of at most kMaxElems elements each, over more CTAs where one does not hold it
@@ -150,13 +165,15 @@ cudaError_t launch_v(const NormsParams &P, cudaStream_t s) {
     int ranks = 1;
     while ((int64_t)ranks * kMaxThreads * kMaxN < runs) ranks *= 2;
     const int per = (runs + ranks - 1) / ranks;
-    int n = 1;
-    while (n < kMaxN && per > 512 * n) n *= 2;
-    const int threads = ((per + n - 1) / n + 31) / 32 * 32;
-    if (V == 1) return launch_n<T, V, kMaxN>(P, min(kMaxThreads, ((per + kMaxN - 1) / kMaxN + 31) / 32 * 32), ranks, s);
-    if (n == 1) return launch_n<T, V, 1>(P, threads, ranks, s);
-    if (n == 2) return launch_n<T, V, 2>(P, threads, ranks, s);
-    return launch_n<T, V, (kMaxN < 4 ? 2 : 4)>(P, threads, ranks, s);
+    // as few accesses per thread as 512 threads allow
+    const int n = (per + kMaxThreads - 1) / kMaxThreads;
+    auto threads = [&](int k) { return ((per + k - 1) / k + 31) / 32 * 32; };
+    if constexpr (V == 1) return launch_n<T, V, kMaxN>(P, threads(kMaxN), ranks, s);
+    else if constexpr (kMaxN == 2) return n == 1 ? launch_n<T, V, 1>(P, threads(1), ranks, s) : launch_n<T, V, 2>(P, threads(2), ranks, s);
+    else return n == 1   ? launch_n<T, V, 1>(P, threads(1), ranks, s)
+                : n == 2 ? launch_n<T, V, 2>(P, threads(2), ranks, s)
+                : n == 3 ? launch_n<T, V, 3>(P, threads(3), ranks, s)
+                         : launch_n<T, V, 4>(P, threads(4), ranks, s);
 }
 
 template <typename T>
