@@ -15,7 +15,7 @@ constexpr int kAttnMaxSeqs = 2048;
 constexpr bool attn_alone(int fmt, int dim, int nt, bool wide) {
     return (nt == 2 && dim != 64) || (dim == 256 && wide && fmt == COLI_KV_BF16);
 }
-constexpr int attn_tile(int fmt, int dim) { return fmt == COLI_KV_E4M3 || dim == 64 ? 32 : 16; }
+constexpr int attn_tile(int fmt, int dim) { return dim == 64 || fmt == COLI_KV_E4M3 ? 32 : 16; }
 constexpr int attn_warps(int dim, int nt) { return dim == 256 && nt == 1 ? 4 : 8; }
 constexpr int attn_ctas_per_sm(int fmt, int dim, int nt, bool wide) { return attn_alone(fmt, dim, nt, wide) ? 1 : 2; }
 constexpr int attn_slots(int fmt, int dim, int nt, bool wide) {
@@ -54,6 +54,7 @@ struct AttnWork {
     int32_t chunks;  // head groups per kv head
     int32_t groups;  // head groups per sequence
     int32_t unit;    // tokens of a unit
+    int32_t whole;   // no item is cut
     KvDivide divide;  // by the page size
     // the cache's strides in steps of 2^off_shift bytes, which divides them all
     uint32_t page_step, token_step, head_step, off_shift;

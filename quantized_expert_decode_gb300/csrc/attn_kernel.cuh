@@ -10,7 +10,8 @@
 //
 // Work. The cached tokens of every (sequence, kv head, group of query heads) are cut into units of
 // kWarps tiles of kTile tokens. All units of the call form one line that is cut into equal runs, one
-// per CTA, so a CTA's share does not depend on how the lengths are spread; an item that a run's
+// per CTA, so a CTA's share does not depend on how the lengths are spread (where the items let themselves be cut
+// evenly each by itself, a run stays within an item); an item that a run's
 // border cuts leaves partial sums in the workspace, which the join kernel adds up in a fixed order.
 //
 // Within a unit each warp owns one tile: it copies the tile's K rows and V rows to its own ring of kSlots
@@ -38,7 +39,10 @@ namespace colimoe {
 
 namespace attn {
 
-__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool valid) {
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy16_or_zero(uint32_t dst, const void *src, bool valid) {
     const int n = valid ? 16 : 0;  // 0: the 16 bytes are zeroed and src is not read
     asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
 }
@@ -47,11 +51,11 @@ template <int N> __device__ __forceinline__ void copy_wait() { asm volatile("cp.
 
 __device__ __forceinline__ void ldm4(uint32_t (&r)[4], uint32_t a) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a));
 }
 __device__ __forceinline__ void ldm4t(uint32_t (&r)[4], uint32_t a) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a));
 }
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
     uint32_t y;
@@ -64,16 +68,18 @@ __device__ __forceinline__ float exp2_fast(float x) {
     return y;
 }
 
-template <int FMT>
+// d = a b (+ d)
+template <int FMT, bool ADD>
 __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    const float c0 = ADD ? d[0] : 0.f, c1 = ADD ? d[1] : 0.f, c2 = ADD ? d[2] : 0.f, c3 = ADD ? d[3] : 0.f;
     if (FMT == COLI_KV_BF16)
-        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
+            : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
     else
-        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
+            : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
 }
 
 // two e4m3 values to two f16 values (exact; NaN stays NaN)
@@ -149,11 +155,11 @@ struct AttnTraits {
     static_assert(kWarps * kTile == attn_unit(FMT, DP, NT), "unit");
     static constexpr size_t smem(int seqs) {
         return (size_t)kWarps * kSlots * kSlotBytes + (size_t)kQWords * 16 + kWarps * kHeads * 8 + kHeads * 4 +
-               kWarps * 4 * 4 + ((size_t)seqs + 1) * 4 + 64;
+               kWarps * 4 * 4 + ((size_t)seqs + 1) * 4 + 160;
     }
     static_assert(kWarps * kSlots * kSlotBytes + kQWords * 16 + kWarps * kHeads * 8 + kHeads * 4 + kWarps * 16 +
-                          (kAttnMaxSeqs + 1) * 4 + 64 <=
-                      (227 << 10) / kCtas - 1024,
+                          (kAttnMaxSeqs + 1) * 4 + 160 <=
+                      (228 << 10) / kCtas - 1024,
                   "shared memory of an SM");
 };
 
@@ -168,7 +174,7 @@ __global__ void __launch_bounds__(T::kWarps * 32, T::kCtas) attn_stream_kernel(c
     float *qs = reinterpret_cast<float *>(ml + T::kWarps * T::kHeads);  // [head] factor of the products
     uint32_t *seen = reinterpret_cast<uint32_t *>(qs + T::kHeads);     // [warp][tile % 4] rows that hold a token
     int *pre = reinterpret_cast<int *>(seen + T::kWarps * 4);          // [seqs + 1] units before a sequence
-    int *scan = pre + P.seqs + 1;                                      // [8]
+    int *scan = pre + P.seqs + 1;                                      // [35]
     static_assert(kThreads % (DP / 4) == 0, "whole heads in a round");
     const int tid = threadIdx.x, w = tid / 32, lane = tid % 32, g = lane >> 2, c = lane & 3;
 
@@ -208,7 +214,6 @@ __global__ void __launch_bounds__(T::kWarps * 32, T::kCtas) attn_stream_kernel(c
     if (tid == 0) pre[0] = 0;
     __syncthreads();
     const uint32_t total = (uint32_t)pre[P.seqs] * W.groups;
-    const AttnRuns R(total, gridDim.x);
 
     // ---- sequences with nothing to see
     for (int b = blockIdx.x; b < P.seqs; b += gridDim.x) {
@@ -219,29 +224,103 @@ __global__ void __launch_bounds__(T::kWarps * 32, T::kCtas) attn_stream_kernel(c
             for (int i = tid; i < P.q_heads; i += kThreads) P.lse[(int64_t)b * P.q_heads + i] = -INFINITY;
     }
 
-    // ---- this CTA's run of units
+    // ---- this CTA's run. Either every item is cut by itself into parts of at most c units and a run is a part, if
+    // that makes no more runs than there are CTAs and none much longer than the others; or runs of equal length
+    // go on from item to item.
     const uint32_t run = blockIdx.x;
-    if (run >= R.runs) {
-        if (run == 0 && tid == 0) W.cuts[0].runs = 0;
-        return;
-    }
-    const uint32_t x0 = R.start(run), x1 = R.start(run + 1);
     Cursor at;
+    int n_units;
+    AttnCut cut{-1, 0, 0, 0};  // for the join
     {
-        // the last sequence whose units begin at or before x0
-        int lo = 0, hi = P.seqs;
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) / 2;
-            if ((uint32_t)pre[mid] * W.groups <= x0) lo = mid;
-            else hi = mid;
+        const uint32_t c0 = max(1u, (total + gridDim.x - 1) / gridDim.x);
+        const uint32_t c[3] = {W.whole ? 0x7fffffffu : c0, c0 + 1, c0 + 2 + c0 / 8};
+        uint32_t sum[3] = {0, 0, 0}, run_to[3];
+        for (int b = b0; b < b1; b++) {
+            const uint32_t u = pre[b + 1] - pre[b];
+#pragma unroll
+            for (int k = 0; k < 3; k++) sum[k] += (u + c[k] - 1) / c[k];
         }
-        at.b = lo;
-        at.units = pre[lo + 1] - pre[lo];
-        const uint32_t r = x0 - (uint32_t)pre[lo] * W.groups;
-        at.hv = (int)(r / (uint32_t)at.units);
-        at.u = (int)r - at.hv * at.units;
+#pragma unroll
+        for (int k = 0; k < 3; k++) {
+            run_to[k] = sum[k];
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const uint32_t v = __shfl_up_sync(0xffffffffu, run_to[k], o);
+                if (lane >= o) run_to[k] += v;
+            }
+            if (lane == 31) scan[8 * (k + 1) + w] = run_to[k];
+        }
+        __syncthreads();
+        uint32_t all[3], mine_from[3];
+#pragma unroll
+        for (int k = 0; k < 3; k++) {
+            all[k] = 0;
+            mine_from[k] = run_to[k] - sum[k];
+#pragma unroll
+            for (int i = 0; i < T::kWarps; i++) {
+                const uint32_t v = scan[8 * (k + 1) + i];
+                if (i < w) mine_from[k] += v;
+                all[k] += v;
+            }
+        }
+        const int k = (uint64_t)all[0] * W.groups <= gridDim.x ? 0 : (uint64_t)all[1] * W.groups <= gridDim.x ? 1 : 2;
+        const uint32_t parts = k == 0 ? all[0] : k == 1 ? all[1] : all[2], cap = k == 0 ? c[0] : k == 1 ? c[1] : c[2];
+        if ((uint64_t)parts * W.groups <= gridDim.x) {
+            cut.runs = parts * W.groups;
+            if (run < (uint32_t)cut.runs) {
+                // the thread whose sequences the run is among tells which one it is
+                uint32_t from = (k == 0 ? mine_from[0] : k == 1 ? mine_from[1] : mine_from[2]) * W.groups;
+                for (int b = b0; b < b1; b++) {
+                    const uint32_t p = ((uint32_t)(pre[b + 1] - pre[b]) + cap - 1) / cap;
+                    if (run >= from && run < from + p * W.groups) {
+                        scan[32] = b;
+                        scan[33] = run - from;
+                        scan[34] = p;
+                    }
+                    from += p * W.groups;
+                }
+            }
+            __syncthreads();
+            if (run >= (uint32_t)cut.runs) {
+                if (run == 0 && tid == 0) W.cuts[0] = cut;
+                return;
+            }
+            const int p = scan[34], part = scan[33] % p;
+            at.b = scan[32];
+            at.hv = scan[33] / p;
+            at.units = pre[at.b + 1] - pre[at.b];
+            at.u = part * (at.units / p) + min(part, at.units % p);
+            n_units = at.units / p + (part < at.units % p ? 1 : 0);
+            if (part == 1) {
+                cut.b = at.b;
+                cut.hv = at.hv;
+                cut.last = run + p - 2;
+            }
+        } else {
+            const AttnRuns R(total, gridDim.x);
+            cut.runs = R.runs;
+            const uint32_t x0 = R.start(run);
+            n_units = R.start(run + 1) - x0;
+            // the last sequence whose units begin at or before x0
+            int lo = 0, hi = P.seqs;
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) / 2;
+                if ((uint32_t)pre[mid] * W.groups <= x0) lo = mid;
+                else hi = mid;
+            }
+            at.b = lo;
+            at.units = pre[lo + 1] - pre[lo];
+            const uint32_t r = x0 - (uint32_t)pre[lo] * W.groups;
+            at.hv = (int)(r / (uint32_t)at.units);
+            at.u = (int)r - at.hv * at.units;
+            const uint32_t i0 = x0 - at.u;
+            if (at.u > 0 && R.start(run - 1) <= i0) {
+                cut.b = at.b;
+                cut.hv = at.hv;
+                cut.last = (int)R.of(i0 + at.units - 1);
+            }
+        }
     }
-    const int n_units = (int)(x1 - x0);
     auto advance = [&](Cursor &k) {
         if (++k.u < k.units) return;
         k.u = 0;
@@ -276,7 +355,9 @@ __global__ void __launch_bounds__(T::kWarps * 32, T::kCtas) attn_stream_kernel(c
     // ---- copies
     unsigned char *my_ring = ring + w * T::kSlots * T::kSlotBytes;
     const uint32_t my_ring_a = smem_u32(my_ring);
-    // 16-byte chunks of a 128-byte line are exchanged so that 8 rows' same chunk lie in 8 bank groups
+    // 16-byte chunks of a 128-byte line are exchanged so that 8 rows' same chunk lie in 8 bank groups. A chunk's
+    // number is only ever or'ed or xor'ed into an address, whose bits from 4 up it then owns (rows start at
+    // multiples of 128 bytes): place(row, c ^ d) = place(row, c) ^ (d << 4).
     auto place = [](int row, int chunk) -> uint32_t {
         if (T::kRow >= 128) return row * T::kRow + ((chunk ^ (row & 7)) << 4);
         const int line = row >> 1;
@@ -285,8 +366,9 @@ __global__ void __launch_bounds__(T::kWarps * 32, T::kCtas) attn_stream_kernel(c
     constexpr uint32_t kAll = T::kTile == 32 ? 0xffffffffu : 0xffffu;
     constexpr int kChunks = T::kRow / 16, kRowsPer = 32 / kChunks;
     const int ch = lane % kChunks, sub = lane / kChunks;
-    const bool in_row = ch * 16 < P.dim * T::kSize;
+    const bool in_row = ch * 16 < P.dim * T::kSize, full_rows = P.dim == DP;
     const char *kbase = (const char *)P.k_cache + (in_row ? ch * 16 : 0), *vbase = (const char *)P.v_cache + (in_row ? ch * 16 : 0);
+    const uint32_t off_step = 1u << W.off_shift, my_place = place(sub, ch);
     Cursor ld = at;
     int ld_left = n_units;
     int ld_first = 0, ld_end = 0, ld_head = 0;
@@ -321,13 +403,25 @@ __global__ void __launch_bounds__(T::kWarps * 32, T::kCtas) attn_stream_kernel(c
     };
     uint32_t cp_rows = 0, cp_off = 0;  // of the tile whose halves are copied
     auto copy_rows = [&](uint32_t dst, const char *base) {
-        if (cp_rows) {
+        // row i * kRowsPer + sub: its place differs from row sub's by a distance and, within 8 rows, by an xor
+        auto to = [&](int i) {
+            const int row = i * kRowsPer;  // of sub 0
+            if (T::kRow >= 128) return (dst + row * T::kRow) + (my_place ^ ((row & 7) << 4));
+            return (dst + row * T::kRow) + (my_place ^ (((row >> 1) & 3) << 4));
+        };
+        if (cp_rows == kAll && full_rows) {
+#pragma unroll
+            for (int i = 0; i < T::kTile / kRowsPer; i++) {
+                const uint32_t o = __shfl_sync(0xffffffffu, cp_off, i * kRowsPer + sub);
+                copy16(to(i), base + (uint64_t)o * off_step);
+            }
+        } else if (cp_rows) {
 #pragma unroll
             for (int i = 0; i < T::kTile / kRowsPer; i++) {
                 const int row = i * kRowsPer + sub;
                 const uint32_t o = __shfl_sync(0xffffffffu, cp_off, row);
                 const bool ok = in_row && ((cp_rows >> row) & 1);
-                copy16(dst + place(row, ch), base + ((uint64_t)(ok ? o : 0) << W.off_shift), ok);
+                copy16_or_zero(to(i), base + (uint64_t)(ok ? o : 0) * off_step, ok);
             }
         }
         copy_commit();
@@ -367,16 +461,7 @@ __global__ void __launch_bounds__(T::kWarps * 32, T::kCtas) attn_stream_kernel(c
     }
 
     // ---- for the join: the item that this run's first border cuts, told by the run behind its first cut
-    if (tid == 0) {
-        AttnCut cut{-1, 0, 0, (int)R.runs};
-        const uint32_t i0 = x0 - at.u;
-        if (at.u > 0 && R.start(run - 1) <= i0) {
-            cut.b = at.b;
-            cut.hv = at.hv;
-            cut.last = (int)R.of(i0 + at.units - 1);
-        }
-        W.cuts[run] = cut;
-    }
+    if (tid == 0 && !W.whole) W.cuts[run] = cut;
 
     float o[T::kKS][NT][4], m[NT][2], l[NT][2], sc[NT][2];
     int slot = 0;
@@ -433,6 +518,7 @@ __global__ void __launch_bounds__(T::kWarps * 32, T::kCtas) attn_stream_kernel(c
                     m[n][j] = -INFINITY;
                     l[n][j] = 0.f;
                     sc[n][j] = qs[n * 8 + 2 * c + j];
+                    if (sc[n][j] == 0.f) sc[n][j] = 1.175494351e-38f;  // so that it keeps an infinity one
                 }
 #pragma unroll
                 for (int i = 0; i < T::kKS; i++)
@@ -457,13 +543,7 @@ __global__ void __launch_bounds__(T::kWarps * 32, T::kCtas) attn_stream_kernel(c
             for (int i = 0; i < T::kMT; i++) {
                 constexpr int kChains = T::kQParts > 1 ? 3 : 2;
                 float acc[kChains][NT][4];
-#pragma unroll
-                for (int k = 0; k < kChains; k++)
-#pragma unroll
-                    for (int n = 0; n < NT; n++)
-#pragma unroll
-                        for (int j = 0; j < 4; j++) acc[k][n][j] = 0.f;
-                const int row = i * 16 + lr + (li & 1) * 8;
+                const uint32_t at_row = kt + place(i * 16 + lr + (li & 1) * 8, li >> 1);
                 // two products of 16 along the head
                 auto product = [&](const uint32_t (&a0)[4], const uint32_t (&a1)[4], int k2) {
 #pragma unroll
@@ -471,20 +551,31 @@ __global__ void __launch_bounds__(T::kWarps * 32, T::kCtas) attn_stream_kernel(c
 #pragma unroll
                         for (int n = 0; n < NT; n++) {
                             const uint4 q = qf[((p * NT + n) * (T::kKS / 2) + k2) * 32 + lane];
-                            mma<FMT>(acc[p ? kChains - 1 : 0][n], a0, q.x, q.y);
-                            mma<FMT>(acc[p ? kChains - 1 : 1][n], a1, q.z, q.w);
+                            if (p == 0) {
+                                if (k2 == 0) {
+                                    mma<FMT, false>(acc[0][n], a0, q.x, q.y);
+                                    mma<FMT, false>(acc[1][n], a1, q.z, q.w);
+                                } else {
+                                    mma<FMT, true>(acc[0][n], a0, q.x, q.y);
+                                    mma<FMT, true>(acc[1][n], a1, q.z, q.w);
+                                }
+                            } else {
+                                if (k2 == 0 && p == 1) mma<FMT, false>(acc[kChains - 1][n], a0, q.x, q.y);
+                                else mma<FMT, true>(acc[kChains - 1][n], a0, q.x, q.y);
+                                mma<FMT, true>(acc[kChains - 1][n], a1, q.z, q.w);
+                            }
                         }
                 };
 #pragma unroll
                 for (int k2 = 0; k2 < T::kKS / 2; k2++) {
                     if (FMT != COLI_KV_E4M3) {
                         uint32_t a0[4], a1[4];
-                        ldm4(a0, kt + place(row, 4 * k2 + (li >> 1)));
-                        ldm4(a1, kt + place(row, 4 * k2 + 2 + (li >> 1)));
+                        ldm4(a0, at_row ^ ((4 * k2) << 4));
+                        ldm4(a1, at_row ^ ((4 * k2 + 2) << 4));
                         product(a0, a1, k2);
                     } else {
                         uint32_t raw[4];
-                        ldm4(raw, kt + place(row, 2 * k2 + (li >> 1)));
+                        ldm4(raw, at_row ^ ((2 * k2) << 4));
                         const uint32_t a0[4] = {widen(raw[0]), widen(raw[1]), widen_hi(raw[0]), widen_hi(raw[1])};
                         const uint32_t a1[4] = {widen(raw[2]), widen(raw[3]), widen_hi(raw[2]), widen_hi(raw[3])};
                         product(a0, a1, k2);
@@ -495,6 +586,15 @@ __global__ void __launch_bounds__(T::kWarps * 32, T::kCtas) attn_stream_kernel(c
 #pragma unroll
                     for (int j = 0; j < 4; j++)
                         s[i][n][j] = acc[0][n][j] + (acc[1][n][j] + (kChains > 2 ? acc[kChains - 1][n][j] : 0.f));
+            }
+            if (rows != kAll) {  // a score of -inf where there is no token
+#pragma unroll
+                for (int i = 0; i < T::kMT; i++)
+#pragma unroll
+                    for (int j = 0; j < 4; j++)
+                        if (!((rows >> (i * 16 + (j >> 1) * 8 + g)) & 1))
+#pragma unroll
+                            for (int n = 0; n < NT; n++) s[i][n][j] = sc[n][j & 1] > 0.f ? -INFINITY : INFINITY;
             }
         }
         __syncwarp();
@@ -509,7 +609,6 @@ __global__ void __launch_bounds__(T::kWarps * 32, T::kCtas) attn_stream_kernel(c
             // ---- softmax over the tile's tokens, head by head
             uint32_t pf[T::kPParts][T::kMT][NT][2];
             float f[NT][2];
-            const bool all = rows == kAll;
 #pragma unroll
             for (int n = 0; n < NT; n++) {
 #pragma unroll
@@ -519,8 +618,7 @@ __global__ void __launch_bounds__(T::kWarps * 32, T::kCtas) attn_stream_kernel(c
                     for (int i = 0; i < T::kMT; i++)
 #pragma unroll
                         for (int r = 0; r < 2; r++) {
-                            const float x = s[i][n][2 * r + j] * sc[n][j];
-                            top = all || ((rows >> (i * 16 + r * 8 + g)) & 1) ? fmaxf(top, x) : top;
+                            top = fmaxf(top, s[i][n][2 * r + j] * sc[n][j]);
                         }
 #pragma unroll
                     for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
@@ -534,8 +632,7 @@ __global__ void __launch_bounds__(T::kWarps * 32, T::kCtas) attn_stream_kernel(c
 #pragma unroll
                         for (int r = 0; r < 2; r++) {
                             // one rounding for the exponent, small where p is large
-                            float p = exp2_fast(fmaf(s[i][n][2 * r + j], sc[n][j], (float)T::kShift - ref));
-                            p = all || ((rows >> (i * 16 + r * 8 + g)) & 1) ? p : 0.f;
+                            const float p = exp2_fast(fmaf(s[i][n][2 * r + j], sc[n][j], (float)T::kShift - ref));
                             s[i][n][2 * r + j] = p;
                             sum += p;
                         }
@@ -552,22 +649,21 @@ __global__ void __launch_bounds__(T::kWarps * 32, T::kCtas) attn_stream_kernel(c
             }
             // ---- O^T += V^T P^T
             if (FMT != COLI_KV_E4M3) {
-                const int row = lr + (li >> 1) * 8;
+                const uint32_t at_row = vt + place(lr + (li >> 1) * 8, li & 1);
 #pragma unroll
                 for (int d = 0; d < T::kKS; d++) {
                     float t[NT][4];
 #pragma unroll
-                    for (int n = 0; n < NT; n++)
-#pragma unroll
-                        for (int j = 0; j < 4; j++) t[n][j] = 0.f;
-#pragma unroll
                     for (int i = 0; i < T::kMT; i++) {
                         uint32_t a[4];
-                        ldm4t(a, vt + place(i * 16 + row, 2 * d + (li & 1)));
+                        ldm4t(a, (at_row ^ ((2 * d) << 4)) + i * 16 * T::kRow);
 #pragma unroll
-                        for (int n = 0; n < NT; n++)
+                        for (int p = T::kPParts - 1; p >= 0; p--)
 #pragma unroll
-                            for (int p = T::kPParts - 1; p >= 0; p--) mma<FMT>(t[n], a, pf[p][i][n][0], pf[p][i][n][1]);
+                            for (int n = 0; n < NT; n++) {
+                                if (i == 0 && p == T::kPParts - 1) mma<FMT, false>(t[n], a, pf[p][i][n][0], pf[p][i][n][1]);
+                                else mma<FMT, true>(t[n], a, pf[p][i][n][0], pf[p][i][n][1]);
+                            }
                     }
 #pragma unroll
                     for (int n = 0; n < NT; n++)
@@ -575,29 +671,26 @@ __global__ void __launch_bounds__(T::kWarps * 32, T::kCtas) attn_stream_kernel(c
                         for (int j = 0; j < 4; j++) o[d][n][j] = fmaf(o[d][n][j], f[n][j & 1], t[n][j]);
                 }
             } else {
+                const uint32_t at_row = vt + place(lr + (li & 1) * 8, li >> 1);
 #pragma unroll
                 for (int d2 = 0; d2 < T::kKS / 2; d2++) {
                     float t[2][NT][4];
 #pragma unroll
-                    for (int hf = 0; hf < 2; hf++)
-#pragma unroll
-                        for (int n = 0; n < NT; n++)
-#pragma unroll
-                            for (int j = 0; j < 4; j++) t[hf][n][j] = 0.f;
-#pragma unroll
                     for (int i = 0; i < T::kMT; i++) {
                         uint32_t raw[4];
-                        ldm4t(raw, vt + place(i * 16 + lr + (li & 1) * 8, 2 * d2 + (li >> 1)));
+                        ldm4t(raw, (at_row ^ ((2 * d2) << 4)) + i * 16 * T::kRow);
 #pragma unroll
                         for (int hf = 0; hf < 2; hf++) {
                             // bytes (token, dim): 00 01 10 11 -> even dim's two tokens, odd dim's two tokens
                             const uint32_t x = __byte_perm(raw[2 * hf], 0, 0x3120), y = __byte_perm(raw[2 * hf + 1], 0, 0x3120);
                             const uint32_t a[4] = {widen(x), widen_hi(x), widen(y), widen_hi(y)};
 #pragma unroll
-                            for (int n = 0; n < NT; n++)
+                            for (int p = T::kPParts - 1; p >= 0; p--)
 #pragma unroll
-                                for (int p = T::kPParts - 1; p >= 0; p--)
-                                    mma<FMT>(t[hf][n], a, pf[p][i][n][0], pf[p][i][n][1]);
+                                for (int n = 0; n < NT; n++) {
+                                    if (i == 0 && p == T::kPParts - 1) mma<FMT, false>(t[hf][n], a, pf[p][i][n][0], pf[p][i][n][1]);
+                                    else mma<FMT, true>(t[hf][n], a, pf[p][i][n][0], pf[p][i][n][1]);
+                                }
                         }
                     }
 #pragma unroll
