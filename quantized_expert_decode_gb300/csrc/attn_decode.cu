@@ -9,7 +9,6 @@ namespace colimoe {
 namespace {
 
 constexpr int kJoinThreads = 256;
-constexpr int kWholeUnits = 3;
 
 // One block per (border between runs, head of the group): the block of an item's first cut adds up the
 // partial sums of all runs that hold units of the item, in the order of the runs within each warp and
@@ -97,10 +96,12 @@ Layout layout_of(const AttnParams &P) {
     const int64_t ctas = (int64_t)num_sms() * attn_ctas_per_sm(P.fmt, L.w.dim, L.w.nt, L.w.wide);
     L.units = most;
     L.grid = (int)(most < ctas ? most : ctas);
-    // short items that all find a place: a CTA each and no join, whose launch costs the host as much as the cut saves
-    // the device (333 tokens of one sequence: 8.2 us against 6.8 on the device, 8.5 against 10.4 called from Python)
+    // short items that all find a place are not cut: a CTA each and no join. Where they are few that costs the device
+    // as much as the cut saves it, but no second launch (333 tokens of one sequence: 8.2 us against 6.8 on the
+    // device, 8.5 against 10.4 called from Python); where they fill a quarter of the places it is faster (16
+    // sequences of 1000 tokens, 8 kv heads: 17 us against 21; 32 of 500: 16 against 20).
     const int64_t items = (int64_t)P.seqs * L.w.groups;
-    if (items <= ctas && most <= kWholeUnits * items) {
+    if (items <= ctas && (most <= 3 * items || (most <= 8 * items && 4 * items >= ctas))) {
         L.w.whole = 1;
         L.grid = (int)items;
     }

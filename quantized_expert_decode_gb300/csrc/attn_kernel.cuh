@@ -224,16 +224,22 @@ __global__ void __launch_bounds__(T::kWarps * 32, T::kCtas) attn_stream_kernel(c
             for (int i = tid; i < P.q_heads; i += kThreads) P.lse[(int64_t)b * P.q_heads + i] = -INFINITY;
     }
 
-    // ---- this CTA's run. Either every item is cut by itself into parts of at most c units and a run is a part, if
-    // that makes no more runs than there are CTAs and none much longer than the others; or runs of equal length
-    // go on from item to item.
+    // ---- this CTA's run: an item; or a part of an item, every item cut by itself into parts of at most c units, if
+    // that makes no more runs than there are CTAs and none much longer than the others; or a run of as many units
+    // as any other's, which may go on from item to item (of one unit where there are CTAs enough).
     const uint32_t run = blockIdx.x;
-    Cursor at;
-    int n_units;
+    Cursor at{0, 0, 0, 0};
+    int n_units = 0;
     AttnCut cut{-1, 0, 0, 0};  // for the join
-    {
-        const uint32_t c0 = max(1u, (total + gridDim.x - 1) / gridDim.x);
-        const uint32_t c[3] = {W.whole ? 0x7fffffffu : c0, c0 + 1, c0 + 2 + c0 / 8};
+    if (W.whole) {
+        at.b = run / W.groups;
+        at.hv = run - at.b * W.groups;
+        at.units = n_units = pre[at.b + 1] - pre[at.b];
+        if (n_units == 0) return;
+    }
+    if (!W.whole && total > gridDim.x) {
+        const uint32_t c0 = (total + gridDim.x - 1) / gridDim.x;
+        const uint32_t c[3] = {c0, c0 + 1, c0 + 2 + c0 / 8};
         uint32_t sum[3] = {0, 0, 0}, run_to[3];
         for (int b = b0; b < b1; b++) {
             const uint32_t u = pre[b + 1] - pre[b];
@@ -296,29 +302,34 @@ __global__ void __launch_bounds__(T::kWarps * 32, T::kCtas) attn_stream_kernel(c
                 cut.hv = at.hv;
                 cut.last = run + p - 2;
             }
-        } else {
-            const AttnRuns R(total, gridDim.x);
-            cut.runs = R.runs;
-            const uint32_t x0 = R.start(run);
-            n_units = R.start(run + 1) - x0;
-            // the last sequence whose units begin at or before x0
-            int lo = 0, hi = P.seqs;
-            while (hi - lo > 1) {
-                const int mid = (lo + hi) / 2;
-                if ((uint32_t)pre[mid] * W.groups <= x0) lo = mid;
-                else hi = mid;
-            }
-            at.b = lo;
-            at.units = pre[lo + 1] - pre[lo];
-            const uint32_t r = x0 - (uint32_t)pre[lo] * W.groups;
-            at.hv = (int)(r / (uint32_t)at.units);
-            at.u = (int)r - at.hv * at.units;
-            const uint32_t i0 = x0 - at.u;
-            if (at.u > 0 && R.start(run - 1) <= i0) {
-                cut.b = at.b;
-                cut.hv = at.hv;
-                cut.last = (int)R.of(i0 + at.units - 1);
-            }
+        }
+    }
+    if (!W.whole && n_units == 0) {
+        const AttnRuns R(total, gridDim.x);
+        cut.runs = R.runs;
+        if (run >= R.runs) {
+            if (run == 0 && tid == 0) W.cuts[0] = cut;
+            return;
+        }
+        const uint32_t x0 = R.start(run);
+        n_units = R.start(run + 1) - x0;
+        // the last sequence whose units begin at or before x0
+        int lo = 0, hi = P.seqs;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) / 2;
+            if ((uint32_t)pre[mid] * W.groups <= x0) lo = mid;
+            else hi = mid;
+        }
+        at.b = lo;
+        at.units = pre[lo + 1] - pre[lo];
+        const uint32_t r = x0 - (uint32_t)pre[lo] * W.groups;
+        at.hv = (int)(r / (uint32_t)at.units);
+        at.u = (int)r - at.hv * at.units;
+        const uint32_t i0 = x0 - at.u;
+        if (at.u > 0 && R.start(run - 1) <= i0) {
+            cut.b = at.b;
+            cut.hv = at.hv;
+            cut.last = (int)R.of(i0 + at.units - 1);
         }
     }
     auto advance = [&](Cursor &k) {
