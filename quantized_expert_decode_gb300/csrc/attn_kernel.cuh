@@ -381,7 +381,6 @@ __global__ void __launch_bounds__(T::kWarps * 32, T::kCtas) attn_stream_kernel(c
     const char *kbase = (const char *)P.k_cache + (in_row ? ch * 16 : 0), *vbase = (const char *)P.v_cache + (in_row ? ch * 16 : 0);
     const uint32_t off_step = 1u << W.off_shift, my_place = place(sub, ch);
     Cursor ld = at;
-    int ld_left = n_units;
     int ld_first = 0, ld_end = 0, ld_head = 0;
     const int32_t *ld_pages = P.table;
     auto enter = [&]() {  // an item
@@ -396,9 +395,9 @@ __global__ void __launch_bounds__(T::kWarps * 32, T::kCtas) attn_stream_kernel(c
         int32_t page, slot, head;
         bool real;
     };
-    auto look_up = [&]() {
+    auto look_up = [&](int left) {  // of how many units
         Look k{0, 0, ld_head, false};
-        if (ld_left <= 0) return k;
+        if (left <= 0) return k;
         const int t = ld_first + ld.u * W.unit + w * T::kTile + lane;
         if (lane < T::kTile && t < ld_end) {
             const int i = kv_quotient(W.divide, t);
@@ -406,7 +405,7 @@ __global__ void __launch_bounds__(T::kWarps * 32, T::kCtas) attn_stream_kernel(c
             k.page = ld_pages[i];
             k.real = true;
         }
-        if (--ld_left > 0) {
+        if (left > 1) {
             advance(ld);
             if (ld.u == 0) enter();
         }
@@ -437,24 +436,18 @@ __global__ void __launch_bounds__(T::kWarps * 32, T::kCtas) attn_stream_kernel(c
         }
         copy_commit();
     };
-    int cp_tile = 0, cp_slot = 0;
     auto next_slot = [](int &s) { s = s + 1 == T::kSlots ? 0 : s + 1; };
-    auto copy_k = [&](Look k) {
+    auto copy_k = [&](Look k, int tile, int into) {
         if (k.real && (uint32_t)k.page >= (uint32_t)P.cache.pages) {
             k.real = false;
             if (P.err) atomicOr(P.err, COLI_LAYER_BAD_PAGE);
         }
         cp_rows = __ballot_sync(0xffffffffu, k.real);
         cp_off = k.page * W.page_step + k.slot * W.token_step + k.head * W.head_step;
-        if (lane == 0) seen[w * 4 + (cp_tile & 3)] = cp_rows;
-        cp_tile++;
-        copy_rows(my_ring_a + cp_slot * T::kSlotBytes, kbase);
-        next_slot(cp_slot);
+        if (lane == 0) seen[w * 4 + (tile & 3)] = cp_rows;
+        copy_rows(my_ring_a + into * T::kSlotBytes, kbase);
     };
-    auto copy_v = [&]() {
-        copy_rows(my_ring_a + cp_slot * T::kSlotBytes, vbase);
-        next_slot(cp_slot);
-    };
+    auto copy_v = [&](int into) { copy_rows(my_ring_a + into * T::kSlotBytes, vbase); };
 
     enter();
     Look next;  // the tile whose K is copied next
@@ -462,12 +455,12 @@ __global__ void __launch_bounds__(T::kWarps * 32, T::kCtas) attn_stream_kernel(c
         constexpr int kFirst = (T::kSlots + 1) / 2;  // K and V in turn
         Look k[kFirst];
 #pragma unroll
-        for (int i = 0; i < kFirst; i++) k[i] = look_up();
-        next = look_up();
+        for (int i = 0; i < kFirst; i++) k[i] = look_up(n_units - i);
+        next = look_up(n_units - kFirst);
 #pragma unroll
         for (int i = 0; i < T::kSlots; i++) {
-            if (i % 2 == 0) copy_k(k[i / 2]);
-            else copy_v();
+            if (i % 2 == 0) copy_k(k[i / 2], i / 2, i);
+            else copy_v(i);
         }
     }
 
@@ -541,7 +534,8 @@ __global__ void __launch_bounds__(T::kWarps * 32, T::kCtas) attn_stream_kernel(c
         copy_wait<T::kSlots - 1>();
         __syncwarp();
         const uint32_t rows = seen[w * 4 + (it & 3)];
-        const uint32_t kt = my_ring_a + slot * T::kSlotBytes;
+        const int k_slot = slot;
+        const uint32_t kt = my_ring_a + k_slot * T::kSlotBytes;
         next_slot(slot);
         const int v_slot = slot;
         const uint32_t vt = my_ring_a + v_slot * T::kSlotBytes;
@@ -609,10 +603,12 @@ __global__ void __launch_bounds__(T::kWarps * 32, T::kCtas) attn_stream_kernel(c
             }
         }
         __syncwarp();
-        if (T::kSlots % 2) copy_v();  // the slots hold K and V in turn
-        else {
-            copy_k(next);
-            next = look_up();
+        // the half that is kSlots behind K takes its slot
+        if (T::kSlots % 2) {
+            copy_v(k_slot);
+        } else {
+            copy_k(next, it + T::kSlots / 2, k_slot);
+            next = look_up(n_units - it - (T::kSlots / 2 + 1));
         }
         copy_wait<T::kSlots - 1>();
         __syncwarp();
@@ -781,10 +777,10 @@ __global__ void __launch_bounds__(T::kWarps * 32, T::kCtas) attn_stream_kernel(c
             fresh = true;
         }
         if (T::kSlots % 2) {
-            copy_k(next);
-            next = look_up();
+            copy_k(next, it + T::kSlots / 2 + 1, v_slot);
+            next = look_up(n_units - it - (T::kSlots / 2 + 2));
         } else {
-            copy_v();
+            copy_v(v_slot);
         }
         advance(at);
     }
