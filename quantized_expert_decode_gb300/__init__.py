@@ -305,27 +305,23 @@ def make_norms_desc(rows, width, act=COLI_ACT_F32, gate=COLI_GATE_NONE, post_eps
                            gate_stride, resid_out_stride, xn_stride)
 
 
-# the calls of a decode step: bound once, their arguments' addresses taken without the type tests of _ptr
+# The calls of a decode step, bound once. Tensors' addresses are taken in place; anything else (an address, an array)
+# goes the general way.
 _kv_append, _attn_decode, _block_norms = _lib.coli_kv_append, _lib.coli_attn_decode, _lib.coli_block_norms
 _byref = ctypes.byref
 
 
-def _adr(a):
-    if a is None:
-        return None
-    try:
-        return a.data_ptr()
-    except AttributeError:
-        return _ptr(a)
-
-
 def coli_kv_append(desc, cache, q, k, v, inv_freq, seq, pos, table, q_out, err=None, stream=None,
                    raise_on_error=True):
-    rc = _kv_append(_byref(desc), _byref(cache), _adr(q), _adr(k), _adr(v), _adr(inv_freq), _adr(seq), _adr(pos),
-                    _adr(table), _adr(q_out), _adr(err), _stream(stream))
-    if rc:
-        _check(rc, "coli_kv_append", raise_on_error)
-    return rc
+    try:
+        rc = _kv_append(_byref(desc), _byref(cache), None if q is None else q.data_ptr(), k.data_ptr(), v.data_ptr(),
+                        None if inv_freq is None else inv_freq.data_ptr(), None if seq is None else seq.data_ptr(),
+                        pos.data_ptr(), table.data_ptr(), None if q_out is None else q_out.data_ptr(),
+                        None if err is None else err.data_ptr(), None if stream is None else stream.cuda_stream)
+    except AttributeError:
+        rc = _kv_append(_byref(desc), _byref(cache), _ptr(q), _ptr(k), _ptr(v), _ptr(inv_freq), _ptr(seq), _ptr(pos),
+                        _ptr(table), _ptr(q_out), _ptr(err), _stream(stream))
+    return _check(rc, "coli_kv_append", raise_on_error) if rc else rc
 
 
 def coli_attn_workspace_bytes(desc, cache) -> int:
@@ -334,16 +330,23 @@ def coli_attn_workspace_bytes(desc, cache) -> int:
 
 def coli_attn_decode(desc, cache, q, table, lens, out, lse=None, err=None, ws=None, ws_bytes=0, stream=None,
                      raise_on_error=True):
-    rc = _attn_decode(_byref(desc), _byref(cache), _adr(q), _adr(table), _adr(lens), _adr(out), _adr(lse), _adr(err),
-                      _adr(ws), ws_bytes, _stream(stream))
-    if rc:
-        _check(rc, "coli_attn_decode", raise_on_error)
-    return rc
+    try:
+        rc = _attn_decode(_byref(desc), _byref(cache), q.data_ptr(), table.data_ptr(), lens.data_ptr(), out.data_ptr(),
+                          None if lse is None else lse.data_ptr(), None if err is None else err.data_ptr(), ws.data_ptr(),
+                          ws_bytes, None if stream is None else stream.cuda_stream)
+    except AttributeError:
+        rc = _attn_decode(_byref(desc), _byref(cache), _ptr(q), _ptr(table), _ptr(lens), _ptr(out), _ptr(lse), _ptr(err),
+                          _ptr(ws), ws_bytes, _stream(stream))
+    return _check(rc, "coli_attn_decode", raise_on_error) if rc else rc
 
 
 def coli_block_norms(desc, y, resid, post_w, gate, pre_w, resid_out, xn, stream=None, raise_on_error=True):
-    rc = _block_norms(_byref(desc), _adr(y), _adr(resid), _adr(post_w), _adr(gate), _adr(pre_w), _adr(resid_out),
-                      _adr(xn), _stream(stream))
-    if rc:
-        _check(rc, "coli_block_norms", raise_on_error)
-    return rc
+    try:
+        rc = _block_norms(_byref(desc), y.data_ptr(), resid.data_ptr(), None if post_w is None else post_w.data_ptr(),
+                          None if gate is None else gate.data_ptr(), None if pre_w is None else pre_w.data_ptr(),
+                          resid_out.data_ptr(), None if xn is None else xn.data_ptr(),
+                          None if stream is None else stream.cuda_stream)
+    except AttributeError:
+        rc = _block_norms(_byref(desc), _ptr(y), _ptr(resid), _ptr(post_w), _ptr(gate), _ptr(pre_w), _ptr(resid_out),
+                          _ptr(xn), _stream(stream))
+    return _check(rc, "coli_block_norms", raise_on_error) if rc else rc
