@@ -49,6 +49,7 @@ struct AttnCut {
 // How the launch is laid out, and the workspace
 struct AttnWork {
     int32_t dim;     // head size rounded up: 64, 128 or 256
+    int32_t use;     // of which the products take: dim, or 96 of 128
     int32_t nt;      // query heads of a CTA / 8
     int32_t wide;    // more parts of q and p
     int32_t chunks;  // head groups per kv head

@@ -78,6 +78,7 @@ Layout layout_of(const AttnParams &P) {
     Layout L{};
     const int group = P.q_heads / P.kv_heads;
     L.w.dim = P.dim <= 64 ? 64 : P.dim <= 128 ? 128 : 256;
+    L.w.use = P.dim > 64 && P.dim <= 96 ? 96 : L.w.dim;
     L.w.nt = group <= 8 ? 1 : 2;
     // q in one part where the cache's type (f16 for e4m3, scaled) holds it
     L.w.wide = P.act == COLI_ACT_F32 || (P.act == COLI_ACT_F16 && P.fmt == COLI_KV_BF16);

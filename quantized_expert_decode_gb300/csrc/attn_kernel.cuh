@@ -39,12 +39,9 @@ namespace colimoe {
 
 namespace attn {
 
-__device__ __forceinline__ void copy16(uint32_t dst, const void *src) {
-    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void copy16_or_zero(uint32_t dst, const void *src, bool valid) {
-    const int n = valid ? 16 : 0;  // 0: the 16 bytes are zeroed and src is not read
-    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+// `bytes` of 16 are copied, the rest are zeros (of 0, src is not read)
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, uint32_t bytes) {
+    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N> __device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
@@ -132,9 +129,10 @@ struct Cursor {
 
 }  // namespace attn
 
-// FMT the cache type, DP the head size rounded up to 64, 128 or 256, NT groups of 8 query heads per CTA,
+// FMT the cache type, DP the head size rounded up to 64, 128 or 256, USE the elements of it that the products
+// take (96 of 128 for heads of up to 96), NT groups of 8 query heads per CTA,
 // WIDE: q (and p in bf16) in more parts
-template <int FMT, int DP, int NT, bool WIDE>
+template <int FMT, int DP, int USE, int NT, bool WIDE>
 struct AttnTraits {
     static constexpr int kFmt = FMT, kDim = DP, kNT = NT;
     static constexpr int kSize = FMT == COLI_KV_E4M3 ? 1 : 2;
@@ -147,7 +145,7 @@ struct AttnTraits {
     static constexpr int kHeads = 8 * NT;
     static constexpr int kQParts = !WIDE ? 1 : FMT == COLI_KV_BF16 ? 3 : 2;
     static constexpr int kPParts = WIDE && FMT == COLI_KV_BF16 ? 3 : 2;
-    static constexpr int kKS = DP / 16;                           // products of 16 along the head
+    static constexpr int kUse = USE, kKS = USE / 16;                           // products of 16 along the head
     static constexpr int kQWords = kQParts * NT * kKS / 2 * 32;   // uint4
     // p is kept times 2^kShift, so that the second f16 part of a small p is still above f16's smallest step
     static constexpr int kShift = FMT == COLI_KV_BF16 ? 0 : 14;
@@ -377,7 +375,9 @@ __global__ void __launch_bounds__(T::kWarps * 32, T::kCtas) attn_stream_kernel(c
     constexpr uint32_t kAll = T::kTile == 32 ? 0xffffffffu : 0xffffu;
     constexpr int kChunks = T::kRow / 16, kRowsPer = 32 / kChunks;
     const int ch = lane % kChunks, sub = lane / kChunks;
-    const bool in_row = ch * 16 < P.dim * T::kSize, full_rows = P.dim == DP;
+    // chunks behind the head's elements are zeros, and behind those that are used nothing
+    const bool in_row = ch * 16 < P.dim * T::kSize, in_use = ch * 16 < T::kUse * T::kSize;
+    const uint32_t ch_bytes = in_row ? 16 : 0;
     const char *kbase = (const char *)P.k_cache + (in_row ? ch * 16 : 0), *vbase = (const char *)P.v_cache + (in_row ? ch * 16 : 0);
     const uint32_t off_step = 1u << W.off_shift, my_place = place(sub, ch);
     Cursor ld = at;
@@ -419,19 +419,19 @@ __global__ void __launch_bounds__(T::kWarps * 32, T::kCtas) attn_stream_kernel(c
             if (T::kRow >= 128) return (dst + row * T::kRow) + (my_place ^ ((row & 7) << 4));
             return (dst + row * T::kRow) + (my_place ^ (((row >> 1) & 3) << 4));
         };
-        if (cp_rows == kAll && full_rows) {
+        if (cp_rows == kAll) {
 #pragma unroll
             for (int i = 0; i < T::kTile / kRowsPer; i++) {
                 const uint32_t o = __shfl_sync(0xffffffffu, cp_off, i * kRowsPer + sub);
-                copy16(to(i), base + (uint64_t)o * off_step);
+                if (T::kUse == DP || in_use) copy16(to(i), base + (uint64_t)o * off_step, ch_bytes);
             }
         } else if (cp_rows) {
 #pragma unroll
             for (int i = 0; i < T::kTile / kRowsPer; i++) {
                 const int row = i * kRowsPer + sub;
                 const uint32_t o = __shfl_sync(0xffffffffu, cp_off, row);
-                const bool ok = in_row && ((cp_rows >> row) & 1);
-                copy16_or_zero(to(i), base + (uint64_t)(ok ? o : 0) * off_step, ok);
+                const bool ok = (cp_rows >> row) & 1;
+                if (T::kUse == DP || in_use) copy16(to(i), base + (uint64_t)(ok ? o : 0) * off_step, ok ? ch_bytes : 0);
             }
         }
         copy_commit();
@@ -501,6 +501,7 @@ __global__ void __launch_bounds__(T::kWarps * 32, T::kCtas) attn_stream_kernel(c
                 for (int i = 0; i < DP / 64; i++) {
                     float a = x[2 * i] * up, b = x[2 * i + 1] * up;
                     const int d = 64 * i + 2 * lane;  // even
+                    if (d >= T::kUse) continue;
                     // which 16-product, lane of the group and register of the fragment hold (d, d + 1)
                     const int k = d & 15;
                     const int cc = FMT == COLI_KV_E4M3 ? k >> 2 : (k & 7) >> 1;
@@ -802,22 +803,21 @@ cudaError_t launch_stream(const AttnParams &P, const AttnWork &W, int grid, cuda
     return launch_overlapped(attn_stream_kernel<T>, dim3(grid), T::kWarps * 32, T::smem(P.seqs), s, P, W);
 }
 
-template <int FMT, int DP, int NT>
-cudaError_t launch_wide(const AttnParams &P, const AttnWork &W, int grid, cudaStream_t s) {
-    return W.wide ? launch_stream<AttnTraits<FMT, DP, NT, true>>(P, W, grid, s)
-                  : launch_stream<AttnTraits<FMT, DP, NT, false>>(P, W, grid, s);
-}
-
-template <int FMT, int DP>
+template <int FMT, int DP, int USE>
 cudaError_t launch_heads(const AttnParams &P, const AttnWork &W, int grid, cudaStream_t s) {
-    return W.nt == 1 ? launch_wide<FMT, DP, 1>(P, W, grid, s) : launch_wide<FMT, DP, 2>(P, W, grid, s);
+    if (W.nt == 1)
+        return W.wide ? launch_stream<AttnTraits<FMT, DP, USE, 1, true>>(P, W, grid, s)
+                      : launch_stream<AttnTraits<FMT, DP, USE, 1, false>>(P, W, grid, s);
+    return W.wide ? launch_stream<AttnTraits<FMT, DP, USE, 2, true>>(P, W, grid, s)
+                  : launch_stream<AttnTraits<FMT, DP, USE, 2, false>>(P, W, grid, s);
 }
 
 template <int FMT>
 cudaError_t launch_dims(const AttnParams &P, const AttnWork &W, int grid, cudaStream_t s) {
-    return W.dim == 64    ? launch_heads<FMT, 64>(P, W, grid, s)
-           : W.dim == 128 ? launch_heads<FMT, 128>(P, W, grid, s)
-                          : launch_heads<FMT, 256>(P, W, grid, s);
+    return W.dim == 64    ? launch_heads<FMT, 64, 64>(P, W, grid, s)
+           : W.use == 96  ? launch_heads<FMT, 128, 96>(P, W, grid, s)
+           : W.dim == 128 ? launch_heads<FMT, 128, 128>(P, W, grid, s)
+                          : launch_heads<FMT, 256, 256>(P, W, grid, s);
 }
 
 }  // namespace colimoe

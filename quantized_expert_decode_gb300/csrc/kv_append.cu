@@ -21,7 +21,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kMaxTokens = 8;                // tokens of a CTA
-constexpr int kFewRounds = 8, kCtasPerSm = 2;
+constexpr int kFewRounds = 8, kCtasPerSm = 3;
 constexpr int kMaxPairs = 128;               // rotary / 2 at most (dim <= 256)
 
 // f / 2 pi as a fraction of a turn in units of 2^-64, modulo one turn
@@ -47,13 +47,26 @@ __device__ __forceinline__ float2 turn(int p, float f) {
     return make_float2(c, s);
 }
 
-template <typename C>
-__device__ __forceinline__ C to_cache(float x, float scale) {
-    return from_f32<C>(x);
+// N values in the cache's type; e4m3 holds value / scale, by the scale's reciprocal, and is converted in pairs
+template <typename C, int N>
+__device__ __forceinline__ void to_cache(C (&to)[N], const float (&x)[N], float per_scale) {
+#pragma unroll
+    for (int j = 0; j < N; j++) to[j] = from_f32<C>(x[j]);
 }
-template <>
-__device__ __forceinline__ __nv_fp8_e4m3 to_cache<__nv_fp8_e4m3>(float x, float scale) {
-    return from_f32<__nv_fp8_e4m3>(x / scale);
+template <int N>
+__device__ __forceinline__ void to_cache(__nv_fp8_e4m3 (&to)[N], const float (&x)[N], float per_scale) {
+    if constexpr (N % 2 == 0) {
+#pragma unroll
+        for (int j = 0; j < N; j += 2) {
+            const __nv_fp8x2_storage_t p =
+                __nv_cvt_float2_to_fp8x2(make_float2(x[j] * per_scale, x[j + 1] * per_scale), __NV_SATFINITE, __NV_E4M3);
+            to[j].__x = (__nv_fp8_storage_t)p;
+            to[j + 1].__x = (__nv_fp8_storage_t)(p >> 8);
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < N; j++) to[j] = from_f32<__nv_fp8_e4m3>(x[j] * per_scale);
+    }
 }
 
 // One item: 2 * V elements of one head of one token. Items below rotary / (2 V) rotate V pairs: V
@@ -130,9 +143,10 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const AppendParams 
         row_k[threadIdx.x] = off;
         if (flag && P.err) atomicOr(P.err, flag);
     }
+    // pair c * V + j of a token at [j][c]: neighbouring threads read neighbouring words
     for (int i = threadIdx.x; i < nt * half; i += kThreads) {
         const int u = i / half, j = i - u * half;
-        cs[i] = turn(P.pos[n0 + u], P.inv_freq[j]);
+        cs[u * half + j % V * turned + j / V] = turn(P.pos[n0 + u], P.inv_freq[j]);
     }
     __syncthreads();
     while (item[0].t >= 0) {
@@ -148,11 +162,11 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const AppendParams 
                 y[j] = to_f32(it.b.e[j]);
             }
             if (vh < 0 && in_turn) {
-                const float2 *w = cs + it.t * half + c * V;
+                const float2 *w = cs + it.t * half + c;
                 if (split) {
 #pragma unroll
                     for (int j = 0; j < V; j++) {
-                        const float2 e = w[j];
+                        const float2 e = w[j * turned];
                         const float u = x[j], v = y[j];
                         x[j] = fmaf(u, e.x, -(v * e.y));
                         y[j] = fmaf(v, e.x, u * e.y);
@@ -167,7 +181,7 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const AppendParams 
                     }
 #pragma unroll
                     for (int j = 0; j < V; j++) {
-                        const float2 e = w[j];
+                        const float2 e = w[j * turned];
                         const float u = z[2 * j], v = z[2 * j + 1];
                         z[2 * j] = fmaf(u, e.x, -(v * e.y));
                         z[2 * j + 1] = fmaf(v, e.x, u * e.y);
@@ -192,14 +206,11 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const AppendParams 
             } else if (row_k[it.t] >= 0) {
                 const int g = vh < 0 ? kh : vh;
                 const float *sc = vh < 0 ? P.k_scale : P.v_scale;
-                const float s = sc ? sc[g] : 1.f;
+                const float per_scale = sc ? 1.f / sc[g] : 1.f;
                 C *dst = (C *)(vh < 0 ? P.k_cache : P.v_cache) + row_k[it.t] + (int64_t)g * P.cache.head_stride;
                 Run<C, V> a, b;
-#pragma unroll
-                for (int j = 0; j < V; j++) {
-                    a.e[j] = to_cache<C>(x[j], s);
-                    b.e[j] = to_cache<C>(y[j], s);
-                }
+                to_cache(a.e, x, per_scale);
+                to_cache(b.e, y, per_scale);
                 a.store(dst + (vh < 0 ? s0 : v0));
                 b.store(dst + (vh < 0 ? s1 : v1));
             }
