@@ -544,10 +544,12 @@ __global__ void __launch_bounds__(T::kWarps * 32, T::kCtas) attn_stream_kernel(c
         const int lr = lane & 7, li = lane >> 3;
         float s[T::kMT][NT][4];
         if (rows) {
-            // ---- S^T = K q^T; the leading parts in two chains, the others in one, added at the end
+            // ---- S^T = K q^T; the leading part in two chains, the others in one, added at the end
 #pragma unroll
             for (int i = 0; i < T::kMT; i++) {
-                constexpr int kChains = T::kQParts > 1 ? 3 : 2;
+                // (one chain where two 16-row blocks follow each other: the second's registers spill there, 94 us
+                // against 78 on an 8-bit cache of 128 elements beside fp32 queries)
+                constexpr int kLead = T::kMT > 1 && FMT == COLI_KV_E4M3 ? 1 : 2, kChains = kLead + (T::kQParts > 1 ? 1 : 0);
                 float acc[kChains][NT][4];
                 const uint32_t at_row = kt + place(i * 16 + lr + (li & 1) * 8, li >> 1);
                 // two products of 16 along the head
@@ -557,19 +559,11 @@ __global__ void __launch_bounds__(T::kWarps * 32, T::kCtas) attn_stream_kernel(c
 #pragma unroll
                         for (int n = 0; n < NT; n++) {
                             const uint4 q = qf[((p * NT + n) * (T::kKS / 2) + k2) * 32 + lane];
-                            if (p == 0) {
-                                if (k2 == 0) {
-                                    mma<FMT, false>(acc[0][n], a0, q.x, q.y);
-                                    mma<FMT, false>(acc[1][n], a1, q.z, q.w);
-                                } else {
-                                    mma<FMT, true>(acc[0][n], a0, q.x, q.y);
-                                    mma<FMT, true>(acc[1][n], a1, q.z, q.w);
-                                }
-                            } else {
-                                if (k2 == 0 && p == 1) mma<FMT, false>(acc[kChains - 1][n], a0, q.x, q.y);
-                                else mma<FMT, true>(acc[kChains - 1][n], a0, q.x, q.y);
-                                mma<FMT, true>(acc[kChains - 1][n], a1, q.z, q.w);
-                            }
+                            float (&first)[4] = acc[p ? kChains - 1 : 0][n], (&second)[4] = acc[p ? kChains - 1 : kLead - 1][n];
+                            if (k2 == 0 && p < 2) mma<FMT, false>(first, a0, q.x, q.y);
+                            else mma<FMT, true>(first, a0, q.x, q.y);
+                            if (k2 == 0 && p == 0 && kLead == 2) mma<FMT, false>(second, a1, q.z, q.w);
+                            else mma<FMT, true>(second, a1, q.z, q.w);
                         }
                 };
 #pragma unroll
@@ -590,8 +584,12 @@ __global__ void __launch_bounds__(T::kWarps * 32, T::kCtas) attn_stream_kernel(c
 #pragma unroll
                 for (int n = 0; n < NT; n++)
 #pragma unroll
-                    for (int j = 0; j < 4; j++)
-                        s[i][n][j] = acc[0][n][j] + (acc[1][n][j] + (kChains > 2 ? acc[kChains - 1][n][j] : 0.f));
+                    for (int j = 0; j < 4; j++) {
+                        float x = acc[kChains - 1][n][j];
+#pragma unroll
+                        for (int k = kChains - 2; k >= 0; k--) x += acc[k][n][j];
+                        s[i][n][j] = x;
+                    }
             }
             if (rows != kAll) {  // a score of -inf where there is no token
 #pragma unroll
