@@ -1,5 +1,7 @@
 // attn_decode.cu — coli_attn_decode: how a call is laid out, and the join of the items that a run's
 // border cut (attn_kernel.cuh has the streaming kernel).
+#include <algorithm>
+
 #include "attn.h"
 #include "host.h"
 #include "pdl.cuh"
@@ -74,6 +76,28 @@ struct Layout {
     size_t ml, o, total;
 };
 
+// Whether a CTA per item, none cut, is the faster way for so many items of at most u units, with room for
+// `ctas` CTAs at once (the others start as those end). Measured on bf16 caches of 128 elements, 8 kv heads, against
+// runs that go on from item to item or parts and their join:
+//   few short items: 333 tokens of one sequence 8.2 us against 6.8 on the device, but without the second launch
+//     8.5 against 10.4 called from Python;
+//   a quarter of the places: 16 sequences of 1000 tokens 17 us against 21, 32 of 500 16 against 20;
+//   more items than places: 64 sequences of 500 tokens 29 us against 37, of 4000 156 against 171; 16 windows of 1024
+//     on 32 heads 23 against 30; but 40 of 2000 (320 items, 304 places) 70 against 62.
+// So where items fill the places the time of the waves is estimated, each the larger of its bytes' time and of
+// one CTA's alone (1.25 us a unit), against the other way's: its bytes' and 15 us of starts, cuts and join. Long
+// items (more than 32 units) are cut in any case: in ragged batches the last of them would end alone (32
+// sequences of 1 to 8192 tokens 134 us against 95).
+bool whole_items(int64_t items, int64_t u, int64_t ctas, double unit_bytes) {
+    if (items > 16 * ctas) return false;
+    if (u <= 3 || (u <= 8 && 4 * items >= ctas)) return true;
+    if (u > 32 || 5 * items < 4 * ctas) return false;
+    const double all = items * u * unit_bytes / 7.2e6, alone = 1.25 * u;  // us
+    const int64_t full = items / ctas, rest = items % ctas;
+    auto wave = [&](int64_t n) { return n ? std::max(all * n / items, alone) : 0.0; };
+    return 6 + full * wave(ctas) + wave(rest) < 15 + 1.06 * all;
+}
+
 Layout layout_of(const AttnParams &P) {
     Layout L{};
     const int group = P.q_heads / P.kv_heads;
@@ -97,12 +121,8 @@ Layout layout_of(const AttnParams &P) {
     const int64_t ctas = (int64_t)num_sms() * attn_ctas_per_sm(P.fmt, L.w.dim, L.w.nt, L.w.wide);
     L.units = most;
     L.grid = (int)(most < ctas ? most : ctas);
-    // short items that all find a place are not cut: a CTA each and no join. Where they are few that costs the device
-    // as much as the cut saves it, but no second launch (333 tokens of one sequence: 8.2 us against 6.8 on the
-    // device, 8.5 against 10.4 called from Python); where they fill a quarter of the places it is faster (16
-    // sequences of 1000 tokens, 8 kv heads: 17 us against 21; 32 of 500: 16 against 20).
     const int64_t items = (int64_t)P.seqs * L.w.groups;
-    if (items <= ctas && (most <= 3 * items || (most <= 8 * items && 4 * items >= ctas))) {
+    if (whole_items(items, most / items, ctas, L.w.unit * (double)L.w.dim * 2 * size)) {
         L.w.whole = 1;
         L.grid = (int)items;
     }
