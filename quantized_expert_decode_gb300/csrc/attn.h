@@ -23,6 +23,30 @@ constexpr int attn_slots(int fmt, int dim, int nt, bool wide) {
 }
 constexpr int attn_unit(int fmt, int dim, int nt) { return attn_warps(dim, nt) * attn_tile(fmt, dim); }
 
+// Whether a CTA per item, none cut, is the faster way for items of u units, with room for `ctas` CTAs at once (the
+// others start as those end). Measured on bf16 caches of 128 elements, 8 kv heads, against runs that go on from
+// item to item, or parts of items, and their join:
+//   few short items: 333 tokens of one sequence 8.2 us against 6.8 on the device, but without the second launch
+//     8.5 against 10.4 called from Python;
+//   a quarter of the places: 16 sequences of 1000 tokens 17 us against 21, 32 of 500 16 against 20;
+//   more items than places: 64 sequences of 500 tokens 29 us against 37, of 4000 156 against 171; 16 windows of 1024
+//     on 32 heads 23 against 30; but 40 of 2000 (320 items, 304 places) 70 against 62.
+// So where items fill the places the time of the waves is estimated, each the larger of its bytes' time and of
+// one CTA's alone (1.25 us a unit), against the other way's: its bytes' and 15 us of starts, cuts and join. Items
+// of more than 32 units count only where all are as long: in a ragged batch the last of them would end alone (32
+// sequences of 1 to 8192 tokens 134 us against 95).
+constexpr int kAttnWhole = 1, kAttnMaybe = 2;
+__host__ __device__ inline bool attn_waves(float items, float u, float ctas, float unit_us) {
+    const float all = items * u * unit_us, alone = 1.25f * u;
+    const float full = floorf(items / ctas), rest = items - full * ctas;
+    return 6.f + full * fmaxf(ctas * u * unit_us, alone) + (rest > 0.f ? fmaxf(rest * u * unit_us, alone) : 0.f) < 15.f + 1.06f * all;
+}
+__host__ __device__ inline bool attn_whole(int64_t items, int64_t u, int64_t ctas, float unit_us) {
+    if (items > 16 * ctas) return false;
+    if (u <= 3 || (u <= 8 && 4 * items >= ctas)) return true;
+    return u <= 32 && 5 * items >= 4 * ctas && attn_waves((float)items, (float)u, (float)ctas, unit_us);
+}
+
 // The line of all units is cut into runs of equal length, the first ones one unit longer; one CTA each. (A
 // second, shorter run per share as further CTAs, to even out the 20 % by which the SMs' bandwidths differ,
 // costs as much in starts as it evens out.)
@@ -55,7 +79,9 @@ struct AttnWork {
     int32_t chunks;  // head groups per kv head
     int32_t groups;  // head groups per sequence
     int32_t unit;    // tokens of a unit
-    int32_t whole;   // no item is cut
+    int32_t whole;   // kAttnWhole: no item is cut; kAttnMaybe: by the lengths; 0: items may be cut
+    int32_t ctas;    // CTAs that share the units where items may be cut
+    float unit_us;   // a unit's bytes at the memory's full rate
     KvDivide divide;  // by the page size
     // the cache's strides in steps of 2^off_shift bytes, which divides them all
     uint32_t page_step, token_step, head_step, off_shift;

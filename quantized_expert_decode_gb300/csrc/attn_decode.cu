@@ -1,7 +1,5 @@
 // attn_decode.cu — coli_attn_decode: how a call is laid out, and the join of the items that a run's
 // border cut (attn_kernel.cuh has the streaming kernel).
-#include <algorithm>
-
 #include "attn.h"
 #include "host.h"
 #include "pdl.cuh"
@@ -76,28 +74,6 @@ struct Layout {
     size_t ml, o, total;
 };
 
-// Whether a CTA per item, none cut, is the faster way for so many items of at most u units, with room for
-// `ctas` CTAs at once (the others start as those end). Measured on bf16 caches of 128 elements, 8 kv heads, against
-// runs that go on from item to item or parts and their join:
-//   few short items: 333 tokens of one sequence 8.2 us against 6.8 on the device, but without the second launch
-//     8.5 against 10.4 called from Python;
-//   a quarter of the places: 16 sequences of 1000 tokens 17 us against 21, 32 of 500 16 against 20;
-//   more items than places: 64 sequences of 500 tokens 29 us against 37, of 4000 156 against 171; 16 windows of 1024
-//     on 32 heads 23 against 30; but 40 of 2000 (320 items, 304 places) 70 against 62.
-// So where items fill the places the time of the waves is estimated, each the larger of its bytes' time and of
-// one CTA's alone (1.25 us a unit), against the other way's: its bytes' and 15 us of starts, cuts and join. Long
-// items (more than 32 units) are cut in any case: in ragged batches the last of them would end alone (32
-// sequences of 1 to 8192 tokens 134 us against 95).
-bool whole_items(int64_t items, int64_t u, int64_t ctas, double unit_bytes) {
-    if (items > 16 * ctas) return false;
-    if (u <= 3 || (u <= 8 && 4 * items >= ctas)) return true;
-    if (u > 32 || 5 * items < 4 * ctas) return false;
-    const double all = items * u * unit_bytes / 7.2e6, alone = 1.25 * u;  // us
-    const int64_t full = items / ctas, rest = items % ctas;
-    auto wave = [&](int64_t n) { return n ? std::max(all * n / items, alone) : 0.0; };
-    return 6 + full * wave(ctas) + wave(rest) < 15 + 1.06 * all;
-}
-
 Layout layout_of(const AttnParams &P) {
     Layout L{};
     const int group = P.q_heads / P.kv_heads;
@@ -122,14 +98,17 @@ Layout layout_of(const AttnParams &P) {
     L.units = most;
     L.grid = (int)(most < ctas ? most : ctas);
     const int64_t items = (int64_t)P.seqs * L.w.groups;
-    if (whole_items(items, most / items, ctas, L.w.unit * (double)L.w.dim * 2 * size)) {
-        L.w.whole = 1;
-        L.grid = (int)items;
-    }
+    L.w.unit_us = (float)L.w.unit * L.w.dim * 2 * size / 7.2e6f;
+    L.w.ctas = L.grid;
+    // certain for the longest items that the tables can name: no second launch; else the kernel decides by the lengths
+    if (attn_whole(items, most / items, ctas, L.w.unit_us)) L.w.whole = kAttnWhole;
+    else if (items <= 16 * ctas && 5 * items >= 4 * ctas) L.w.whole = kAttnMaybe;
+    if (L.w.whole == kAttnWhole) L.grid = (int)items;
+    if (L.w.whole == kAttnMaybe && items > L.grid) L.grid = (int)items;
     auto up = [](size_t n) { return (n + 255) / 256 * 256; };
-    L.ml = up((size_t)L.grid * sizeof(AttnCut));
-    L.o = L.ml + up((size_t)2 * L.grid * 8 * L.w.nt * sizeof(float2));
-    L.total = L.o + up((size_t)2 * L.grid * 8 * L.w.nt * L.w.dim * 4);
+    L.ml = up((size_t)L.w.ctas * sizeof(AttnCut));
+    L.o = L.ml + up((size_t)2 * L.w.ctas * 8 * L.w.nt * sizeof(float2));
+    L.total = L.o + up((size_t)2 * L.w.ctas * 8 * L.w.nt * L.w.dim * 4);
     return L;
 }
 
@@ -162,9 +141,9 @@ cudaError_t launch_attn_decode(const AttnParams &P, cudaStream_t s) {
     const cudaError_t e = P.fmt == COLI_KV_BF16  ? launch_attn_bf16(P, L.w, L.grid, s)
                           : P.fmt == COLI_KV_F16 ? launch_attn_f16(P, L.w, L.grid, s)
                                                  : launch_attn_e4m3(P, L.w, L.grid, s);
-    if (e != cudaSuccess || L.w.whole || L.grid == 1) return e;  // no borders
+    if (e != cudaSuccess || L.w.whole == kAttnWhole || L.w.ctas == 1) return e;  // no borders
     // the join's blocks start while the streaming kernel runs and wait for its end
-    const dim3 grid(L.grid - 1, 8 * L.w.nt);
+    const dim3 grid(L.w.ctas - 1, 8 * L.w.nt);
     const int shift = P.fmt == COLI_KV_BF16 ? 0 : 14;
     return L.w.dim == 64    ? launch_overlapped(attn_join_kernel<64>, grid, kJoinThreads, 0, s, P, L.w, shift)
            : L.w.dim == 128 ? launch_overlapped(attn_join_kernel<128>, grid, kJoinThreads, 0, s, P, L.w, shift)

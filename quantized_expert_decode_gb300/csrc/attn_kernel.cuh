@@ -153,10 +153,10 @@ struct AttnTraits {
     static_assert(kWarps * kTile == attn_unit(FMT, DP, NT), "unit");
     static constexpr size_t smem(int seqs) {
         return (size_t)kWarps * kSlots * kSlotBytes + (size_t)kQWords * 16 + kWarps * kHeads * 8 + kHeads * 4 +
-               kWarps * 4 * 4 + ((size_t)seqs + 1) * 4 + 160;
+               kWarps * 4 * 4 + ((size_t)seqs + 1) * 4 + 176;
     }
     static_assert(kWarps * kSlots * kSlotBytes + kQWords * 16 + kWarps * kHeads * 8 + kHeads * 4 + kWarps * 16 +
-                          (kAttnMaxSeqs + 1) * 4 + 160 <=
+                          (kAttnMaxSeqs + 1) * 4 + 176 <=
                       (228 << 10) / kCtas - 1024,
                   "shared memory of an SM");
 };
@@ -172,7 +172,7 @@ __global__ void __launch_bounds__(T::kWarps * 32, T::kCtas) attn_stream_kernel(c
     float *qs = reinterpret_cast<float *>(ml + T::kWarps * T::kHeads);  // [head] factor of the products
     uint32_t *seen = reinterpret_cast<uint32_t *>(qs + T::kHeads);     // [warp][tile % 4] rows that hold a token
     int *pre = reinterpret_cast<int *>(seen + T::kWarps * 4);          // [seqs + 1] units before a sequence
-    int *scan = pre + P.seqs + 1;                                      // [35]
+    int *scan = pre + P.seqs + 1;                                      // [44]
     static_assert(kThreads % (DP / 4) == 0, "whole heads in a round");
     const int tid = threadIdx.x, w = tid / 32, lane = tid % 32, g = lane >> 2, c = lane & 3;
 
@@ -188,19 +188,24 @@ __global__ void __launch_bounds__(T::kWarps * 32, T::kCtas) attn_stream_kernel(c
     };
     const int per = (P.seqs + kThreads - 1) / kThreads;
     const int b0 = min(tid * per, P.seqs), b1 = min(b0 + per, P.seqs);
-    int mine = 0;
+    int mine = 0, longest = 0;
     for (int b = b0; b < b1; b++) {
         const int u = units_of(b);
         pre[b + 1] = u;
         mine += u;
+        longest = max(longest, u);
     }
+    longest = __reduce_max_sync(0xffffffffu, longest);
     int incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const int v = __shfl_up_sync(0xffffffffu, incl, o);
         if (lane >= o) incl += v;
     }
-    if (lane == 31) scan[w] = incl;
+    if (lane == 31) {
+        scan[w] = incl;
+        scan[36 + w] = longest;
+    }
     __syncthreads();
     int before = incl - mine;
     for (int i = 0; i < w; i++) before += scan[i];
@@ -222,6 +227,17 @@ __global__ void __launch_bounds__(T::kWarps * 32, T::kCtas) attn_stream_kernel(c
             for (int i = tid; i < P.q_heads; i += kThreads) P.lse[(int64_t)b * P.q_heads + i] = -INFINITY;
     }
 
+    bool whole_mode = W.whole == kAttnWhole;
+    if (W.whole == kAttnMaybe) {
+        int u = 0;
+#pragma unroll
+        for (int i = 0; i < T::kWarps; i++) u = max(u, scan[36 + i]);
+        const float items = (float)(P.seqs * W.groups);
+        whole_mode = attn_whole(P.seqs * W.groups, u, W.ctas, W.unit_us) ||
+                     ((float)total >= 0.9f * items * (float)u && attn_waves(items, (float)u, (float)W.ctas, W.unit_us));
+        if (whole_mode && blockIdx.x == 0 && tid == 0) W.cuts[0].runs = 0;  // nothing for the join
+    }
+
     // ---- this CTA's run: an item; or a part of an item, every item cut by itself into parts of at most c units, if
     // that makes no more runs than there are CTAs and none much longer than the others; or a run of as many units
     // as any other's, which may go on from item to item (of one unit where there are CTAs enough).
@@ -229,14 +245,16 @@ __global__ void __launch_bounds__(T::kWarps * 32, T::kCtas) attn_stream_kernel(c
     Cursor at{0, 0, 0, 0};
     int n_units = 0;
     AttnCut cut{-1, 0, 0, 0};  // for the join
-    if (W.whole) {
+    if (whole_mode) {
+        if (run >= (uint32_t)(P.seqs * W.groups)) return;
         at.b = run / W.groups;
         at.hv = run - at.b * W.groups;
         at.units = n_units = pre[at.b + 1] - pre[at.b];
         if (n_units == 0) return;
     }
-    if (!W.whole && total > gridDim.x) {
-        const uint32_t c0 = (total + gridDim.x - 1) / gridDim.x;
+    const uint32_t ctas = W.ctas;
+    if (!whole_mode && total > ctas) {
+        const uint32_t c0 = (total + ctas - 1) / ctas;
         const uint32_t c[3] = {c0, c0 + 1, c0 + 2 + c0 / 8};
         uint32_t sum[3] = {0, 0, 0}, run_to[3];
         for (int b = b0; b < b1; b++) {
@@ -267,9 +285,9 @@ __global__ void __launch_bounds__(T::kWarps * 32, T::kCtas) attn_stream_kernel(c
                 all[k] += v;
             }
         }
-        const int k = (uint64_t)all[0] * W.groups <= gridDim.x ? 0 : (uint64_t)all[1] * W.groups <= gridDim.x ? 1 : 2;
+        const int k = (uint64_t)all[0] * W.groups <= ctas ? 0 : (uint64_t)all[1] * W.groups <= ctas ? 1 : 2;
         const uint32_t parts = k == 0 ? all[0] : k == 1 ? all[1] : all[2], cap = k == 0 ? c[0] : k == 1 ? c[1] : c[2];
-        if ((uint64_t)parts * W.groups <= gridDim.x) {
+        if ((uint64_t)parts * W.groups <= ctas) {
             cut.runs = parts * W.groups;
             if (run < (uint32_t)cut.runs) {
                 // the thread whose sequences the run is among tells which one it is
@@ -302,8 +320,8 @@ __global__ void __launch_bounds__(T::kWarps * 32, T::kCtas) attn_stream_kernel(c
             }
         }
     }
-    if (!W.whole && n_units == 0) {
-        const AttnRuns R(total, gridDim.x);
+    if (!whole_mode && n_units == 0) {
+        const AttnRuns R(total, ctas);
         cut.runs = R.runs;
         if (run >= R.runs) {
             if (run == 0 && tid == 0) W.cuts[0] = cut;
@@ -465,7 +483,7 @@ __global__ void __launch_bounds__(T::kWarps * 32, T::kCtas) attn_stream_kernel(c
     }
 
     // ---- for the join: the item that this run's first border cuts, told by the run behind its first cut
-    if (tid == 0 && !W.whole) W.cuts[run] = cut;
+    if (tid == 0 && !whole_mode) W.cuts[run] = cut;
 
     float o[T::kKS][NT][4], m[NT][2], l[NT][2], sc[NT][2];
     int slot = 0;
