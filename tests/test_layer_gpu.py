@@ -397,6 +397,31 @@ def test_attention_many_sequences(q):
     check_attend(q, 19, [0] * 30 + [3000] + [0] * 5, (8, 8), 64)
 
 
+@pytest.mark.parametrize("seqs,ragged,kv", [(64, False, "bf16"), (64, True, "bf16"), (40, False, "f16"), (40, True, "e4m3"), (30, False, "bf16"),
+                                            (160, True, "f16"), (320, True, "bf16")])
+def test_attention_long_items_beyond_one_wave(q, seqs, ragged, kv):
+    # 8 kv heads: more items than the GPU holds CTAs at once, or about as many, long ones: whole, cut evenly or
+    # in runs that go on from item to item, as their lengths say
+    rng = np.random.default_rng(seqs)
+    top = 9000 if seqs <= 64 else 2500
+    lens = [int(x) for x in rng.integers(0, top, seqs)] if ragged else [top - 300 + i % 5 for i in range(seqs)]
+    check_attend(q, seqs, lens, (8, 8), 16, kv=kv, page=64)
+
+
+def test_attention_short_sequences_in_wide_tables(q):
+    # the table could name far longer sequences: what is decided by its width must not be wrong for short ones
+    for seqs, width in ((3, 4000), (64, 200), (50, 1000)):
+        rng = np.random.default_rng(seqs)
+        c = Cache(q, rng, "bf16", seqs * 4 + 2, 16, 8, 64)
+        lens = [int(x) for x in rng.integers(0, 60, seqs)]
+        table = fill(rng, c, lens, width)
+        xq = randn(rng, seqs, 16, 64)
+        err = err_word()
+        out, lse = run_attend(q, c, xq, table, lens, 0.125, err=err)
+        assert q.coli_moe_check(err) == q.COLI_MOE_OK
+        compare_attend(c, out, lse, attend64(c, xq, table, lens, 0.125), lens, "f32", "bf16")
+
+
 def test_attention_most_sequences(q):
     check_attend(q, 20, [i % 3 for i in range(2048)], (2, 1), 16, page=2)
 
