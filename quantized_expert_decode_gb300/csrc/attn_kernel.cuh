@@ -5,14 +5,21 @@
 // maximum rounded up), l = sum 2^(x_t - m) and o = sum 2^(x_t - m) v_t. A later, larger m' scales l
 // and o by 2^(m - m'), which is exact because both are integers; so is every later join of parts.
 //
-// What bounds it: the bytes of K and V, read once for all query heads of a kv head (4 * heads
-// operations per 2 * dim-element pair: far below the tensor cores' rate up to 16 heads).
+// What bounds it: the bytes of K and V, read once for all query heads of a kv head up to 16 (4 * heads
+// operations per pair of K and V elements: far below the tensor cores' rate). 64 sequences of 8000 tokens
+// on 8 kv heads of 128 bf16 elements (2.1 GB) take 306 us, 6.9 TB/s; ragged and middling batches (0.2 to 0.6
+// GB) reach 65 to 90 % of the copy's 6.8 TB/s: a start of some 4 us (launch, plan, page numbers, first rows), the
+// spread of the SMs' bandwidths by 20 % and the join's 3 us are the rest. The instructions of a tile
+// (about 350 for 16 tokens of 128 bf16 elements, 600 beside fp32 queries, 700 for 32 e4m3 tokens) keep an SM's
+// issue slots 40 to 55 % busy; e4m3 and 16 heads come near being bound by them.
 //
-// Work. The cached tokens of every (sequence, kv head, group of query heads) are cut into units of
-// kWarps tiles of kTile tokens. All units of the call form one line that is cut into equal runs, one
-// per CTA, so a CTA's share does not depend on how the lengths are spread (where the items let themselves be cut
-// evenly each by itself, a run stays within an item); an item that a run's
-// border cuts leaves partial sums in the workspace, which the join kernel adds up in a fixed order.
+// Work. An item is the cached tokens of a (sequence, kv head, group of query heads), cut into units of
+// kWarps tiles of kTile tokens. attn_whole() says when a CTA takes a whole item; otherwise every item is cut
+// into parts by itself where that gives equal parts for all CTAs, or all units form one line that is cut into
+// equal runs, one per CTA, so that a CTA's share does not depend on how the lengths are spread. An item
+// that is cut leaves partial sums in the workspace, which the join kernel adds up in a fixed order. (The last
+// CTA to end adding them up in this kernel takes registers from its loop: 107 us against 88 for one sequence of
+// 131071 tokens. Rows by tensor copies, boxes of 8 to 32 tokens, were 4 to 8 % slower than 16-byte copies.)
 //
 // Within a unit each warp owns one tile: it copies the tile's K rows and V rows to its own ring of kSlots
 // slots with 16-byte asynchronous copies, K and V of a tile apart, so that a slot is copied into as
@@ -145,7 +152,7 @@ struct AttnTraits {
     static constexpr int kHeads = 8 * NT;
     static constexpr int kQParts = !WIDE ? 1 : FMT == COLI_KV_BF16 ? 3 : 2;
     static constexpr int kPParts = WIDE && FMT == COLI_KV_BF16 ? 3 : 2;
-    static constexpr int kUse = USE, kKS = USE / 16;                           // products of 16 along the head
+    static constexpr int kUse = USE, kKS = USE / 16;              // products of 16 along the head
     static constexpr int kQWords = kQParts * NT * kKS / 2 * 32;   // uint4
     // p is kept times 2^kShift, so that the second f16 part of a small p is still above f16's smallest step
     static constexpr int kShift = FMT == COLI_KV_BF16 ? 0 : 14;
