@@ -34,7 +34,8 @@ constexpr int attn_unit(int fmt, int dim, int nt) { return attn_warps(dim, nt) *
 // So where items fill the places the time of the waves is estimated, each the larger of its bytes' time and of
 // one CTA's alone (1.25 us a unit), against the other way's: its bytes' and 15 us of starts, cuts and join. Items
 // of more than 32 units count only where all are as long: in a ragged batch the last of them would end alone (32
-// sequences of 1 to 8192 tokens 134 us against 95).
+// sequences of 1 to 8192 tokens 134 us against 95). Up to there ragged items fill the waves' gaps (40 sequences of 1
+// to 2000 tokens 35 us against 47, of 1 to 4000 64 against 72).
 constexpr int kAttnWhole = 1, kAttnMaybe = 2;
 __host__ __device__ inline bool attn_waves(float items, float u, float ctas, float unit_us) {
     const float all = items * u * unit_us, alone = 1.25f * u;
@@ -45,6 +46,14 @@ __host__ __device__ inline bool attn_whole(int64_t items, int64_t u, int64_t cta
     if (items > 16 * ctas) return false;
     if (u <= 3 || (u <= 8 && 4 * items >= ctas)) return true;
     return u <= 32 && 5 * items >= 4 * ctas && attn_waves((float)items, (float)u, (float)ctas, unit_us);
+}
+
+// The same by the lengths themselves: `total` units, the longest item's u.
+__device__ inline bool attn_whole_now(uint32_t total, int64_t items, int64_t u, int64_t ctas, float unit_us) {
+    if (attn_whole(items, u, ctas, unit_us)) return true;
+    if (items > 16 * ctas || 5 * items < 4 * ctas) return false;
+    const float full = (float)total / ((float)items * (float)u);  // 1: all as long
+    return full >= 0.9f ? attn_waves((float)items, (float)u, (float)ctas, unit_us) : full < 0.75f && u <= 32;
 }
 
 // The line of all units is cut into runs of equal length, the first ones one unit longer; one CTA each. (A

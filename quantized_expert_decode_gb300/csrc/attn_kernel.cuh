@@ -239,9 +239,7 @@ __global__ void __launch_bounds__(T::kWarps * 32, T::kCtas) attn_stream_kernel(c
         int u = 0;
 #pragma unroll
         for (int i = 0; i < T::kWarps; i++) u = max(u, scan[36 + i]);
-        const float items = (float)(P.seqs * W.groups);
-        whole_mode = attn_whole(P.seqs * W.groups, u, W.ctas, W.unit_us) ||
-                     ((float)total >= 0.9f * items * (float)u && attn_waves(items, (float)u, (float)W.ctas, W.unit_us));
+        whole_mode = attn_whole_now(total, P.seqs * W.groups, u, W.ctas, W.unit_us);
         if (whole_mode && blockIdx.x == 0 && tid == 0) W.cuts[0].runs = 0;  // nothing for the join
     }
 
