@@ -10,18 +10,30 @@ constexpr int kAttnMaxSeqs = 2048;
 
 // A slot is K or V of a tile: 16 rows of 256 bytes or more, or 32 shorter ones, 4 KB at 128 elements. Two CTAs
 // share an SM, each with three slots per warp there, except where the sums of 16 heads take the
-// registers of one, or the three parts of q at 256 elements too much shared memory: that one has the
-// slots of both.
+// registers of one, or the three parts of q at 256 elements too much shared memory: that one has as many
+// slots as both would (at 256 elements and 16 heads, no room: three).
 constexpr bool attn_alone(int fmt, int dim, int nt, bool wide) {
     return (nt == 2 && dim != 64) || (dim == 256 && wide && fmt == COLI_KV_BF16);
 }
 constexpr int attn_tile(int fmt, int dim) { return dim == 64 || fmt == COLI_KV_E4M3 ? 32 : 16; }
-constexpr int attn_warps(int dim, int nt) { return dim == 256 && nt == 1 ? 4 : 8; }
+// 16 heads of 128 elements leave 168 registers a lane to 12 warps, which hide more of each other's waiting than 8 with
+// 255 (32 sequences of 3051 tokens, 128 query heads on 8: 82.5 -> 77.3 us in bf16; 4000 tokens of 96 elements: 102 -> 92).
+// The wide form on e4m3 spills too much there (123 us with 8, 136 with 12).
+constexpr bool attn_twelve(int fmt, int dim, int nt, bool wide) {
+    return dim == 128 && nt == 2 && !(wide && fmt == COLI_KV_E4M3);
+}
+constexpr int attn_warps(int fmt, int dim, int nt, bool wide) {
+    return attn_twelve(fmt, dim, nt, wide) ? 12 : dim == 256 && nt == 1 ? 4 : 8;
+}
 constexpr int attn_ctas_per_sm(int fmt, int dim, int nt, bool wide) { return attn_alone(fmt, dim, nt, wide) ? 1 : 2; }
 constexpr int attn_slots(int fmt, int dim, int nt, bool wide) {
-    return (dim == 64 && fmt == COLI_KV_E4M3) || (attn_alone(fmt, dim, nt, wide) && !(dim == 256 && nt == 2)) ? 6 : 3;
+    return attn_twelve(fmt, dim, nt, wide) ? 4
+           : (dim == 64 && fmt == COLI_KV_E4M3) || (attn_alone(fmt, dim, nt, wide) && !(dim == 256 && nt == 2)) ? 6
+                                                                                                              : 3;
 }
-constexpr int attn_unit(int fmt, int dim, int nt) { return attn_warps(dim, nt) * attn_tile(fmt, dim); }
+constexpr int attn_unit(int fmt, int dim, int nt, bool wide) {
+    return attn_warps(fmt, dim, nt, wide) * attn_tile(fmt, dim);
+}
 
 // Whether a CTA per item, none cut, is the faster way for items of u units, with room for `ctas` CTAs at once (the
 // others start as those end). Measured on bf16 caches of 128 elements, 8 kv heads, against runs that go on from

@@ -84,7 +84,7 @@ Layout layout_of(const AttnParams &P) {
     L.w.wide = P.act == COLI_ACT_F32 || (P.act == COLI_ACT_F16 && P.fmt == COLI_KV_BF16);
     L.w.chunks = (group + 8 * L.w.nt - 1) / (8 * L.w.nt);
     L.w.groups = P.kv_heads * L.w.chunks;
-    L.w.unit = attn_unit(P.fmt, L.w.dim, L.w.nt);
+    L.w.unit = attn_unit(P.fmt, L.w.dim, L.w.nt, L.w.wide);
     L.w.divide = kv_divide_by(P.cache.page_size);
     const int size = P.fmt == COLI_KV_E4M3 ? 1 : 2;
     attn_steps(P.cache, P.kv_heads, size, L.w.off_shift);

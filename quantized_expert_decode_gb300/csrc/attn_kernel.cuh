@@ -146,7 +146,7 @@ struct AttnTraits {
     static constexpr int kRow = DP * kSize;                       // bytes of a row in shared memory
     static constexpr int kTile = attn_tile(FMT, DP);              // tokens of a warp's tile
     static constexpr int kMT = kTile / 16;
-    static constexpr int kWarps = attn_warps(DP, NT);
+    static constexpr int kWarps = attn_warps(FMT, DP, NT, WIDE);
     static constexpr int kCtas = attn_ctas_per_sm(FMT, DP, NT, WIDE), kSlots = attn_slots(FMT, DP, NT, WIDE);
     static constexpr int kSlotBytes = kTile * kRow;               // K or V of a tile
     static constexpr int kHeads = 8 * NT;
@@ -157,13 +157,13 @@ struct AttnTraits {
     // p is kept times 2^kShift, so that the second f16 part of a small p is still above f16's smallest step
     static constexpr int kShift = FMT == COLI_KV_BF16 ? 0 : 14;
     static_assert(8 * DP * 4 <= kSlotBytes, "a warp's sums of 8 heads fit its free slot");
-    static_assert(kWarps * kTile == attn_unit(FMT, DP, NT), "unit");
+    static_assert(kWarps * kTile == attn_unit(FMT, DP, NT, WIDE), "unit");
     static constexpr size_t smem(int seqs) {
         return (size_t)kWarps * kSlots * kSlotBytes + (size_t)kQWords * 16 + kWarps * kHeads * 8 + kHeads * 4 +
-               kWarps * 4 * 4 + ((size_t)seqs + 1) * 4 + 176;
+               kWarps * 4 * 4 + ((size_t)seqs + 1) * 4 + 336;
     }
     static_assert(kWarps * kSlots * kSlotBytes + kQWords * 16 + kWarps * kHeads * 8 + kHeads * 4 + kWarps * 16 +
-                          (kAttnMaxSeqs + 1) * 4 + 176 <=
+                          (kAttnMaxSeqs + 1) * 4 + 336 <=
                       (228 << 10) / kCtas - 1024,
                   "shared memory of an SM");
 };
@@ -179,8 +179,7 @@ __global__ void __launch_bounds__(T::kWarps * 32, T::kCtas) attn_stream_kernel(c
     float *qs = reinterpret_cast<float *>(ml + T::kWarps * T::kHeads);  // [head] factor of the products
     uint32_t *seen = reinterpret_cast<uint32_t *>(qs + T::kHeads);     // [warp][tile % 4] rows that hold a token
     int *pre = reinterpret_cast<int *>(seen + T::kWarps * 4);          // [seqs + 1] units before a sequence
-    int *scan = pre + P.seqs + 1;                                      // [44]
-    static_assert(kThreads % (DP / 4) == 0, "whole heads in a round");
+    int *scan = pre + P.seqs + 1;                                      // [83]
     const int tid = threadIdx.x, w = tid / 32, lane = tid % 32, g = lane >> 2, c = lane & 3;
 
     wait_for_previous();
@@ -211,7 +210,7 @@ __global__ void __launch_bounds__(T::kWarps * 32, T::kCtas) attn_stream_kernel(c
     }
     if (lane == 31) {
         scan[w] = incl;
-        scan[36 + w] = longest;
+        scan[16 + w] = longest;
     }
     __syncthreads();
     int before = incl - mine;
@@ -238,7 +237,7 @@ __global__ void __launch_bounds__(T::kWarps * 32, T::kCtas) attn_stream_kernel(c
     if (W.whole == kAttnMaybe) {
         int u = 0;
 #pragma unroll
-        for (int i = 0; i < T::kWarps; i++) u = max(u, scan[36 + i]);
+        for (int i = 0; i < T::kWarps; i++) u = max(u, scan[16 + i]);
         whole_mode = attn_whole_now(total, P.seqs * W.groups, u, W.ctas, W.unit_us);
         if (whole_mode && blockIdx.x == 0 && tid == 0) W.cuts[0].runs = 0;  // nothing for the join
     }
@@ -275,7 +274,7 @@ __global__ void __launch_bounds__(T::kWarps * 32, T::kCtas) attn_stream_kernel(c
                 const uint32_t v = __shfl_up_sync(0xffffffffu, run_to[k], o);
                 if (lane >= o) run_to[k] += v;
             }
-            if (lane == 31) scan[8 * (k + 1) + w] = run_to[k];
+            if (lane == 31) scan[16 * (k + 2) + w] = run_to[k];
         }
         __syncthreads();
         uint32_t all[3], mine_from[3];
@@ -285,7 +284,7 @@ __global__ void __launch_bounds__(T::kWarps * 32, T::kCtas) attn_stream_kernel(c
             mine_from[k] = run_to[k] - sum[k];
 #pragma unroll
             for (int i = 0; i < T::kWarps; i++) {
-                const uint32_t v = scan[8 * (k + 1) + i];
+                const uint32_t v = scan[16 * (k + 2) + i];
                 if (i < w) mine_from[k] += v;
                 all[k] += v;
             }
@@ -300,9 +299,9 @@ __global__ void __launch_bounds__(T::kWarps * 32, T::kCtas) attn_stream_kernel(c
                 for (int b = b0; b < b1; b++) {
                     const uint32_t p = ((uint32_t)(pre[b + 1] - pre[b]) + cap - 1) / cap;
                     if (run >= from && run < from + p * W.groups) {
-                        scan[32] = b;
-                        scan[33] = run - from;
-                        scan[34] = p;
+                        scan[80] = b;
+                        scan[81] = run - from;
+                        scan[82] = p;
                     }
                     from += p * W.groups;
                 }
@@ -312,9 +311,9 @@ __global__ void __launch_bounds__(T::kWarps * 32, T::kCtas) attn_stream_kernel(c
                 if (run == 0 && tid == 0) W.cuts[0] = cut;
                 return;
             }
-            const int p = scan[34], part = scan[33] % p;
-            at.b = scan[32];
-            at.hv = scan[33] / p;
+            const int p = scan[82], part = scan[81] % p;
+            at.b = scan[80];
+            at.hv = scan[81] / p;
             at.units = pre[at.b + 1] - pre[at.b];
             at.u = part * (at.units / p) + min(part, at.units % p);
             n_units = at.units / p + (part < at.units % p ? 1 : 0);
@@ -366,14 +365,14 @@ __global__ void __launch_bounds__(T::kWarps * 32, T::kCtas) attn_stream_kernel(c
 
     // ---- q of an item: read early, turned into parts when the item begins. A warp has the heads w, w + kWarps, ..,
     // a lane the pairs of elements 2 * lane + 64 * i.
-    constexpr int kMyHeads = T::kHeads / T::kWarps;
+    constexpr int kMyHeads = (T::kHeads + T::kWarps - 1) / T::kWarps;
     const int group = P.q_heads / P.kv_heads;
     float qx[kMyHeads][DP / 32];
     auto load_q = [&](const Cursor &k) {
         const int kh = k.hv / W.chunks, h0 = (k.hv - kh * W.chunks) * T::kHeads;
 #pragma unroll
         for (int a = 0; a < kMyHeads; a++) {
-            const int h = h0 + w + a * T::kWarps;
+            const int h = w + a * T::kWarps < T::kHeads ? h0 + w + a * T::kWarps : group;  // group: none
             const int64_t src = k.b * P.q_stride + (int64_t)(kh * group + h) * P.dim;
 #pragma unroll
             for (int i = 0; i < DP / 32; i++) {
@@ -503,6 +502,7 @@ __global__ void __launch_bounds__(T::kWarps * 32, T::kCtas) attn_stream_kernel(c
 #pragma unroll
             for (int hh = 0; hh < kMyHeads; hh++) {
                 const int h = w + hh * T::kWarps;
+                if (h >= T::kHeads) continue;
                 float (&x)[DP / 32] = qx[hh];
                 float top = 0.f;
 #pragma unroll

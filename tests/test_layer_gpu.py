@@ -408,6 +408,17 @@ def test_attention_long_items_beyond_one_wave(q, seqs, ragged, kv):
     check_attend(q, seqs, lens, (8, 8), 16, kv=kv, page=64)
 
 
+@pytest.mark.parametrize("heads", [(16, 1), (9, 1), (24, 2), (50, 2)])
+@pytest.mark.parametrize("act,kv", [("bf16", "bf16"), ("f32", "f16"), ("bf16", "e4m3"), ("f32", "e4m3")])
+def test_attention_of_wide_groups_around_their_units(q, heads, act, kv):
+    # 9 to 16 query heads of 81 to 128 elements: units of 128, 192, 256 or 384 tokens
+    lens = [1, 191, 192, 193, 255, 257, 383, 384, 385, 0, 576, 769, 2305]
+    check_attend(q, 41, lens, heads, 128, act=act, kv=kv, page=16)
+    check_attend(q, 42, lens, heads, 96, act=act, kv=kv, page=7)
+    check_attend(q, 43, lens + [12001], heads, 80, act=act, kv=kv, page=48, window=385)
+    check_attend(q, 44, [i * 97 % 411 for i in range(500)], heads, 128, act=act, kv=kv, page=16)
+
+
 def test_attention_short_sequences_in_wide_tables(q):
     # the table could name far longer sequences: what is decided by its width must not be wrong for short ones
     for seqs, width in ((3, 4000), (64, 200), (50, 1000)):
