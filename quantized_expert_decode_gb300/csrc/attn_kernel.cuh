@@ -190,7 +190,7 @@ __global__ void __launch_bounds__(T::kWarps * 32, T::kCtas) attn_stream_kernel(c
         int first, end, why;
         kv_span(P.lens[b], P.table_width, P.cache.page_size, P.window, first, end, why);
         if (why && blockIdx.x == 0 && P.err) atomicOr(P.err, COLI_LAYER_BAD_POSITION);
-        return (end - first + W.unit - 1) / W.unit;
+        return kv_units(end - first, W.unit);
     };
     const int per = (P.seqs + kThreads - 1) / kThreads;
     const int b0 = min(tid * per, P.seqs), b1 = min(b0 + per, P.seqs);
@@ -420,8 +420,8 @@ __global__ void __launch_bounds__(T::kWarps * 32, T::kCtas) attn_stream_kernel(c
     auto look_up = [&](int left) {  // of how many units
         Look k{0, 0, ld_head, false};
         if (left <= 0) return k;
-        const int t = ld_first + ld.u * W.unit + w * T::kTile + lane;
-        if (lane < T::kTile && t < ld_end) {
+        int t;
+        if (kv_unit_token(ld_first, ld_end, W.unit, ld.u, w * T::kTile + lane, t) && lane < T::kTile) {
             const int i = kv_quotient(W.divide, t);
             k.slot = t - i * P.cache.page_size;
             k.page = ld_pages[i];

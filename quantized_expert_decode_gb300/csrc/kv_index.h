@@ -65,4 +65,16 @@ COLI_HD void kv_span(int32_t n, int32_t width, int32_t page_size, int32_t window
     first = (window > 0 && end > window) ? end - window : 0;
 }
 
+// Units of `unit` tokens (the last one ragged) that hold `tokens` of them, and the token at place `at` of unit u
+// behind `first`. A sequence may end at 2^31 - 1, and the places of its last unit behind the end pass 2^31: sums
+// are unsigned.
+COLI_HD int32_t kv_units(int32_t tokens, int32_t unit) {
+    return (int32_t)(((uint32_t)tokens + (uint32_t)unit - 1) / (uint32_t)unit);
+}
+COLI_HD bool kv_unit_token(int32_t first, int32_t end, int32_t unit, int32_t u, int32_t at, int32_t &t) {
+    const uint32_t x = (uint32_t)first + (uint32_t)u * (uint32_t)unit + (uint32_t)at;
+    t = (int32_t)x;
+    return x < (uint32_t)end;
+}
+
 }  // namespace colimoe

@@ -530,6 +530,30 @@ def test_attention_bad_lengths_are_clamped_and_flagged(q):
         compare_attend(c, out, lse, attend64(c, xq, table, seen, 0.125), seen, "f32", "bf16")
 
 
+def test_attention_at_the_longest_lengths(q):
+    # tables that name all but 2^31 tokens on few pages; the window's end lies within a unit of 2^31
+    rng = np.random.default_rng(48)
+    for ps in (64, 1023):
+        width = (2 ** 31 - 1) // ps
+        top = width * ps
+        c = Cache(q, rng, "f16", 3, ps, 2, 64)
+        first_page = (top - 100) // ps
+        table = torch.zeros(3, width, dtype=torch.int32, device="cuda")
+        table[:, first_page:] = torch.arange(width - first_page, dtype=torch.int32, device="cuda") % 2 + 1
+        for t in range(top - 30, top):
+            page = int(table[0, t // ps])
+            for which in (0, 1):
+                c.put(which, torch.tensor([page]), torch.tensor([t % ps]), randn(rng, 1, 2, 64))
+        xq = randn(rng, 3, 4, 64)
+        seen = [top, top, top - 1]
+        for given, flag in (([top, 2 ** 31 - 1, top - 1], 0 if top == 2 ** 31 - 1 else q.COLI_LAYER_BAD_POSITION), (seen, 0)):
+            err = err_word()
+            out, lse = run_attend(q, c, xq, table, given, 0.125, 20, err=err)
+            assert int(err.item()) == flag
+            ref = attend64(c, xq, table, seen, 0.125, 20)
+            compare_attend(c, out, lse, ref, [20], "f32", "f16")
+
+
 def test_attention_strided_rows_and_no_lse(q):
     rng = np.random.default_rng(29)
     c = Cache(q, rng, "f16", 12, 16, 2, 80)

@@ -153,6 +153,11 @@ extern "C" long long row(long long ps_, long long ts, long long hs, int pages, i
 extern "C" void span(int n, int width, int page_size, int window, int *out) {
     kv_span(n, width, page_size, window, out[0], out[1], out[2]);
 }
+extern "C" int units(int tokens, int unit) { return kv_units(tokens, unit); }
+extern "C" int unit_token(int first, int end, int unit, int u, int at) {
+    int t;
+    return kv_unit_token(first, end, unit, u, at, t) ? t : -1;
+}
 extern "C" int quotient(int size, int t) { return kv_quotient(kv_divide_by(size), t); }
 ''')
     so = d / "libkv.so"
@@ -213,3 +218,17 @@ def test_page_quotients(index, size):
         for t in (m * size - 1, m * size, m * size + 1, m * size + size - 1):
             if 0 <= t < 2 ** 31:
                 assert index.quotient(size, t) == t // size, (size, t)
+
+
+@pytest.mark.parametrize("unit", [64, 128, 192, 256, 384])
+@pytest.mark.parametrize("end", [1, 100, 5000, 2 ** 31 - 400, 2 ** 31 - 64, 2 ** 31 - 2, 2 ** 31 - 1])
+@pytest.mark.parametrize("window", [0, 1, 20, 129, 385])
+def test_units_up_to_the_longest_sequence(index, unit, end, window):
+    # the places of the last unit pass 2^31, the tokens do not
+    first = end - window if 0 < window < end else 0
+    n = index.units(end - first, unit)
+    assert n == -(-(end - first) // unit)
+    for u in {0, n - 1}:
+        for at in (0, 1, 15, 31, unit // 2, unit - 17, unit - 1):
+            t = first + u * unit + at
+            assert index.unit_token(first, end, unit, u, at) == (t if t < end else -1)
