@@ -92,7 +92,8 @@ Layout layout_of(const AttnParams &P) {
     L.w.token_step = (uint32_t)(P.cache.token_stride * size >> L.w.off_shift);
     L.w.head_step = (uint32_t)(P.cache.head_stride * size >> L.w.off_shift);
     // no more CTAs than units that the page tables can name
-    const int64_t seen = P.window > 0 ? P.window : (int64_t)P.table_width * P.cache.page_size;
+    const int64_t held = (int64_t)P.table_width * P.cache.page_size;
+    const int64_t seen = P.window > 0 && P.window < held ? P.window : held;
     const int64_t most = ((seen + L.w.unit - 1) / L.w.unit) * P.seqs * L.w.groups;
     const int64_t ctas = (int64_t)num_sms() * attn_ctas_per_sm(P.fmt, L.w.dim, L.w.nt, L.w.wide);
     L.units = most;

@@ -383,6 +383,12 @@ def test_attention_windows(q, window):
     check_attend(q, 17, [0, 1, 99, 100, 101, 500, 1300], (8, 2), 64, window=window, page=24)
 
 
+def test_attention_windows_beyond_the_table(q):
+    lens = [(i * 37) % 513 for i in range(63)] + [512]
+    for window in (513, 2 ** 30, 2 ** 31 - 1):
+        check_attend(q, 49, lens, (16, 8), 64, window=window)
+
+
 def test_attention_long(q):
     check_attend(q, 18, [40000], (8, 1), 128, act="f32", kv="bf16", page=64)
     check_attend(q, 18, [70001], (5, 1), 64, act="bf16", kv="e4m3", page=32)

@@ -120,6 +120,15 @@ def test_attention_workspace(q):
                               raise_on_error=False) == q.COLI_MOE_EWORKSPACE
 
 
+@pytest.mark.parametrize("seqs,q_heads,width,window", [(64, 64, 32, 2 ** 31 - 1), (64, 64, 64, 2 ** 30), (2048, 8, 4, 2 ** 31 - 1),
+                                                       (1, 8, 500, 8001), (5, 16, 31, 4096)])
+def test_a_window_beyond_the_table_is_no_window(q, seqs, q_heads, width, window):
+    # as many units, so the same workspace, as without a window
+    c = cache(q, heads=8 if q_heads % 8 == 0 else 4)
+    none, wide = (q.make_attn_desc(seqs, q_heads, width, 0, 0.1, window=w) for w in (0, window))
+    assert q.coli_attn_workspace_bytes(wide, c) == q.coli_attn_workspace_bytes(none, c) > 0
+
+
 @pytest.mark.parametrize("desc,args,code", [
     (dict(rows=0), {}, "EINVAL"), (dict(width=0), {}, "EINVAL"), (dict(width=65537), {}, "EINVAL"),
     (dict(act=5), {}, "EINVAL"), (dict(gate=4), {}, "EINVAL"), (dict(gate=1), {}, "EINVAL"),
