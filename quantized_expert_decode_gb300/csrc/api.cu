@@ -223,8 +223,15 @@ int run_forward_decode(const coli_moe_desc *d, const float *x, const float *W_r,
     cudaError_t e = cudaSuccess;
     if (P.single) {
         // the single-token kernel resets its own counters: CTA 0 zeroes them and publishes this
-        // call's id, which no earlier call (of this or another process) has used
+        // call's id, which no earlier call (of this or another process) has used. The replays of a
+        // captured call all have the id of the capture: there the kept id is cleared before each
+        // (ids are odd), so that no CTA takes the counters of the replay before for its own.
         P.call_id = next_call_id();
+        cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+        if ((e = cudaStreamIsCapturing(st, &cap)) != cudaSuccess) return cuda_fail(e);
+        if (cap == cudaStreamCaptureStatusActive &&
+            (e = cudaMemsetAsync(&P.ctrl->call, 0, sizeof(P.ctrl->call), st)) != cudaSuccess)
+            return cuda_fail(e);
     } else if ((e = cudaMemsetAsync(P.ctrl, 0, sizeof(DecCtrl), st)) != cudaSuccess) {
         return cuda_fail(e);
     }

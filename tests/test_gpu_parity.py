@@ -346,6 +346,45 @@ def test_one_token_many_calls(qed, blocks):
         assert_out_close(out[0], ro[0], what=f"call {i}")
 
 
+@pytest.mark.parametrize("T", [1, 4, 20, 70])
+@pytest.mark.parametrize("tail", [False, True])
+def test_captured_calls_replay(qed, T, tail):
+    """A captured call replayed on new inputs gives each time what the call itself gives."""
+    from quantized_expert_decode_gb300.device import DeviceBlock
+    blk = make(dict(T=T, H=512, I=256, E=32, K=4, I_shared=128, norm_topk=1, routed_scale=2.5, routed_fmt=2, shared_fmt=2,
+                    zipf=False), seed=61)
+    dev = DeviceBlock(blk)
+    x, out = torch.empty(T, 512, device="cuda"), torch.empty(T, 512, device="cuda")
+    nw = torch.ones(512, device="cuda")
+    s = torch.cuda.Stream()
+
+    def call():
+        if tail:
+            qed.coli_moe_forward_tail(dev.desc, x, nw, 1e-5, dev.Wr, dev.bias, dev.table, dev.shared, out, None, None, dev.ws,
+                                      dev.ws_bytes, s)
+        else:
+            qed.coli_moe_forward(dev.desc, x, dev.Wr, dev.bias, dev.table, dev.shared, out, None, None, dev.ws, dev.ws_bytes, s)
+
+    xs = [torch.randn(T, 512, device="cuda", generator=torch.Generator("cuda").manual_seed(i)) for i in range(8)]
+    want = []
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        for v in xs:
+            x.copy_(v)
+            call()
+            want.append(out.clone())
+        g = torch.cuda.CUDAGraph()
+        s.synchronize()
+        with torch.cuda.graph(g, stream=s):
+            call()
+        for _ in range(3):
+            for v, w in zip(xs, want):
+                x.copy_(v)
+                g.replay()
+                assert torch.equal(out, w)
+        qed.coli_moe_check(dev.ws, s)
+
+
 # ------------------------------------------------------------------ prefill (tensor-core GEMMs)
 # T > 64: every format pair, token counts that leave ragged N tiles, more tokens per expert than
 # one N tile holds, no shared expert, and a 16-bit-unfriendly activation scale.
