@@ -14,7 +14,8 @@ _TORCH = {COLI_KV_BF16: torch.bfloat16, COLI_KV_F16: torch.float16, COLI_KV_E4M3
 
 class PagedCache:
     """Pools of `pages` pages for keys and values, and a page table for `seqs` sequences. Pages are handed
-    out as sequences grow and come back when a sequence ends; nothing is copied or cleared."""
+    out as sequences grow and come back when a sequence ends; nothing is copied or cleared. The table is
+    written on torch's current stream."""
 
     def __init__(self, seqs, pages, page_size, heads, dim, fmt=COLI_KV_BF16, max_tokens=None, k_scale=None,
                  v_scale=None, device="cuda"):
@@ -81,7 +82,33 @@ class DecodeLayer:
 
     def step(self, xn, resid, pos, lens, stream=None):
         """xn [n, H]: the normalised input, resid [n, H] the residual (updated in place), pos and lens [n]
-        int32: each sequence's new position and its tokens with the new one. Returns the next layer's xn."""
+        int32: each sequence's new position and its tokens with the new one. Returns the next layer's xn.
+
+        Everything runs on one stream: torch's current one, or `stream` (a torch stream or a handle). What is
+        given must be ready on the current stream, and the result is: another `stream` waits for the current one
+        before the step, and the current one for it after. Can be captured into a graph (after one step outside
+        it, which sets up the library products)."""
+        now, on = self._streams(stream)
+        if on is None:
+            return self._run(xn, resid, pos, lens, now)
+        on.wait_stream(now)
+        try:
+            with torch.cuda.stream(on):
+                out = self._run(xn, resid, pos, lens, on)
+        finally:  # what is under way still reads the arguments
+            now.wait_stream(on)
+        out.record_stream(now)  # it is on's memory
+        return out
+
+    def _streams(self, stream):
+        """torch's current stream, and the one given if that is another."""
+        dev = self.cache.device
+        now = torch.cuda.current_stream(dev)
+        if isinstance(stream, int):
+            stream = torch.cuda.ExternalStream(stream, dev) if stream else torch.cuda.default_stream(dev)
+        return now, None if stream is None or stream.cuda_stream == now.cuda_stream else stream
+
+    def _run(self, xn, resid, pos, lens, stream):
         c, d, qd = self.cache, self.cache.dim, self.q_heads * self.cache.dim
         kd = c.heads * d
         qkv = xn @ self.w_qkv.T
@@ -100,6 +127,7 @@ class DecodeLayer:
         return out
 
     def check(self, stream=None):
-        """Raises if a kernel flagged an error since the last check (synchronises)."""
-        coli_moe_check(self.err, stream)
-        coli_moe_check(self.block.ws, stream)
+        """Raises if a kernel flagged an error since the last check (synchronises `stream`, or the current one)."""
+        now, on = self._streams(stream)
+        coli_moe_check(self.err, on or now)
+        coli_moe_check(self.block.ws, on or now)
