@@ -53,7 +53,7 @@ class PagedCache:
 
 
 class DecodeLayer:
-    """One decoder layer's step for one new token of every sequence, fp32 activations:
+    """One decoder layer's step for one new token of every sequence (slot), fp32 activations:
     attention over the cache, the norms around it, the MoE block (`block`, a DeviceBlock), and the norm
     that the next layer reads.
 
@@ -80,9 +80,13 @@ class DecodeLayer:
         self.heads_out = torch.empty(n, q_heads * d, device=dev)
         self.block_out = torch.empty(n, h, device=dev)
 
-    def step(self, xn, resid, pos, lens, stream=None):
+    def step(self, xn, resid, pos, lens, stream=None, seq=None):
         """xn [n, H]: the normalised input, resid [n, H] the residual (updated in place), pos and lens [n]
         int32: each sequence's new position and its tokens with the new one. Returns the next layer's xn.
+
+        seq [n] int32, needed where a slot is idle (its sequence has ended and none has taken its place): -1 for
+        such a slot, its own number for any other. Nothing is cached for an idle slot and its attention is 0, as
+        its lens must be; its rows of xn and resid go through the block and mean nothing.
 
         Everything runs on one stream: torch's current one, or `stream` (a torch stream or a handle). What is
         given must be ready on the current stream, and the result is: another `stream` waits for the current one
@@ -90,11 +94,11 @@ class DecodeLayer:
         it, which sets up the library products)."""
         now, on = self._streams(stream)
         if on is None:
-            return self._run(xn, resid, pos, lens, now)
+            return self._run(xn, resid, pos, lens, seq, now)
         on.wait_stream(now)
         try:
             with torch.cuda.stream(on):
-                out = self._run(xn, resid, pos, lens, on)
+                out = self._run(xn, resid, pos, lens, seq, on)
         finally:  # what is under way still reads the arguments
             now.wait_stream(on)
         out.record_stream(now)  # it is on's memory
@@ -108,12 +112,12 @@ class DecodeLayer:
             stream = torch.cuda.ExternalStream(stream, dev) if stream else torch.cuda.default_stream(dev)
         return now, None if stream is None or stream.cuda_stream == now.cuda_stream else stream
 
-    def _run(self, xn, resid, pos, lens, stream):
+    def _run(self, xn, resid, pos, lens, seq, stream):
         c, d, qd = self.cache, self.cache.dim, self.q_heads * self.cache.dim
         kd = c.heads * d
         qkv = xn @ self.w_qkv.T
         q, k, v = qkv[:, :qd], qkv[:, qd:qd + kd], qkv[:, qd + kd:]
-        coli_kv_append(self.append, c.desc, q, k, v, self.inv_freq, None, pos, c.table, q, self.err, stream)
+        coli_kv_append(self.append, c.desc, q, k, v, self.inv_freq, seq, pos, c.table, q, self.err, stream)
         coli_attn_decode(self.attn, c.desc, q, c.table, lens, self.heads_out, None, self.err, self.ws, self.ws.numel(),
                          stream)
         y = self.heads_out @ self.w_o.T

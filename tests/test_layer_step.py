@@ -104,6 +104,15 @@ def test_a_step_runs_on_one_stream(fake):
     assert [e[1:3] for e in calls()] == [(7, 7)] * 5 + [(9, 7)] * 2 and len(fake.log) == 7
 
 
+def test_a_step_hands_the_slots_on(fake):
+    # which slots append, -1 for an idle one
+    seq = torch.tensor([-1, 1], dtype=torch.int32)
+    for given in (None, seq):
+        fake.log.clear()
+        fake.layer.step(*fake.args, seq=given)
+        assert fake.log[0][0] == "coli_kv_append" and fake.log[0][3] is given
+
+
 def run_steps(mode, fmt, n, steps=6):
     """The outputs of some steps of a layer, the same layer and inputs for every mode: on the default stream, on a
     side stream that is torch's current one, on a stream that is not, or replayed from a graph."""
@@ -222,3 +231,55 @@ def test_steps_match_the_definition(q, window, interleaved, sandwich):
             err = np.abs(got.cpu().numpy() - want).max()
             assert err <= 1e-3 * np.sqrt((want ** 2).mean()), (step, err)
     layer.check()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("idle", [{2: (3, 6)}, {0: (2, 8), 3: (4, 5)}])
+def test_idle_slots(q, idle):
+    # Slots {slot: (first idle step, step of its next sequence)}: the other slots' rows are those of a batch without
+    # idle slots, a slot's next sequence is its first one over again, nothing is flagged and nothing cached for an
+    # idle slot. Rows are computed apart from each other but for the block's order of sums (1e-4 rms of its oracle).
+    import synth
+    from quantized_expert_decode_gb300.device import DeviceBlock
+    from quantized_expert_decode_gb300.layer import DecodeLayer, PagedCache
+    blk = synth.make_block(0)
+    n, steps, h, qh, kh, d = 4, 9, blk["cfg"]["H"], 6, 2, 32
+    g = torch.Generator("cuda").manual_seed(5)
+    rand = lambda *s: torch.randn(*s, device="cuda", generator=g)  # noqa: E731
+    w_qkv, w_o, inv = rand((qh + 2 * kh) * d, h) / h ** 0.5, rand(h, qh * d) / (qh * d) ** 0.5, torch.rand(d // 2, device="cuda")
+    ones, x0, r0 = torch.ones(h, device="cuda"), rand(n, h), rand(n, h)
+
+    def run(idle):
+        cache = PagedCache(n, 20, 4, kh, d)
+        for pool in (cache.k, cache.v):
+            pool.zero_()
+        layer = DecodeLayer(DeviceBlock(blk), cache, w_qkv, w_o, ones, ones, inv, qh)
+        x, r, out = x0.clone(), r0.clone(), []
+        for step in range(steps):
+            for s, (first, again) in idle.items():
+                if step == first:
+                    cache.end(s)
+                if step == again:
+                    x[s], r[s] = x0[s], r0[s]
+            on = [not (s in idle and idle[s][0] <= step < idle[s][1]) for s in range(n)]
+            at = [cache.grow(s) if on[s] else 0 for s in range(n)]
+            pos, live = torch.tensor(at, dtype=torch.int32, device="cuda"), torch.tensor(on, device="cuda")
+            seq = torch.arange(n, dtype=torch.int32, device="cuda").masked_fill(~live, -1) if idle else None
+            pools = [cache.k.clone(), cache.v.clone()]
+            x = layer.step(x, r, pos, (pos + 1) * live, seq=seq)
+            layer.check()
+            rows = {(int(cache.table[s, at[s] // 4]), at[s] % 4) for s in range(n) if on[s]}
+            for pool, was in zip((cache.k, cache.v), pools):
+                changed = (pool.view(torch.int16) != was.view(torch.int16)).any(3).any(1)
+                assert {tuple(e) for e in changed.nonzero().tolist()} <= rows
+            out.append((x.clone(), r.clone(), on))
+        return out
+
+    full, some = run({}), run(idle)
+    for step in range(steps):
+        for s in range(n):
+            if not some[step][2][s]:
+                continue
+            like = step - idle[s][1] if s in idle and step >= idle[s][1] else step
+            for a, b in zip(some[step][:2], full[like][:2]):
+                assert float((a[s] - b[s]).abs().max()) <= 1e-3 * float(b[s].square().mean().sqrt()), (step, s)
