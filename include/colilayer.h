@@ -48,8 +48,8 @@ extern "C" {
  * 16-byte aligned (COLI_MOE_EALIGN). dim: a multiple of 16 bytes of elements, at most 256
  * (COLI_MOE_ENOTSUP). The attention reaches rows by 32-bit multiples of the strides' largest common power of
  * two, which is at least 16 bytes: 64 GB of keys at that least, 1 TB at rows of 256 bytes; beyond, it
- * answers COLI_MOE_ENOTSUP. COLI_KV_E4M3 stores value * (1 / scale[head]), saturated to +-448 (NaN stays NaN);
- * a NULL scale stands for 1. The scales are ignored for the other types. */
+ * answers COLI_MOE_ENOTSUP. COLI_KV_E4M3 stores value / scale[head] (the quotient rounded to fp32, then to
+ * e4m3), saturated to +-448 (NaN stays NaN); a NULL scale stands for 1. The scales are ignored for the other types. */
 typedef struct {
     void *k, *v;
     const float *k_scale, *v_scale; /* [heads] each */

@@ -225,6 +225,35 @@ def test_append_saturates_and_keeps_nan(q):
         assert torch.equal(got.nan_to_num(777.0), want.nan_to_num(777.0))
 
 
+@pytest.mark.parametrize("scale", [1.0, 3.0, 0.75, 0.1, 7.0, 1.1, 2.0 ** -100, 2.0 ** -127, 3.0 * 2.0 ** -130, 2.0 ** -149, 2.0 ** 127, 3e38])
+@pytest.mark.parametrize("rot", [0, 2])
+def test_append_divides_by_the_scale(q, scale, rot):
+    # values on and next to the borders between e4m3 values: the quotient's own side, as an IEEE division has it
+    steps = torch.arange(0x7e, dtype=torch.uint8).view(torch.float8_e4m3fn).double()
+    border = (steps[1:] + steps[:-1]) / 2
+    s32 = torch.tensor(scale, dtype=torch.float32)
+    x = torch.cat([steps, border]) * s32.double()
+    x = torch.cat([x, x * (1 + 2.0 ** -23), x * (1 - 2.0 ** -23), -x, torch.tensor([math.inf, -math.inf, math.nan, 500 * scale])])
+    x = x.float()
+    n = -(-len(x) // 64)
+    x = torch.cat([x, x.new_zeros(n * 64 - len(x))]).view(n, 1, 64)
+    x[..., :2] = x[..., :2].nan_to_num(0.0, 0.0, 0.0)  # (turned by 0, an infinity would be NaN)
+    x = x.cuda()
+    c = Cache(q, np.random.default_rng(50), "e4m3", n, 1, 1, 64)
+    c.scale.fill_(float(s32))
+    err = err_word()
+    # the odd rotary size takes the elements one by one; at position 0 it turns nothing
+    q.coli_kv_append(q.make_append_desc(n, 0, n, 1, 0, rot), c.desc, None, x, x, torch.ones(1, device="cuda") if rot else None, None,
+                     torch.zeros(n, dtype=torch.int32, device="cuda"), torch.arange(n, dtype=torch.int32, device="cuda").view(n, 1),
+                     None, err)
+    assert q.coli_moe_check(err) == q.COLI_MOE_OK
+    want = torch.from_numpy((x.cpu().numpy() / s32.numpy()).astype(np.float32)).clamp(-448, 448).to(torch.float8_e4m3fn)
+    want = want.float().nan_to_num(777.0)
+    for pool in (c.k, c.v):
+        got = pool[:, :, 0].contiguous().view(torch.float8_e4m3fn).float().cpu()
+        assert torch.equal(got.nan_to_num(777.0), want)
+
+
 def test_append_in_place_and_default_sequences(q):
     rng = np.random.default_rng(9)
     c = Cache(q, rng, "bf16", 4, 4, 2, 64)
