@@ -655,13 +655,24 @@ __global__ void __launch_bounds__(T::kWarps * 32, T::kCtas) attn_stream_kernel(c
                     const float ref = mn == -INFINITY ? 0.f : mn;
                     f[n][j] = exp2_fast(m[n][j] - ref);  // exact: an integer power; 0 from -inf
                     m[n][j] = mn;
-                    float sum = 0.f;
+                    // One rounding for the exponent, of the exact product, small where p is large. But the maximum is of
+                    // rounded products, from 2^23 on steps of 1 and more away from the exact ones (p would pass f16's
+                    // range, or be 0 for every token): there the exponents are of those too. (64 sequences of 24,576
+                    // e4m3 tokens 497 -> 500 us; by a vote and a branch other forms pay up to 6 % through the registers.)
+                    const float off = __fsub_rd((float)T::kShift, ref);
+                    float sum = 0.f, by = sc[n][j];
+                    if (!(fabsf(mn) < 0x1p23f)) {
+#pragma unroll
+                        for (int i = 0; i < T::kMT; i++)
+#pragma unroll
+                            for (int r = 0; r < 2; r++) s[i][n][2 * r + j] = __fmul_rn(s[i][n][2 * r + j], by);
+                        by = 1.f;
+                    }
 #pragma unroll
                     for (int i = 0; i < T::kMT; i++)
 #pragma unroll
                         for (int r = 0; r < 2; r++) {
-                            // one rounding for the exponent, small where p is large
-                            const float p = exp2_fast(fmaf(s[i][n][2 * r + j], sc[n][j], (float)T::kShift - ref));
+                            const float p = exp2_fast(fmaf(s[i][n][2 * r + j], by, off));
                             s[i][n][2 * r + j] = p;
                             sum += p;
                         }

@@ -480,6 +480,35 @@ def test_attention_peaked_and_flat_scores(q):
     check_attend(q, 22, [300, 1000], (8, 2), 64, boost=0.0)
 
 
+@pytest.mark.parametrize("act,kv,low,high,key", [("f32", "f16", 16, 30, 0), ("f32", "e4m3", 16, 30, 0), ("bf16", "f16", 16, 40, 0),
+                                                 ("bf16", "e4m3", 16, 30, 0), ("f16", "f16", 10, 15, 9), ("f16", "e4m3", 12, 15, 7),
+                                                 ("f32", "bf16", 20, 60, 0), ("bf16", "bf16", 20, 60, 0), ("f16", "bf16", 10, 15, 20)])
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_attention_huge_scores(q, act, kv, low, high, key, sign):
+    # One token's score is twice the others', all of them so large that they are many steps of 1 apart in fp32: its
+    # value is the output, whatever the score's own rounding (p of the token is the whole sum: the parts' 22 or 16 bits).
+    rng = np.random.default_rng(51)
+    c = Cache(q, rng, kv, 20, 16, 2, 64, scales=False)
+    lens = [200, 33, 64]
+    table = fill(rng, c, lens)
+    u = torch.from_numpy(rng.choice([-1.0, 1.0], (2, 64))).cuda() * 2.0 ** key
+    best = [int(rng.integers(0, n)) for n in lens]
+    for b, n in enumerate(lens):
+        t = torch.arange(n, device="cuda")
+        k = u.float()[None] * torch.where(t == best[b], 2.0, 1.0)[:, None, None]
+        c.put(0, table[b].long()[t // 16], t % 16, k)
+    size = torch.from_numpy(2.0 ** rng.uniform(low, high, (3, 16, 1)) * rng.uniform(0.9, 1.1, (3, 16, 64))).cuda()
+    xq = (size * u.sign().repeat_interleave(8, 0)[None] * sign).to(ACT[act][1])
+    out, lse = run_attend(q, c, xq, table, lens, 0.125 * sign, act=act)
+    _, wlse, _, amp = attend64(c, xq, table, lens, 0.125 * sign)
+    close(lse, wlse, amp * ((64 / 16 + 4) * 2 * U + 2.0 ** -22 + 8 * U) + 36 * U * wlse.abs())
+    for b in range(3):
+        v = c.rows(1, table[b].long()[best[b] // 16].view(1), torch.tensor([best[b] % 16], device="cuda"))[0]
+        want = v.repeat_interleave(8, 0)
+        parts = 2.0 ** -16 if act != "f32" and kv == "bf16" else 2.0 ** -22
+        close(out[b], want, half_ulp(want, ACT[act][1]) + (parts + 8 * U) * want.abs())
+
+
 def test_attention_large_and_small_values(q):
     # values far from 1 in the cache's own range, queries that make up for the keys
     for kv, f in (("bf16", 2.0 ** 60), ("bf16", 2.0 ** -60), ("f16", 2.0 ** 10), ("f16", 2.0 ** -12)):
