@@ -75,7 +75,10 @@ class DecodeLayer:
                                        q_stride=row, k_stride=row, v_stride=row, q_out_stride=row)
         self.attn = make_attn_desc(n, q_heads, cache.width, COLI_ACT_F32, d ** -0.5, window=window, q_stride=row)
         self.norms = make_norms_desc(n, h, COLI_ACT_F32, COLI_GATE_NONE, eps, eps)
-        self.ws = torch.empty(coli_attn_workspace_bytes(self.attn, cache.desc), dtype=torch.uint8, device=dev)
+        ws_bytes = coli_attn_workspace_bytes(self.attn, cache.desc)
+        if ws_bytes == 0:
+            raise ValueError("the attention does not take this cache with these heads and sequences")
+        self.ws = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
         self.err = torch.zeros(1, dtype=torch.int32, device=dev)
         self.heads_out = torch.empty(n, q_heads * d, device=dev)
         self.block_out = torch.empty(n, h, device=dev)

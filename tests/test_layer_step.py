@@ -113,6 +113,17 @@ def test_a_step_hands_the_slots_on(fake):
         assert fake.log[0][0] == "coli_kv_append" and fake.log[0][3] is given
 
 
+@pytest.mark.parametrize("seqs,q_heads", [(2049, 2), (2, 3), (2, 2048)])
+def test_a_layer_that_the_attention_refuses_is_not_built(q, seqs, q_heads):
+    import types
+
+    from quantized_expert_decode_gb300.layer import DecodeLayer, PagedCache
+    block = types.SimpleNamespace(set_tokens=lambda n: None)
+    cache = PagedCache(seqs, 2, 4, 2, 16, max_tokens=4, device="cpu")
+    with pytest.raises(ValueError):
+        DecodeLayer(block, cache, torch.zeros((q_heads + 4) * 16, 8), torch.zeros(8, q_heads * 16), None, None, torch.ones(8), q_heads)
+
+
 def run_steps(mode, fmt, n, steps=6):
     """The outputs of some steps of a layer, the same layer and inputs for every mode: on the default stream, on a
     side stream that is torch's current one, on a stream that is not, or replayed from a graph."""
