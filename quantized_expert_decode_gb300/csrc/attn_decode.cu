@@ -99,7 +99,7 @@ Layout layout_of(const AttnParams &P) {
     L.units = most;
     L.grid = (int)(most < ctas ? most : ctas);
     const int64_t items = (int64_t)P.seqs * L.w.groups;
-    L.w.unit_us = (float)L.w.unit * L.w.dim * 2 * size / 7.2e6f;
+    L.w.unit_us = (float)L.w.unit * P.dim * 2 * size / 7.2e6f;
     L.w.ctas = L.grid;
     // certain for the longest items that the tables can name: no second launch; else the kernel decides by the lengths
     if (attn_whole(items, most / items, ctas, L.w.unit_us)) L.w.whole = kAttnWhole;

@@ -241,3 +241,51 @@ def test_units_up_to_the_longest_sequence(index, unit, end, window):
         for at in (0, 1, 15, 31, unit // 2, unit - 17, unit - 1):
             t = first + u * unit + at
             assert index.unit_token(first, end, unit, u, at) == (t if t < end else -1)
+
+
+# ---------------------------------------------------------------------- how a call is laid out
+@pytest.fixture(scope="module")
+def layout(tmp_path_factory):
+    """attn_decode.cu's layout of a call, built for the host with the launches left out."""
+    d = tmp_path_factory.mktemp("layout")
+    src = d / "layout.cu"
+    src.write_text('''
+#include "attn_decode.cu"
+namespace colimoe {
+int num_sms() { return 152; }
+cudaError_t launch_attn_bf16(const AttnParams &, const AttnWork &, int, cudaStream_t) { return cudaSuccess; }
+cudaError_t launch_attn_f16(const AttnParams &, const AttnWork &, int, cudaStream_t) { return cudaSuccess; }
+cudaError_t launch_attn_e4m3(const AttnParams &, const AttnWork &, int, cudaStream_t) { return cudaSuccess; }
+}
+extern "C" void layout(int fmt, int act, int dim, int heads, int kv_heads, int seqs, int width, int page_size, int window, double *out) {
+    using namespace colimoe;
+    AttnParams P{};
+    P.fmt = fmt, P.act = act, P.dim = dim, P.q_heads = heads, P.kv_heads = kv_heads, P.seqs = seqs, P.table_width = width;
+    P.window = window;
+    P.cache = KvShape{(int64_t)kv_heads * page_size * dim, dim, (int64_t)page_size * dim, 1000, page_size};
+    const Layout L = layout_of(P);
+    out[0] = L.w.unit, out[1] = L.w.unit_us, out[2] = L.w.whole, out[3] = L.grid, out[4] = (double)L.units;
+}
+''')
+    from quantized_expert_decode_gb300 import build
+    so = d / "liblayout.so"
+    subprocess.run([os.path.join(build.cuda_home(), "bin", "nvcc"), *build.ARCH, "-std=c++17", "-shared", "-Xcompiler", "-fPIC", "-I",
+                    build.CSRC, "-I", build.INCLUDE, "--expt-relaxed-constexpr", str(src), "-o", str(so)], check=True)
+    lib = ctypes.CDLL(str(so))
+
+    def call(**a):
+        d = dict(fmt=1, act=1, dim=128, heads=32, kv_heads=8, seqs=32, width=100, page_size=16, window=0)
+        d.update(a)
+        out = (ctypes.c_double * 5)()
+        lib.layout(*d.values(), out)
+        return dict(zip(("unit", "unit_us", "whole", "grid", "units"), out))
+    return call
+
+
+@pytest.mark.parametrize("fmt,size", [(1, 2), (2, 2), (3, 1)])
+@pytest.mark.parametrize("dim", [16, 32, 48, 64, 80, 96, 112, 128, 160, 192, 256])
+def test_a_units_time_is_of_the_bytes_it_has(layout, fmt, size, dim):
+    # K and V of the head's own elements, not of the size that shared memory rounds it up to
+    for heads in (8, 128):
+        got = layout(fmt=fmt, dim=dim, heads=heads)
+        assert got["unit_us"] == pytest.approx(got["unit"] * dim * 2 * size / 7.2e6, rel=1e-6)
