@@ -36,8 +36,8 @@ constexpr int attn_unit(int fmt, int dim, int nt, bool wide) {
 }
 
 // Whether a CTA per item, none cut, is the faster way for items of u units, with room for `ctas` CTAs at once (the
-// others start as those end). Measured on bf16 caches of 128 elements, 8 kv heads, against runs that go on from
-// item to item, or parts of items, and their join:
+// others start as those end). Measured on bf16 caches of 128 elements, 8 kv heads, groups of 8 heads (units of 128
+// tokens), against runs that go on from item to item, or parts of items, and their join:
 //   few short items: 333 tokens of one sequence 8.2 us against 6.8 on the device, but without the second launch
 //     8.5 against 10.4 called from Python;
 //   a quarter of the places: 16 sequences of 1000 tokens 17 us against 21, 32 of 500 16 against 20;
@@ -54,15 +54,23 @@ __host__ __device__ inline bool attn_waves(float items, float u, float ctas, flo
     const float full = floorf(items / ctas), rest = items - full * ctas;
     return 6.f + full * fmaxf(ctas * u * unit_us, alone) + (rest > 0.f ? fmaxf(rest * u * unit_us, alone) : 0.f) < 15.f + 1.06f * all;
 }
-__host__ __device__ inline bool attn_whole(int64_t items, int64_t u, int64_t ctas, float unit_us) {
+// The 9 to 16 heads of 65 to 128 elements that a CTA takes alone on its SM (`big`; units of 192 to 384 tokens) pay
+// more a unit, and cutting finds more places free: one sequence of 576 bf16 tokens on 8 kv heads 11.7 us whole against 9.7,
+// 5 of 1500 21.8 against 16.6, 8 of 1500 21.8 against 19.2, 12 of 1500 22.0 against 25.9; 5 of 700 13.4 against 14.4.
+__host__ __device__ constexpr bool attn_big(int dim, int nt) { return dim == 128 && nt == 2; }
+__host__ __device__ inline bool attn_whole(int64_t items, int64_t u, int64_t ctas, float unit_us, bool big) {
     if (items > 16 * ctas) return false;
-    if (u <= 3 || (u <= 8 && 4 * items >= ctas)) return true;
+    if (big) {
+        if (u <= 2 || (u <= 4 && 4 * items >= ctas) || (u <= 8 && 5 * items >= 3 * ctas)) return true;
+    } else if (u <= 3 || (u <= 8 && 4 * items >= ctas)) {
+        return true;
+    }
     return u <= 32 && 5 * items >= 4 * ctas && attn_waves((float)items, (float)u, (float)ctas, unit_us);
 }
 
 // The same by the lengths themselves: `total` units, the longest item's u.
-__device__ inline bool attn_whole_now(uint32_t total, int64_t items, int64_t u, int64_t ctas, float unit_us) {
-    if (attn_whole(items, u, ctas, unit_us)) return true;
+__device__ inline bool attn_whole_now(uint32_t total, int64_t items, int64_t u, int64_t ctas, float unit_us, bool big) {
+    if (attn_whole(items, u, ctas, unit_us, big)) return true;
     if (items > 16 * ctas || 5 * items < 4 * ctas) return false;
     const float full = (float)total / ((float)items * (float)u);  // 1: all as long
     return full >= 0.9f ? attn_waves((float)items, (float)u, (float)ctas, unit_us) : full < 0.75f && u <= 32;

@@ -102,7 +102,7 @@ Layout layout_of(const AttnParams &P) {
     L.w.unit_us = (float)L.w.unit * P.dim * 2 * size / 7.2e6f;
     L.w.ctas = L.grid;
     // certain for the longest items that the tables can name: no second launch; else the kernel decides by the lengths
-    if (attn_whole(items, most / items, ctas, L.w.unit_us)) L.w.whole = kAttnWhole;
+    if (attn_whole(items, most / items, ctas, L.w.unit_us, attn_big(L.w.dim, L.w.nt))) L.w.whole = kAttnWhole;
     else if (items <= 16 * ctas && 5 * items >= 4 * ctas) L.w.whole = kAttnMaybe;
     if (L.w.whole == kAttnWhole) L.grid = (int)items;
     if (L.w.whole == kAttnMaybe && items > L.grid) L.grid = (int)items;

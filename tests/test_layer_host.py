@@ -289,3 +289,19 @@ def test_a_units_time_is_of_the_bytes_it_has(layout, fmt, size, dim):
     for heads in (8, 128):
         got = layout(fmt=fmt, dim=dim, heads=heads)
         assert got["unit_us"] == pytest.approx(got["unit"] * dim * 2 * size / 7.2e6, rel=1e-6)
+
+
+@pytest.mark.parametrize("fmt,act,unit", [(1, 1, 192), (2, 0, 192), (3, 1, 384), (3, 0, 256)])
+def test_long_items_of_wide_groups_are_cut(layout, fmt, act, unit):
+    # 9 to 16 heads a kv head, 65 to 128 elements: whole items of few CTAs take longer than cut ones and their join
+    # from 3 units on, from 5 where a quarter of the places is taken, from 9 where most are
+    for dim, heads in ((128, 128), (96, 72)):
+        for seqs, units, whole in ((1, 2, 1), (1, 3, 0), (4, 3, 0), (5, 3, 1), (5, 4, 1), (5, 5, 0), (8, 4, 1), (8, 5, 0), (8, 8, 0),
+                                   (12, 5, 1), (12, 8, 1)):
+            got = layout(fmt=fmt, act=act, dim=dim, heads=heads, seqs=seqs, page_size=unit, width=units)
+            assert got["unit"] == unit and (got["whole"] == 1) == bool(whole), (dim, seqs, units)
+    # others as they were
+    for dim, heads in ((128, 64), (64, 128), (256, 128)):
+        unit = int(layout(fmt=fmt, act=act, dim=dim, heads=heads)["unit"])
+        assert layout(fmt=fmt, act=act, dim=dim, heads=heads, seqs=1, page_size=unit, width=3)["whole"] == 1
+        assert layout(fmt=fmt, act=act, dim=dim, heads=heads, seqs=10, page_size=unit, width=8)["whole"] == 1
