@@ -45,35 +45,46 @@ constexpr int attn_unit(int fmt, int dim, int nt, bool wide) {
 //     on 32 heads 23 against 30; but 40 of 2000 (320 items, 304 places) 70 against 62.
 // So where items fill the places the time of the waves is estimated, each the larger of its bytes' time and of
 // one CTA's alone (1.25 us a unit), against the other way's: its bytes' and 15 us of starts, cuts and join. Items
-// of more than 32 units count only where all are as long: in a ragged batch the last of them would end alone (32
-// sequences of 1 to 8192 tokens 134 us against 95). Up to there ragged items fill the waves' gaps (40 sequences of 1
-// to 2000 tokens 35 us against 47, of 1 to 4000 64 against 72).
+// of more than 40 us alone (32 units) count only where all are as long: in a ragged batch the last of them would end
+// alone (32 sequences of 1 to 8192 tokens 134 us against 95). Up to there ragged items fill the waves' gaps (40 sequences
+// of 1 to 2000 tokens 35 us against 47, of 1 to 4000 64 against 72).
+//   The 9 to 16 heads of 65 to 128 elements that a CTA takes alone on its SM (`big`, units of 192 to 384 tokens) take
+// longer for a unit, and no less beside each other; and cutting short items finds more places free: one sequence of
+// 576 bf16 tokens on 8 kv heads 11.7 us whole against 9.7, 5 of 1500 21.8 against 16.6, 8 of 1500 21.8 against 19.2; but
+// 12 of 1500 22.0 against 25.9, 5 of 700 13.4 against 14.4; 20 of 3000 e4m3 tokens 58 against 44, in ragged batches 19
+// of 1 to 4000 bf16 tokens 52 whole against 72, 16 of 1 to 6000 75 against 66.
 constexpr int kAttnWhole = 1, kAttnMaybe = 2;
-__host__ __device__ inline bool attn_waves(float items, float u, float ctas, float unit_us) {
-    const float all = items * u * unit_us, alone = 1.25f * u;
-    const float full = floorf(items / ctas), rest = items - full * ctas;
-    return 6.f + full * fmaxf(ctas * u * unit_us, alone) + (rest > 0.f ? fmaxf(rest * u * unit_us, alone) : 0.f) < 15.f + 1.06f * all;
+struct AttnTimes {  // us
+    float bytes;  // of a unit's bytes at the memory's full rate
+    float alone;  // of a unit on a CTA that has none beside it
+    bool big;
+    __host__ __device__ bool short_item(int64_t u) const { return (float)u * alone <= (big ? 50.f : 40.f); }
+};
+inline AttnTimes attn_times(int fmt, int dim, int nt, int unit, int64_t unit_bytes) {
+    const bool big = dim == 128 && nt == 2;
+    return {(float)unit_bytes / 7.2e6f, !big ? 1.25f : fmt == COLI_KV_E4M3 ? unit / 125.f : unit / 100.f, big};
 }
-// The 9 to 16 heads of 65 to 128 elements that a CTA takes alone on its SM (`big`; units of 192 to 384 tokens) pay
-// more a unit, and cutting finds more places free: one sequence of 576 bf16 tokens on 8 kv heads 11.7 us whole against 9.7,
-// 5 of 1500 21.8 against 16.6, 8 of 1500 21.8 against 19.2, 12 of 1500 22.0 against 25.9; 5 of 700 13.4 against 14.4.
-__host__ __device__ constexpr bool attn_big(int dim, int nt) { return dim == 128 && nt == 2; }
-__host__ __device__ inline bool attn_whole(int64_t items, int64_t u, int64_t ctas, float unit_us, bool big) {
+__host__ __device__ inline bool attn_waves(float items, float u, float ctas, AttnTimes t) {
+    const float alone = t.alone * u, full = floorf(items / ctas), rest = items - full * ctas;
+    const float cut = items * u * (t.big ? fmaxf(t.bytes, t.alone / ctas) : t.bytes);
+    return 6.f + full * fmaxf(ctas * u * t.bytes, alone) + (rest > 0.f ? fmaxf(rest * u * t.bytes, alone) : 0.f) < 15.f + 1.06f * cut;
+}
+__host__ __device__ inline bool attn_whole(int64_t items, int64_t u, int64_t ctas, AttnTimes t) {
     if (items > 16 * ctas) return false;
-    if (big) {
-        if (u <= 2 || (u <= 4 && 4 * items >= ctas) || (u <= 8 && 5 * items >= 3 * ctas)) return true;
+    if (t.big) {
+        if (u <= 2 || (u <= 4 && 4 * items >= ctas) || (u <= 8 && 5 * items >= 3 * ctas && items <= ctas)) return true;
     } else if (u <= 3 || (u <= 8 && 4 * items >= ctas)) {
         return true;
     }
-    return u <= 32 && 5 * items >= 4 * ctas && attn_waves((float)items, (float)u, (float)ctas, unit_us);
+    return t.short_item(u) && 5 * items >= 4 * ctas && attn_waves((float)items, (float)u, (float)ctas, t);
 }
 
 // The same by the lengths themselves: `total` units, the longest item's u.
-__device__ inline bool attn_whole_now(uint32_t total, int64_t items, int64_t u, int64_t ctas, float unit_us, bool big) {
-    if (attn_whole(items, u, ctas, unit_us, big)) return true;
+__device__ inline bool attn_whole_now(uint32_t total, int64_t items, int64_t u, int64_t ctas, AttnTimes t) {
+    if (attn_whole(items, u, ctas, t)) return true;
     if (items > 16 * ctas || 5 * items < 4 * ctas) return false;
     const float full = (float)total / ((float)items * (float)u);  // 1: all as long
-    return full >= 0.9f ? attn_waves((float)items, (float)u, (float)ctas, unit_us) : full < 0.75f && u <= 32;
+    return full >= 0.9f ? attn_waves((float)items, (float)u, (float)ctas, t) : full < 0.75f && t.short_item(u);
 }
 
 // The line of all units is cut into runs of equal length, the first ones one unit longer; one CTA each. (A
@@ -110,7 +121,7 @@ struct AttnWork {
     int32_t unit;    // tokens of a unit
     int32_t whole;   // kAttnWhole: no item is cut; kAttnMaybe: by the lengths; 0: items may be cut
     int32_t ctas;    // CTAs that share the units where items may be cut
-    float unit_us;   // a unit's bytes at the memory's full rate
+    AttnTimes times;
     KvDivide divide;  // by the page size
     // the cache's strides in steps of 2^off_shift bytes, which divides them all
     uint32_t page_step, token_step, head_step, off_shift;

@@ -99,10 +99,10 @@ Layout layout_of(const AttnParams &P) {
     L.units = most;
     L.grid = (int)(most < ctas ? most : ctas);
     const int64_t items = (int64_t)P.seqs * L.w.groups;
-    L.w.unit_us = (float)L.w.unit * P.dim * 2 * size / 7.2e6f;
+    L.w.times = attn_times(P.fmt, L.w.dim, L.w.nt, L.w.unit, (int64_t)L.w.unit * P.dim * 2 * size);
     L.w.ctas = L.grid;
     // certain for the longest items that the tables can name: no second launch; else the kernel decides by the lengths
-    if (attn_whole(items, most / items, ctas, L.w.unit_us, attn_big(L.w.dim, L.w.nt))) L.w.whole = kAttnWhole;
+    if (attn_whole(items, most / items, ctas, L.w.times)) L.w.whole = kAttnWhole;
     else if (items <= 16 * ctas && 5 * items >= 4 * ctas) L.w.whole = kAttnMaybe;
     if (L.w.whole == kAttnWhole) L.grid = (int)items;
     if (L.w.whole == kAttnMaybe && items > L.grid) L.grid = (int)items;

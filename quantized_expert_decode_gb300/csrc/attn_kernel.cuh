@@ -238,7 +238,7 @@ __global__ void __launch_bounds__(T::kWarps * 32, T::kCtas) attn_stream_kernel(c
         int u = 0;
 #pragma unroll
         for (int i = 0; i < T::kWarps; i++) u = max(u, scan[16 + i]);
-        whole_mode = attn_whole_now(total, P.seqs * W.groups, u, W.ctas, W.unit_us, attn_big(DP, NT));
+        whole_mode = attn_whole_now(total, P.seqs * W.groups, u, W.ctas, W.times);
         if (whole_mode && blockIdx.x == 0 && tid == 0) W.cuts[0].runs = 0;  // nothing for the join
     }
 

@@ -264,7 +264,7 @@ extern "C" void layout(int fmt, int act, int dim, int heads, int kv_heads, int s
     P.window = window;
     P.cache = KvShape{(int64_t)kv_heads * page_size * dim, dim, (int64_t)page_size * dim, 1000, page_size};
     const Layout L = layout_of(P);
-    out[0] = L.w.unit, out[1] = L.w.unit_us, out[2] = L.w.whole, out[3] = L.grid, out[4] = (double)L.units;
+    out[0] = L.w.unit, out[1] = L.w.times.bytes, out[2] = L.w.whole, out[3] = L.grid, out[4] = (double)L.units;
 }
 ''')
     from quantized_expert_decode_gb300 import build
@@ -297,7 +297,8 @@ def test_long_items_of_wide_groups_are_cut(layout, fmt, act, unit):
     # from 3 units on, from 5 where a quarter of the places is taken, from 9 where most are
     for dim, heads in ((128, 128), (96, 72)):
         for seqs, units, whole in ((1, 2, 1), (1, 3, 0), (4, 3, 0), (5, 3, 1), (5, 4, 1), (5, 5, 0), (8, 4, 1), (8, 5, 0), (8, 8, 0),
-                                   (12, 5, 1), (12, 8, 1)):
+                                   (12, 5, 1), (12, 8, 1),
+                                   (20, 6, 0)):
             got = layout(fmt=fmt, act=act, dim=dim, heads=heads, seqs=seqs, page_size=unit, width=units)
             assert got["unit"] == unit and (got["whole"] == 1) == bool(whole), (dim, seqs, units)
     # others as they were
