@@ -115,8 +115,10 @@ size_t coli_attn_workspace_bytes(const coli_attn_desc *desc, const coli_kv_cache
  * are left out (and flagged); a length outside [0, table_width * page_size] is clamped (and flagged).
  * What the pages hold behind a sequence's end, before its window, or on pages that no table names
  * is never used, whatever its bits. The products of q and k and the sums are fp32 (q and p enter the
- * tensor cores as sums of 16-bit parts, so that fp32 activations keep 22 bits or more); scores,
- * maxima and sums of the softmax are fp32.
+ * tensor cores as sums of 16-bit parts, so that fp32 activations keep 22 bits or more; beside 16-bit activations
+ * p keeps 16 bits on a bf16 cache, 22 on the others); scores, maxima and sums of the softmax are fp32.
+ * Keys and values that are seen should be finite: an infinity among them may give NaN where the formula has
+ * an infinity or leaves a token out (the parts make it 0 times infinity).
  *   q [seqs][q_heads][dim], out alike, lse [seqs][q_heads] fp32 or NULL, lens [seqs] int32,
  *   table [seqs][table_width] int32 (entries behind a sequence's end are not read).
  * The same call gives the same bits: the split over the length and the order of its join are fixed

@@ -37,6 +37,8 @@
  *    kernel-detected conditions (no selectable expert, a misaligned routed-expert pointer,
  *    an expired bounded wait) set an error word in the workspace that coli_moe_check reads.
  *    route / forward calls clear that word when they start, so it reports the latest call.
+ *  - route and forward calls (not coli_moe_forward_host) can be captured into a graph; its replays,
+ *    like any other calls on the same workspace, must be ordered.
  *  - There is no CPU fallback: every step runs in this library's kernels.
  *  - Packed weight rows must start on 16-byte boundaries: H and I must be multiples of 16
  *    (int8), 32 (int4, int4-grouped) or 64 (int2), and every weight and scale pointer 16-byte aligned;

@@ -31,8 +31,9 @@
 // V^T P^T, where P^T comes from S^T's registers by an 8x8 transposition. K and V enter in the cache's
 // own type (e4m3 widened to f16, exactly). q and p are sums of parts in that type: a bf16 or f16 q
 // that the type holds is one part; an fp32 q is three bf16 parts or two f16 parts (scaled by a power of
-// two per head); p is two parts, or three in bf16 beside an fp32 q. Each tile's O is summed from zero
-// and added in fp32, so that the matrix unit's truncating accumulation never runs over more than a tile.
+// two per head); p is two parts, or three in bf16 beside an fp32 q (two bf16 parts leave 2^-17 of p, against the
+// 2^-9 or 2^-12 of the 16-bit output they are for; l is summed from p before it is split). Each tile's O is summed
+// from zero and added in fp32, so that the matrix unit's truncating accumulation never runs over more than a tile.
 #pragma once
 
 #include <atomic>
