@@ -126,7 +126,8 @@ def test_a_layer_that_the_attention_refuses_is_not_built(q, seqs, q_heads):
 
 def run_steps(mode, fmt, n, steps=6):
     """The outputs of some steps of a layer, the same layer and inputs for every mode: on the default stream, on a
-    side stream that is torch's current one, on a stream that is not, or replayed from a graph."""
+    side stream that is torch's current one, on a stream that is not (by its handle, the default one beside a side stream),
+    or replayed from a graph."""
     import synth
     from quantized_expert_decode_gb300.device import DeviceBlock
     from quantized_expert_decode_gb300.layer import DecodeLayer, PagedCache
@@ -144,7 +145,7 @@ def run_steps(mode, fmt, n, steps=6):
     lens = torch.zeros_like(pos)
     torch.cuda.synchronize()
     side, out, graph, y = torch.cuda.Stream(), [], None, None
-    with torch.cuda.stream(side if mode in ("current", "graph") else torch.cuda.default_stream()):
+    with torch.cuda.stream(side if mode in ("current", "graph", "zero") else torch.cuda.default_stream()):
         for i in range(steps):
             at = [cache.grow(s) for s in range(n)]
             torch.cuda._sleep(2_000_000)  # what does not wait for the current stream runs ahead of it
@@ -158,7 +159,8 @@ def run_steps(mode, fmt, n, steps=6):
             if graph is not None:
                 graph.replay()
             else:
-                y = layer.step(x, r, pos, lens, *((side,) if mode == "other" else ()))
+                given = {"other": (side,), "handle": (side.cuda_stream,), "zero": (0,)}.get(mode, ())
+                y = layer.step(x, r, pos, lens, *given)
             x.copy_(y)
             out.append((x.clone(), r.clone()))
         layer.check()
@@ -173,7 +175,7 @@ def test_steps_on_streams_and_in_graphs(q, fmt, n):
     # may move a cached value over a rounding border: an e4m3 step is 2^-3 of one element among 32). What is read too
     # early is off by the size of the values.
     want = run_steps("default", fmt, n)
-    for mode in ("current", "other", "graph"):
+    for mode in ("current", "other", "handle", "zero", "graph"):
         for i, (got, ref) in enumerate(zip(run_steps(mode, fmt, n), want)):
             for a, b in zip(got, ref):
                 assert float((a - b).abs().max()) <= 0.05 * float(b.square().mean().sqrt()), (mode, i)
