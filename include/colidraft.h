@@ -1,0 +1,160 @@
+/* colidraft.h — C ABI of libcolimoe, third part: a decoder's step on drafted tokens. Each sequence brings a
+ * chain or a tree of drafted tokens (nodes) behind its cached ones, the model sees all nodes in one pass, and
+ * the nodes that the target's probabilities accept stay in the cache.
+ *
+ *   coli_norm_append    norms of queries and keys per head, their rotation by position, and the append of keys
+ *                       and values at places of the paged cache that need not be the positions
+ *   coli_attn_tree      attention of every node to its sequence's cached tokens, its ancestors and itself
+ *   coli_draft_verify   which nodes are accepted, from given random numbers, and the token drawn behind them
+ *   coli_kv_compact     the cached rows of the accepted nodes move up behind the committed tokens
+ *   coli_kv_copy_pages  pages are copied (a fork of a sequence)
+ *
+ * Conventions are those of colimoe.h and colilayer.h: device memory, the caller owns every buffer, nothing is
+ * allocated, freed or synchronised inside a call, work is enqueued on `stream` on the current device (so every
+ * call can be captured into a graph), arguments are validated on the host before anything is launched, and the
+ * return value is COLI_MOE_OK or a COLI_MOE_E* code. Conditions that only the device can see never lead to an
+ * access; they set a bit of `err` (device int32, may be NULL), which coli_moe_check(err, stream) reads and clears.
+ *
+ * Nodes. Sequence b's nodes are the rows first[b] .. first[b+1]-1 (first [seqs + 1] int32, first[0] need not be 0)
+ * of every array that has a row per node; rows that no sequence names are left alone. parent[row] is the node's
+ * parent counted within its sequence (node 0 is the sequence's first row); parents come before their children,
+ * and -1 stands for a node behind the last committed token. parent NULL: a chain, each node behind the one before.
+ * A node's depth is 0 without a parent and its parent's depth + 1 otherwise. In the cache node i of sequence b lies
+ * at place past[b] + i, whatever its depth; its position is past[b] + depth.
+ * A sequence whose rows lie outside [0, rows) or are more than `nodes` is clamped to what there is
+ * (COLI_LAYER_BAD_SEQUENCE); a parent that is not -1 and not an earlier node counts as -1 (COLI_DRAFT_BAD_NODE). */
+#ifndef COLIDRAFT_H
+#define COLIDRAFT_H
+
+#include "colilayer.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/* a further bit of the error word, beside COLI_LAYER_* */
+#define COLI_DRAFT_BAD_NODE 8 /* a parent, a token or an entry of a path that cannot be */
+
+/* Append with norms: as coli_append_desc, and `eps` of the norms. */
+typedef struct {
+    int32_t tokens;      /* >= 1 */
+    int32_t q_heads;     /* heads of q; 0: no q */
+    int32_t seqs;        /* rows of the page table */
+    int32_t table_width; /* entries per row of the page table */
+    int32_t act;         /* COLI_ACT_* of q, k, v and q_out */
+    int32_t rotary;      /* leading elements of each head that are rotated: even, 0..dim */
+    int32_t interleaved; /* 1: pairs (2i, 2i+1); 0: pairs (i, i + rotary/2) */
+    float eps;           /* >= 0 */
+    int64_t q_stride, k_stride, v_stride, q_out_stride;
+} coli_norm_append_desc;
+
+/* For every token n, with b = seq[n] (seq NULL: b = n) and every head x of q[n] and k[n]:
+ *   x' = x * w / sqrt(mean(x^2) + eps),  w = q_norm or k_norm [dim] fp32 (NULL: x' = x)
+ *   the first `rotary` elements of x' are rotated pairwise by pos[n] * inv_freq[i], as coli_kv_append does
+ *   q_out[n] = q's heads, rounded once to q's type (q_out may be q itself)
+ *   place place[n] of sequence b in the cache = k's heads and v[n], rounded once to the cache's type
+ * in fp32. place NULL: place[n] = pos[n]. A position may be any int32 where place is given. seq[n] = -1 is padding: its q is
+ * normalised and rotated and nothing is cached. Two tokens must not name the same place. Other arguments as for
+ * coli_kv_append. */
+int coli_norm_append(const coli_norm_append_desc *desc, const coli_kv_cache *cache, const void *q, const void *k,
+                     const void *v, const float *q_norm, const float *k_norm, const float *inv_freq,
+                     const int32_t *seq, const int32_t *pos, const int32_t *place, const int32_t *table, void *q_out,
+                     int32_t *err, coli_stream_t stream);
+
+/* Attention of nodes. */
+typedef struct {
+    int32_t seqs;        /* 1..1024 */
+    int32_t rows;        /* rows of q, out, lse and parent, >= 1 */
+    int32_t nodes;       /* of a sequence at most, 1..256 */
+    int32_t q_heads;     /* a multiple of cache->heads, <= 1024; head h reads kv head h / (q_heads / heads) */
+    int32_t table_width; /* entries per row of the page table; table_width * page_size < 2^31 */
+    int32_t act;         /* COLI_ACT_* of q and out */
+    int32_t window;      /* > 0: a node at position p sees positions > p - window; 0: all */
+    float scale;         /* factor of q . k, usually 1 / sqrt(dim); finite */
+    int64_t q_stride, out_stride; /* elements from one row to the next; 0: q_heads * dim */
+} coli_tree_desc;
+
+/* Bytes of device workspace (256-byte aligned) coli_attn_tree needs; 0 if a description is invalid. The workspace needs
+ * no preparation and may be shared with other calls on one stream. */
+size_t coli_tree_workspace_bytes(const coli_tree_desc *desc, const coli_kv_cache *cache);
+
+/* For node i of sequence b (row r = first[b] + i) and head h, over the cached places t < past[b] and the places
+ * past[b] + j of i's ancestors j and of i itself, within the window:
+ *   s_t = scale * q[r][h] . k_t,  p = softmax(s),  out[r][h] = sum_t p_t v_t,  lse[r][h] = ln(sum_t exp(s_t))
+ * out is rounded once to q's type. The keys and values of the nodes are in the cache before the call (coli_norm_append).
+ * A row that sees nothing (its pages are bad) gives out = 0 and lse = -inf. Tokens whose page number is outside the pool
+ * are left out (and flagged); past[b] is clamped to [0, table_width * page_size - nodes of b] (and flagged); a
+ * sequence with more nodes than the table has places keeps those that fit. What the pages hold behind a sequence's
+ * nodes, before its window, at nodes that a row does not see, or on pages that no table names does not reach a row,
+ * whatever its bits. Precision is that of coli_attn_decode; keys and values that are seen should be finite.
+ *   q [rows][q_heads][dim], out alike, lse [rows][q_heads] fp32 or NULL, first [seqs + 1], past [seqs], parent [rows] or
+ *   NULL, table [seqs][table_width] int32 (entries behind a sequence's nodes are not read).
+ * The same call gives the same bits. */
+int coli_attn_tree(const coli_tree_desc *desc, const coli_kv_cache *cache, const void *q, const int32_t *first,
+                   const int32_t *past, const int32_t *parent, const int32_t *table, void *out, float *lse, int32_t *err,
+                   void *ws, size_t ws_bytes, coli_stream_t stream);
+
+/* how nodes are verified */
+#define COLI_VERIFY_SAMPLE 0 /* by random numbers: the tokens are distributed as the target's own samples */
+#define COLI_VERIFY_GREEDY 1 /* by the target's largest entry */
+
+/* Verification. Rows of target and draft start *_stride elements apart; 0 stands for vocab. */
+typedef struct {
+    int32_t seqs;  /* 1..65535 */
+    int32_t rows;  /* rows of target, draft, tokens, parent and uniform, >= 1 */
+    int32_t nodes; /* of a sequence at most, 1..1024; entries of a row of path */
+    int32_t vocab; /* 1..2^20 */
+    int32_t act;   /* COLI_ACT_* of target and draft */
+    int32_t mode;  /* COLI_VERIFY_* */
+    int64_t target_stride, draft_stride;
+} coli_verify_desc;
+
+/* Node 0 of every sequence is its last committed token (the root): it is not tested. target[row] is the target's
+ * distribution behind that node (COLI_VERIFY_GREEDY: any scores, logits too), draft[row] the distribution that the
+ * tokens of its children were drawn from, tokens[row] the node's own token. From the root, at each accepted node c, its
+ * children x_1, x_2, ... are tested in the order of their rows:
+ *   with a draft, u_j = uniform[x_j's row] in [0, 1):
+ *     r_1 = target[c];  x_j is accepted if u_j * draft[c][x_j] < r_j[x_j] / m_j, with m_1 = 1 and m_j = sum(r_j);
+ *     otherwise r_{j+1} = max(r_j - m_j * draft[c], 0)
+ *   without a draft (NULL; the tokens were not drawn at random):
+ *     accepted if u_j * m_j < r_j[x_j]; otherwise r_{j+1} = r_j without x_j
+ *   COLI_VERIFY_GREEDY: accepted if x_j is the index of the largest entry of target[c] (the lowest of several; a NaN is
+ *     below all numbers). draft and uniform are NULL.
+ * The first accepted child becomes c. Where none is, the next token is the smallest y with
+ * r[0] + ... + r[y] > uniform[root's row] * sum(r), r what the last test at c left (target[c] where nothing is left);
+ * greedy: the index of c's largest entry.
+ * target and draft are finite and not negative, with rows that sum to 1 up to rounding. Sums and tests carry
+ * 45 bits or more, so that with fp32 inputs hardly ever a number falls on another side than in exact arithmetic.
+ *   path [seqs][nodes] int32: the accepted nodes in order, the root (0) first, -1 behind them; count [seqs]: how many;
+ *   next [seqs]: the token drawn behind the last. A sequence without rows gets count 0 and next -1.
+ * A node whose token is outside [0, vocab) is not accepted (COLI_DRAFT_BAD_NODE). */
+int coli_draft_verify(const coli_verify_desc *desc, const void *target, const void *draft, const int32_t *tokens,
+                      const int32_t *parent, const float *uniform, const int32_t *first, int32_t *path, int32_t *count,
+                      int32_t *next, int32_t *err, coli_stream_t stream);
+
+/* Compaction. */
+typedef struct {
+    int32_t seqs;        /* 1..65535 */
+    int32_t nodes;       /* entries of a row of path, >= 1 */
+    int32_t table_width; /* entries per row of the page table; table_width * page_size < 2^31 */
+    int32_t layers;      /* 1..4096 */
+} coli_compact_desc;
+
+/* For every layer (caches [layers], HOST array: pools of the same type, shape and strides under one page table), every
+ * sequence b and i = 1 .. count[b]-1: the row of K and of V at place past[b] + path[b][i] moves to place past[b] + i. path[b]
+ * must ascend and its entry i must not be below i (as coli_draft_verify gives it); entries that do not are not moved
+ * (COLI_DRAFT_BAD_NODE), nor are entries whose pages are bad (flagged). count[b] <= 1 moves nothing, a larger count than
+ * `nodes` is clamped (and flagged). Scales of e4m3 pools play no part. */
+int coli_kv_compact(const coli_compact_desc *desc, const coli_kv_cache *caches, const int32_t *past,
+                    const int32_t *path, const int32_t *count, const int32_t *table, int32_t *err, coli_stream_t stream);
+
+/* Pages dst[i] = pages src[i], i < n, of K and V of every layer (caches as above). A pair with a -1 is skipped, one with
+ * another page number outside the pool is skipped and flagged. No page may be the dst of two pairs, or the dst of one and
+ * the src of another. src, dst [n] int32, n >= 1, layers in 1..4096. */
+int coli_kv_copy_pages(const coli_kv_cache *caches, int32_t layers, int32_t n, const int32_t *src, const int32_t *dst,
+                       int32_t *err, coli_stream_t stream);
+
+#ifdef __cplusplus
+}
+#endif
+#endif /* COLIDRAFT_H */

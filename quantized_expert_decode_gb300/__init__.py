@@ -1,4 +1,5 @@
-"""Python binding of libcolimoe (include/colimoe.h, include/colilayer.h): argument marshalling only.
+"""Python binding of libcolimoe (include/colimoe.h, include/colilayer.h, include/colidraft.h): argument
+marshalling only.
 
 Every function here has the name of the C entry point it calls and passes device pointers
 (ints, or torch tensors whose data_ptr() is taken) and a CUDA stream handle straight through.
@@ -40,6 +41,14 @@ COLI_LAYER_BAD_PAGE, COLI_LAYER_BAD_POSITION, COLI_LAYER_BAD_SEQUENCE = 1, 2, 4
 
 # every symbol include/colilayer.h declares
 LAYER_EXPORTS = ("coli_kv_append", "coli_attn_workspace_bytes", "coli_attn_decode", "coli_block_norms")
+
+# include/colidraft.h: a step on drafted tokens
+COLI_DRAFT_BAD_NODE = 8
+COLI_VERIFY_SAMPLE, COLI_VERIFY_GREEDY = 0, 1
+
+# every symbol include/colidraft.h declares
+DRAFT_EXPORTS = ("coli_norm_append", "coli_tree_workspace_bytes", "coli_attn_tree", "coli_draft_verify",
+                 "coli_kv_compact", "coli_kv_copy_pages")
 
 
 class coli_moe_desc(ctypes.Structure):
@@ -85,6 +94,32 @@ class coli_norms_desc(ctypes.Structure):
                 ("y_stride", ctypes.c_int64), ("resid_stride", ctypes.c_int64),
                 ("gate_stride", ctypes.c_int64), ("resid_out_stride", ctypes.c_int64),
                 ("xn_stride", ctypes.c_int64)]
+
+
+class coli_norm_append_desc(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int32), ("q_heads", ctypes.c_int32), ("seqs", ctypes.c_int32),
+                ("table_width", ctypes.c_int32), ("act", ctypes.c_int32), ("rotary", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64),
+                ("v_stride", ctypes.c_int64), ("q_out_stride", ctypes.c_int64)]
+
+
+class coli_tree_desc(ctypes.Structure):
+    _fields_ = [("seqs", ctypes.c_int32), ("rows", ctypes.c_int32), ("nodes", ctypes.c_int32),
+                ("q_heads", ctypes.c_int32), ("table_width", ctypes.c_int32), ("act", ctypes.c_int32),
+                ("window", ctypes.c_int32), ("scale", ctypes.c_float), ("q_stride", ctypes.c_int64),
+                ("out_stride", ctypes.c_int64)]
+
+
+class coli_verify_desc(ctypes.Structure):
+    _fields_ = [("seqs", ctypes.c_int32), ("rows", ctypes.c_int32), ("nodes", ctypes.c_int32),
+                ("vocab", ctypes.c_int32), ("act", ctypes.c_int32), ("mode", ctypes.c_int32),
+                ("target_stride", ctypes.c_int64), ("draft_stride", ctypes.c_int64)]
+
+
+class coli_compact_desc(ctypes.Structure):
+    _fields_ = [("seqs", ctypes.c_int32), ("nodes", ctypes.c_int32), ("table_width", ctypes.c_int32),
+                ("layers", ctypes.c_int32)]
 
 
 class ColiMoeError(RuntimeError):
@@ -138,6 +173,18 @@ def _load():
     lib.coli_attn_decode.restype = ctypes.c_int
     lib.coli_block_norms.argtypes = [ctypes.POINTER(coli_norms_desc), P, P, P, P, P, P, P, P]
     lib.coli_block_norms.restype = ctypes.c_int
+    lib.coli_norm_append.argtypes = [ctypes.POINTER(coli_norm_append_desc), C] + [P] * 13
+    lib.coli_norm_append.restype = ctypes.c_int
+    lib.coli_tree_workspace_bytes.argtypes = [ctypes.POINTER(coli_tree_desc), C]
+    lib.coli_tree_workspace_bytes.restype = SZ
+    lib.coli_attn_tree.argtypes = [ctypes.POINTER(coli_tree_desc), C] + [P] * 9 + [SZ, P]
+    lib.coli_attn_tree.restype = ctypes.c_int
+    lib.coli_draft_verify.argtypes = [ctypes.POINTER(coli_verify_desc)] + [P] * 11
+    lib.coli_draft_verify.restype = ctypes.c_int
+    lib.coli_kv_compact.argtypes = [ctypes.POINTER(coli_compact_desc), C] + [P] * 6
+    lib.coli_kv_compact.restype = ctypes.c_int
+    lib.coli_kv_copy_pages.argtypes = [C, I32, I32] + [P] * 4
+    lib.coli_kv_copy_pages.restype = ctypes.c_int
     lib.coli_moe_last_cuda_error.argtypes = []
     lib.coli_moe_last_cuda_error.restype = ctypes.c_int
     return lib
@@ -350,3 +397,74 @@ def coli_block_norms(desc, y, resid, post_w, gate, pre_w, resid_out, xn, stream=
         rc = _block_norms(_byref(desc), _ptr(y), _ptr(resid), _ptr(post_w), _ptr(gate), _ptr(pre_w), _ptr(resid_out),
                           _ptr(xn), _stream(stream))
     return _check(rc, "coli_block_norms", raise_on_error) if rc else rc
+
+
+# ---------------------------------------------------------------- a step on drafted tokens
+def make_norm_append_desc(tokens, q_heads, seqs, table_width, act=COLI_ACT_F32, rotary=0, interleaved=False, eps=0.0,
+                          q_stride=0, k_stride=0, v_stride=0, q_out_stride=0):
+    return coli_norm_append_desc(tokens, q_heads, seqs, table_width, act, rotary, int(interleaved), eps, q_stride,
+                                 k_stride, v_stride, q_out_stride)
+
+
+def make_tree_desc(seqs, rows, nodes, q_heads, table_width, act, scale, window=0, q_stride=0, out_stride=0):
+    return coli_tree_desc(seqs, rows, nodes, q_heads, table_width, act, window, scale, q_stride, out_stride)
+
+
+def make_verify_desc(seqs, rows, nodes, vocab, act=COLI_ACT_F32, mode=COLI_VERIFY_SAMPLE, target_stride=0,
+                     draft_stride=0):
+    return coli_verify_desc(seqs, rows, nodes, vocab, act, mode, target_stride, draft_stride)
+
+
+def make_compact_desc(seqs, nodes, table_width, layers=1):
+    return coli_compact_desc(seqs, nodes, table_width, layers)
+
+
+def make_kv_caches(caches):
+    """The caches of several layers as the array that coli_kv_compact and coli_kv_copy_pages take."""
+    caches = list(caches)
+    return (coli_kv_cache * len(caches))(*caches)
+
+
+_norm_append, _attn_tree, _draft_verify = _lib.coli_norm_append, _lib.coli_attn_tree, _lib.coli_draft_verify
+
+
+def coli_norm_append(desc, cache, q, k, v, q_norm, k_norm, inv_freq, seq, pos, place, table, q_out, err=None, stream=None,
+                     raise_on_error=True):
+    rc = _norm_append(_byref(desc), _byref(cache), _ptr(q), _ptr(k), _ptr(v), _ptr(q_norm), _ptr(k_norm), _ptr(inv_freq),
+                      _ptr(seq), _ptr(pos), _ptr(place), _ptr(table), _ptr(q_out), _ptr(err), _stream(stream))
+    return _check(rc, "coli_norm_append", raise_on_error) if rc else rc
+
+
+def coli_tree_workspace_bytes(desc, cache) -> int:
+    return int(_lib.coli_tree_workspace_bytes(ctypes.byref(desc), ctypes.byref(cache)))
+
+
+def coli_attn_tree(desc, cache, q, first, past, parent, table, out, lse=None, err=None, ws=None, ws_bytes=0, stream=None,
+                   raise_on_error=True):
+    rc = _attn_tree(_byref(desc), _byref(cache), _ptr(q), _ptr(first), _ptr(past), _ptr(parent), _ptr(table), _ptr(out),
+                    _ptr(lse), _ptr(err), _ptr(ws), ws_bytes, _stream(stream))
+    return _check(rc, "coli_attn_tree", raise_on_error) if rc else rc
+
+
+def coli_draft_verify(desc, target, draft, tokens, parent, uniform, first, path, count, next, err=None, stream=None,
+                      raise_on_error=True):
+    rc = _draft_verify(_byref(desc), _ptr(target), _ptr(draft), _ptr(tokens), _ptr(parent), _ptr(uniform), _ptr(first),
+                       _ptr(path), _ptr(count), _ptr(next), _ptr(err), _stream(stream))
+    return _check(rc, "coli_draft_verify", raise_on_error) if rc else rc
+
+
+def coli_kv_compact(desc, caches, past, path, count, table, err=None, stream=None, raise_on_error=True):
+    """caches: make_kv_caches(...) of desc.layers caches."""
+    if len(caches) < desc.layers:
+        raise ValueError("fewer caches than layers")
+    rc = _lib.coli_kv_compact(_byref(desc), caches, _ptr(past), _ptr(path), _ptr(count), _ptr(table), _ptr(err),
+                              _stream(stream))
+    return _check(rc, "coli_kv_compact", raise_on_error) if rc else rc
+
+
+def coli_kv_copy_pages(caches, layers, n, src, dst, err=None, stream=None, raise_on_error=True):
+    """caches: make_kv_caches(...) of `layers` caches."""
+    if len(caches) < layers:
+        raise ValueError("fewer caches than layers")
+    rc = _lib.coli_kv_copy_pages(caches, layers, n, _ptr(src), _ptr(dst), _ptr(err), _stream(stream))
+    return _check(rc, "coli_kv_copy_pages", raise_on_error) if rc else rc

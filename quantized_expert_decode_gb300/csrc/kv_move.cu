@@ -1,0 +1,146 @@
+// kv_move.cu — rows of accepted nodes moved up behind a sequence's committed tokens, and copies of whole pages, for all
+// layers of a model in one launch (of up to 64).
+//
+// What bounds it: bytes, each read and written once; a single sequence's rows take one round of dependent loads (path,
+// page numbers, rows) and little else.
+#include "act.cuh"
+#include "draft.h"
+#include "host.h"
+#include "pdl.cuh"
+
+namespace colimoe {
+namespace {
+
+constexpr int kThreads = 128;
+constexpr int kMoves = 256;  // moves whose places are held at once
+constexpr int kDeep = 8;     // rows of a thread on their way
+
+// A CTA: K or V of one layer, one sequence, and 16-byte columns of its rows (all kv heads). A thread reads kDeep rows
+// of its column before it writes them. A move goes to a place that is not behind its own source, and sources ascend, so
+// no write reaches a row that the same thread reads later; other threads have other columns.
+__global__ void __launch_bounds__(kThreads) kv_compact_kernel(const CompactParams P, const __grid_constant__ Pools pools) {
+    __shared__ int64_t from[kMoves], to[kMoves];
+    wait_for_previous();
+    let_next_start();
+    const int b = blockIdx.y, layer = blockIdx.z >> 1;
+    char *pool = (char *)((blockIdx.z & 1) ? pools.v[layer] : pools.k[layer]);
+    int n = P.count[b], flags = 0;
+    if (n > P.nodes) {
+        n = P.nodes;
+        flags = COLI_DRAFT_BAD_NODE;
+    }
+    const int past = P.past[b];
+    const int32_t *path = P.path + (int64_t)b * P.nodes, *pages = P.table + (int64_t)b * P.table_width;
+    const int per_head = P.row_bytes / 16, columns = P.heads * per_head;
+    const int col = blockIdx.x * kThreads + threadIdx.x;
+    const int head = col / per_head;
+    char *base = pool + (int64_t)head * P.cache.head_stride * P.elem_bytes + (col - head * per_head) * 16;
+    for (int i0 = 1; i0 < n; i0 += kMoves) {
+        const int m = min(kMoves, n - i0);
+        __syncthreads();
+        for (int k = threadIdx.x; k < m; k += kThreads) {
+            const int i = i0 + k, node = path[i];
+            int64_t f = -1, t = -1;
+            if (node < i || node <= path[i - 1] || past < 0 || (int64_t)past + node > INT32_MAX) {
+                flags |= past < 0 ? COLI_LAYER_BAD_POSITION : COLI_DRAFT_BAD_NODE;
+            } else if (node != i) {
+                int wf, wt;
+                f = kv_row(P.cache, pages, P.table_width, past + node, 0, wf);
+                t = kv_row(P.cache, pages, P.table_width, past + i, 0, wt);
+                const int why = wf ? wf : wt;
+                if (why) {
+                    f = -1;
+                    flags |= why == kKvBadPage ? COLI_LAYER_BAD_PAGE : COLI_LAYER_BAD_POSITION;
+                }
+            }
+            from[k] = f;
+            to[k] = t;
+        }
+        __syncthreads();
+        if (col >= columns) continue;
+        for (int k0 = 0; k0 < m; k0 += kDeep) {
+            uint4 row[kDeep];
+#pragma unroll
+            for (int k = 0; k < kDeep; k++)
+                if (k0 + k < m && from[k0 + k] >= 0) row[k] = *(const uint4 *)(base + from[k0 + k] * P.elem_bytes);
+#pragma unroll
+            for (int k = 0; k < kDeep; k++)
+                if (k0 + k < m && from[k0 + k] >= 0) *(uint4 *)(base + to[k0 + k] * P.elem_bytes) = row[k];
+        }
+    }
+    if (flags && P.err && blockIdx.x == 0 && blockIdx.z == 0) atomicOr(P.err, flags);
+}
+
+// Whole pages. A CTA moves kUnroll * kThreads columns of 16 bytes of one page (K or V of a layer). kFlat: a page lies in one
+// piece.
+constexpr int kUnroll = 8;
+template <bool kFlat>
+__global__ void __launch_bounds__(kThreads) kv_copy_kernel(const CopyParams P, const __grid_constant__ Pools pools) {
+    wait_for_previous();
+    let_next_start();
+    const int pair = blockIdx.y, layer = blockIdx.z >> 1;
+    const int src = P.src[pair], dst = P.dst[pair];
+    if (src == -1 || dst == -1) return;
+    if ((uint32_t)src >= (uint32_t)P.cache.pages || (uint32_t)dst >= (uint32_t)P.cache.pages) {
+        if (threadIdx.x == 0 && blockIdx.x == 0 && blockIdx.z == 0 && P.err) atomicOr(P.err, COLI_LAYER_BAD_PAGE);
+        return;
+    }
+    char *pool = (char *)((blockIdx.z & 1) ? pools.v[layer] : pools.k[layer]);
+    const int64_t page = P.cache.page_stride * P.elem_bytes;
+    const char *s = pool + src * page;
+    char *d = pool + dst * page;
+    const int per_row = P.row_bytes / 16;
+    const int64_t columns = (int64_t)P.heads * P.cache.page_size * per_row;
+    const int64_t c0 = (int64_t)blockIdx.x * (kUnroll * kThreads) + threadIdx.x;
+    int64_t off[kUnroll];
+    uint4 v[kUnroll];
+#pragma unroll
+    for (int i = 0; i < kUnroll; i++) {
+        const int64_t c = c0 + i * kThreads;
+        if (c >= columns) continue;
+        if (kFlat) {
+            off[i] = c * 16;
+        } else {
+            const int64_t row = c / per_row;
+            const int slot = (int)(row / P.heads), head = (int)(row - (int64_t)slot * P.heads);
+            off[i] = (slot * P.cache.token_stride + head * P.cache.head_stride) * P.elem_bytes + (c - row * per_row) * 16;
+        }
+        v[i] = *(const uint4 *)(s + off[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < kUnroll; i++)
+        if (c0 + i * kThreads < columns) *(uint4 *)(d + off[i]) = v[i];
+}
+
+}  // namespace
+
+cudaError_t launch_kv_compact(const CompactParams &P, const Pools &pools, cudaStream_t s) {
+    const int columns = P.heads * (P.row_bytes / 16);
+    const dim3 grid((columns + kThreads - 1) / kThreads, P.seqs, 2 * P.layers);
+    return launch_overlapped(kv_compact_kernel, grid, kThreads, 0, s, P, pools);
+}
+
+cudaError_t launch_kv_copy(const CopyParams &P, const Pools &pools, cudaStream_t s) {
+    const KvShape &c = P.cache;
+    const int64_t dim = P.row_bytes / P.elem_bytes;
+    // (an axis of one entry has no stride to speak of)
+    const bool slots_in = (c.page_size == 1 || c.token_stride == dim) && (P.heads == 1 || c.head_stride == c.page_size * dim);
+    const bool heads_in = (P.heads == 1 || c.head_stride == dim) && (c.page_size == 1 || c.token_stride == P.heads * dim);
+    const int64_t columns = (int64_t)P.heads * c.page_size * (P.row_bytes / 16);
+    const int64_t parts = (columns + kUnroll * kThreads - 1) / (kUnroll * kThreads);
+    if (parts > INT32_MAX) return cudaErrorInvalidValue;
+    constexpr int kMost = 65535;
+    for (int at = 0; at < P.n; at += kMost) {
+        CopyParams part = P;
+        part.n = P.n - at < kMost ? P.n - at : kMost;
+        part.src = P.src + at;
+        part.dst = P.dst + at;
+        const dim3 grid((unsigned)parts, part.n, 2 * P.layers);
+        const cudaError_t e = slots_in || heads_in ? launch_overlapped(kv_copy_kernel<true>, grid, kThreads, 0, s, part, pools)
+                                                   : launch_overlapped(kv_copy_kernel<false>, grid, kThreads, 0, s, part, pools);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
+}
+
+}  // namespace colimoe

@@ -1,0 +1,1063 @@
+"""A step on drafted tokens (include/colidraft.h) against its definitions in 64 bits, on a GPU.
+
+Tolerances. u = 2^-24 is the relative error of one fp32 rounding; an output rounded to type t adds
+finfo(t).eps / 2 of its value (and, below its normal range, half its smallest step).
+
+  append   the rotation as in the tests of coli_kv_append: (2 pi 2^-24 + 3 u) (|a| + |b|). A norm's sum of at most 256
+           squares goes through at most 17 roundings of positive terms (16 of a lane's, 5 of the lanes'), of which half
+           reach the factor; the division, eps, the inverse square root (2 ulp) and two products: 32 u of each element.
+  tree     a score is q . k in fp32 partial sums of 16 products: at most 3 (dim / 16) + 4 roundings, each by a
+           truncation (2 u), of A = scale * sum |q_i k_i|, the 22 bits kept of q another 2^-22 A, and the step to base 2
+           8 u |s|. p is off by that relatively, numerator and denominator both; the sums over the tokens go
+           through at most 64 + tokens / 64 roundings; p in parts keeps 16 bits (16-bit activations on a bf16 cache) or
+           22 bits (all others).
+  verify   whole numbers: equal. Random inputs come within 2^-40 of a border with a chance of 2^-40 times the tokens.
+  moves    copies: equal bits."""
+import math
+
+import numpy as np
+import pytest
+import torch
+from test_layer_gpu import ACT, KV, U, Cache, close, err_word, half_ulp, randn, rotate64
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def q():
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+    import quantized_expert_decode_gb300 as q
+    return q
+
+
+def ints(*x):
+    return torch.tensor(*x, dtype=torch.int32, device="cuda")
+
+
+# ------------------------------------------------------------------------------------ append
+def norm64(x, w, eps):
+    x = x.double()
+    return x if w is None else x * w.double() / (x.square().mean(-1, keepdim=True) + eps).sqrt()
+
+
+def check_append(q, rng, act="f32", kv="bf16", heads=(8, 2), dim=64, rot=64, interleaved=False, page=16, layout="hnd",
+                 seq=(0, 0, 1, 2), pos=(5, 6, 31, 0), place=(7, 6, 40, 3), pad=0, offset=0, base=1e4, norms=(True, True), eps=1e-6,
+                 inplace=False, scales=True):
+    code, dtype = ACT[act]
+    n, (qh, kh) = len(seq), heads
+    at = pos if place is None else place
+    seqs, width = max(max(seq) + 1, 1), max(at) // page + 1
+    c = Cache(q, rng, kv, seqs * min(width, 4) + 3, page, kh, dim, layout, scales)
+    table = torch.from_numpy(rng.integers(0, c.pages, (seqs, width)).astype(np.int32))
+    free = list(rng.permutation(c.pages))
+    page_of = {}
+    for b, p in zip(seq, at):
+        if b >= 0 and (b, p // page) not in page_of:
+            page_of[b, p // page] = int(free.pop())
+            table[b, p // page] = page_of[b, p // page]
+    table = table.cuda()
+    # one fused buffer [token][q heads, k heads, v heads], its rows padded and shifted
+    row = (qh + 2 * kh) * dim + pad
+    buf = (randn(rng, n * row + offset) * 3).to(dtype)
+    x = buf[offset:].view(n, row)
+    parts = [x[:, :qh * dim], x[:, qh * dim:(qh + kh) * dim], x[:, (qh + kh) * dim:(qh + 2 * kh) * dim]]
+    xq, xk, xv = (p.unflatten(1, (-1, dim)).clone() if p.shape[1] else p.reshape(n, 0, dim) for p in parts)
+    w = torch.from_numpy(rng.uniform(0.5, 1.5, (2, dim + 1)).astype(np.float32)).cuda()
+    # (the second weights start 4 bytes off a 16-byte boundary where the width is odd)
+    wq, wk = (w[i, :dim] if use else None for i, use in enumerate(norms))
+    if not qh:
+        wq = None
+    inv = torch.from_numpy((base ** (-np.arange(0, rot, 2) / max(rot, 1))).astype(np.float32)).cuda()
+    tpos, tseq = ints(pos), ints(seq)
+    qo = parts[0] if inplace else torch.full((n, qh, dim), float("nan"), dtype=dtype, device="cuda")
+    err = err_word()
+    before = [c.k.clone(), c.v.clone()]
+    d = q.make_norm_append_desc(n, qh, seqs, width, code, rot, interleaved, eps, row, row, row, row if inplace else 0)
+    q.coli_norm_append(d, c.desc, parts[0] if qh else None, parts[1], parts[2], wq, wk, inv if rot else None, tseq, tpos,
+                       None if place is None else ints(place), table, qo if qh else None, err)
+    assert q.coli_moe_check(err) == q.COLI_MOE_OK
+    angle = 2 * math.pi * 2.0 ** -24
+    if qh:
+        want, mag = rotate64(norm64(xq, wq, eps), tpos, inv, rot, interleaved)
+        mag = torch.maximum(mag, want.abs())
+        close(qo.reshape(n, qh, dim), want, half_ulp(want, dtype) + (angle + 35 * U) * mag)
+    keep = [i for i in range(n) if seq[i] >= 0]
+    pg = torch.tensor([page_of[seq[i], at[i] // page] for i in keep], dtype=torch.long, device="cuda")
+    sl = torch.tensor([at[i] % page for i in keep], dtype=torch.long, device="cuda")
+    want, mag = rotate64(norm64(xk, wk, eps), tpos, inv, rot, interleaved)
+    mag = torch.maximum(mag, want.abs())
+    f = c.factor(0)[None, :, None]
+    want, mag = want[keep] / f, mag[keep] / f
+    got = c.rows(0, pg, sl)
+    lim = 448.0 if kv == "e4m3" else math.inf
+    close(got, want.clamp(-lim, lim), half_ulp(want, c.dtype) + (angle + 36 * U) * mag * (1 + torch.finfo(c.dtype).eps))
+    # values are only converted: the same bits as one rounding
+    fv = c.factor(1).float()[None, :, None]
+    assert torch.equal(c.v[pg, :, sl], c.bits(xv.float()[keep] / fv))
+    # and nothing else has changed
+    for now, was in zip((c.k, c.v), before):
+        was[pg, :, sl] = now[pg, :, sl]
+        assert torch.equal(now, was)
+
+
+@pytest.mark.parametrize("act", sorted(ACT))
+@pytest.mark.parametrize("kv", sorted(KV))
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("norms", [(True, True), (False, True), (False, False)])
+def test_append_types(q, act, kv, interleaved, norms):
+    check_append(q, np.random.default_rng(1), act, kv, interleaved=interleaved, norms=norms)
+
+
+@pytest.mark.parametrize("dim,rot", [(16, 16), (80, 80), (80, 40), (96, 48), (128, 64), (256, 256), (128, 0), (128, 2), (128, 126),
+                                     (8, 8), (24, 8), (256, 2), (72, 72)])
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("act", ["f32", "bf16"])
+def test_append_head_sizes(q, dim, rot, interleaved, act):
+    check_append(q, np.random.default_rng(2), act, dim=dim, rot=rot, interleaved=interleaved)
+
+
+@pytest.mark.parametrize("layout", ["hnd", "nhd", "hpn"])
+@pytest.mark.parametrize("page", [1, 3, 16, 24])
+def test_append_pages(q, layout, page):
+    check_append(q, np.random.default_rng(3), page=page, layout=layout)
+
+
+@pytest.mark.parametrize("pad,offset", [(0, 0), (8, 0), (4, 4), (1, 0), (0, 1), (3, 5)])
+@pytest.mark.parametrize("act", ["f32", "f16"])
+@pytest.mark.parametrize("inplace", [False, True])
+def test_append_strides_and_alignment(q, pad, offset, act, inplace):
+    check_append(q, np.random.default_rng(4), act, pad=pad, offset=offset, inplace=inplace)
+
+
+def test_append_places_are_not_positions(q):
+    # positions beyond any table, places before them; branches of one depth share a position
+    top = 2 ** 31 - 1
+    check_append(q, np.random.default_rng(5), dim=128, rot=128, base=1e6, seq=(0, 0, 0, 0), pos=(200000, 200001, 200001, top),
+                 place=(0, 1, 2, 3))
+    check_append(q, np.random.default_rng(6), seq=(0, 1, 2, 3), pos=(5, 6, 31, 0), place=None)
+
+
+def test_append_padding_and_no_queries(q):
+    check_append(q, np.random.default_rng(7), seq=(0, -1, 1, -1), place=(7, 0, 40, 0))
+    check_append(q, np.random.default_rng(8), heads=(0, 3), norms=(False, True), scales=False, kv="e4m3")
+
+
+@pytest.mark.parametrize("act,heads,dim", [("f32", (48, 8), 128), ("bf16", (5, 1), 80), ("f16", (64, 8), 64)])
+def test_append_many_tokens(q, act, heads, dim):
+    n = 2500
+    seq = tuple(i % 7 for i in range(n))
+    place = tuple(i // 7 for i in range(n))
+    pos = tuple(p // 2 for p in place)
+    check_append(q, np.random.default_rng(9), act, heads=heads, dim=dim, rot=dim, seq=seq, pos=pos, place=place, page=128)
+
+
+@pytest.mark.parametrize("value", [0.0, 1e-30, 1e18])
+def test_append_norms_of_small_and_large_heads(q, value):
+    # the squares of 1e18 fit fp32, those of 1e-30 vanish beside eps
+    rng = np.random.default_rng(10)
+    c = Cache(q, rng, "bf16", 4, 16, 1, 64)
+    x = torch.full((1, 64), value, device="cuda")
+    w = torch.ones(64, device="cuda")
+    out = torch.full((1, 64), float("nan"), device="cuda")
+    q.coli_norm_append(q.make_norm_append_desc(1, 1, 1, 1, eps=1e-6), c.desc, x, x, x, w, w, None, None, ints([0]), None, ints([[2]]),
+                       out)
+    want = norm64(x, w, 1e-6)
+    close(out, want, want.abs() * 32 * U)
+
+
+def test_append_without_norms_is_coli_kv_append(q):
+    for act, kv, dim, rot, inter in (("f32", "bf16", 128, 128, False), ("bf16", "e4m3", 128, 64, True), ("f16", "f16", 80, 40, False)):
+        got = []
+        for normed in (False, True):
+            rng = np.random.default_rng(11)
+            c = Cache(q, rng, kv, 40, 16, 4, dim)
+            n = 50
+            x = [(randn(rng, n, h * dim) * 3).to(ACT[act][1]) for h in (16, 4, 4)]
+            inv = (1e4 ** (-torch.arange(0, rot, 2, dtype=torch.float64) / rot)).float().cuda()
+            seq, pos = ints([i % 3 for i in range(n)]), ints([100 + i // 3 for i in range(n)])
+            table = ints(rng.permutation(40)[:30].reshape(3, 10))
+            out = torch.empty_like(x[0])
+            if normed:
+                d = q.make_norm_append_desc(n, 16, 3, 10, ACT[act][0], rot, inter)
+                q.coli_norm_append(d, c.desc, *x, None, None, inv, seq, pos, None, table, out)
+            else:
+                d = q.make_append_desc(n, 16, 3, 10, ACT[act][0], rot, inter)
+                q.coli_kv_append(d, c.desc, *x, inv, seq, pos, table, out)
+            got.append((out, c.k, c.v))
+        for a, b in zip(*got):
+            assert torch.equal(a, b)
+
+
+def test_append_bad_places_are_skipped_and_flagged(q):
+    rng = np.random.default_rng(12)
+    for seq, place, page, bit in ((0, 64, 3, 2), (0, -1, 3, 2), (0, 5, -1, 1), (0, 5, 9, 1), (7, 5, 3, 4), (-2, 5, 3, 4), (0, 2 ** 31 - 1, 3, 2)):
+        c = Cache(q, rng, "bf16", 9, 16, 1, 64)
+        x = randn(rng, 1, 64)
+        before, err, out = c.k.clone(), err_word(), torch.full((1, 64), float("nan"), device="cuda")
+        d = q.make_norm_append_desc(1, 1, 2, 4, eps=1e-6)
+        table = ints([[page] * 4] * 2)
+        q.coli_norm_append(d, c.desc, x, x, x, None, None, None, ints([seq]), ints([1]), ints([place]), table, out, err)
+        assert int(err.item()) == bit
+        assert q.coli_moe_check(err, raise_on_error=False) == q.COLI_MOE_EKERNEL
+        assert torch.equal(c.k, before) and torch.equal(out, x)
+
+
+# ------------------------------------------------------------------------------------ trees
+def random_tree(rng, n, chain=False):
+    return [i - 1 if chain or i == 0 else int(rng.integers(0, i)) for i in range(n)]
+
+
+def lines_of(parent):
+    """Each node's ancestors from itself up."""
+    out = []
+    for i, p in enumerate(parent):
+        out.append([i] + (out[p] if p >= 0 else []))
+    return out
+
+
+class Trees:
+    """Sequences with committed tokens and nodes in a paged cache of random contents."""
+
+    def __init__(self, q, seed, past, nodes, heads=(8, 2), dim=64, act="f32", kv="bf16", page=16, layout="hnd", window=0,
+                 boost=1.5, chain=False, parents=None, extra=0, first=0, width=0, most=0):
+        rng = np.random.default_rng(seed)
+        self.q, self.past, self.nodes, self.act, self.kv, self.window = q, past, nodes, act, kv, window
+        qh, kh = heads
+        used = [(p + n + page - 1) // page for p, n in zip(past, nodes)]
+        self.c = c = Cache(q, rng, kv, sum(used) + 2, page, kh, dim, layout)
+        perm = rng.permutation(c.pages)
+        width = max(width, max(used), 1)
+        table = torch.full((len(past), width), -7, dtype=torch.int32)  # entries behind the end are not read
+        at = 0
+        for b, u in enumerate(used):
+            table[b, :u] = torch.from_numpy(perm[at:at + u].astype(np.int32))
+            at += u
+            t = torch.arange(past[b] + nodes[b])
+            pg, sl = table[b, t // page].long().cuda(), (t % page).cuda()
+            for which in (0, 1):
+                c.put(which, pg, sl, randn(rng, len(t), kh, dim) * (16 if kv == "e4m3" else 1))
+        self.table = table.cuda()
+        self.parents = parents or [random_tree(rng, n, chain) for n in nodes]
+        self.first = [first]
+        for n in nodes:
+            self.first.append(self.first[-1] + n)
+        self.rows = self.first[-1] + extra
+        self.x = (randn(rng, self.rows, qh, dim) * boost).to(ACT[act][1])
+        flat = [0] * first + [p for b in self.parents for p in b[:]] + [0] * extra
+        self.parent = None if chain else ints(flat)
+        self.scale = dim ** -0.5
+        self.most = most or max(max(nodes), 1)
+
+    def desc(self, **over):
+        a = dict(seqs=len(self.past), rows=self.rows, nodes=self.most, q_heads=self.x.shape[1], table_width=self.table.shape[1],
+                 act=ACT[self.act][0], scale=self.scale, window=self.window)
+        a.update(over)
+        return self.q.make_tree_desc(**a)
+
+    def run(self, x=None, err=None, stream=None, out=None, lse=True, past=None, first=None, parent=0, ws=None, **over):
+        q, c = self.q, self.c
+        x = self.x if x is None else x
+        d = self.desc(**over)
+        n = q.coli_tree_workspace_bytes(d, c.desc)
+        assert n > 0
+        ws = torch.full((n,), 0xff, dtype=torch.uint8, device="cuda") if ws is None else ws  # NaN wherever it is read unwritten
+        out = torch.full(self.x.shape, float("nan"), dtype=self.x.dtype, device="cuda") if out is None else out
+        lse = torch.full(self.x.shape[:2], float("nan"), device="cuda") if lse else None
+        q.coli_attn_tree(d, c.desc, x, ints(self.first if first is None else first), ints(self.past if past is None else past),
+                         self.parent if isinstance(parent, int) else parent, self.table, out, lse, err, ws, n, stream)
+        return out, lse
+
+    def exact(self, skip=(), skip_places=()):
+        """out, lse, sum p |v|, A = max scale * sum |q k| in 64 bits and the tokens seen, of each named row."""
+        c, g = self.c, self.x.shape[1] // self.c.heads
+        shape = self.x.shape
+        out = torch.zeros(shape, dtype=torch.float64, device="cuda")
+        mass, lse = torch.zeros_like(out), torch.full(shape[:2], -math.inf, dtype=torch.float64, device="cuda")
+        amp = torch.zeros_like(lse)
+        for b, (past, n) in enumerate(zip(self.past, self.nodes)):
+            if not n:
+                continue
+            t = torch.arange(past + n, device="cuda")
+            page, slot = self.table[b].long()[t // c.ps], t % c.ps
+            gone = torch.tensor([(b, u) in skip for u in range((past + n - 1) // c.ps + 1)], device="cuda")[t // c.ps]
+            page = page.masked_fill(gone, 0)
+            k = (c.rows(0, page, slot) * c.factor(0)[None, :, None]).masked_fill(gone[:, None, None], 0.0)
+            v = (c.rows(1, page, slot) * c.factor(1)[None, :, None]).masked_fill(gone[:, None, None], 0.0)
+            lines = lines_of(self.parents[b])
+            hide = torch.ones(n, past + n, dtype=torch.bool)
+            for i, line in enumerate(lines):
+                if self.window:
+                    hide[i, max(0, past + len(line) - self.window):past] = False
+                    line = line[: self.window]
+                else:
+                    hide[i, :past] = False
+                hide[i, past + torch.tensor(line)] = False
+            hide = hide.cuda() | gone[None, :]
+            seen = ~hide
+            x = self.x[self.first[b]:self.first[b] + n].double().view(n, c.heads, g, -1)
+            rows = slice(self.first[b], self.first[b] + n)
+            s = torch.einsum("nhgd,thd->nhgt", x, k) * self.scale
+            s = s.masked_fill(hide[:, None, None], -math.inf)
+            p = torch.softmax(s, -1).nan_to_num(0.0)
+            # what a row does not see does not reach it, whatever it is
+            clean = torch.where(torch.isfinite(v), v, 0.0)
+            out[rows] = torch.einsum("nhgt,thd->nhgd", p, clean).reshape(n, *shape[1:])
+            mass[rows] = torch.einsum("nhgt,thd->nhgd", p, clean.abs()).reshape(n, *shape[1:])
+            lse[rows] = torch.logsumexp(s, -1).reshape(n, -1)
+            a = torch.einsum("nhgd,thd->nhgt", x.abs(), k.abs()) * abs(self.scale)
+            amp[rows] = a.masked_fill(~seen[:, None, None], 0.0).amax(-1).reshape(n, -1)
+        return out, lse, mass, amp
+
+    def compare(self, got, ref=None):
+        out, lse = got
+        want, wlse, mass, amp = ref or self.exact()
+        named = slice(self.first[0], self.first[-1])
+        n = max(p + k for p, k in zip(self.past, self.nodes))
+        ds = amp * ((3 * self.c.dim / 16 + 4) * 2 * U + 2.0 ** -22 + 8 * U)
+        sums = (64 + n / 64) * U
+        parts = 2.0 ** -16 if (self.act != "f32" and self.kv == "bf16") else 2.0 ** -22
+        empty = torch.isinf(wlse)
+        if lse is not None:
+            assert torch.equal((torch.isinf(lse) & (lse < 0))[named], empty[named])
+            close(lse.masked_fill(empty, 0.0)[named], wlse.masked_fill(empty, 0.0)[named],
+                  (ds + sums + 4 * U * (1 + wlse.masked_fill(empty, 0.0).abs()))[named])
+        bound = half_ulp(want, ACT[self.act][1]) + (2 * ds + 2 * sums + parts)[..., None] * mass * 1.01
+        close(out[named], want[named], bound[named])
+
+
+def check_tree(q, seed, past, nodes, **a):
+    t = Trees(q, seed, past, nodes, **a)
+    err = err_word()
+    got = t.run(err=err)
+    assert q.coli_moe_check(err) == q.COLI_MOE_OK
+    t.compare(got)
+    return t, got
+
+
+@pytest.mark.parametrize("act", sorted(ACT))
+@pytest.mark.parametrize("kv", sorted(KV))
+def test_tree_types(q, act, kv):
+    check_tree(q, 20, [70, 0, 300], [9, 5, 31], act=act, kv=kv, dim=128)
+
+
+@pytest.mark.parametrize("heads", [(1, 1), (7, 1), (8, 8), (16, 1), (12, 4), (24, 1), (10, 2), (40, 1), (17, 1), (64, 2), (128, 1)])
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+def test_tree_heads(q, heads, kv):
+    check_tree(q, 21, [100, 33], [7, 12], heads=heads, kv=kv)
+
+
+@pytest.mark.parametrize("dim", [16, 32, 48, 64, 80, 96, 112, 128, 144, 192, 208, 256])
+@pytest.mark.parametrize("kv", sorted(KV))
+@pytest.mark.parametrize("act", ["f32", "bf16"])
+def test_tree_head_sizes(q, dim, kv, act):
+    check_tree(q, 22, [150, 20], [10, 40], dim=dim, kv=kv, act=act)
+
+
+@pytest.mark.parametrize("dim", [8, 24, 72, 120, 248])
+def test_tree_odd_head_sizes(q, dim):
+    check_tree(q, 23, [150, 20], [10, 40], dim=dim)
+
+
+@pytest.mark.parametrize("nodes", [1, 2, 3, 15, 16, 17, 31, 32, 33, 63, 64, 65, 127, 128, 129, 200, 255, 256])
+@pytest.mark.parametrize("chain", [False, True])
+def test_tree_nodes(q, nodes, chain):
+    check_tree(q, 24, [77, 129, 0], [nodes, 1, nodes], heads=(4, 2), chain=chain)
+
+
+@pytest.mark.parametrize("past", [0, 1, 2, 31, 32, 33, 63, 64, 65, 95, 112, 127, 128, 129, 255, 257, 1000, 4097])
+def test_tree_lengths(q, past):
+    check_tree(q, 25, [past], [13], act="bf16", dim=128)
+
+
+@pytest.mark.parametrize("page", [1, 2, 3, 5, 8, 24, 48, 100, 128, 333])
+@pytest.mark.parametrize("layout", ["hnd", "nhd", "hpn"])
+def test_tree_pages(q, page, layout):
+    check_tree(q, 26, [300, 41], [11, 6], page=page, layout=layout)
+
+
+@pytest.mark.parametrize("window", [1, 2, 3, 5, 16, 31, 64, 100, 129, 500, 10 ** 6])
+@pytest.mark.parametrize("chain", [False, True])
+def test_tree_windows(q, window, chain):
+    check_tree(q, 27, [300, 17, 0], [40, 9, 25], window=window, chain=chain)
+
+
+def test_tree_shapes(q):
+    # stars, chains written as trees, several nodes behind the last committed token, two chains side by side
+    star, line = [-1] + [0] * 20, list(range(-1, 20))
+    roots, pair = [-1] * 21, [-1, -1] + list(range(19))
+    check_tree(q, 28, [50, 51, 52, 53], [21] * 4, parents=[star, line, roots, pair])
+    check_tree(q, 28, [50, 51, 52, 53], [21] * 4, parents=[star, line, roots, pair], window=7)
+
+
+def test_tree_chain_is_the_tree_without_branches(q):
+    a = Trees(q, 29, [100, 7], [20, 33], chain=True)
+    parent = ints([p for b in a.parents for p in b])
+    for x, y in zip(a.run(), a.run(parent=parent)):
+        assert torch.equal(x, y)
+
+
+def test_tree_single_node_is_coli_attn_decode(q):
+    # one node per sequence: the single-token attention's formula, to both sides' roundings
+    for act, kv in (("f32", "bf16"), ("bf16", "bf16"), ("bf16", "e4m3")):
+        t = Trees(q, 30, [500, 0, 63, 2000], [1] * 4, dim=128, act=act, kv=kv)
+        out, lse = t.run()
+        t.compare((out, lse))
+        d = q.make_attn_desc(4, 8, t.table.shape[1], ACT[act][0], t.scale)
+        n = q.coli_attn_workspace_bytes(d, t.c.desc)
+        other, lse2 = torch.empty_like(out), torch.empty_like(lse)
+        q.coli_attn_decode(d, t.c.desc, t.x, t.table, ints([501, 1, 64, 2001]), other, lse2, None,
+                           torch.empty(n, dtype=torch.uint8, device="cuda"), n)
+        t.compare((other, lse2))
+
+
+def test_tree_ragged_batches_and_idle_slots(q):
+    past = [int(p) for p in np.random.default_rng(31).integers(0, 3000, 40)]
+    nodes = [i * 7 % 30 for i in range(40)]  # some have none
+    check_tree(q, 31, past, nodes, act="bf16", heads=(32, 4), dim=128)
+    check_tree(q, 31, past, nodes, act="f32", kv="f16", heads=(12, 4), dim=64, window=200)
+
+
+def test_tree_long(q):
+    check_tree(q, 32, [70000], [64], act="bf16", heads=(12, 2), dim=128, page=64)
+    check_tree(q, 33, [40001], [30], act="f32", heads=(6, 1), dim=128, page=64)
+    check_tree(q, 34, [50000], [100], act="f16", kv="e4m3", heads=(16, 2), dim=64, page=64)
+
+
+@pytest.mark.parametrize("act,kv,dim", [("bf16", "bf16", 128), ("f32", "bf16", 128), ("f32", "f16", 64), ("bf16", "e4m3", 128),
+                                        ("bf16", "bf16", 256), ("f32", "bf16", 256), ("f32", "e4m3", 256)])
+def test_tree_many_rows(q, act, kv, dim):
+    # more rows than one tile of the products: 256 nodes of 5 heads on a kv head, beside few
+    check_tree(q, 35, [900, 2000, 0], [256, 3, 100], act=act, kv=kv, heads=(10, 2), dim=dim)
+
+
+def test_tree_most_sequences(q):
+    check_tree(q, 36, [i % 70 for i in range(1024)], [1 + i % 3 for i in range(1024)], heads=(2, 1), act="bf16")
+
+
+def test_tree_wide_table(q):
+    check_tree(q, 37, [10, 400], [5, 6], width=5000)
+
+
+def test_tree_peaked_and_flat_scores(q):
+    check_tree(q, 38, [1000, 100], [10, 20], boost=60.0)
+    check_tree(q, 39, [1000, 100], [10, 20], boost=0.0)
+
+
+def test_tree_large_and_small_values(q):
+    for kv, f in (("bf16", 2.0 ** 60), ("bf16", 2.0 ** -60), ("f16", 2.0 ** 10), ("f16", 2.0 ** -12)):
+        t = Trees(q, 40, [200, 31], [10, 20], kv=kv)
+        for b in range(2):
+            u = torch.arange(t.past[b] + t.nodes[b], device="cuda")
+            page, slot = t.table[b].long()[u // 16], u % 16
+            for which in (0, 1):
+                t.c.put(which, page, slot, t.c.rows(which, page, slot) * f)
+        t.x = t.x / f
+        out, lse = t.run()
+        want, wlse, mass, amp = t.exact()
+        t.compare((out / f, lse), (want / f, wlse, mass / f, amp))
+
+
+@pytest.mark.parametrize("kv,bits", [("bf16", 0x7f80), ("bf16", 0x7fff), ("f16", 0x7c00), ("f16", 0x7e00), ("e4m3", 0x7f)])
+@pytest.mark.parametrize("which", [0, 1])
+@pytest.mark.parametrize("window", [0, 30])
+def test_tree_what_a_row_does_not_see_does_not_reach_it(q, kv, bits, which, window):
+    # infinities and NaN in a node that few rows see, in a place that the window of the deeper nodes has left, behind
+    # the nodes and on other pages: rows that do not see them are as without
+    def make():
+        t = Trees(q, 41, [100, 61], [24, 40], kv=kv, window=window, dim=128, act="f32")
+        return t
+    clean = make()
+    t = make()
+    pool = (t.c.k, t.c.v)[which]
+    lines = [lines_of(p) for p in t.parents]
+    hit = torch.zeros(t.rows, dtype=torch.bool)
+    for b, node in ((0, 3), (0, 17), (1, 30)):
+        place = t.past[b] + node
+        pool[t.table[b, place // 16].long(), :, place % 16, 5] = bits
+        for i, line in enumerate(lines[b]):
+            hit[t.first[b] + i] |= node in (line[:window] if window else line)
+    if window:
+        # the root still sees this place, nodes of depth 2 and more do not
+        place = t.past[0] + 2 - window
+        pool[t.table[0, place // 16].long(), :, place % 16, 9] = bits
+        for i, line in enumerate(lines[0]):
+            hit[t.first[0] + i] |= len(line) - 1 < 2
+    for b in range(2):
+        end = t.past[b] + t.nodes[b]
+        if end % 16:
+            pool[t.table[b, end // 16].long(), :, end % 16:] = bits
+    got, want = t.run(), clean.run()
+    for a, b in zip(got, want):
+        assert torch.equal(a[~hit], b[~hit])
+    assert 0 < int(hit.sum()) < t.rows
+    if which == 1:
+        # what a row does see does: the one element, of all heads
+        bad = ~torch.isfinite(got[0])
+        seen5 = torch.zeros(t.rows, dtype=torch.bool)
+        for b, node in ((0, 3), (0, 17), (1, 30)):
+            for i, line in enumerate(lines[b]):
+                seen5[t.first[b] + i] |= node in (line[:window] if window else line)
+        assert bool(bad[seen5][..., 5].all()) and not bool(bad[~hit].any())
+        assert not bool(bad[..., :5].any()) and not bool(bad[..., 10:].any())
+
+
+def test_tree_rows_that_no_sequence_names_are_left_alone(q):
+    t = Trees(q, 42, [50, 0, 90], [7, 0, 12], first=5, extra=9)
+    out, lse = t.run()
+    t.compare((out, lse))
+    for x in (out, lse):
+        assert bool(torch.isnan(x[:5]).all()) and bool(torch.isnan(x[-9:]).all())
+
+
+def test_tree_no_nodes_at_all(q):
+    t = Trees(q, 43, [50, 20], [0, 0], extra=3)
+    out, lse = t.run()
+    assert bool(torch.isnan(out).all()) and bool(torch.isnan(lse).all())
+
+
+def test_tree_bad_pages_are_left_out_and_flagged(q):
+    for bad in (-1, 10 ** 6, 2 ** 31 - 1, -2 ** 31):
+        t = Trees(q, 44, [100, 0, 300], [10, 9, 20])
+        t.table[0, 2], t.table[1, 0], t.table[2, 19] = bad, bad, bad
+        err = err_word()
+        out, lse = t.run(err=err)
+        assert int(err.item()) == q.COLI_LAYER_BAD_PAGE
+        assert q.coli_moe_check(err, raise_on_error=False) == q.COLI_MOE_EKERNEL
+        t.compare((out, lse), t.exact(skip={(0, 2), (1, 0), (2, 19)}))
+        rows = slice(t.first[1], t.first[2])
+        assert bool((out[rows] == 0).all()) and bool((lse[rows] == -math.inf).all())
+
+
+def test_tree_bad_counts_are_clamped_and_flagged(q):
+    # committed tokens beyond the table
+    for given, means in ((2 ** 31 - 1, 48 - 5), (44, 43), (-1, 0), (-2 ** 31, 0)):
+        t = Trees(q, 45, [43, 20], [5, 5], width=3)
+        err = err_word()
+        got = t.run(err=err, past=[given, 20])
+        assert int(err.item()) == q.COLI_LAYER_BAD_POSITION
+        t.past = [means, 20]
+        t.compare(got)
+    # rows outside the arrays, more than there may be, backwards
+    t = Trees(q, 46, [43, 20], [5, 5])
+    for first, nodes, at in (([-3, 5, 10], [5, 5], [0, 5, 10]), ([0, 5, 99], [5, 5], [0, 5, 10]), ([0, 5, 3], [5, 0], [0, 5, 5]),
+                             ([0, 2 ** 31 - 1, -5], [5, 0], [0, 5, 5])):
+        err = err_word()
+        got = t.run(err=err, first=first)
+        assert int(err.item()) & q.COLI_LAYER_BAD_SEQUENCE
+        if nodes == [5, 5]:
+            t.compare(got)
+        else:
+            keep = t.nodes, t.first
+            t.nodes, t.first = nodes, at
+            named = Trees.exact(t)
+            t.compare(got, named)
+            t.nodes, t.first = keep
+    # more nodes than `nodes`: the first ones
+    t = Trees(q, 47, [43], [9], most=6)
+    err = err_word()
+    out, lse = t.run(err=err)
+    assert int(err.item()) == q.COLI_LAYER_BAD_SEQUENCE
+    t.nodes, t.first, t.parents = [6], [0, 6], [t.parents[0][:6]]
+    t.compare((out, lse))
+    assert bool(torch.isnan(out[6:]).all())
+
+
+def test_tree_bad_parents_count_as_none_and_are_flagged(q):
+    for at, bad in ((4, 4), (4, 9), (0, 0), (7, -2), (7, 2 ** 31 - 1), (3, -2 ** 31)):
+        t = Trees(q, 48, [50], [10])
+        flat = t.parent.tolist()
+        flat[at] = bad
+        err = err_word()
+        got = t.run(err=err, parent=ints(flat))
+        assert int(err.item()) == q.COLI_DRAFT_BAD_NODE
+        t.parents[0][at] = -1
+        t.compare(got)
+
+
+def test_tree_more_nodes_than_the_table_has_places(q):
+    t = Trees(q, 49, [0], [20], page=4)
+    err = err_word()
+    t.table = t.table[:, :4].contiguous()
+    out, lse = t.run(err=err)
+    assert int(err.item()) == q.COLI_LAYER_BAD_POSITION
+    t.nodes, t.first, t.parents = [16], [0, 16], [t.parents[0][:16]]
+    t.compare((out, lse))
+
+
+@pytest.mark.parametrize("act", ["f32", "bf16"])
+@pytest.mark.parametrize("pad,offset", [(8, 0), (1, 0), (0, 1), (3, 5), (4, 4)])
+def test_tree_strided_rows_and_no_lse(q, act, pad, offset):
+    t = Trees(q, 50, [90, 10], [8, 21], act=act)
+    row = t.x[0].numel() + pad
+    buf = torch.zeros(offset + t.rows * row, dtype=t.x.dtype, device="cuda")
+    x = buf[offset:].view(t.rows, row)
+    x[:, : t.x[0].numel()] = t.x.view(t.rows, -1)
+    o = torch.full((offset + t.rows * row,), float("nan"), dtype=t.x.dtype, device="cuda")
+    out = o[offset:].view(t.rows, row)
+    t.run(x=x, out=out, lse=False, q_stride=row, out_stride=row)
+    t.compare((out[:, : t.x[0].numel()].reshape(t.x.shape), None))
+    assert bool(torch.isnan(out[:, t.x[0].numel():]).all())
+
+
+def test_tree_behind_two_to_the_31_elements(q):
+    # a pool of more than 2^31 elements, the tokens on its last pages
+    pages, page, heads, dim = 2 ** 31 // (64 * 2 * 128) + 40, 64, 2, 128
+    k = torch.zeros(pages, heads, page, dim, dtype=torch.float16, device="cuda")
+    v = torch.zeros_like(k)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    k[-30:] = torch.randn(30, heads, page, dim, generator=g, device="cuda").half()
+    v[-30:] = torch.randn(30, heads, page, dim, generator=g, device="cuda").half()
+    small = [x[-30:].clone() for x in (k, v)]
+    x = torch.randn(20, 8, dim, generator=g, device="cuda")
+    got = []
+    for pools, shift in (((k, v), pages - 30), (small, 0)):
+        c = q.make_kv_cache(pools[0], pools[1], q.COLI_KV_F16, len(pools[0]), page, heads, dim)
+        table = (torch.randperm(30, generator=torch.Generator().manual_seed(2)) + shift).int().cuda().view(1, 30)
+        d = q.make_tree_desc(1, 20, 20, 8, 30, 0, dim ** -0.5)
+        n = q.coli_tree_workspace_bytes(d, c)
+        out, ws = torch.empty_like(x), torch.empty(n, dtype=torch.uint8, device="cuda")
+        q.coli_attn_tree(d, c, x, ints([0, 20]), ints([1880]), None, table, out, None, None, ws, n)
+        got.append(out)
+    assert torch.equal(*got) and bool(torch.isfinite(got[0]).all())
+
+
+def test_tree_repeats_on_streams_and_in_graphs(q):
+    t = Trees(q, 51, [3000, 40, 900], [30, 5, 64], heads=(16, 2), dim=128, act="bf16")
+    want = t.run()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        got = t.run(stream=side)
+    side.synchronize()
+    for a, b in zip(want, got):
+        assert torch.equal(a, b)
+    # two graphs that share a workspace, replayed in turn on one stream, with other lengths and trees in place
+    d = t.desc()
+    n = q.coli_tree_workspace_bytes(d, t.c.desc)
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+    first, past, parent = ints(t.first), ints(t.past), t.parent.clone()
+    graphs, outs = [], []
+    for _ in range(2):
+        out = torch.zeros_like(t.x)
+        lse = torch.zeros(t.x.shape[:2], device="cuda")
+        with torch.cuda.stream(side):
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph, stream=side):
+                q.coli_attn_tree(d, t.c.desc, t.x, first, past, parent, t.table, out, lse, None, ws, n, side)
+        graphs.append(graph)
+        outs.append((out, lse))
+    for _ in range(3):
+        for graph in graphs:
+            graph.replay()
+    torch.cuda.synchronize()
+    for got in outs:
+        for a, b in zip(want, got):
+            assert torch.equal(a, b)
+    past.copy_(ints([100, 40, 7]))
+    graphs[0].replay()
+    torch.cuda.synchronize()
+    t.past = [100, 40, 7]
+    # (the nodes' places are others now: what lies there is finite)
+    t.compare(outs[0])
+
+
+# ------------------------------------------------------------------------------------ verification
+def verify64(target, draft, tokens, parents, uniform, vocab, greedy=False):
+    """path and next token of one sequence, by the definition in 64 bits."""
+    path, n = [0], len(parents)
+    while True:
+        c = path[-1]
+        p = target[c].double()
+        kids = [i for i in range(1, n) if parents[i] == c and 0 <= tokens[i] < vocab]
+        if greedy:
+            p = torch.where(torch.isnan(p), -math.inf, p)
+            best = int((p == p.max()).nonzero()[0])
+            hit = [i for i in kids if tokens[i] == best]
+            if not hit:
+                return path, best
+            path.append(hit[0])
+            continue
+        r, m, taken = p.clone(), 1.0, None
+        for i in kids:
+            x, u = tokens[i], float(uniform[i])
+            if draft is not None:
+                if u * float(draft[c, x].double()) * m < float(r[x]):
+                    taken = i
+                    break
+                r = (r - m * draft[c].double()).clamp(min=0.0)
+            else:
+                if u * m < float(r[x]):
+                    taken = i
+                    break
+                r[x] = 0.0
+            m = float(r.sum())
+        if taken is not None:
+            path.append(taken)
+            continue
+        if not float(r.sum()) > 0:
+            r = p
+        run = r.cumsum(0)
+        return path, int((run > float(uniform[0]) * run[-1]).int().argmax())
+
+
+def check_verify(q, seed, nodes, vocab, act="f32", draft=True, greedy=False, chain=False, near=0.5, sharp=3.0, pad=0, offset=0, extra=0,
+                 most=0, parents=None):
+    rng = np.random.default_rng(seed)
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    dtype, rows, b = ACT[act][1], sum(nodes) + extra, len(nodes)
+    trees = parents or [random_tree(rng, n, chain) for n in nodes]
+    first = np.concatenate([[0], np.cumsum(nodes)]).tolist()
+
+    def table(x):
+        buf = torch.zeros(offset + rows * (vocab + pad), dtype=dtype, device="cuda")
+        view = buf[offset:].view(rows, vocab + pad)
+        view[:, :vocab] = x.to(dtype)
+        return view
+
+    logits = torch.randn(rows, vocab, generator=g, device="cuda") * sharp
+    target = table(logits if greedy else torch.softmax(logits, 1))
+    dist = table(torch.softmax(logits + near * torch.randn(rows, vocab, generator=g, device="cuda"), 1))
+    tokens = []
+    for s, tree in enumerate(trees):
+        for i, p in enumerate(tree):
+            row = dist[first[s] + max(p, 0), :vocab].double()
+            x = int((row.cumsum(0) > rng.random() * row.sum()).int().argmax())
+            if greedy and rng.random() < 0.7:
+                x = int(target[first[s] + max(p, 0), :vocab].float().argmax())
+            tokens.append(x)
+    tokens += [0] * extra
+    uniform = torch.rand(rows, generator=g, device="cuda")
+    flat = [p for t in trees for p in t] + [0] * extra
+    most = most or max(max(nodes), 1)
+    path = torch.full((b, most), 77, dtype=torch.int32, device="cuda")
+    count, token, err = ints([77] * b), ints([77] * b), err_word()
+    d = q.make_verify_desc(b, rows, most, vocab, ACT[act][0], int(greedy), vocab + pad, vocab + pad)
+    q.coli_draft_verify(d, target, dist if draft and not greedy else None, ints(tokens), None if chain else ints(flat),
+                        None if greedy else uniform, ints(first), path, count, token, err)
+    assert q.coli_moe_check(err) == q.COLI_MOE_OK
+    lengths = []
+    for s, tree in enumerate(trees):
+        if not tree:
+            assert (int(count[s]), int(token[s])) == (0, -1) and bool((path[s] == -1).all())
+            continue
+        r = slice(first[s], first[s + 1])
+        want, last = verify64(target[r, :vocab], dist[r, :vocab] if draft and not greedy else None, tokens[first[s]:first[s + 1]], tree,
+                              uniform[r], vocab, greedy)
+        assert path[s, :len(want)].tolist() == want and bool((path[s, len(want):] == -1).all())
+        assert (int(count[s]), int(token[s])) == (len(want), last)
+        lengths.append(len(want))
+    return lengths
+
+
+@pytest.mark.parametrize("act", sorted(ACT))
+@pytest.mark.parametrize("draft", [True, False])
+@pytest.mark.parametrize("chain", [True, False])
+def test_verify_types(q, act, draft, chain):
+    lengths = check_verify(q, 60, [6, 12, 1, 0, 30, 8, 9, 10], 1000, act, draft, chain=chain)
+    assert max(lengths) > 1 or not draft  # (without a draft a token is accepted as seldom as the target has it)
+
+
+@pytest.mark.parametrize("vocab", [1, 2, 3, 31, 511, 512, 513, 4095, 4096, 4097, 32000, 100003, 151000])
+@pytest.mark.parametrize("draft", [True, False])
+def test_verify_vocabularies(q, vocab, draft):
+    check_verify(q, 61, [7, 16, 3], vocab, draft=draft)
+
+
+def test_verify_the_largest_vocabulary(q):
+    check_verify(q, 62, [4, 9], 2 ** 20)
+    check_verify(q, 62, [4, 9], 2 ** 20, draft=False, sharp=6.0)
+
+
+@pytest.mark.parametrize("near", [0.01, 0.3, 1.0, 3.0])
+@pytest.mark.parametrize("draft", [True, False])
+def test_verify_near_and_far_drafts(q, near, draft):
+    # many children at a node: several rejections there
+    star = [-1] + [0] * 12 + [1 + i // 2 for i in range(20)]
+    check_verify(q, 63, [33] * 20, 700, near=near, draft=draft, sharp=2.0, parents=[star] * 20)
+
+
+@pytest.mark.parametrize("act", sorted(ACT))
+@pytest.mark.parametrize("chain", [True, False])
+def test_verify_greedy(q, act, chain):
+    # bf16 logits of a small vocabulary tie often
+    lengths = check_verify(q, 64, [6, 12, 1, 0, 30], 3000, act, greedy=True, chain=chain, sharp=0.5 if act == "bf16" else 3.0)
+    assert max(lengths) > 2
+
+
+def test_verify_greedy_with_ties_and_nan(q):
+    nan = float("nan")
+    rows = torch.tensor([[1.0, 5.0, 5.0, nan, 2.0], [nan] * 5, [-math.inf] * 5, [nan, -math.inf, nan, 3.0, 3.0]], device="cuda")
+    path, count, token = ints([[0] * 4] * 4), ints([0] * 4), ints([0] * 4)
+    q.coli_draft_verify(q.make_verify_desc(4, 4, 4, 5, mode=q.COLI_VERIFY_GREEDY), rows, None, ints([0] * 4), None, None,
+                        ints([0, 1, 2, 3, 4]), path, count, token)
+    assert token.tolist() == [1, 0, 0, 3] and count.tolist() == [1] * 4
+
+
+@pytest.mark.parametrize("pad,offset", [(0, 0), (4, 0), (1, 0), (0, 1), (3, 2)])
+@pytest.mark.parametrize("act", ["f32", "bf16"])
+def test_verify_strides_and_alignment(q, pad, offset, act):
+    check_verify(q, 65, [9, 14], 1234, act, pad=pad, offset=offset, extra=3)
+
+
+def test_verify_many_sequences(q):
+    check_verify(q, 66, [1 + i % 6 for i in range(500)], 300)
+    check_verify(q, 67, [1024, 700], 50, near=0.02)
+    check_verify(q, 68, [5, 6], 100, most=40)
+
+
+def test_verify_certain_rows(q):
+    # one-hot targets: the drafted token is accepted whatever the number, or rejected and the target's drawn; nothing left
+    # of the residual: the target itself
+    v = 600
+    hot = lambda x: torch.nn.functional.one_hot(torch.tensor(x), v).float().cuda()  # noqa: E731
+    target, draft = hot([3, 4, 5, 6]), hot([3, 9, 5, 6])
+    uniform = torch.tensor([0.999, 0.9999999, 0.0, 0.5], device="cuda")
+    for drafted in (draft, None):
+        path, count, token = ints([[0] * 4]), ints([0]), ints([0])
+        q.coli_draft_verify(q.make_verify_desc(1, 4, 4, v), target, drafted, ints([0, 3, 9, 0]), None, uniform, ints([0, 4]), path, count,
+                            token)
+        assert path.tolist() == [[0, 1, -1, -1]] and count.tolist() == [2] and token.tolist() == [4]
+    # the draft's row covers the target's: the residual is empty only where they are equal, and then u = 1 - 2^-24 accepts
+    path, count, token = ints([[0] * 2]), ints([0]), ints([0])
+    p = torch.zeros(2, v, device="cuda")
+    p[:, 7] = 1 - 2.0 ** -20
+    big = torch.zeros(2, v, device="cuda")
+    big[:, 7] = 1.0
+    q.coli_draft_verify(q.make_verify_desc(1, 2, 2, v), p, big, ints([0, 7]), None, torch.tensor([0.5, 1 - 2.0 ** -24], device="cuda"),
+                        ints([0, 2]), path, count, token)
+    assert count.tolist() == [1] and token.tolist() == [7]
+
+
+def test_verify_the_ends_of_a_row(q):
+    # numbers at and next to 0 and 1; leading and trailing zeros are never drawn
+    v = 2000
+    p = torch.zeros(3, v, device="cuda")
+    p[:, 700], p[:, 1300] = 0.25, 0.75
+    for u, want in ((0.0, 700), (0.25 - 2.0 ** -25, 700), (0.25, 1300), (1 - 2.0 ** -24, 1300)):
+        path, count, token = ints([[0]] * 3), ints([0] * 3), ints([0] * 3)
+        q.coli_draft_verify(q.make_verify_desc(3, 3, 1, v), p, None, ints([0] * 3), None, torch.full((3,), u, device="cuda"),
+                            ints([0, 1, 2, 3]), path, count, token)
+        assert token.tolist() == [want] * 3
+
+
+def test_verify_no_distribution_stays_within_the_vocabulary(q):
+    # not what the call is for, but nothing leaves its arrays
+    v = 900
+    for value in (0.0, float("nan"), float("inf"), -1.0):
+        for u in (0.5, 0.0, float("nan"), 2.0, -1.0):
+            p = torch.full((4, v), value, device="cuda")
+            path, count, token = ints([[0] * 4]), ints([0]), ints([-5])
+            for drafted in (p, None):
+                q.coli_draft_verify(q.make_verify_desc(1, 4, 4, v), p, drafted, ints([1, 2, 3, 4]), None, torch.full((4,), u, device="cuda"),
+                                    ints([0, 4]), path, count, token)
+                assert 0 <= int(token[0]) < v and 1 <= int(count[0]) <= 4
+
+
+def test_verify_bad_nodes_are_not_accepted_and_flagged(q):
+    v = 50
+    p = torch.full((4, v), 1 / v, device="cuda")
+    for tokens, parent, bit in (([0, v, 1, 1], [-1, 0, 0, 2], 8), ([0, -1, 1, 1], [-1, 0, 0, 2], 8), ([0, 1, 1, 1], [-1, 1, 0, 2], 8),
+                                ([0, 1, 1, 1], [-1, -7, 0, 2], 8), ([0, 1, 1, 1], [-1, 2 ** 31 - 1, 0, 2], 8)):
+        path, count, token, err = ints([[0] * 4]), ints([0]), ints([0]), err_word()
+        q.coli_draft_verify(q.make_verify_desc(1, 4, 4, v), p, p, ints(tokens), ints(parent), torch.zeros(4, device="cuda"), ints([0, 4]),
+                            path, count, token, err)
+        assert int(err.item()) == bit
+        assert path.tolist() == [[0, 2, 3, -1]]
+    for first, want in (([0, 9], 4), ([-2, 4], 4), ([3, 1], 0), ([2 ** 31 - 1, -2 ** 31], 0)):
+        path, count, token, err = ints([[0] * 4]), ints([7]), ints([7]), err_word()
+        q.coli_draft_verify(q.make_verify_desc(1, 4, 4, v), p, p, ints([0, 1, 1, 1]), None, torch.zeros(4, device="cuda"), ints(first),
+                            path, count, token, err)
+        assert int(err.item()) == q.COLI_LAYER_BAD_SEQUENCE and int(count[0]) == want
+
+
+@pytest.mark.parametrize("draft", [True, False])
+def test_verify_gives_the_targets_distribution(q, draft):
+    # the first token behind the root, drawn or accepted, over many sequences that share one target: each frequency is
+    # within 6 standard deviations of its binomial
+    g = torch.Generator(device="cuda").manual_seed(69)
+    v, b, kids = 7, 60000, 3
+    p = torch.tensor([0.3, 0.05, 0.2, 0.0, 0.15, 0.1, 0.2], device="cuda")
+    s = torch.tensor([0.1, 0.3, 0.2, 0.1, 0.05, 0.05, 0.2], device="cuda")
+    n = kids + 1
+    target = p.repeat(b * n, 1)
+    rows = s.repeat(b * n, 1)
+    tokens = torch.multinomial(s, b * n, replacement=True, generator=g).int()
+    if not draft:
+        tokens = ints([0, 1, 2, 4]).repeat(b)
+    parent = ints([-1, 0, 0, 0]).repeat(b)
+    first = torch.arange(0, b * n + 1, n, device="cuda").int()
+    path, count, token = ints([[0] * n]).repeat(b, 1), ints([0]).repeat(b), ints([0]).repeat(b)
+    q.coli_draft_verify(q.make_verify_desc(b, b * n, n, v), target, rows if draft else None, tokens, parent,
+                        torch.rand(b * n, generator=g, device="cuda"), first, path, count, token)
+    taken = tokens.view(b, n).gather(1, path[:, 1:2].clamp(min=0).long())[:, 0]
+    got = torch.where(count > 1, taken, token)
+    freq = torch.bincount(got.long(), minlength=v).double() / b
+    assert bool(((freq - p.double()).abs() <= 6 * (p.double() * (1 - p.double()) / b).sqrt()).all())
+    assert 0.2 < float((count > 1).double().mean()) < 1.0
+
+
+def test_verify_repeats_on_streams_and_in_graphs(q):
+    g = torch.Generator(device="cuda").manual_seed(70)
+    b, n, v = 9, 8, 5000
+    p = torch.softmax(torch.randn(b * n, v, generator=g, device="cuda") * 2, 1)
+    s = torch.softmax(torch.randn(b * n, v, generator=g, device="cuda"), 1)
+    tokens = torch.multinomial(s, 1, generator=g)[:, 0].int()
+    u = torch.rand(b * n, generator=g, device="cuda")
+    first = torch.arange(0, b * n + 1, n, device="cuda").int()
+    d = q.make_verify_desc(b, b * n, n, v)
+    outs = [(ints([[0] * n]).repeat(b, 1), ints([0]).repeat(b), ints([0]).repeat(b)) for _ in range(2)]
+    call = lambda o, stream: q.coli_draft_verify(d, p, s, tokens, None, u, first, *o, None, stream)  # noqa: E731
+    call(outs[0], torch.cuda.current_stream())
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        call(outs[1], side)
+    for x in outs[1]:
+        x.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    for x, y in zip(*outs):
+        assert torch.equal(x, y)
+
+
+# ------------------------------------------------------------------------------------ moves
+def pools_of(q, rng, layers, kv, pages, page, heads, dim, layout):
+    cs = [Cache(q, rng, kv, pages, page, heads, dim, layout) for _ in range(layers)]
+    for c in cs:
+        for x in (c.k, c.v):
+            x.copy_(torch.from_numpy(rng.integers(0, 120, tuple(x.shape))).to(x.dtype))
+    return cs, q.make_kv_caches([c.desc for c in cs])
+
+
+@pytest.mark.parametrize("kv", sorted(KV))
+@pytest.mark.parametrize("layout", ["hnd", "nhd", "hpn"])
+@pytest.mark.parametrize("page,heads,dim", [(16, 2, 64), (1, 3, 128), (5, 8, 256), (24, 1, 16)])
+def test_compact(q, kv, layout, page, heads, dim):
+    rng = np.random.default_rng(80)
+    past, nodes = [37, 0, 100, 11, 60], 40
+    paths = [[0, 2, 3, 7, 20], [0], [0, 1, 2, 5, 6, 7, 8, 9, 10, 30, 39], [], [3, 9] + list(range(12, 40))]
+    width = 140 // page + 1
+    cs, caches = pools_of(q, rng, 3, kv, 5 * width, page, heads, dim, layout)
+    table = rng.permutation(5 * width).reshape(5, width)
+    old = [(c.k.clone(), c.v.clone()) for c in cs]
+    path = np.full((5, nodes), -1)
+    for b, p in enumerate(paths):
+        path[b, :len(p)] = p
+    err = err_word()
+    q.coli_kv_compact(q.make_compact_desc(5, nodes, width, 3), caches, ints(past), ints(path), ints([len(p) for p in paths]), ints(table), err)
+    assert q.coli_moe_check(err) == q.COLI_MOE_OK
+    for c, was in zip(cs, old):
+        for now, x in zip((c.k, c.v), was):
+            want = x.clone()
+            for b, p in enumerate(paths):
+                for i, node in enumerate(p):
+                    if i:
+                        f, t = past[b] + node, past[b] + i
+                        want[table[b][t // page], :, t % page] = x[table[b][f // page], :, f % page]
+            assert torch.equal(now, want)
+
+
+def test_compact_many_layers_and_long_paths(q):
+    # more layers than one launch takes, more moves than are held at once
+    rng = np.random.default_rng(81)
+    cs, caches = pools_of(q, rng, 70, "e4m3", 9, 100, 1, 16, "hnd")
+    path = [0] + sorted(rng.choice(np.arange(1, 800), 599, replace=False).tolist())
+    table = rng.permutation(9)
+    old = [(c.k.clone(), c.v.clone()) for c in cs]
+    q.coli_kv_compact(q.make_compact_desc(1, 800, 9, 70), caches, ints([50]), ints([path + [-1] * 200]), ints([600]), ints([table]))
+    t = torch.tensor(path[1:], device="cuda") + 50
+    at = torch.arange(1, 600, device="cuda") + 50
+    tab = torch.from_numpy(table).cuda()
+    for c, was in zip(cs, old):
+        for now, x in zip((c.k, c.v), was):
+            want = x.clone()
+            want[tab[at // 100], :, at % 100] = x[tab[t // 100], :, t % 100]
+            assert torch.equal(now, want)
+
+
+def test_compact_bad_entries_are_not_moved_and_flagged(q):
+    rng = np.random.default_rng(82)
+    top = 2 ** 31 - 1
+    for path, count, past, page, bit in (([0, 3, 3, -1], 3, 5, 0, 8), ([0, 3, 2, -1], 3, 5, 0, 8), ([0, 0, 2, -1], 2, 5, 0, 8),
+                                         ([0, -1, 2, -1], 2, 5, 0, 8), ([0, 2, 3, 9], 9, 5, 0, 8), ([0, 2, 60, -1], 3, 5, 0, 2),
+                                         ([0, top, top, top], 2, 5, 0, 8), ([0, 2, -1, -1], 2, -1, 0, 2), ([0, 2, -1, -1], 2, 5, -1, 1),
+                                         ([0, 2, -1, -1], 2, 5, 99, 1), ([0, 2, -1, -1], 2, top, 0, 8)):
+        cs, caches = pools_of(q, rng, 1, "bf16", 2, 16, 1, 16, "hnd")
+        x = cs[0].k.clone()
+        err = err_word()
+        q.coli_kv_compact(q.make_compact_desc(1, 4, 2), caches, ints([past]), ints([path]), ints([count]), ints([[page, 1]]), err)
+        assert int(err.item()) == bit, (path, count, past, page)
+        for i in range(1, min(count, 4)):
+            good = path[i] >= i and path[i] > path[i - 1] and past == 5 and past + path[i] < 32 and page == 0
+            if good:
+                x[0, :, past + i] = cs[0].k[0, :, past + i] if past + path[i] >= 16 else x[0, :, past + path[i]]
+        assert torch.equal(cs[0].k, x)
+
+
+@pytest.mark.parametrize("kv", sorted(KV))
+@pytest.mark.parametrize("layout", ["hnd", "nhd", "hpn"])
+@pytest.mark.parametrize("page,heads,dim", [(16, 2, 64), (1, 3, 128), (5, 8, 256), (64, 8, 128), (24, 1, 16)])
+def test_copy_pages(q, kv, layout, page, heads, dim):
+    rng = np.random.default_rng(83)
+    cs, caches = pools_of(q, rng, 3, kv, 20, page, heads, dim, layout)
+    perm = rng.permutation(20)
+    src, dst = perm[:7].copy(), perm[7:14].copy()
+    src[6] = src[0]  # a page may be copied twice
+    src[2], dst[4] = -1, -1  # skipped
+    old = [(c.k.clone(), c.v.clone()) for c in cs]
+    err = err_word()
+    q.coli_kv_copy_pages(caches, 3, 7, ints(src), ints(dst), err)
+    assert q.coli_moe_check(err) == q.COLI_MOE_OK
+    for c, was in zip(cs, old):
+        for now, x in zip((c.k, c.v), was):
+            for s, d in zip(src, dst):
+                if s >= 0 and d >= 0:
+                    x[d] = x[s].clone()
+            assert torch.equal(now, x)
+
+
+def test_copy_pages_of_a_padded_pool(q):
+    # pages with gaps between heads and slots, which stay as they are
+    rng = np.random.default_rng(84)
+    raw = [torch.from_numpy(rng.integers(0, 120, (6, 3, 5, 48))).to(torch.int16).cuda() for _ in range(2)]
+    c = q.make_kv_cache(raw[0], raw[1], q.COLI_KV_F16, 6, 4, 2, 32, 3 * 5 * 48, 48, 5 * 48)
+    old = [x.clone() for x in raw]
+    q.coli_kv_copy_pages(q.make_kv_caches([c]), 1, 2, ints([0, 1]), ints([4, 2]))
+    for x, was in zip(raw, old):
+        for s, d in ((0, 4), (1, 2)):
+            was[d, :2, :4, :32] = was[s, :2, :4, :32]
+        assert torch.equal(x, was)
+
+
+def test_copy_pages_bad_and_many(q):
+    rng = np.random.default_rng(85)
+    for bad in (20, -2, 2 ** 31 - 1, -2 ** 31):
+        for src, dst in (([bad, 1], [2, 3]), ([0, 1], [bad, 3])):
+            cs, caches = pools_of(q, rng, 1, "bf16", 20, 4, 1, 16, "hnd")
+            want, err = cs[0].k.clone(), err_word()
+            want[3] = want[1]
+            q.coli_kv_copy_pages(caches, 1, 2, ints(src), ints(dst), err)
+            assert int(err.item()) == q.COLI_LAYER_BAD_PAGE and torch.equal(cs[0].k, want)
+    # more pairs than one launch takes
+    n = 70000
+    k = torch.arange(2 * n, device="cuda", dtype=torch.int16)[:, None].repeat(1, 8).contiguous()
+    c = q.make_kv_cache(k, k.clone(), q.COLI_KV_BF16, 2 * n, 1, 1, 8)
+    v = k.clone()
+    c.v = v.data_ptr()
+    q.coli_kv_copy_pages(q.make_kv_caches([c]), 1, n, torch.arange(n, device="cuda").int(), torch.arange(n, 2 * n, device="cuda").int())
+    for x in (k, v):
+        assert torch.equal(x[n:], x[:n]) and int(x[5, 0]) == 5
+
+
+def test_moves_behind_two_to_the_31_elements(q):
+    pages, page, heads, dim = 2 ** 31 // (64 * 2 * 128) + 4, 64, 2, 128
+    k = torch.zeros(pages, heads, page, dim, dtype=torch.int16, device="cuda")
+    v = torch.zeros_like(k)
+    k[0], v[0] = 3, 4
+    c = q.make_kv_caches([q.make_kv_cache(k, v, q.COLI_KV_F16, pages, page, heads, dim)])
+    q.coli_kv_copy_pages(c, 1, 1, ints([0]), ints([pages - 1]))
+    assert bool((k[-1] == 3).all()) and bool((v[-1] == 4).all()) and int(k[pages - 2].abs().sum()) == 0
+    k[-1, :, 9], v[-1, :, 9] = 7, 8
+    q.coli_kv_compact(q.make_compact_desc(1, 10, 1), c, ints([2]), ints([[0, 7] + [-1] * 8]), ints([2]), ints([[pages - 1]]))
+    assert bool((k[-1, :, 3] == 7).all()) and bool((v[-1, :, 3] == 8).all()) and bool((k[-1, :, 4] == 3).all())

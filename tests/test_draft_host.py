@@ -1,0 +1,252 @@
+"""Host-side checks of include/colidraft.h: the binding declares what the header does, bad arguments are refused with
+the documented codes before the GPU is touched, and the arithmetic of nodes and places that the kernels share
+(csrc/draft_index.h) is right at its borders."""
+import ctypes
+import os
+import re
+import subprocess
+
+import pytest
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+FAKE = 1 << 40  # a 256-byte aligned address never dereferenced: validation fails first
+
+
+@pytest.fixture(scope="module")
+def q():
+    import __graft_entry__
+    __graft_entry__._builder().build()
+    import quantized_expert_decode_gb300 as q
+    return q
+
+
+def test_header_and_binding_agree(q):
+    with open(os.path.join(ROOT, "include", "colidraft.h")) as f:
+        text = f.read()
+    names = sorted(re.findall(r"^(?:int|size_t)\s+(coli_[a-z_]+)\s*\(", text, re.M))
+    assert names == sorted(q.DRAFT_EXPORTS)
+    lib = ctypes.CDLL(q.LIB_PATH)
+    for n in names:
+        getattr(lib, n)
+    found = re.findall(r"^#define (COLI_(?:DRAFT|VERIFY)_\w+) (\d+)", text, re.M)
+    assert len(found) == 3
+    for name, value in found:
+        assert getattr(q, name) == int(value), name
+
+
+def test_struct_layouts_match_the_header(q, tmp_path):
+    src = tmp_path / "l.c"
+    names = {"coli_norm_append_desc": "q_out_stride", "coli_tree_desc": "out_stride", "coli_verify_desc": "draft_stride",
+             "coli_compact_desc": "layers"}
+    body = "".join(f'printf("%zu %zu\\n", sizeof({n}), offsetof({n}, {f}));' for n, f in names.items())
+    src.write_text('#include <stdio.h>\n#include "colidraft.h"\nint main(void){' + body + "return 0;}")
+    exe = tmp_path / "l"
+    subprocess.run(["gcc", "-I", os.path.join(ROOT, "include"), str(src), "-o", str(exe)], check=True)
+    got = [tuple(map(int, l.split())) for l in subprocess.run([str(exe)], capture_output=True, text=True,
+                                                              check=True).stdout.splitlines()]
+    want = [(ctypes.sizeof(getattr(q, n)), getattr(getattr(q, n), f).offset) for n, f in names.items()]
+    assert got == want
+
+
+def cache(q, **over):
+    d = dict(k=FAKE, v=FAKE, fmt=1, pages=10, page_size=16, heads=4, dim=128)
+    d.update(over)
+    return q.make_kv_cache(**d)
+
+
+def call(lib, fn, make, desc, args, over):
+    d, a = dict(desc), dict(args)
+    for k, v in over.items():
+        (d if k in d else a)[k] = v
+    return fn(make(**d), raise_on_error=False, **a)
+
+
+def append(lib, c=None, **over):
+    desc = dict(tokens=3, q_heads=8, seqs=3, table_width=5, act=0, rotary=64, interleaved=0, eps=1e-6, q_stride=0, k_stride=0,
+                v_stride=0, q_out_stride=0)
+    args = dict(cache=c or cache(lib), q=FAKE, k=FAKE, v=FAKE, q_norm=FAKE, k_norm=FAKE, inv_freq=FAKE, seq=FAKE, pos=FAKE,
+                place=FAKE, table=FAKE, q_out=FAKE, err=None)
+    return call(lib, lib.coli_norm_append, lib.make_norm_append_desc, desc, args, over)
+
+
+def tree(lib, c=None, **over):
+    desc = dict(seqs=2, rows=20, nodes=10, q_heads=8, table_width=5, act=0, scale=0.1, window=0, q_stride=0, out_stride=0)
+    args = dict(cache=c or cache(lib), q=FAKE, first=FAKE, past=FAKE, parent=FAKE, table=FAKE, out=FAKE, lse=FAKE, err=None, ws=FAKE,
+                ws_bytes=1 << 40)
+    return call(lib, lib.coli_attn_tree, lib.make_tree_desc, desc, args, over)
+
+
+def verify(lib, **over):
+    desc = dict(seqs=2, rows=20, nodes=10, vocab=1000, act=0, mode=0, target_stride=0, draft_stride=0)
+    args = dict(target=FAKE, draft=FAKE, tokens=FAKE, parent=FAKE, uniform=FAKE, first=FAKE, path=FAKE, count=FAKE, next=FAKE,
+                err=None)
+    return call(lib, lib.coli_draft_verify, lib.make_verify_desc, desc, args, over)
+
+
+def compact(lib, caches=None, **over):
+    desc = dict(seqs=2, nodes=10, table_width=5, layers=2)
+    args = dict(caches=lib.make_kv_caches(caches or [cache(lib)] * 2), past=FAKE, path=FAKE, count=FAKE, table=FAKE, err=None)
+    return call(lib, lib.coli_kv_compact, lib.make_compact_desc, desc, args, over)
+
+
+def copy(lib, caches=None, **over):
+    a = dict(layers=2, n=3, src=FAKE, dst=FAKE, err=None)
+    a.update(over)
+    return lib.coli_kv_copy_pages(lib.make_kv_caches(caches or [cache(lib)] * 2), raise_on_error=False, **a)
+
+
+@pytest.mark.parametrize("over,code", [
+    (dict(k=None), "EINVAL"), (dict(v=None), "EINVAL"), (dict(fmt=0), "EINVAL"), (dict(fmt=4), "EINVAL"), (dict(pages=0), "EINVAL"),
+    (dict(page_size=0), "EINVAL"), (dict(heads=0), "EINVAL"), (dict(heads=2000), "EINVAL"), (dict(dim=0), "EINVAL"),
+    (dict(dim=100), "ENOTSUP"), (dict(dim=264), "ENOTSUP"), (dict(fmt=3, dim=72), "ENOTSUP"), (dict(k=FAKE + 8), "EALIGN"),
+    (dict(v=FAKE + 2), "EALIGN"), (dict(token_stride=64), "EINVAL"), (dict(head_stride=-128), "EINVAL"),
+    (dict(page_stride=0), "EINVAL"), (dict(token_stride=132), "EALIGN"), (dict(k_scale=FAKE + 1), "EALIGN")])
+def test_bad_caches_are_refused_everywhere(q, over, code):
+    want = getattr(q, "COLI_MOE_" + code)
+    c = cache(q, **over)
+    assert append(q, c) == want
+    assert tree(q, c) == want
+    assert q.coli_tree_workspace_bytes(q.make_tree_desc(2, 20, 10, 8, 5, 0, 0.1), c) == 0
+    assert compact(q, [c, cache(q)]) == want
+    assert copy(q, [c, cache(q)]) == want
+    # in the second layer too, where another shape is refused first
+    assert compact(q, [cache(q), c]) in (want, q.COLI_MOE_EINVAL) and copy(q, [cache(q), c]) in (want, q.COLI_MOE_EINVAL)
+
+
+@pytest.mark.parametrize("over,code", [
+    (dict(tokens=0), "EINVAL"), (dict(q_heads=-1), "EINVAL"), (dict(q_heads=2000), "EINVAL"), (dict(seqs=0), "EINVAL"),
+    (dict(table_width=0), "EINVAL"), (dict(table_width=1 << 28), "EINVAL"), (dict(act=3), "EINVAL"),
+    (dict(rotary=-2), "EINVAL"), (dict(rotary=63), "EINVAL"), (dict(rotary=130), "EINVAL"), (dict(interleaved=2), "EINVAL"),
+    (dict(eps=-1e-6), "EINVAL"), (dict(eps=float("nan")), "EINVAL"), (dict(eps=float("inf")), "EINVAL"),
+    (dict(k=None), "EINVAL"), (dict(v=None), "EINVAL"), (dict(pos=None), "EINVAL"), (dict(table=None), "EINVAL"),
+    (dict(inv_freq=None), "EINVAL"), (dict(q=None), "EINVAL"), (dict(q_out=None), "EINVAL"), (dict(q_heads=0), "EINVAL"),
+    (dict(q_heads=0, q=None, q_out=None), "EINVAL"), (dict(seq=None, tokens=4), "EINVAL"), (dict(q_stride=1000), "EINVAL"),
+    (dict(k_stride=511), "EINVAL"), (dict(v_stride=-1), "EINVAL"), (dict(q_stride=1100), "EINVAL"), (dict(q=FAKE + 2), "EALIGN"),
+    (dict(k=FAKE + 1), "EALIGN"), (dict(err=FAKE + 2), "EALIGN"), (dict(pos=FAKE + 1), "EALIGN"), (dict(place=FAKE + 2), "EALIGN"),
+    (dict(q_norm=FAKE + 2), "EALIGN"), (dict(k_norm=FAKE + 1), "EALIGN")])
+def test_append_refusals(q, over, code):
+    # q and q_out are the same rows here, so unequal strides are refused too; norms of no queries as well
+    assert append(q, **over) == getattr(q, "COLI_MOE_" + code)
+
+
+@pytest.mark.parametrize("over,code", [
+    (dict(seqs=0), "EINVAL"), (dict(seqs=1025), "EINVAL"), (dict(rows=0), "EINVAL"), (dict(nodes=0), "EINVAL"),
+    (dict(nodes=257), "EINVAL"), (dict(q_heads=0), "EINVAL"), (dict(q_heads=6), "EINVAL"), (dict(q_heads=2048), "EINVAL"),
+    (dict(table_width=0), "EINVAL"), (dict(table_width=1 << 27), "EINVAL"), (dict(act=-1), "EINVAL"), (dict(window=-1), "EINVAL"),
+    (dict(scale=float("nan")), "EINVAL"), (dict(scale=float("inf")), "EINVAL"), (dict(q_stride=8), "EINVAL"),
+    (dict(out_stride=-8), "EINVAL"), (dict(q=None), "EINVAL"), (dict(out=None), "EINVAL"), (dict(first=None), "EINVAL"),
+    (dict(past=None), "EINVAL"), (dict(table=None), "EINVAL"), (dict(q=FAKE + 1), "EALIGN"), (dict(first=FAKE + 2), "EALIGN"),
+    (dict(parent=FAKE + 2), "EALIGN"), (dict(lse=FAKE + 2), "EALIGN"), (dict(ws=None), "EWORKSPACE"),
+    (dict(ws=FAKE + 16), "EWORKSPACE"), (dict(ws_bytes=0), "EWORKSPACE")])
+def test_tree_refusals(q, over, code):
+    assert tree(q, **over) == getattr(q, "COLI_MOE_" + code)
+
+
+def test_tree_workspace(q):
+    d = q.make_tree_desc(2, 20, 10, 8, 5, 0, 0.1)
+    n = q.coli_tree_workspace_bytes(d, cache(q))
+    assert n > 0 and n % 256 == 0
+    assert tree(q, ws_bytes=n - 1) == q.COLI_MOE_EWORKSPACE
+    assert q.coli_tree_workspace_bytes(q.make_tree_desc(2, 20, 300, 8, 5, 0, 0.1), cache(q)) == 0
+
+
+@pytest.mark.parametrize("over,code", [
+    (dict(seqs=0), "EINVAL"), (dict(seqs=65536), "EINVAL"), (dict(rows=0), "EINVAL"), (dict(nodes=0), "EINVAL"),
+    (dict(nodes=1025), "EINVAL"), (dict(vocab=0), "EINVAL"), (dict(vocab=2 ** 20 + 1), "EINVAL"), (dict(act=3), "EINVAL"),
+    (dict(mode=2), "EINVAL"), (dict(mode=1), "EINVAL"), (dict(mode=1, draft=None), "EINVAL"), (dict(uniform=None), "EINVAL"),
+    (dict(target=None), "EINVAL"), (dict(tokens=None), "EINVAL"), (dict(first=None), "EINVAL"), (dict(path=None), "EINVAL"),
+    (dict(count=None), "EINVAL"), (dict(next=None), "EINVAL"), (dict(target_stride=999), "EINVAL"), (dict(draft_stride=-1), "EINVAL"),
+    (dict(target=FAKE + 2), "EALIGN"), (dict(draft=FAKE + 1), "EALIGN"), (dict(tokens=FAKE + 2), "EALIGN"),
+    (dict(uniform=FAKE + 1), "EALIGN"), (dict(err=FAKE + 2), "EALIGN")])
+def test_verify_refusals(q, over, code):
+    assert verify(q, **over) == getattr(q, "COLI_MOE_" + code)
+
+
+@pytest.mark.parametrize("over,code", [
+    (dict(seqs=0), "EINVAL"), (dict(seqs=65536), "EINVAL"), (dict(nodes=0), "EINVAL"), (dict(table_width=0), "EINVAL"),
+    (dict(table_width=1 << 28), "EINVAL"), (dict(layers=0), "EINVAL"), (dict(past=None), "EINVAL"), (dict(path=None), "EINVAL"),
+    (dict(count=None), "EINVAL"), (dict(table=None), "EINVAL"), (dict(path=FAKE + 2), "EALIGN"), (dict(err=FAKE + 1), "EALIGN")])
+def test_compact_refusals(q, over, code):
+    assert compact(q, **over) == getattr(q, "COLI_MOE_" + code)
+
+
+@pytest.mark.parametrize("over,code", [
+    (dict(n=0), "EINVAL"), (dict(layers=0), "EINVAL"), (dict(src=None), "EINVAL"), (dict(dst=None), "EINVAL"),
+    (dict(src=FAKE + 2), "EALIGN"), (dict(dst=FAKE + 1), "EALIGN"), (dict(err=FAKE + 1), "EALIGN")])
+def test_copy_refusals(q, over, code):
+    assert copy(q, **over) == getattr(q, "COLI_MOE_" + code)
+
+
+@pytest.mark.parametrize("other", [dict(fmt=2), dict(pages=11), dict(page_size=8), dict(heads=2), dict(dim=64), dict(page_stride=16 * 4 * 256)])
+def test_layers_of_other_shapes_are_refused(q, other):
+    caches = [cache(q), cache(q, **other)]
+    assert compact(q, caches) == q.COLI_MOE_EINVAL and copy(q, caches) == q.COLI_MOE_EINVAL
+
+
+def test_fewer_caches_than_layers(q):
+    for f in (compact, copy):
+        with pytest.raises(ValueError):
+            f(q, [cache(q)])
+
+
+# ---------------------------------------------------------------------- nodes and places
+@pytest.fixture(scope="module")
+def index(tmp_path_factory):
+    d = tmp_path_factory.mktemp("draft")
+    src = d / "draft.cc"
+    src.write_text('''
+#include "draft_index.h"
+using namespace colimoe;
+extern "C" void rows(int r0, int r1, int rows, int nodes, int *out) { draft_rows(r0, r1, rows, nodes, out[0], out[1], out[2]); }
+extern "C" void places(int given, int n, int width, int page_size, int *out) {
+    out[1] = n;
+    draft_places(given, width, page_size, out[0], out[1], out[2]);
+}
+extern "C" int start(int past, int window) { return draft_start(past, window); }
+extern "C" int sees(int past, int depth, int window, int t) { return draft_sees(past, depth, window, t); }
+''')
+    so = d / "libdraft.so"
+    inc = os.path.join(ROOT, "quantized_expert_decode_gb300", "csrc")
+    subprocess.run(["g++", "-std=c++17", "-shared", "-fPIC", "-I", inc, str(src), "-o", str(so)], check=True)
+    return ctypes.CDLL(str(so))
+
+
+TOP = 2 ** 31 - 1
+
+
+@pytest.mark.parametrize("r0,r1,rows,nodes,want", [
+    (0, 5, 10, 8, (0, 5, 0)), (3, 3, 10, 8, (3, 0, 0)), (10, 10, 10, 8, (10, 0, 0)), (2, 10, 10, 8, (2, 8, 0)),
+    (2, 11, 10, 16, (2, 8, 1)), (0, 9, 10, 8, (0, 8, 1)), (-1, 4, 10, 8, (0, 4, 1)), (5, 4, 10, 8, (5, 0, 1)),
+    (12, 14, 10, 8, (10, 0, 1)), (-2 ** 31, TOP, 10, 8, (0, 8, 1)), (TOP, -2 ** 31, 10, 8, (10, 0, 1)),
+    (0, TOP, TOP, 256, (0, 256, 1)), (TOP - 1, TOP, TOP, 256, (TOP - 1, 1, 0)), (-5, -3, 10, 8, (0, 0, 1))])
+def test_rows_of_a_sequence(index, r0, r1, rows, nodes, want):
+    out = (ctypes.c_int * 3)()
+    index.rows(r0, r1, rows, nodes, out)
+    assert tuple(out) == want
+
+
+@pytest.mark.parametrize("given,n,width,ps,want", [
+    (0, 5, 4, 16, (0, 5, 0)), (59, 5, 4, 16, (59, 5, 0)), (60, 5, 4, 16, (59, 5, 2)), (-1, 5, 4, 16, (0, 5, 2)),
+    (0, 64, 4, 16, (0, 64, 0)), (0, 65, 4, 16, (0, 64, 2)), (7, 65, 4, 16, (0, 64, 2)), (TOP, 5, 4, 16, (59, 5, 2)),
+    (-2 ** 31, 1, 1, 1, (0, 1, 2)), (TOP - 3, 3, TOP, 1, (TOP - 3, 3, 0)), (TOP, 3, TOP, 1, (TOP - 3, 3, 2)),
+    (99, 0, 4, 16, (64, 0, 0)), (64, 0, 4, 16, (64, 0, 0))])
+def test_places_of_nodes(index, given, n, width, ps, want):
+    # (what a sequence without nodes has committed does not matter)
+    out = (ctypes.c_int * 3)()
+    index.places(given, n, width, ps, out)
+    assert tuple(out) == want
+
+
+@pytest.mark.parametrize("past", [0, 1, 5, 64, 1000, TOP - 300])
+@pytest.mark.parametrize("window", [0, 1, 2, 5, 6, 64, 1001, TOP])
+def test_what_a_window_leaves(index, past, window):
+    first = index.start(past, window)
+    for depth in (0, 1, 4, 200):
+        for t in {0, 1, past // 2, max(0, past - window - 1), max(0, past - window), max(0, past - window + 1), past - 1}:
+            if 0 <= t < past:
+                want = window == 0 or past + depth - t < window
+                assert bool(index.sees(past, depth, window, t)) == want
+                assert not want or t >= first
+    if 0 < first:
+        assert index.sees(past, 0, window, first) or first == past
+        assert not index.sees(past, 0, window, first - 1)
