@@ -32,8 +32,9 @@
 extern "C" {
 #endif
 
-/* a further bit of the error word, beside COLI_LAYER_* */
+/* further bits of the error word, beside COLI_LAYER_* */
 #define COLI_DRAFT_BAD_NODE 8 /* a parent, a token or an entry of a path that cannot be */
+#define COLI_DRAFT_EXPIRED 16 /* a wait inside the attention was given up (its output is void) */
 
 /* Append with norms: as coli_append_desc, and `eps` of the norms. */
 typedef struct {

@@ -43,7 +43,7 @@ COLI_LAYER_BAD_PAGE, COLI_LAYER_BAD_POSITION, COLI_LAYER_BAD_SEQUENCE = 1, 2, 4
 LAYER_EXPORTS = ("coli_kv_append", "coli_attn_workspace_bytes", "coli_attn_decode", "coli_block_norms")
 
 # include/colidraft.h: a step on drafted tokens
-COLI_DRAFT_BAD_NODE = 8
+COLI_DRAFT_BAD_NODE, COLI_DRAFT_EXPIRED = 8, 16
 COLI_VERIFY_SAMPLE, COLI_VERIFY_GREEDY = 0, 1
 
 # every symbol include/colidraft.h declares

@@ -40,19 +40,13 @@
 
 #include "act.cuh"
 #include "attn.h"
+#include "attn_parts.cuh"
 #include "pdl.cuh"
 #include "ptx.cuh"  // smem_u32
 
 namespace colimoe {
 
 namespace attn {
-
-// `bytes` of 16 are copied, the rest are zeros (of 0, src is not read)
-__device__ __forceinline__ void copy16(uint32_t dst, const void *src, uint32_t bytes) {
-    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N> __device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
 __device__ __forceinline__ void ldm4(uint32_t (&r)[4], uint32_t a) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -67,12 +61,6 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
     return y;
 }
-__device__ __forceinline__ float exp2_fast(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
 // d = a b (+ d)
 template <int FMT, bool ADD>
 __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -85,42 +73,6 @@ __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint3
         asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
             : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
             : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
-}
-
-// two e4m3 values to two f16 values (exact; NaN stays NaN)
-__device__ __forceinline__ uint32_t widen(uint32_t two_bytes) {
-    uint32_t y;
-    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}" : "=r"(y) : "r"(two_bytes));
-    return y;
-}
-__device__ __forceinline__ uint32_t widen_hi(uint32_t four_bytes) {
-    uint32_t y;
-    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, hi;\n\t}" : "=r"(y) : "r"(four_bytes));
-    return y;
-}
-
-// the leading part of (a, b) in the matrix type as two packed 16-bit values; a, b keep the rest
-template <int FMT>
-__device__ __forceinline__ uint32_t take_part(float &a, float &b) {
-    uint32_t r;
-    if (FMT == COLI_KV_BF16) {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-        a -= __low2float(h);
-        b -= __high2float(h);
-        r = *reinterpret_cast<const uint32_t *>(&h);
-    } else {
-        const __half2 h = __floats2half2_rn(a, b);
-        a -= __low2float(h);
-        b -= __high2float(h);
-        r = *reinterpret_cast<const uint32_t *>(&h);
-    }
-    return r;
-}
-
-__device__ __forceinline__ float load_act(const void *p, int64_t i, int act) {
-    return act == COLI_ACT_F32 ? ((const float *)p)[i]
-           : act == COLI_ACT_BF16 ? to_f32(((const __nv_bfloat16 *)p)[i])
-                                  : to_f32(((const __half *)p)[i]);
 }
 
 __device__ __forceinline__ void add_scaled(float4 &x, const float4 &y, float f) {

@@ -1,127 +1,146 @@
-// attn_tree.cu — coli_attn_tree: attention of drafted nodes over a paged cache.
-//
-// A CTA per node and query head; its warps take every fourth token, a lane holds 8 elements of the head, and each warp
-// keeps a running maximum and sum; the warps' parts are joined at the end.
-#include <cmath>
-
-#include "act.cuh"
-#include "attn.h"
-#include "draft.h"
+// attn_tree.cu — coli_attn_tree: how a call is laid out, and the join of the items that a run's border cut
+// (tree_kernel.cuh has the streaming kernel).
 #include "host.h"
 #include "pdl.cuh"
+#include "tree.h"
 
 namespace colimoe {
+
 namespace {
 
-constexpr int kWarps = 4;
+constexpr int kPer = 2;  // float4 columns of a thread
 
-template <typename C>
-__global__ void __launch_bounds__(kWarps * 32) attn_tree_kernel(const TreeParams P) {
-    constexpr int kPer = 8;
-    __shared__ uint32_t line[8];  // the node's ancestors and itself
-    __shared__ int depth_of;
-    __shared__ float red[kWarps][256], red_m[kWarps], red_l[kWarps];
-    wait_for_previous();
+// One block per (border between runs, kPer columns of four): the blocks of an item's first cut add up the partial sums
+// of all runs that hold units of the item, in their order. A thread has a row. Everything is scaled to the largest m, by
+// exact powers of two.
+__global__ void __launch_bounds__(kTreeRows) attn_tree_join_kernel(const TreeParams P, const TreeWork W, int shift) {
     let_next_start();
-    const int b = blockIdx.x / P.nodes, i = blockIdx.x % P.nodes, h = blockIdx.y, kh = h / (P.q_heads / P.kv_heads);
-    const int w = threadIdx.x / 32, lane = threadIdx.x % 32;
-    int row, n, past, why, why2;
-    draft_rows(P.first[b], P.first[b + 1], P.rows, P.nodes, row, n, why);
-    draft_places(P.past[b], P.table_width, P.cache.page_size, past, n, why2);
-    if ((why || why2) && i == 0 && h == 0 && threadIdx.x == 0 && P.err)
-        atomicOr(P.err, (why ? COLI_LAYER_BAD_SEQUENCE : 0) | (why2 ? COLI_LAYER_BAD_POSITION : 0));
-    if (i >= n) return;
-    if (threadIdx.x < 8) line[threadIdx.x] = 0;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        auto parent = [&](int x) {
-            int p = P.parent ? P.parent[row + x] : x - 1;
-            if (p < -1 || p >= x) {
-                p = -1;
-                if (P.err) atomicOr(P.err, COLI_DRAFT_BAD_NODE);
-            }
-            return p;
-        };
-        int d = 0;
-        for (int x = i; x >= 0; x = parent(x), d++)
-            if (P.window == 0 || d < P.window) line[x / 32] |= 1u << x % 32;
-        depth_of = d - 1;
+    wait_for_previous();
+    const int c = blockIdx.x + 1, runs = W.cuts[0].runs;
+    if (c >= runs) return;
+    const TreeCut cut = W.cuts[c];
+    if (cut.b < 0) return;
+    const int group = P.q_heads / P.kv_heads, r = threadIdx.x;
+    int row, n, past, why;
+    draft_rows(P.first[cut.b], P.first[cut.b + 1], P.rows, P.nodes, row, n, why);
+    draft_places(P.past[cut.b], P.table_width, P.cache.page_size, past, n, why);
+    const TreeItem it = tree_item(cut.item, (n * group + kTreeRows - 1) / kTreeRows, W.halves);
+    const int at = it.tile * kTreeRows + r;
+    if (at >= n * group) return;
+    const int c0 = c - 1, col = blockIdx.y * kPer;
+    float4 o[kPer];
+    float l = 0.f, m = -INFINITY;
+#pragma unroll
+    for (int j = 0; j < kPer; j++) o[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+    for (int k = c0; k <= cut.last; k++) {
+        const int64_t s = 2 * (int64_t)k + (k == c0 ? 1 : 0);
+        const float2 e = W.part_ml[s * kTreeRows + r];
+        float4 v[kPer];
+#pragma unroll
+        for (int j = 0; j < kPer; j++) v[j] = W.part_o[(s * (W.cols / 4) + col + j) * kTreeRows + r];
+        const float top = fmaxf(m, e.x), ref = top == -INFINITY ? 0.f : top;
+        const float f0 = exp2f(m - ref), f1 = exp2f(e.x - ref);
+        m = top;
+        l = fmaf(l, f0, e.y * f1);
+#pragma unroll
+        for (int j = 0; j < kPer; j++) {
+            o[j].x = fmaf(o[j].x, f0, v[j].x * f1);
+            o[j].y = fmaf(o[j].y, f0, v[j].y * f1);
+            o[j].z = fmaf(o[j].z, f0, v[j].z * f1);
+            o[j].w = fmaf(o[j].w, f0, v[j].w * f1);
+        }
     }
-    __syncthreads();
-    const int depth = depth_of;
-    const bool in = lane * kPer < P.dim;
-    float q[kPer], o[kPer], m = -INFINITY, l = 0.f;
-    const int64_t at = (row + i) * P.q_stride + (int64_t)h * P.dim + lane * kPer;
-    const float ks = (P.k_scale ? P.k_scale[kh] : 1.f) * P.scale, vs = P.v_scale ? P.v_scale[kh] : 1.f;
+    const int node = at / group, head = it.kh * group + at - node * group;
+    const float norm = l == 0.f ? 0.f : (P.v_scale ? P.v_scale[it.kh] : 1.f) / l;
+    const int64_t out = (int64_t)(row + node) * P.out_stride + (int64_t)head * P.dim;
 #pragma unroll
     for (int j = 0; j < kPer; j++) {
-        o[j] = 0.f;
-        q[j] = !in ? 0.f
-               : P.act == COLI_ACT_F32 ? ((const float *)P.q)[at + j]
-               : P.act == COLI_ACT_BF16 ? to_f32(((const __nv_bfloat16 *)P.q)[at + j])
-                                        : to_f32(((const __half *)P.q)[at + j]);
+        const int d = it.half * W.cols + (col + j) * 4;
+        if (d >= P.dim) continue;  // (a multiple of 8)
+        store_act(P.out, out + d, o[j].x * norm, P.act);
+        store_act(P.out, out + d + 1, o[j].y * norm, P.act);
+        store_act(P.out, out + d + 2, o[j].z * norm, P.act);
+        store_act(P.out, out + d + 3, o[j].w * norm, P.act);
     }
-    const int32_t *pages = P.table + (int64_t)b * P.table_width;
-    for (int64_t t = (int64_t)draft_start(past, P.window) + w; t < (int64_t)past + n; t += kWarps) {
-        const int j = (int)(t - past);
-        if (t >= past ? !(line[j / 32] >> j % 32 & 1) : !draft_sees(past, depth, P.window, (int)t)) continue;
-        int bad;
-        const int64_t off = kv_row(P.cache, pages, P.table_width, (int)t, kh, bad);
-        if (bad) {
-            if (lane == 0 && P.err) atomicOr(P.err, COLI_LAYER_BAD_PAGE);
-            continue;
-        }
-        Run<C, kPer> k, v;
-        float s = 0.f;
-        if (in) {
-            k.load((const C *)P.k_cache + off + lane * kPer);
-            v.load((const C *)P.v_cache + off + lane * kPer);
-#pragma unroll
-            for (int e = 0; e < kPer; e++) s = fmaf(q[e], to_f32(k.e[e]), s);
-        }
-#pragma unroll
-        for (int x = 16; x; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-        s *= ks;
-        const float top = fmaxf(m, s), f = m == -INFINITY ? 0.f : expf(m - top), p = expf(s - top);
-        m = top;
-        l = fmaf(l, f, p);
-        if (in)
-#pragma unroll
-            for (int e = 0; e < kPer; e++) o[e] = fmaf(o[e], f, p * to_f32(v.e[e]));
-    }
-    if (in)
-#pragma unroll
-        for (int e = 0; e < kPer; e++) red[w][lane * kPer + e] = o[e];
-    if (lane == 0) red_m[w] = m, red_l[w] = l;
-    __syncthreads();
-    float top = -INFINITY, sum = 0.f, f[kWarps];
-#pragma unroll
-    for (int k = 0; k < kWarps; k++) top = fmaxf(top, red_m[k]);
-#pragma unroll
-    for (int k = 0; k < kWarps; k++) {
-        f[k] = red_m[k] == -INFINITY ? 0.f : expf(red_m[k] - top);
-        sum = fmaf(red_l[k], f[k], sum);
-    }
-    for (int d = threadIdx.x; d < P.dim; d += kWarps * 32) {
-        float v = 0.f;
-#pragma unroll
-        for (int k = 0; k < kWarps; k++) v = fmaf(red[k][d], f[k], v);
-        store_act(P.out, (row + i) * P.out_stride + (int64_t)h * P.dim + d, sum == 0.f ? 0.f : v / sum * vs, P.act);
-    }
-    if (threadIdx.x == 0 && P.lse) P.lse[(int64_t)(row + i) * P.q_heads + h] = sum == 0.f ? -INFINITY : top + logf(sum);
+    if (P.lse && it.half == 0 && col == 0)
+        P.lse[(int64_t)(row + node) * P.q_heads + head] = attn_lse(m == -INFINITY ? 0.f : m, l, shift);
+}
+
+struct Layout {
+    TreeWork w;
+    int64_t units;  // at most
+    int grid;
+    size_t ml, o, total;
+};
+
+template <int FMT, int DP, bool WIDE>
+void take(TreeWork &w) {
+    using T = TreeTraits<FMT, DP, WIDE>;
+    w.cols = T::kCols;
+    w.tile = T::kTile;
+    w.halves = T::kHalves;
+}
+template <int FMT>
+void take_format(TreeWork &w) {
+    if (w.dim == 64) w.wide ? take<FMT, 64, true>(w) : take<FMT, 64, false>(w);
+    else if (w.dim == 128) w.wide ? take<FMT, 128, true>(w) : take<FMT, 128, false>(w);
+    else w.wide ? take<FMT, 256, true>(w) : take<FMT, 256, false>(w);
+}
+
+Layout layout_of(const TreeParams &P) {
+    Layout L{};
+    const int group = P.q_heads / P.kv_heads;
+    L.w.dim = P.dim <= 64 ? 64 : P.dim <= 128 ? 128 : 256;
+    // q in one part where the cache's type (f16 for e4m3, scaled) holds it
+    L.w.wide = P.act == COLI_ACT_F32 || (P.act == COLI_ACT_F16 && P.fmt == COLI_KV_BF16);
+    if (P.fmt == COLI_KV_BF16) take_format<COLI_KV_BF16>(L.w);
+    else if (P.fmt == COLI_KV_F16) take_format<COLI_KV_F16>(L.w);
+    else take_format<COLI_KV_E4M3>(L.w);
+    L.w.divide = kv_divide_by(P.cache.page_size);
+    const int size = P.fmt == COLI_KV_E4M3 ? 1 : 2;
+    attn_steps(P.cache, P.kv_heads, size, L.w.off_shift);
+    L.w.page_step = (uint32_t)(P.cache.page_stride * size >> L.w.off_shift);
+    L.w.token_step = (uint32_t)(P.cache.token_stride * size >> L.w.off_shift);
+    L.w.head_step = (uint32_t)(P.cache.head_stride * size >> L.w.off_shift);
+    const int ab = P.act == COLI_ACT_F32 ? 4 : 2;
+    L.w.q_vec = reinterpret_cast<uintptr_t>(P.q) % 16 == 0 && P.q_stride * ab % 16 == 0;
+    L.w.out_vec = reinterpret_cast<uintptr_t>(P.out) % 16 == 0 && P.out_stride * ab % 16 == 0;
+    // no more CTAs than units that the page tables and the rows can name
+    const int64_t held = (int64_t)P.table_width * P.cache.page_size;
+    const int64_t nodes = P.nodes < held ? P.nodes : held;
+    const int64_t seen = P.window > 0 && P.window + nodes < held ? P.window + nodes : held;
+    const int64_t row_tiles = (nodes * group + kTreeRows - 1) / kTreeRows;
+    L.units = (seen + L.w.tile - 1) / L.w.tile * P.seqs * P.kv_heads * L.w.halves * row_tiles;
+    L.w.ctas = (int)(L.units < num_sms() ? L.units : num_sms());
+    L.grid = L.w.ctas;
+    auto up = [](size_t n) { return (n + 255) / 256 * 256; };
+    L.ml = up((size_t)L.w.ctas * sizeof(TreeCut));
+    L.o = L.ml + up((size_t)2 * L.w.ctas * kTreeRows * sizeof(float2));
+    L.total = L.o + up((size_t)2 * L.w.ctas * kTreeRows * L.w.cols * 4);
+    return L;
 }
 
 }  // namespace
 
-size_t tree_workspace_bytes(const TreeParams &P) { return 256; }
+size_t tree_workspace_bytes(const TreeParams &P) {
+    const Layout L = layout_of(P);
+    return L.units > INT32_MAX ? 0 : L.total;  // units are counted in 32 bits
+}
 
 cudaError_t launch_attn_tree(const TreeParams &P, cudaStream_t s) {
-    const dim3 grid((unsigned)P.seqs * P.nodes, P.q_heads);
-    switch (P.fmt) {
-    case COLI_KV_BF16: return launch_overlapped(attn_tree_kernel<__nv_bfloat16>, grid, kWarps * 32, 0, s, P);
-    case COLI_KV_F16: return launch_overlapped(attn_tree_kernel<__half>, grid, kWarps * 32, 0, s, P);
-    default: return launch_overlapped(attn_tree_kernel<__nv_fp8_e4m3>, grid, kWarps * 32, 0, s, P);
-    }
+    Layout L = layout_of(P);
+    char *ws = (char *)P.ws;
+    L.w.cuts = (TreeCut *)ws;
+    L.w.part_ml = (float2 *)(ws + L.ml);
+    L.w.part_o = (float4 *)(ws + L.o);
+    const cudaError_t e = P.fmt == COLI_KV_BF16  ? launch_tree_bf16(P, L.w, L.grid, s)
+                          : P.fmt == COLI_KV_F16 ? launch_tree_f16(P, L.w, L.grid, s)
+                                                 : launch_tree_e4m3(P, L.w, L.grid, s);
+    if (e != cudaSuccess || L.w.ctas == 1) return e;  // no borders
+    // the join's blocks start while the streaming kernel runs and wait for its end
+    return launch_overlapped(attn_tree_join_kernel, dim3(L.w.ctas - 1, L.w.cols / (4 * kPer)), kTreeRows, 0, s, P, L.w,
+                             P.fmt == COLI_KV_BF16 ? 0 : 14);
 }
 
 }  // namespace colimoe

@@ -1,0 +1,10 @@
+// tree_bf16.cu — the streaming kernel of coli_attn_tree on bf16 caches.
+#include "tree_kernel.cuh"
+
+namespace colimoe {
+
+cudaError_t launch_tree_bf16(const TreeParams &P, const TreeWork &W, int grid, cudaStream_t s) {
+    return launch_tree<COLI_KV_BF16>(P, W, grid, s);
+}
+
+}  // namespace colimoe

@@ -1,0 +1,876 @@
+// tree_kernel.cuh — the streaming kernel of coli_attn_tree. Internal to libcolimoe; instantiated per cache type by
+// tree_bf16.cu, tree_f16.cu and tree_e4m3.cu.
+//
+// Mathematics. As in coli_attn_decode: with x_t = scale * log2(e) * q . k_t a running integer m >= max x_t is kept (the
+// maximum rounded up), l = sum 2^(x_t - m) and o = sum 2^(x_t - m) v_t; a larger m' scales l and o by 2^(m - m'), which
+// is exact, and so is every join of parts.
+//
+// Work. The rows of a sequence on one kv head are its (node, query head of the group) pairs, in tiles of 128 rows. An
+// item is a row tile (and, of heads beyond 128 elements, a half of V's columns) over the places that any of the
+// sequence's nodes sees, cut into units of kTile places. All items' units form one line that is cut into equal runs, one
+// per CTA; an item that is cut leaves partial sums in the workspace, which the join kernel adds up in a fixed order.
+//
+// Products, on the 5th-generation tensor cores: S [128 rows x kTile] = Q K^T from shared memory into tensor memory, then
+// O [128 x columns] = P V, with P written over S as 16-bit parts and V read from its rows as they lie (MN-major). q and p
+// enter as sums of parts in the cache's type (e4m3 widened to f16, exactly): a q that the type holds is one part (f16:
+// scaled by a power of two per row), an fp32 q three bf16 or two f16 parts; p two parts, or three in bf16 beside an
+// fp32 q; the smaller parts come first, so that fewer of the unit's truncations are of the whole sum. Each tile's O is
+// summed from zero and added in fp32 registers, so that the truncating accumulation never runs over more than a
+// tile and a rescaling costs nothing extra.
+//
+// Roles, 16 warps. Two groups of four warps take the tiles in turn, a thread has a row: maximum, exponents and parts of p.
+// The running maximum goes from one group to the other through shared memory. Four warps add the tiles' sums in
+// registers and write the results. Three warps copy K and V rows into a ring of slots (16-byte asynchronous copies into
+// the 128-byte swizzled layout; e4m3 through 8-bit staging that the same threads widen). One thread issues the products.
+// What a thread of one role leaves for another lies in rings of four tiles: the products of a tile wait for the sums of
+// two tiles before, and its scores for the products of two tiles before, so that no role runs four tiles ahead.
+//
+// Places that some rows see and others do not (nodes, the window's edge) lie in `mixed` tiles. There a row's visible
+// places are bits, what is not seen has p = 0, and infinities and NaN of V are taken out of the tile (0 times infinity
+// would reach every row) and added to the sums of the rows that do see them.
+#pragma once
+
+#include <atomic>
+
+#include "attn_parts.cuh"
+#include "pdl.cuh"
+#include "tc.cuh"
+#include "tree.h"
+
+namespace colimoe {
+
+namespace tree {
+
+constexpr int kWarps = 16, kThreads = kWarps * 32;
+constexpr int kSums = 8, kCopies = 12, kProducts = 15;  // the roles' first warps
+constexpr int kCopiers = (kProducts - kCopies) * 32;
+// registers of a thread: 128 at the launch, 2 * 120 + 184 + 88 = 4 * 128 behind it
+constexpr uint64_t kWaitNs = 2000000000;  // of a wait that should take microseconds
+constexpr uint32_t kNapNs = 1000000;      // a thread sleeps at most so long before it looks at the clock
+
+__device__ __forceinline__ void sync_softmax() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+__device__ __forceinline__ void sync_copiers() { asm volatile("bar.sync 2, 96;" ::: "memory"); }
+static_assert(kCopiers == 96, "sync_copiers");
+// arrives when this thread's copies so far have
+__device__ __forceinline__ void arrive_behind_copies(uint64_t *bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+template <int N> __device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N> __device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+
+// Small things in shared memory
+struct Misc {
+    uint32_t mask[kTreeRows][kTreeMaxNodes / 32];  // the nodes that a row sees
+    float qs[kTreeRows];                           // factor of a row's products, >= 0
+    int32_t low[kTreeRows];                        // the first cached place that a row sees
+    float m[4][kTreeRows], l[4][kTreeRows];        // behind a tile: the maximum; its group's sum of p
+    int16_t parent[kTreeMaxNodes];
+    int32_t pre[kTreeMaxSeqs + 1];  // units before a sequence
+    int32_t scan[kWarps];
+    uint32_t row_off[4][kTreeRows];  // of a tile's places in the pool, in steps
+    uint32_t seen[16][4];  // places of a tile that lie on good pages
+    uint32_t odd[4][4];    // places of a tile whose values' infinities and NaN are taken out
+    uint64_t full[8], empty[8], s_full[2], m_ready[2], p_ready[2], o_full[2], o_free[2], q_full, done;
+    uint32_t tmem;
+    int32_t dead;
+};
+
+// A sequence's share of the work
+struct Seq {
+    int32_t row, n, past, start, row_tiles, tiles, items;
+};
+template <typename T>
+__device__ __forceinline__ Seq seq_of(const TreeParams &P, int b, int &flags) {
+    Seq s;
+    int why, why2;
+    draft_rows(P.first[b], P.first[b + 1], P.rows, P.nodes, s.row, s.n, why);
+    draft_places(P.past[b], P.table_width, P.cache.page_size, s.past, s.n, why2);
+    flags = (why ? COLI_LAYER_BAD_SEQUENCE : 0) | (why2 ? COLI_LAYER_BAD_POSITION : 0);
+    s.start = draft_start(s.past, P.window);
+    s.row_tiles = (s.n * (P.q_heads / P.kv_heads) + kTreeRows - 1) / kTreeRows;
+    s.tiles = kv_units(s.past + s.n - s.start, T::kTile);
+    s.items = P.kv_heads * T::kHalves * s.row_tiles;
+    return s;
+}
+
+// A run's walk over the parts of items: `cnt` tiles of an item from tile u on
+template <typename T>
+struct Walk {
+    Seq s;
+    int32_t b, item, u, cnt;
+    uint32_t left;
+    __device__ __forceinline__ void begin(const TreeParams &P, const int32_t *pre, uint32_t at, uint32_t units) {
+        int lo = 0, hi = P.seqs;  // pre[lo] <= at < pre[hi]
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) / 2;
+            if ((uint32_t)pre[mid] <= at) lo = mid;
+            else hi = mid;
+        }
+        b = lo;
+        int f;
+        s = seq_of<T>(P, b, f);
+        const int off = (int)(at - (uint32_t)pre[b]);
+        item = off / s.tiles;
+        u = off - item * s.tiles;
+        left = units;
+        cnt = min((int)left, s.tiles - u);
+    }
+    __device__ __forceinline__ bool next(const TreeParams &P, const int32_t *pre) {
+        left -= cnt;
+        if (left == 0) return false;
+        u = 0;
+        if (++item == s.items) {
+            item = 0;
+            do b++;
+            while (pre[b + 1] == pre[b]);
+            int f;
+            s = seq_of<T>(P, b, f);
+        }
+        cnt = min((int)left, s.tiles);
+        return true;
+    }
+};
+
+// The places of copies in the order K0, K1, V0, K2, V1, ... of a part of an item
+__device__ __forceinline__ int k_copy(int j) { return j ? 2 * j - 1 : 0; }
+__device__ __forceinline__ int v_copy(int j, int cnt) { return j == cnt - 1 ? 2 * cnt - 1 : 2 * j + 2; }
+
+// Whether node i sees place t, from the parents themselves (for the rare places whose values are not finite)
+__device__ __forceinline__ bool node_sees(const TreeParams &P, Seq s, int i, int64_t t) {
+    int depth = 0;
+    bool hit = false;
+    for (int x = i; x >= 0; depth++) {
+        if (x == t - s.past) hit = P.window == 0 || depth < P.window;
+        int p = P.parent ? P.parent[s.row + x] : x - 1;
+        x = p < -1 || p >= x ? -1 : p;
+    }
+    return t < s.past ? draft_sees(s.past, depth - 1, P.window, (int32_t)t) : hit;
+}
+
+}  // namespace tree
+
+template <typename T>
+__global__ void __launch_bounds__(tree::kThreads, 1) attn_tree_kernel(const TreeParams P, const TreeWork W) {
+    using namespace tree;
+    using namespace attn;
+    constexpr int FMT = T::kFmt, DP = T::kDim, TN = T::kTile, NC = T::kCols;
+    constexpr int kSlab = TN * 128;  // bytes of a tile's 64 elements
+    using C = std::conditional_t<FMT == COLI_KV_BF16, __nv_bfloat16, std::conditional_t<FMT == COLI_KV_F16, __half, __nv_fp8_e4m3>>;
+    extern __shared__ __align__(1024) unsigned char sm[];
+    unsigned char *slots = sm + T::kQBytes, *raws = slots + T::kSlots * T::kSlotBytes;
+    Misc &S = *reinterpret_cast<Misc *>(raws + T::kRawSlots * T::kRawBytes);
+    static_assert(sizeof(Misc) <= T::kMiscBytes, "small things");
+    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+    const int group = P.q_heads / P.kv_heads;
+
+    wait_for_previous();
+    let_next_start();  // the join's blocks may wait beside this
+
+    // ---- units before each sequence
+    const int per = (P.seqs + kThreads - 1) / kThreads;
+    const int b0 = min(tid * per, P.seqs), b1 = min(b0 + per, P.seqs);
+    int mine = 0;
+    for (int b = b0; b < b1; b++) {
+        int flags;
+        const Seq s = seq_of<T>(P, b, flags);
+        if (flags && blockIdx.x == 0 && P.err) atomicOr(P.err, flags);
+        const int u = s.n ? s.items * s.tiles : 0;
+        S.pre[b + 1] = u;
+        mine += u;
+    }
+    int incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += v;
+    }
+    if (lane == 31) S.scan[warp] = incl;
+    __syncthreads();
+    int before = incl - mine;
+    for (int i = 0; i < warp; i++) before += S.scan[i];
+    for (int b = b0; b < b1; b++) {
+        before += S.pre[b + 1];
+        S.pre[b + 1] = before;
+    }
+    if (tid == 0) S.pre[0] = 0;
+    __syncthreads();
+    const AttnRuns R((uint32_t)S.pre[P.seqs], (uint32_t)W.ctas);
+    const uint32_t run = blockIdx.x;
+    if (R.runs == 0 && run == 0 && tid == 0) W.cuts[0].runs = 0;
+    if (run >= R.runs) return;
+    const uint32_t from = R.start(run), units = R.start(run + 1) - from;
+
+    // ---- barriers, tensor memory
+    if (tid == 0) {
+        for (int i = 0; i < T::kSlots; i++) {
+            mbar_init(&S.full[i], kCopiers);
+            mbar_init(&S.empty[i], 1);
+        }
+        for (int g = 0; g < 2; g++) {
+            mbar_init(&S.s_full[g], 1);
+            mbar_init(&S.m_ready[g], 128);
+            mbar_init(&S.p_ready[g], 128);
+            mbar_init(&S.o_full[g], 1);
+            mbar_init(&S.o_free[g], 128);
+        }
+        mbar_init(&S.q_full, 256);
+        mbar_init(&S.done, 1);
+        fence_mbar_init();
+        S.dead = 0;
+    }
+    if (warp == kProducts) {
+        tmem_alloc(&S.tmem, 512);
+        tmem_relinquish();
+        tc_fence_before_sync();
+    }
+    __syncthreads();
+    tc_fence_after_sync();
+    const uint32_t tmem = S.tmem;
+    auto score_at = [&](int g) { return tmem + g * T::kScoreCols; };
+    auto sums_at = [&](int g) { return tmem + 2 * T::kScoreCols + g * NC; };
+
+    // A wait that never ends is given up for good: the flag lets every other wait of the CTA pass, so that all threads
+    // reach their ends (with wrong sums, and an error told).
+    auto wait = [&](uint64_t *bar, uint32_t parity) {
+        if (mbar_try_wait(bar, parity)) return;
+        uint64_t since = 0;
+        while (!mbar_try_wait_for(bar, parity, kNapNs)) {
+            if (*(volatile int32_t *)&S.dead) return;
+            const uint64_t now = globaltimer_ns();
+            if (since == 0) since = now;
+            if (now - since > kWaitNs) {
+                *(volatile int32_t *)&S.dead = 1;
+                if (P.err) atomicOr(P.err, COLI_DRAFT_EXPIRED);
+                return;
+            }
+        }
+    };
+    auto wait_warp = [&](uint64_t *bar, uint32_t parity) {  // and the warp is together again
+        wait(bar, parity);
+        __syncwarp();
+    };
+
+    Walk<T> at;
+    if (warp < 8) {
+        // ================================================================ softmax: a thread has a row
+        regs_down<120>();
+        const int g = warp / 4, quad = warp % 4, r = quad * 32 + lane, wt = tid % 128;
+        const uint32_t lanes = (uint32_t)(quad * 32) << 16;
+        uint32_t count = 0, copies = 0, part = 0;
+        int last_b = -1;
+        at.begin(P, S.pre, from, units);
+        do {
+            const TreeItem it = tree_item(at.item, at.s.row_tiles, T::kHalves);
+            const int row0 = it.tile * kTreeRows, rows = min(kTreeRows, at.s.n * group - row0);
+            const bool active = quad * 32 < rows, real = r < rows;
+            if (part) sync_softmax();  // both groups are done with the queries and masks before
+            // ---- parents, visible nodes
+            if (P.parent && last_b != at.b) {
+                for (int i = tid; i < at.s.n; i += 256) {
+                    int p = P.parent[at.s.row + i];
+                    if (p < -1 || p >= i) {
+                        p = -1;
+                        if (P.err) atomicOr(P.err, COLI_DRAFT_BAD_NODE);
+                    }
+                    S.parent[i] = (int16_t)p;
+                }
+                last_b = at.b;
+                sync_softmax();
+            }
+            if (g == 0 && real) {
+                const int node = (row0 + r) / group;
+#pragma unroll
+                for (int i = 0; i < kTreeMaxNodes / 32; i++) S.mask[r][i] = 0;
+                int depth = 0;
+                for (int x = node; x >= 0; depth++) {
+                    if (P.window == 0 || depth < P.window) S.mask[r][x >> 5] |= 1u << (x & 31);
+                    x = P.parent ? S.parent[x] : x - 1;
+                }
+                const int64_t low = P.window ? (int64_t)at.s.past + depth - P.window : 0;  // (depth counts the node itself)
+                S.low[r] = low < 0 ? 0 : (int32_t)low;
+            }
+            // ---- queries: neighbouring lanes have neighbouring 8-element chunks of a row
+            {
+                constexpr int kCh = DP / 8, kRows = 32 / kCh;
+                const float ks = P.scale * 1.4426950408889634f * (P.k_scale ? P.k_scale[it.kh] : 1.f);
+                const float sign = ks < 0.f ? -1.f : 1.f;
+                const int ch = lane % kCh, sub = lane / kCh;
+#pragma unroll 2
+                for (int i = warp * kRows + sub; i < (rows + kRows - 1) / kRows * kRows; i += 8 * kRows) {
+                    float x[8];
+#pragma unroll
+                    for (int e = 0; e < 8; e++) x[e] = 0.f;
+                    if (i < rows && ch * 8 < P.dim) {
+                        const int nd = (row0 + i) / group, h = it.kh * group + (row0 + i - nd * group);
+                        const int64_t off = (int64_t)(at.s.row + nd) * P.q_stride + (int64_t)h * P.dim + ch * 8;
+                        if (W.q_vec) {
+                            if (P.act == COLI_ACT_F32) {
+                                Run<float, 8> v;
+                                v.load((const float *)P.q + off);
+#pragma unroll
+                                for (int e = 0; e < 8; e++) x[e] = v.e[e];
+                            } else if (P.act == COLI_ACT_BF16) {
+                                Run<__nv_bfloat16, 8> v;
+                                v.load((const __nv_bfloat16 *)P.q + off);
+#pragma unroll
+                                for (int e = 0; e < 8; e++) x[e] = to_f32(v.e[e]);
+                            } else {
+                                Run<__half, 8> v;
+                                v.load((const __half *)P.q + off);
+#pragma unroll
+                                for (int e = 0; e < 8; e++) x[e] = to_f32(v.e[e]);
+                            }
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 8; e++) x[e] = load_act(P.q, off + e, P.act);
+                        }
+                    }
+                    float up = 1.f, down = 1.f;
+                    if (FMT != COLI_KV_BF16) {
+                        // the row's largest element to [2^13, 2^14)
+                        float big = 0.f;
+#pragma unroll
+                        for (int e = 0; e < 8; e++) big = fmaxf(big, fabsf(x[e]));
+#pragma unroll
+                        for (int o = kCh / 2; o; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
+                        if (big > 0.f && big < INFINITY) {
+                            int e = 13 + 127 - (int)(__float_as_uint(big) >> 23);
+                            e = e > 126 ? 126 : e;
+                            up = __uint_as_float((uint32_t)(e + 127) << 23);
+                            down = __uint_as_float((uint32_t)(127 - e) << 23);
+                        }
+                    }
+                    if (ch == 0) S.qs[i] = fabsf(ks) * down;
+#pragma unroll
+                    for (int e = 0; e < 8; e++) x[e] *= up * sign;
+                    unsigned char *dst = sm + (ch / 8) * (kTreeRows * 128) + i * 128 + (((ch % 8) ^ (i & 7)) << 4);
+#pragma unroll
+                    for (int p = 0; p < T::kQParts; p++) {
+                        uint4 v;
+                        v.x = take_part<FMT>(x[0], x[1]);
+                        v.y = take_part<FMT>(x[2], x[3]);
+                        v.z = take_part<FMT>(x[4], x[5]);
+                        v.w = take_part<FMT>(x[6], x[7]);
+                        *(uint4 *)(dst + p * (kTreeRows * DP * 2)) = v;
+                    }
+                }
+            }
+            fence_async_smem();
+            mbar_arrive(&S.q_full);
+            wait_warp(&S.q_full, part & 1);
+            const float qs = real ? S.qs[r] : 0.f;
+            const int low = real ? S.low[r] : 0;
+            const int past = at.s.past;
+            float m = -INFINITY, l = 0.f;  // at this group's last tile
+
+            constexpr int kPieces = TN / 32, kPair = kPieces < 2 ? 1 : 2;
+            // the places of 32 from t on that the row sees, of those on good pages
+            auto visible = [&](int64_t t, uint32_t good) {
+                uint32_t v = 0;
+                if (t < past) {
+                    const int64_t a = low - t, e = past - t;  // cached: [a, e)
+                    v = a >= 32 ? 0u : a <= 0 ? 0xffffffffu : 0xffffffffu << (int)a;
+                    if (e < 32) v &= (1u << (int)e) - 1;
+                }
+                const int64_t j = t - past;  // nodes from here on
+                if (j > -32 && j < kTreeMaxNodes) {
+                    if (j >= 0) {
+                        const int w = (int)j >> 5;
+                        v |= __funnelshift_r(S.mask[r][w], w + 1 < kTreeMaxNodes / 32 ? S.mask[r][w + 1] : 0u, (int)j & 31);
+                    } else {
+                        v |= S.mask[r][0] << (int)-j;
+                    }
+                }
+                return real ? v & good : 0u;
+            };
+
+            for (int j = 0; j < at.cnt; j++) {
+                const uint32_t k = count + j;
+                if ((k & 1) != (uint32_t)g) continue;
+                const uint32_t parity = (k >> 1) & 1;
+                const int64_t t0 = (int64_t)at.s.start + (int64_t)(at.u + j) * TN;
+                wait_warp(&S.s_full[g], parity);
+                tc_fence_after_sync();
+                bool mixed = t0 + TN > past || (P.window && t0 <= (int64_t)past + at.s.n - 1 - P.window);
+#pragma unroll
+                for (int c = 0; c < kPieces; c++) mixed |= S.seen[k & 15][c] != 0xffffffffu;
+                // ---- the maximum. The row's scores are read twice, for the maximum and for the exponents, in pieces of 32
+                // columns; a load from tensor memory takes 200 to 400 cycles, so one is on its way behind the other.
+                const uint32_t sc = score_at(g) + lanes;
+                float top = -INFINITY;
+                if (active) {
+                    if (!mixed) {
+                        float most[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll 1
+                        for (int c = 0; c < kPieces; c += kPair) {
+                            uint32_t s[kPair][32];
+#pragma unroll
+                            for (int i = 0; i < kPair; i++) tmem_ld_x32(sc + 32 * (c + i), s[i]);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int i = 0; i < 32 * kPair; i++) most[i & 3] = fmaxf(most[i & 3], __uint_as_float(s[i / 32][i % 32]));
+                        }
+                        top = fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3]));
+                    } else {
+#pragma unroll 1
+                        for (int c = 0; c < kPieces; c++) {
+                            uint32_t s[32];
+                            tmem_ld_x32(sc + 32 * c, s);
+                            const uint32_t v = visible(t0 + 32 * c, S.seen[k & 15][c]);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int i = 0; i < 32; i++)
+                                if (v >> i & 1) top = fmaxf(top, __uint_as_float(s[i]));
+                        }
+                    }
+                }
+                float before = -INFINITY;
+                if (j > 0) {
+                    wait_warp(&S.m_ready[1 - g], ((k - 1) >> 1) & 1);
+                    before = S.m[(k - 1) & 3][r];
+                }
+                const float mn = fmaxf(before, ceilf(top * qs));
+                S.m[k & 3][r] = mn;
+                mbar_arrive(&S.m_ready[g]);
+                // ---- the exponents and their parts
+                if (active) {
+                    const float ref = mn == -INFINITY ? 0.f : mn;
+                    const float f = m == mn ? 1.f : exp2f(m - mn);
+                    m = mn;
+                    const float sub = ref - (float)T::kShift;
+                    float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+                    // scores of 16 places to parts of p in their place: 8 columns of first parts, then 8 of second ones
+                    auto parts = [&](uint32_t (&s)[16], int c, auto masked, uint32_t v) {
+                        uint32_t w[16], w3[8];
+#pragma unroll
+                        for (int i = 0; i < 8; i++) {
+                            float2 p = __ffma2_rn(make_float2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])),
+                                                  make_float2(qs, qs), make_float2(-sub, -sub));
+                            if (masked.value) {
+                                // beyond 2^22 the maximum, of rounded products, may lie below the exact ones; a NaN stays one
+                                p.x = p.x > (float)T::kShift ? (float)T::kShift : p.x;
+                                p.y = p.y > (float)T::kShift ? (float)T::kShift : p.y;
+                                if (!(v >> (2 * i) & 1)) p.x = -INFINITY;
+                                if (!(v >> (2 * i + 1) & 1)) p.y = -INFINITY;
+                            }
+                            p.x = exp2_fast(p.x);
+                            p.y = exp2_fast(p.y);
+                            sum[i & 1] = __fadd2_rn(sum[i & 1], p);
+                            w[i] = take_part2<FMT>(p);
+                            w[8 + i] = take_part2<FMT>(p);
+                            if (T::kPParts == 3) w3[i] = take_part2<FMT>(p);
+                        }
+                        tmem_st_x16(sc + 16 * c, w);
+                        if (T::kPParts == 3) tmem_st_x8(sc + TN + 8 * c, w3);
+                    };
+                    if (!mixed && !__any_sync(0xffffffffu, fabsf(ref) >= 0x1p22f)) {
+                        uint32_t s0[16], s1[16];
+                        tmem_ld_x16(sc, s0);
+#pragma unroll 1
+                        for (int c = 0; c < TN / 16; c += 2) {
+                            tmem_ld_wait();
+                            tmem_ld_x16(sc + 16 * (c + 1), s1);
+                            parts(s0, c, std::false_type{}, 0u);
+                            tmem_ld_wait();
+                            if (c + 2 < TN / 16) tmem_ld_x16(sc + 16 * (c + 2), s0);
+                            parts(s1, c + 1, std::false_type{}, 0u);
+                        }
+                    } else {
+#pragma unroll 1
+                        for (int c = 0; c < TN / 16; c++) {
+                            uint32_t s[16];
+                            tmem_ld_x16(sc + 16 * c, s);
+                            const uint32_t v = mixed ? visible(t0 + 16 * c, S.seen[k & 15][c / 2] >> (c % 2 * 16)) : 0xffffffffu;
+                            tmem_ld_wait();
+                            parts(s, c, std::true_type{}, v);
+                        }
+                    }
+                    l = fmaf(l, f, (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y));
+                    tmem_st_wait();
+                }
+                S.l[k & 3][r] = l;
+                const int vc = copies + v_copy(j, at.cnt);
+                uint32_t odds = 0;
+                if (mixed) {
+                    // ---- infinities and NaN among the values of this tile
+                    const int slot = vc % T::kSlots;
+                    wait_warp(&S.full[slot], (vc / T::kSlots) & 1);
+                    bool odd = false;
+                    if (wt < TN) {
+                        unsigned char *row = slots + slot * T::kSlotBytes + wt * 128;
+                        constexpr uint32_t kExp = FMT == COLI_KV_BF16 ? 0x7f807f80u : 0x7c007c00u;
+                        constexpr uint32_t kOne = FMT == COLI_KV_BF16 ? 0x00800080u : 0x04000400u;
+#pragma unroll
+                        for (int c = 0; c < NC / 8; c++) {
+                            uint4 v = *(uint4 *)(row + (c / 8) * kSlab + (((c % 8) ^ (wt & 7)) << 4));
+                            uint32_t hit = 0;
+#pragma unroll
+                            for (int e = 0; e < 4; e++) hit |= (((&v.x)[e] & kExp) + kOne) & 0x80008000u;
+                            if (hit) {
+                                odd = true;
+#pragma unroll
+                                for (int e = 0; e < 4; e++) {
+                                    const uint32_t x = (((&v.x)[e] & kExp) + kOne) & 0x80008000u;
+                                    if (x & 0x8000u) (&v.x)[e] &= 0xffff0000u;
+                                    if (x >> 31) (&v.x)[e] &= 0x0000ffffu;
+                                }
+                                *(uint4 *)(row + (c / 8) * kSlab + (((c % 8) ^ (wt & 7)) << 4)) = v;
+                            }
+                        }
+                    }
+                    odds = __ballot_sync(0xffffffffu, odd);
+                    fence_async_smem();
+                }
+                if (lane == 0) S.odd[k & 3][quad] = odds;
+                tc_fence_before_sync();
+                mbar_arrive(&S.p_ready[g]);
+            }
+            count += at.cnt;
+            copies += 2 * at.cnt;
+            part++;
+        } while (at.next(P, S.pre));
+    } else if (warp < kCopies) {
+        // ================================================================ sums: a thread has a row
+        regs_up<184>();
+        const int quad = warp % 4, r = quad * 32 + lane;
+        const uint32_t lanes = (uint32_t)(quad * 32) << 16;
+        uint32_t count = 0;
+        at.begin(P, S.pre, from, units);
+        do {
+            const TreeItem it = tree_item(at.item, at.s.row_tiles, T::kHalves);
+            const int row0 = it.tile * kTreeRows, rows = min(kTreeRows, at.s.n * group - row0);
+            const bool active = quad * 32 < rows, real = r < rows;
+            const int node = real ? (row0 + r) / group : 0;
+            float2 acc[NC / 2];
+            float m = -INFINITY, l = 0.f;
+#pragma unroll
+            for (int c = 0; c < NC / 2; c++) acc[c] = make_float2(0.f, 0.f);
+            for (int j = 0; j < at.cnt; j++) {
+                const uint32_t k = count + j, g = k & 1;
+                wait_warp(&S.o_full[g], (k >> 1) & 1);
+                tc_fence_after_sync();
+                if (active) {
+                    const float mn = S.m[k & 3][r];
+                    const float f = m == mn ? 1.f : exp2f(m - mn);
+                    m = mn;
+                    // the groups' sums of p are scaled to their own last maxima
+                    l = fmaf(j + 1 == at.cnt ? l : 0.f, f, S.l[k & 3][r]);
+#pragma unroll
+                    for (int c = 0; c < NC / 32; c++) {
+                        uint32_t o[32];
+                        tmem_ld_x32(sums_at(g) + lanes + 32 * c, o);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int i = 0; i < 16; i++)
+                            acc[16 * c + i] = __ffma2_rn(acc[16 * c + i], make_float2(f, f),
+                                                         make_float2(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1])));
+                    }
+#pragma unroll 1
+                    for (int c = 0; c < TN / 32; c++) {
+                        uint32_t odds = S.odd[k & 3][c];
+#pragma unroll 1
+                        while (odds) {
+                            const int64_t t = (int64_t)at.s.start + (int64_t)(at.u + j) * TN + 32 * c + __ffs(odds) - 1;
+                            odds &= odds - 1;
+                            int bad;
+                            const int64_t off = kv_row(P.cache, P.table + (int64_t)at.b * P.table_width, P.table_width, (int)t,
+                                                       it.kh, bad);
+                            if (!real || bad || !node_sees(P, at.s, node, t)) continue;
+                            const C *v = (const C *)P.v_cache + off + it.half * NC;
+#pragma unroll
+                            for (int d = 0; d < NC; d++) {
+                                if (it.half * NC + d >= P.dim) continue;
+                                const float x = to_f32(v[d]);
+                                if (!(fabsf(x) < INFINITY)) (d % 2 ? acc[d / 2].y : acc[d / 2].x) += x;
+                            }
+                        }
+                    }
+                }
+                tc_fence_before_sync();
+                mbar_arrive(&S.o_free[g]);
+            }
+            count += at.cnt;
+            if (real) {
+                const bool whole = at.cnt == at.s.tiles;
+                const int64_t slot = 2 * (int64_t)run + (at.u == 0 ? 1 : 0);
+                const int head = it.kh * group + (row0 + r - node * group);
+                if (!whole) {
+#pragma unroll
+                    for (int i = 0; i < NC; i += 4)
+                        W.part_o[(slot * (NC / 4) + i / 4) * kTreeRows + r] = make_float4(acc[i / 2].x, acc[i / 2].y, acc[i / 2 + 1].x, acc[i / 2 + 1].y);
+                    W.part_ml[slot * kTreeRows + r] = make_float2(m, l);
+                } else {
+                    const float norm = l == 0.f ? 0.f : (P.v_scale ? P.v_scale[it.kh] : 1.f) / l;
+                    const int64_t out = (int64_t)(at.s.row + node) * P.out_stride + (int64_t)head * P.dim + it.half * NC;
+#pragma unroll
+                    for (int i = 0; i < NC; i += 8) {
+                        if (it.half * NC + i >= P.dim) continue;
+                        float x[8];
+#pragma unroll
+                        for (int e = 0; e < 8; e++) x[e] = (e % 2 ? acc[(i + e) / 2].y : acc[(i + e) / 2].x) * norm;
+                        if (W.out_vec) {
+                            if (P.act == COLI_ACT_F32) {
+                                Run<float, 8> v;
+#pragma unroll
+                                for (int e = 0; e < 8; e++) v.e[e] = x[e];
+                                v.store((float *)P.out + out + i);
+                            } else if (P.act == COLI_ACT_BF16) {
+                                Run<__nv_bfloat16, 8> v;
+#pragma unroll
+                                for (int e = 0; e < 8; e++) v.e[e] = from_f32<__nv_bfloat16>(x[e]);
+                                v.store((__nv_bfloat16 *)P.out + out + i);
+                            } else {
+                                Run<__half, 8> v;
+#pragma unroll
+                                for (int e = 0; e < 8; e++) v.e[e] = from_f32<__half>(x[e]);
+                                v.store((__half *)P.out + out + i);
+                            }
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 8; e++) store_act(P.out, out + i + e, x[e], P.act);
+                        }
+                    }
+                    if (P.lse && it.half == 0)
+                        P.lse[(int64_t)(at.s.row + node) * P.q_heads + head] = attn_lse(m == -INFINITY ? 0.f : m, l, T::kShift);
+                }
+            }
+        } while (at.next(P, S.pre));
+    } else if (regs_down<88>(); warp < kProducts) {
+        // ================================================================ copies
+        constexpr int kBytes = T::kRaw ? 1 : 2;
+        constexpr int kAhead = T::kRaw ? T::kRawSlots - 1 : 0;  // 8-bit copies on their way behind the newest
+        constexpr int kRing = T::kRaw ? T::kRawSlots : T::kSlots;
+        const int ct = tid - kCopies * 32;
+        const uint32_t slots_a = smem_u32(slots), raws_a = smem_u32(raws);
+        uint32_t copy = 0, tile = 0, kinds = 0;  // kinds: bit i: whether copy - 1 - i is of K
+        const uint64_t step = (uint64_t)1 << W.off_shift;
+
+        // K or V of a tile, in 16-byte chunks: CH of them in a row, the same one for every row of a thread
+        auto issue = [&](auto is_k, const char *pool, uint32_t of_tile, int half) {
+            constexpr int CH = (is_k.value ? DP : NC) * kBytes / 16, kRows = kCopiers / CH;
+            const int ch = ct % CH, sub = ct / CH;
+            const int elem = half * NC + ch * (16 / kBytes);  // (half is 0 for K)
+            const bool in = elem < P.dim;
+            const char *src = pool + (in ? elem * kBytes : 0);
+            const uint32_t slot = copy % kRing;
+            if (!T::kRaw) wait_warp(&S.empty[slot], ((copy / T::kSlots) & 1) ^ 1);
+            const uint32_t *offs = S.row_off[of_tile & 3], *seen = S.seen[of_tile & 15];
+            bool all = in;
+#pragma unroll
+            for (int i = 0; i < TN / 32; i++) all &= seen[i] == 0xffffffffu;
+            const uint32_t to = T::kRaw ? raws_a + slot * T::kRawBytes + ch * 16 : slots_a + slot * T::kSlotBytes + (ch / 8) * kSlab;
+            auto move = [&](int row, bool ok) {
+                // (8-bit rows: where this thread itself finds them again; rows that are none have offset 0)
+                copy16(T::kRaw ? to + row * CH * 16 : to + row * 128 + (((ch % 8) ^ (row & 7)) << 4), src + offs[row] * step, ok ? 16 : 0);
+            };
+            constexpr int kFull = TN / kRows;  // rounds of all threads
+            if (all) {
+#pragma unroll 11
+                for (int i = 0; i < kFull; i++) move(i * kRows + sub, true);
+                if (TN % kRows && kFull * kRows + sub < TN) move(kFull * kRows + sub, true);
+            } else {
+#pragma unroll 1
+                for (int row = sub; row < TN; row += kRows) move(row, in && (seen[row >> 5] >> (row & 31) & 1));
+            }
+            if (T::kRaw) copy_commit();
+            else arrive_behind_copies(&S.full[slot]);
+            copy++;
+            kinds = kinds << 1 | (is_k.value ? 1 : 0);
+        };
+        // e4m3 rows of copy c to f16 in their slot
+        auto widen_rows = [&](auto is_k, uint32_t c) {
+            constexpr int CH = (is_k.value ? DP : NC) / 16, kRows = kCopiers / CH;
+            const int ch = ct % CH, sub = ct / CH;
+            unsigned char *slot = slots + (c % T::kSlots) * T::kSlotBytes + (ch / 4) * kSlab;
+            const unsigned char *raw = raws + (c % kRing) * T::kRawBytes;
+            auto one = [&](int row) {
+                const uint4 v = *(const uint4 *)(raw + (row * CH + ch) * 16);
+                uint4 a, b;
+                a.x = widen(v.x);
+                a.y = widen_hi(v.x);
+                a.z = widen(v.y);
+                a.w = widen_hi(v.y);
+                b.x = widen(v.z);
+                b.y = widen_hi(v.z);
+                b.z = widen(v.w);
+                b.w = widen_hi(v.w);
+                unsigned char *to = slot + row * 128;
+                *(uint4 *)(to + (((2 * ch) % 8 ^ (row & 7)) << 4)) = a;
+                *(uint4 *)(to + (((2 * ch + 1) % 8 ^ (row & 7)) << 4)) = b;
+            };
+            constexpr int kFull = TN / kRows;
+#pragma unroll 5
+            for (int i = 0; i < kFull; i++) one(i * kRows + sub);
+            if (TN % kRows && kFull * kRows + sub < TN) one(kFull * kRows + sub);
+            fence_async_smem();
+        };
+        // 8-bit copy c has arrived (its group is waited for)
+        auto hand_on = [&](uint32_t c) {
+            wait_warp(&S.empty[c % T::kSlots], ((c / T::kSlots) & 1) ^ 1);
+            if (kinds >> (copy - 1 - c) & 1) widen_rows(std::true_type{}, c);
+            else widen_rows(std::false_type{}, c);
+            mbar_arrive(&S.full[c % T::kSlots]);
+        };
+        auto advance = [&]() {
+            if (T::kRaw && copy > (uint32_t)kAhead) {
+                copy_wait<kAhead>();
+                hand_on(copy - 1 - kAhead);
+            }
+        };
+
+        at.begin(P, S.pre, from, units);
+        do {
+            const TreeItem it = tree_item(at.item, at.s.row_tiles, T::kHalves);
+            const int32_t *pages = P.table + (int64_t)at.b * P.table_width;
+            const int end = at.s.past + at.s.n;
+            // a thread looks rows ct and ct + 96 of a tile up; page numbers are not looked at before the copy
+            int page[2], slot[2];
+            bool ok[2];
+            auto look_up = [&](int j) {
+#pragma unroll
+                for (int i = 0; i < 2; i++) {
+                    const int row = ct + i * kCopiers;
+                    int t;
+                    ok[i] = j < at.cnt && row < TN && kv_unit_token(at.s.start, end, TN, at.u + j, row, t);
+                    page[i] = slot[i] = 0;
+                    if (ok[i]) {
+                        const int x = kv_quotient(W.divide, t);
+                        slot[i] = t - x * P.cache.page_size;
+                        page[i] = pages[x];
+                    }
+                }
+            };
+            look_up(0);
+            for (int j = 0; j <= at.cnt; j++) {
+                if (j < at.cnt) {
+#pragma unroll
+                    for (int i = 0; i < 2; i++) {
+                        const int row = ct + i * kCopiers;
+                        if (ok[i] && (uint32_t)page[i] >= (uint32_t)P.cache.pages) {
+                            ok[i] = false;
+                            if (P.err) atomicOr(P.err, COLI_LAYER_BAD_PAGE);
+                        }
+                        const uint32_t good = __ballot_sync(0xffffffffu, ok[i]);
+                        if (row < TN) {
+                            S.row_off[tile & 3][row] =
+                                ok[i] ? (uint32_t)page[i] * W.page_step + (uint32_t)slot[i] * W.token_step + (uint32_t)it.kh * W.head_step : 0;
+                            if (lane == 0) S.seen[tile & 15][row >> 5] = good;
+                        }
+                    }
+                    look_up(j + 1);
+                    sync_copiers();
+                    issue(std::true_type{}, (const char *)P.k_cache, tile, 0);
+                    tile++;
+                    advance();
+                }
+                if (j >= 1) {
+                    issue(std::false_type{}, (const char *)P.v_cache, tile - (j < at.cnt ? 2 : 1), it.half);
+                    advance();
+                }
+            }
+        } while (at.next(P, S.pre));
+        copy_wait<0>();
+        if (T::kRaw)
+            for (uint32_t c = copy > (uint32_t)kAhead ? copy - kAhead : 0; c < copy; c++) hand_on(c);
+    } else {
+        // ================================================================ products: one thread issues them
+        if (lane == 0) {
+            constexpr bool kBf = FMT == COLI_KV_BF16;
+            constexpr uint32_t kQk = idesc_f32acc(kTreeRows, TN, kBf), kPv = idesc_f32acc(kTreeRows, NC, kBf) | kIdescBMnMajor;
+            const uint64_t q_desc = sdesc_k_sw128(smem_u32(sm));
+            const uint32_t slots_a = smem_u32(slots);
+            uint32_t count = 0, copies = 0, part = 0;
+            at.begin(P, S.pre, from, units);
+            do {
+                wait(&S.q_full, part & 1);
+                for (int j = 0; j <= at.cnt; j++) {
+                    if (j < at.cnt) {
+                        const uint32_t k = count + j, g = k & 1, use = k >> 1, c = copies + k_copy(j), slot = c % T::kSlots;
+                        wait(&S.full[slot], (c / T::kSlots) & 1);
+                        // the scores' place still holds the p of two tiles before until its products have ended
+                        if (use) wait(&S.o_full[g], (use - 1) & 1);
+                        fence_async_smem();  // what the copies wrote is read by the tensor core
+                        tc_fence_after_sync();
+                        const uint64_t kd = sdesc_k_sw128(slots_a + slot * T::kSlotBytes);
+#pragma unroll
+                        for (int p = T::kQParts - 1; p >= 0; p--)
+#pragma unroll
+                            for (int s = 0; s < DP / 16; s++)
+                                tc_mma_f16kind(score_at(g),
+                                               q_desc + ((p * (kTreeRows * DP * 2) + (s / 4) * (kTreeRows * 128) + (s % 4) * 32) >> 4),
+                                               kd + (((s / 4) * kSlab + (s % 4) * 32) >> 4), kQk, p < T::kQParts - 1 || s > 0);
+                        tc_commit(&S.s_full[g]);
+                        tc_commit(&S.empty[slot]);
+                    }
+                    if (j >= 1) {
+                        const uint32_t k = count + j - 1, g = k & 1, use = k >> 1, c = copies + v_copy(j - 1, at.cnt), slot = c % T::kSlots;
+                        wait(&S.full[slot], (c / T::kSlots) & 1);
+                        if (use) wait(&S.o_free[g], (use - 1) & 1);
+                        wait(&S.p_ready[g], use & 1);
+                        fence_async_smem();
+                        tc_fence_after_sync();
+                        const uint64_t vd = sdesc_mn_sw128(slots_a + slot * T::kSlotBytes, kSlab);
+#pragma unroll
+                        for (int p = T::kPParts - 1; p >= 0; p--)
+#pragma unroll
+                            for (int s = 0; s < TN / 16; s++) {
+                                const uint32_t a = score_at(g) + (p < 2 ? 16 * s + 8 * p : TN + 8 * s);
+                                tc_mma_f16kind_ta(sums_at(g), a, vd + (s * 2048 >> 4), kPv, p < T::kPParts - 1 || s > 0);
+                            }
+                        tc_commit(&S.o_full[g]);
+                        tc_commit(&S.empty[slot]);
+                    }
+                }
+                count += at.cnt;
+                copies += 2 * at.cnt;
+                part++;
+            } while (at.next(P, S.pre));
+            tc_commit(&S.done);
+            wait(&S.done, 0);
+        } else if (lane == 1) {
+            // the border before this run, for the join
+            TreeCut cut{-1, 0, 0, (int32_t)R.runs};
+            at.begin(P, S.pre, from, units);
+            if (at.u > 0 && run > 0 && from - (uint32_t)at.u >= R.start(run - 1)) {
+                cut.b = at.b;
+                cut.item = at.item;
+                cut.last = R.of(from - (uint32_t)at.u + (uint32_t)at.s.tiles - 1);
+            }
+            W.cuts[run] = cut;
+        }
+        __syncwarp();
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    if (warp == kProducts) tmem_dealloc(tmem, 512);
+}
+
+template <typename T>
+cudaError_t launch_tree_typed(const TreeParams &P, const TreeWork &W, int grid, cudaStream_t s) {
+    // once per device
+    static std::atomic<uint64_t> set{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev >= 64 || !(set.load() >> dev & 1)) {
+        e = cudaFuncSetAttribute(attn_tree_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, T::kSmem);
+        if (e != cudaSuccess) return e;
+        if (dev < 64) set.fetch_or((uint64_t)1 << dev);
+    }
+    return launch_overlapped(attn_tree_kernel<T>, dim3(grid), tree::kThreads, T::kSmem, s, P, W);
+}
+
+template <int FMT, int DP>
+cudaError_t launch_tree_dim(const TreeParams &P, const TreeWork &W, int grid, cudaStream_t s) {
+    return W.wide ? launch_tree_typed<TreeTraits<FMT, DP, true>>(P, W, grid, s)
+                  : launch_tree_typed<TreeTraits<FMT, DP, false>>(P, W, grid, s);
+}
+template <int FMT>
+cudaError_t launch_tree(const TreeParams &P, const TreeWork &W, int grid, cudaStream_t s) {
+    return W.dim == 64    ? launch_tree_dim<FMT, 64>(P, W, grid, s)
+           : W.dim == 128 ? launch_tree_dim<FMT, 128>(P, W, grid, s)
+                          : launch_tree_dim<FMT, 256>(P, W, grid, s);
+}
+
+}  // namespace colimoe

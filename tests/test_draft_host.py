@@ -29,7 +29,7 @@ def test_header_and_binding_agree(q):
     for n in names:
         getattr(lib, n)
     found = re.findall(r"^#define (COLI_(?:DRAFT|VERIFY)_\w+) (\d+)", text, re.M)
-    assert len(found) == 3
+    assert len(found) == 4
     for name, value in found:
         assert getattr(q, name) == int(value), name
 
