@@ -21,7 +21,7 @@
 // Roles, 16 warps. Two groups of four warps take the tiles in turn, a thread has a row: maximum, exponents and parts of p.
 // The running maximum goes from one group to the other through shared memory. Four warps add the tiles' sums in
 // registers and write the results. Three warps copy K and V rows into a ring of slots (16-byte asynchronous copies into
-// the 128-byte swizzled layout; e4m3 through 8-bit staging that the same threads widen). One thread issues the products.
+// the 128-byte swizzled layout; e4m3 through 8-bit staging that the same threads widen). One warp issues the products.
 // What a thread of one role leaves for another lies in rings of four tiles: the products of a tile wait for the sums of
 // two tiles before, and its scores for the products of two tiles before, so that no role runs four tiles ahead.
 //
@@ -70,7 +70,7 @@ struct Misc {
     uint32_t row_off[4][kTreeRows];  // of a tile's places in the pool, in steps
     uint32_t seen[16][4];  // places of a tile that lie on good pages
     uint32_t odd[4][4];    // places of a tile whose values' infinities and NaN are taken out
-    uint64_t full[8], empty[8], s_full[2], m_ready[2], p_ready[2], o_full[2], o_free[2], q_full, done;
+    uint64_t full[8], empty[8], s_full[2], m_ready[2], v_full[2], p_ready[2], o_full[2], o_free[2], q_full, done;
     uint32_t tmem;
     int32_t dead;
 };
@@ -209,6 +209,7 @@ __global__ void __launch_bounds__(tree::kThreads, 1) attn_tree_kernel(const Tree
         for (int g = 0; g < 2; g++) {
             mbar_init(&S.s_full[g], 1);
             mbar_init(&S.m_ready[g], 128);
+            mbar_init(&S.v_full[g], 1);
             mbar_init(&S.p_ready[g], 128);
             mbar_init(&S.o_full[g], 1);
             mbar_init(&S.o_free[g], 128);
@@ -494,7 +495,7 @@ __global__ void __launch_bounds__(tree::kThreads, 1) attn_tree_kernel(const Tree
                 if (mixed) {
                     // ---- infinities and NaN among the values of this tile
                     const int slot = vc % T::kSlots;
-                    wait_warp(&S.full[slot], (vc / T::kSlots) & 1);
+                    wait_warp(&S.v_full[g], parity);
                     bool odd = false;
                     if (wt < TN) {
                         unsigned char *row = slots + slot * T::kSlotBytes + wt * 128;
@@ -640,15 +641,16 @@ __global__ void __launch_bounds__(tree::kThreads, 1) attn_tree_kernel(const Tree
         constexpr int kBytes = T::kRaw ? 1 : 2;
         constexpr int kAhead = T::kRaw ? T::kRawSlots - 1 : 0;  // 8-bit copies on their way behind the newest
         constexpr int kRing = T::kRaw ? T::kRawSlots : T::kSlots;
-        const int ct = tid - kCopies * 32;
+        constexpr int kBlock = 8;  // rows that a warp takes at once: the swizzle repeats behind them
+        const int ct = tid - kCopies * 32, cw = warp - kCopies;
         const uint32_t slots_a = smem_u32(slots), raws_a = smem_u32(raws);
         uint32_t copy = 0, tile = 0, kinds = 0;  // kinds: bit i: whether copy - 1 - i is of K
-        const uint64_t step = (uint64_t)1 << W.off_shift;
+        const uint32_t step = 1u << W.off_shift;
 
         // K or V of a tile, in 16-byte chunks: CH of them in a row, the same one for every row of a thread
         auto issue = [&](auto is_k, const char *pool, uint32_t of_tile, int half) {
-            constexpr int CH = (is_k.value ? DP : NC) * kBytes / 16, kRows = kCopiers / CH;
-            const int ch = ct % CH, sub = ct / CH;
+            constexpr int CH = (is_k.value ? DP : NC) * kBytes / 16, kRows = 32 / CH;  // (of an instruction)
+            const int ch = lane % CH, sub = lane / CH;
             const int elem = half * NC + ch * (16 / kBytes);  // (half is 0 for K)
             const bool in = elem < P.dim;
             const char *src = pool + (in ? elem * kBytes : 0);
@@ -658,19 +660,24 @@ __global__ void __launch_bounds__(tree::kThreads, 1) attn_tree_kernel(const Tree
             bool all = in;
 #pragma unroll
             for (int i = 0; i < TN / 32; i++) all &= seen[i] == 0xffffffffu;
-            const uint32_t to = T::kRaw ? raws_a + slot * T::kRawBytes + ch * 16 : slots_a + slot * T::kSlotBytes + (ch / 8) * kSlab;
-            auto move = [&](int row, bool ok) {
-                // (8-bit rows: where this thread itself finds them again; rows that are none have offset 0)
-                copy16(T::kRaw ? to + row * CH * 16 : to + row * 128 + (((ch % 8) ^ (row & 7)) << 4), src + offs[row] * step, ok ? 16 : 0);
+            const uint32_t to = T::kRaw ? raws_a + slot * T::kRawBytes + lane * 16 : slots_a + slot * T::kSlotBytes + (ch / 8) * kSlab;
+            // (8-bit rows: into this thread's own places, of K and of V, as no other thread waits for their use; rows that are
+            // none have offset 0)
+            auto move = [&](int block, bool good) {
+#pragma unroll
+                for (int i = 0; i < kBlock / kRows; i++) {
+                    const int row = i * kRows + sub;  // of the block
+                    const bool ok = good || (in && (seen[block >> 2] >> ((block & 3) * 8 + row) & 1));
+                    copy16(to + (T::kRaw ? block * (kBlock * DP) + i * 512 : block * (kBlock * 128) + row * 128 + (((ch % 8) ^ row) << 4)),
+                           src + (uint64_t)offs[block * kBlock + row] * step, ok ? 16 : 0);
+                }
             };
-            constexpr int kFull = TN / kRows;  // rounds of all threads
             if (all) {
-#pragma unroll 11
-                for (int i = 0; i < kFull; i++) move(i * kRows + sub, true);
-                if (TN % kRows && kFull * kRows + sub < TN) move(kFull * kRows + sub, true);
+#pragma unroll 2
+                for (int block = cw; block < TN / kBlock; block += kCopiers / 32) move(block, true);
             } else {
 #pragma unroll 1
-                for (int row = sub; row < TN; row += kRows) move(row, in && (seen[row >> 5] >> (row & 31) & 1));
+                for (int block = cw; block < TN / kBlock; block += kCopiers / 32) move(block, false);
             }
             if (T::kRaw) copy_commit();
             else arrive_behind_copies(&S.full[slot]);
@@ -679,29 +686,30 @@ __global__ void __launch_bounds__(tree::kThreads, 1) attn_tree_kernel(const Tree
         };
         // e4m3 rows of copy c to f16 in their slot
         auto widen_rows = [&](auto is_k, uint32_t c) {
-            constexpr int CH = (is_k.value ? DP : NC) / 16, kRows = kCopiers / CH;
-            const int ch = ct % CH, sub = ct / CH;
+            constexpr int CH = (is_k.value ? DP : NC) / 16, kRows = 32 / CH;
+            const int ch = lane % CH, sub = lane / CH;
             unsigned char *slot = slots + (c % T::kSlots) * T::kSlotBytes + (ch / 4) * kSlab;
-            const unsigned char *raw = raws + (c % kRing) * T::kRawBytes;
-            auto one = [&](int row) {
-                const uint4 v = *(const uint4 *)(raw + (row * CH + ch) * 16);
-                uint4 a, b;
-                a.x = widen(v.x);
-                a.y = widen_hi(v.x);
-                a.z = widen(v.y);
-                a.w = widen_hi(v.y);
-                b.x = widen(v.z);
-                b.y = widen_hi(v.z);
-                b.z = widen(v.w);
-                b.w = widen_hi(v.w);
-                unsigned char *to = slot + row * 128;
-                *(uint4 *)(to + (((2 * ch) % 8 ^ (row & 7)) << 4)) = a;
-                *(uint4 *)(to + (((2 * ch + 1) % 8 ^ (row & 7)) << 4)) = b;
-            };
-            constexpr int kFull = TN / kRows;
-#pragma unroll 5
-            for (int i = 0; i < kFull; i++) one(i * kRows + sub);
-            if (TN % kRows && kFull * kRows + sub < TN) one(kFull * kRows + sub);
+            const unsigned char *raw = raws + (c % kRing) * T::kRawBytes + lane * 16;
+#pragma unroll 2
+            for (int block = cw; block < TN / kBlock; block += kCopiers / 32) {
+#pragma unroll
+                for (int i = 0; i < kBlock / kRows; i++) {
+                    const int row = i * kRows + sub;  // of the block
+                    const uint4 v = *(const uint4 *)(raw + block * (kBlock * DP) + i * 512);
+                    uint4 a, b;
+                    a.x = widen(v.x);
+                    a.y = widen_hi(v.x);
+                    a.z = widen(v.y);
+                    a.w = widen_hi(v.y);
+                    b.x = widen(v.z);
+                    b.y = widen_hi(v.z);
+                    b.z = widen(v.w);
+                    b.w = widen_hi(v.w);
+                    unsigned char *to = slot + block * (kBlock * 128) + row * 128;
+                    *(uint4 *)(to + (((2 * ch) % 8 ^ row) << 4)) = a;
+                    *(uint4 *)(to + (((2 * ch + 1) % 8 ^ row) << 4)) = b;
+                }
+            }
             fence_async_smem();
         };
         // 8-bit copy c has arrived (its group is waited for)
@@ -773,61 +781,8 @@ __global__ void __launch_bounds__(tree::kThreads, 1) attn_tree_kernel(const Tree
         if (T::kRaw)
             for (uint32_t c = copy > (uint32_t)kAhead ? copy - kAhead : 0; c < copy; c++) hand_on(c);
     } else {
-        // ================================================================ products: one thread issues them
-        if (lane == 0) {
-            constexpr bool kBf = FMT == COLI_KV_BF16;
-            constexpr uint32_t kQk = idesc_f32acc(kTreeRows, TN, kBf), kPv = idesc_f32acc(kTreeRows, NC, kBf) | kIdescBMnMajor;
-            const uint64_t q_desc = sdesc_k_sw128(smem_u32(sm));
-            const uint32_t slots_a = smem_u32(slots);
-            uint32_t count = 0, copies = 0, part = 0;
-            at.begin(P, S.pre, from, units);
-            do {
-                wait(&S.q_full, part & 1);
-                for (int j = 0; j <= at.cnt; j++) {
-                    if (j < at.cnt) {
-                        const uint32_t k = count + j, g = k & 1, use = k >> 1, c = copies + k_copy(j), slot = c % T::kSlots;
-                        wait(&S.full[slot], (c / T::kSlots) & 1);
-                        // the scores' place still holds the p of two tiles before until its products have ended
-                        if (use) wait(&S.o_full[g], (use - 1) & 1);
-                        fence_async_smem();  // what the copies wrote is read by the tensor core
-                        tc_fence_after_sync();
-                        const uint64_t kd = sdesc_k_sw128(slots_a + slot * T::kSlotBytes);
-#pragma unroll
-                        for (int p = T::kQParts - 1; p >= 0; p--)
-#pragma unroll
-                            for (int s = 0; s < DP / 16; s++)
-                                tc_mma_f16kind(score_at(g),
-                                               q_desc + ((p * (kTreeRows * DP * 2) + (s / 4) * (kTreeRows * 128) + (s % 4) * 32) >> 4),
-                                               kd + (((s / 4) * kSlab + (s % 4) * 32) >> 4), kQk, p < T::kQParts - 1 || s > 0);
-                        tc_commit(&S.s_full[g]);
-                        tc_commit(&S.empty[slot]);
-                    }
-                    if (j >= 1) {
-                        const uint32_t k = count + j - 1, g = k & 1, use = k >> 1, c = copies + v_copy(j - 1, at.cnt), slot = c % T::kSlots;
-                        wait(&S.full[slot], (c / T::kSlots) & 1);
-                        if (use) wait(&S.o_free[g], (use - 1) & 1);
-                        wait(&S.p_ready[g], use & 1);
-                        fence_async_smem();
-                        tc_fence_after_sync();
-                        const uint64_t vd = sdesc_mn_sw128(slots_a + slot * T::kSlotBytes, kSlab);
-#pragma unroll
-                        for (int p = T::kPParts - 1; p >= 0; p--)
-#pragma unroll
-                            for (int s = 0; s < TN / 16; s++) {
-                                const uint32_t a = score_at(g) + (p < 2 ? 16 * s + 8 * p : TN + 8 * s);
-                                tc_mma_f16kind_ta(sums_at(g), a, vd + (s * 2048 >> 4), kPv, p < T::kPParts - 1 || s > 0);
-                            }
-                        tc_commit(&S.o_full[g]);
-                        tc_commit(&S.empty[slot]);
-                    }
-                }
-                count += at.cnt;
-                copies += 2 * at.cnt;
-                part++;
-            } while (at.next(P, S.pre));
-            tc_commit(&S.done);
-            wait(&S.done, 0);
-        } else if (lane == 1) {
+        // ================================================================ products: one warp issues them
+        if (lane == 1) {
             // the border before this run, for the join
             TreeCut cut{-1, 0, 0, (int32_t)R.runs};
             at.begin(P, S.pre, from, units);
@@ -837,6 +792,66 @@ __global__ void __launch_bounds__(tree::kThreads, 1) attn_tree_kernel(const Tree
                 cut.last = R.of(from - (uint32_t)at.u + (uint32_t)at.s.tiles - 1);
             }
             W.cuts[run] = cut;
+        }
+        __syncwarp();
+        {
+            // (the warp walks together, so that what the instructions take is uniform)
+            const uint32_t lead = tc_elect();
+            constexpr bool kBf = FMT == COLI_KV_BF16;
+            constexpr uint32_t kQk = idesc_f32acc(kTreeRows, TN, kBf), kPv = idesc_f32acc(kTreeRows, NC, kBf) | kIdescBMnMajor;
+            const uint64_t q_desc = sdesc_k_sw128(smem_u32(sm));
+            const uint32_t slots_a = smem_u32(slots);
+            uint32_t count = 0, copies = 0, part = 0;
+            at.begin(P, S.pre, from, units);
+            do {
+                wait_warp(&S.q_full, part & 1);
+                for (int j = 0; j <= at.cnt; j++) {
+                    if (j < at.cnt) {
+                        const uint32_t k = count + j, g = k & 1, use = k >> 1, c = copies + k_copy(j), slot = c % T::kSlots;
+                        wait_warp(&S.full[slot], (c / T::kSlots) & 1);
+                        // the scores' place still holds the p of two tiles before until its products have ended
+                        if (use) wait_warp(&S.o_full[g], (use - 1) & 1);
+                        fence_async_smem();  // what the copies wrote is read by the tensor core
+                        tc_fence_after_sync();
+                        const uint64_t kd = sdesc_k_sw128(slots_a + slot * T::kSlotBytes);
+#pragma unroll
+                        for (int p = T::kQParts - 1; p >= 0; p--)
+#pragma unroll
+                            for (int s = 0; s < DP / 16; s++)
+                                tc_mma_f16kind(score_at(g),
+                                               q_desc + ((p * (kTreeRows * DP * 2) + (s / 4) * (kTreeRows * 128) + (s % 4) * 32) >> 4),
+                                               kd + (((s / 4) * kSlab + (s % 4) * 32) >> 4), kQk, p < T::kQParts - 1 || s > 0, lead);
+                        tc_commit(&S.s_full[g], lead);
+                        tc_commit(&S.empty[slot], lead);
+                    }
+                    if (j >= 1) {
+                        const uint32_t k = count + j - 1, g = k & 1, use = k >> 1, c = copies + v_copy(j - 1, at.cnt), slot = c % T::kSlots;
+                        wait_warp(&S.full[slot], (c / T::kSlots) & 1);
+                        // for those who look at the values. (They cannot wait for the slot: who waits for some phases of a barrier
+                        // only must not be two behind, and here a phase ends with the products of two tiles before.)
+                        if (lead) mbar_arrive(&S.v_full[g]);
+                        if (use) wait_warp(&S.o_free[g], (use - 1) & 1);
+                        wait_warp(&S.p_ready[g], use & 1);
+                        fence_async_smem();
+                        tc_fence_after_sync();
+                        const uint64_t vd = sdesc_mn_sw128(slots_a + slot * T::kSlotBytes, kSlab);
+#pragma unroll
+                        for (int p = T::kPParts - 1; p >= 0; p--)
+#pragma unroll
+                            for (int s = 0; s < TN / 16; s++) {
+                                const uint32_t a = score_at(g) + (p < 2 ? 16 * s + 8 * p : TN + 8 * s);
+                                tc_mma_f16kind_ta(sums_at(g), a, vd + (s * 2048 >> 4), kPv, p < T::kPParts - 1 || s > 0, lead);
+                            }
+                        tc_commit(&S.o_full[g], lead);
+                        tc_commit(&S.empty[slot], lead);
+                    }
+                }
+                count += at.cnt;
+                copies += 2 * at.cnt;
+                part++;
+            } while (at.next(P, S.pre));
+            tc_commit(&S.done, lead);
+            wait_warp(&S.done, 0);
         }
         __syncwarp();
     }
