@@ -67,6 +67,40 @@ __global__ void __launch_bounds__(kTreeRows) attn_tree_join_kernel(const TreePar
         P.lse[(int64_t)(row + node) * P.q_heads + head] = attn_lse(m == -INFINITY ? 0.f : m, l, shift);
 }
 
+using Encode = decltype(&cuTensorMapEncodeTiled);
+Encode encoder() {
+    static const Encode f = []() -> Encode {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult found;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &found) != cudaSuccess ||
+            found != cudaDriverEntryPointSuccess) {
+            cudaGetLastError();
+            return nullptr;
+        }
+        return (Encode)p;
+    }();
+    return f;
+}
+
+// A pool as (element, slot, head, page) in boxes of `wide` elements by `rows` slots
+bool encode(CUtensorMap *map, const TreeParams &P, const void *pool, int wide, int rows) {
+    const Encode f = encoder();
+    if (!f) return false;
+    const bool e4m3 = P.fmt == COLI_KV_E4M3;
+    const int64_t size = e4m3 ? 1 : 2, least = (P.dim * size + 15) / 16 * 16;
+    // (an axis of one entry takes no step, but the map wants one)
+    auto step = [&](int n, int64_t stride) { return (cuuint64_t)(n > 1 ? stride * size : least); };
+    const cuuint64_t dims[4] = {(cuuint64_t)P.dim, (cuuint64_t)P.cache.page_size, (cuuint64_t)P.kv_heads, (cuuint64_t)P.cache.pages};
+    const cuuint64_t strides[3] = {step(P.cache.page_size, P.cache.token_stride), step(P.kv_heads, P.cache.head_stride),
+                                   step(P.cache.pages, P.cache.page_stride)};
+    const cuuint32_t box[4] = {(cuuint32_t)wide, (cuuint32_t)rows, 1, 1}, one[4] = {1, 1, 1, 1};
+    const CUtensorMapDataType type = e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                                     : P.fmt == COLI_KV_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    return f(map, type, 4, const_cast<void *>(pool), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             e4m3 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 struct Layout {
     TreeWork w;
     int64_t units;  // at most
@@ -103,13 +137,17 @@ Layout layout_of(const TreeParams &P) {
     L.w.page_step = (uint32_t)(P.cache.page_stride * size >> L.w.off_shift);
     L.w.token_step = (uint32_t)(P.cache.token_stride * size >> L.w.off_shift);
     L.w.head_step = (uint32_t)(P.cache.head_stride * size >> L.w.off_shift);
+    // boxes of 8 rows or more, as the swizzle repeats after 8
+    L.w.box = L.w.tile;
+    while (P.cache.page_size % L.w.box) L.w.box /= 2;
+    if (L.w.box < 8) L.w.box = 0;
     const int ab = P.act == COLI_ACT_F32 ? 4 : 2;
     L.w.q_vec = reinterpret_cast<uintptr_t>(P.q) % 16 == 0 && P.q_stride * ab % 16 == 0;
     L.w.out_vec = reinterpret_cast<uintptr_t>(P.out) % 16 == 0 && P.out_stride * ab % 16 == 0;
     // no more CTAs than units that the page tables and the rows can name
     const int64_t held = (int64_t)P.table_width * P.cache.page_size;
     const int64_t nodes = P.nodes < held ? P.nodes : held;
-    const int64_t seen = P.window > 0 && P.window + nodes < held ? P.window + nodes : held;
+    const int64_t seen = P.window > 0 && P.window + nodes + L.w.box < held ? P.window + nodes + L.w.box : held;
     const int64_t row_tiles = (nodes * group + kTreeRows - 1) / kTreeRows;
     L.units = (seen + L.w.tile - 1) / L.w.tile * P.seqs * P.kv_heads * L.w.halves * row_tiles;
     L.w.ctas = (int)(L.units < num_sms() ? L.units : num_sms());
@@ -134,9 +172,14 @@ cudaError_t launch_attn_tree(const TreeParams &P, cudaStream_t s) {
     L.w.cuts = (TreeCut *)ws;
     L.w.part_ml = (float2 *)(ws + L.ml);
     L.w.part_o = (float4 *)(ws + L.o);
-    const cudaError_t e = P.fmt == COLI_KV_BF16  ? launch_tree_bf16(P, L.w, L.grid, s)
-                          : P.fmt == COLI_KV_F16 ? launch_tree_f16(P, L.w, L.grid, s)
-                                                 : launch_tree_e4m3(P, L.w, L.grid, s);
+    TreeMaps maps{};
+    const bool e4m3 = P.fmt == COLI_KV_E4M3;
+    if (L.w.box && !(encode(&maps.k, P, P.k_cache, e4m3 ? L.w.dim : 64, L.w.box) &&
+                     encode(&maps.v, P, P.v_cache, e4m3 ? L.w.cols : 64, L.w.box)))
+        L.w.box = 0;
+    const cudaError_t e = P.fmt == COLI_KV_BF16  ? launch_tree_bf16(P, L.w, maps, L.grid, s)
+                          : P.fmt == COLI_KV_F16 ? launch_tree_f16(P, L.w, maps, L.grid, s)
+                                                 : launch_tree_e4m3(P, L.w, maps, L.grid, s);
     if (e != cudaSuccess || L.w.ctas == 1) return e;  // no borders
     // the join's blocks start while the streaming kernel runs and wait for its end
     return launch_overlapped(attn_tree_join_kernel, dim3(L.w.ctas - 1, L.w.cols / (4 * kPer)), kTreeRows, 0, s, P, L.w,

@@ -1,6 +1,8 @@
 // tree.h — what the streaming and the join kernel of coli_attn_tree share. Internal to libcolimoe.
 #pragma once
 
+#include <cuda.h>
+
 #include "act.cuh"
 #include "attn.h"
 #include "draft.h"
@@ -49,10 +51,16 @@ struct TreeWork {
     KvDivide divide;  // by the page size
     // the cache's strides in steps of 2^off_shift bytes, which divides them all
     uint32_t page_step, token_step, head_step, off_shift;
+    int32_t box;             // places of a box of the tensor maps: a power of two that divides the page size; 0: none
     int32_t q_vec, out_vec;  // rows of q and out may be moved 16 bytes at a time
     TreeCut *cuts;           // [ctas] at the border before a run
     float2 *part_ml;         // [2 * ctas][128] (m, l) of a run's first and last cut item
     float4 *part_o;          // [2 * ctas][cols / 4][128]
+};
+
+// K and V pools as (element, slot, head, page)
+struct TreeMaps {
+    CUtensorMap k, v;
 };
 
 // What an item is: rows [row0, row0 + rows) of a sequence's (node, head) pairs on one kv head, and a half of V
@@ -69,8 +77,8 @@ __host__ __device__ __forceinline__ TreeItem tree_item(int32_t item, int32_t row
     return t;
 }
 
-cudaError_t launch_tree_bf16(const TreeParams &P, const TreeWork &W, int grid, cudaStream_t s);
-cudaError_t launch_tree_f16(const TreeParams &P, const TreeWork &W, int grid, cudaStream_t s);
-cudaError_t launch_tree_e4m3(const TreeParams &P, const TreeWork &W, int grid, cudaStream_t s);
+cudaError_t launch_tree_bf16(const TreeParams &P, const TreeWork &W, const TreeMaps &maps, int grid, cudaStream_t s);
+cudaError_t launch_tree_f16(const TreeParams &P, const TreeWork &W, const TreeMaps &maps, int grid, cudaStream_t s);
+cudaError_t launch_tree_e4m3(const TreeParams &P, const TreeWork &W, const TreeMaps &maps, int grid, cudaStream_t s);
 
 }  // namespace colimoe

@@ -3,8 +3,8 @@
 
 namespace colimoe {
 
-cudaError_t launch_tree_e4m3(const TreeParams &P, const TreeWork &W, int grid, cudaStream_t s) {
-    return launch_tree<COLI_KV_E4M3>(P, W, grid, s);
+cudaError_t launch_tree_e4m3(const TreeParams &P, const TreeWork &W, const TreeMaps &maps, int grid, cudaStream_t s) {
+    return launch_tree<COLI_KV_E4M3>(P, W, maps, grid, s);
 }
 
 }  // namespace colimoe

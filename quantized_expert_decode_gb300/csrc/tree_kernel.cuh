@@ -20,8 +20,9 @@
 //
 // Roles, 16 warps. Two groups of four warps take the tiles in turn, a thread has a row: maximum, exponents and parts of p.
 // The running maximum goes from one group to the other through shared memory. Four warps add the tiles' sums in
-// registers and write the results. Three warps copy K and V rows into a ring of slots (16-byte asynchronous copies into
-// the 128-byte swizzled layout; e4m3 through 8-bit staging that the same threads widen). One warp issues the products.
+// registers and write the results. Three warps bring K and V rows into a ring of slots in the 128-byte swizzled layout:
+// where pages are multiples of 8 tokens as boxes through tensor maps, else by 16-byte asynchronous copies; e4m3 through
+// 8-bit staging that they widen. One warp issues the products.
 // What a thread of one role leaves for another lies in rings of four tiles: the products of a tile wait for the sums of
 // two tiles before, and its scores for the products of two tiles before, so that no role runs four tiles ahead.
 //
@@ -51,6 +52,16 @@ constexpr uint32_t kNapNs = 1000000;      // a thread sleeps at most so long bef
 __device__ __forceinline__ void sync_softmax() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 __device__ __forceinline__ void sync_copiers() { asm volatile("bar.sync 2, 96;" ::: "memory"); }
 static_assert(kCopiers == 96, "sync_copiers");
+// a box of a pool (its first element, slot, head, page) to shared memory; its bytes are counted on bar
+__device__ __forceinline__ void copy_box(uint32_t dst, const CUtensorMap *map, int x, int slot, int head, int page, uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+        "l"(map), "r"(x), "r"(slot), "r"(head), "r"(page), "r"(smem_u32(bar))
+        : "memory");
+}
+__device__ __forceinline__ void expect_bytes(uint64_t *bar, uint32_t bytes) {
+    asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
+}
 // arrives when this thread's copies so far have
 __device__ __forceinline__ void arrive_behind_copies(uint64_t *bar) {
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
@@ -70,7 +81,7 @@ struct Misc {
     uint32_t row_off[4][kTreeRows];  // of a tile's places in the pool, in steps
     uint32_t seen[16][4];  // places of a tile that lie on good pages
     uint32_t odd[4][4];    // places of a tile whose values' infinities and NaN are taken out
-    uint64_t full[8], empty[8], s_full[2], m_ready[2], v_full[2], p_ready[2], o_full[2], o_free[2], q_full, done;
+    uint64_t full[8], empty[8], raw_full[4], raw_empty[4], s_full[2], m_ready[2], v_full[2], p_ready[2], o_full[2], o_free[2], q_full, done;
     uint32_t tmem;
     int32_t dead;
 };
@@ -80,13 +91,14 @@ struct Seq {
     int32_t row, n, past, start, row_tiles, tiles, items;
 };
 template <typename T>
-__device__ __forceinline__ Seq seq_of(const TreeParams &P, int b, int &flags) {
+__device__ __forceinline__ Seq seq_of(const TreeParams &P, const TreeWork &W, int b, int &flags) {
     Seq s;
     int why, why2;
     draft_rows(P.first[b], P.first[b + 1], P.rows, P.nodes, s.row, s.n, why);
     draft_places(P.past[b], P.table_width, P.cache.page_size, s.past, s.n, why2);
     flags = (why ? COLI_LAYER_BAD_SEQUENCE : 0) | (why2 ? COLI_LAYER_BAD_POSITION : 0);
     s.start = draft_start(s.past, P.window);
+    if (W.box) s.start &= -W.box;  // boxes lie within pages
     s.row_tiles = (s.n * (P.q_heads / P.kv_heads) + kTreeRows - 1) / kTreeRows;
     s.tiles = kv_units(s.past + s.n - s.start, T::kTile);
     s.items = P.kv_heads * T::kHalves * s.row_tiles;
@@ -99,7 +111,7 @@ struct Walk {
     Seq s;
     int32_t b, item, u, cnt;
     uint32_t left;
-    __device__ __forceinline__ void begin(const TreeParams &P, const int32_t *pre, uint32_t at, uint32_t units) {
+    __device__ __forceinline__ void begin(const TreeParams &P, const TreeWork &W, const int32_t *pre, uint32_t at, uint32_t units) {
         int lo = 0, hi = P.seqs;  // pre[lo] <= at < pre[hi]
         while (hi - lo > 1) {
             const int mid = (lo + hi) / 2;
@@ -108,14 +120,14 @@ struct Walk {
         }
         b = lo;
         int f;
-        s = seq_of<T>(P, b, f);
+        s = seq_of<T>(P, W, b, f);
         const int off = (int)(at - (uint32_t)pre[b]);
         item = off / s.tiles;
         u = off - item * s.tiles;
         left = units;
         cnt = min((int)left, s.tiles - u);
     }
-    __device__ __forceinline__ bool next(const TreeParams &P, const int32_t *pre) {
+    __device__ __forceinline__ bool next(const TreeParams &P, const TreeWork &W, const int32_t *pre) {
         left -= cnt;
         if (left == 0) return false;
         u = 0;
@@ -124,7 +136,7 @@ struct Walk {
             do b++;
             while (pre[b + 1] == pre[b]);
             int f;
-            s = seq_of<T>(P, b, f);
+            s = seq_of<T>(P, W, b, f);
         }
         cnt = min((int)left, s.tiles);
         return true;
@@ -150,7 +162,9 @@ __device__ __forceinline__ bool node_sees(const TreeParams &P, Seq s, int i, int
 }  // namespace tree
 
 template <typename T>
-__global__ void __launch_bounds__(tree::kThreads, 1) attn_tree_kernel(const TreeParams P, const TreeWork W) {
+__global__ void __launch_bounds__(tree::kThreads, 1) attn_tree_kernel(const TreeParams P, const TreeWork W,
+                                                                     const __grid_constant__ CUtensorMap k_map,
+                                                                     const __grid_constant__ CUtensorMap v_map) {
     using namespace tree;
     using namespace attn;
     constexpr int FMT = T::kFmt, DP = T::kDim, TN = T::kTile, NC = T::kCols;
@@ -172,7 +186,7 @@ __global__ void __launch_bounds__(tree::kThreads, 1) attn_tree_kernel(const Tree
     int mine = 0;
     for (int b = b0; b < b1; b++) {
         int flags;
-        const Seq s = seq_of<T>(P, b, flags);
+        const Seq s = seq_of<T>(P, W, b, flags);
         if (flags && blockIdx.x == 0 && P.err) atomicOr(P.err, flags);
         const int u = s.n ? s.items * s.tiles : 0;
         S.pre[b + 1] = u;
@@ -203,8 +217,12 @@ __global__ void __launch_bounds__(tree::kThreads, 1) attn_tree_kernel(const Tree
     // ---- barriers, tensor memory
     if (tid == 0) {
         for (int i = 0; i < T::kSlots; i++) {
-            mbar_init(&S.full[i], kCopiers);
+            mbar_init(&S.full[i], W.box && !T::kRaw ? 1 : kCopiers);
             mbar_init(&S.empty[i], 1);
+        }
+        for (int i = 0; i < T::kRawSlots; i++) {
+            mbar_init(&S.raw_full[i], 1);
+            mbar_init(&S.raw_empty[i], kCopiers);
         }
         for (int g = 0; g < 2; g++) {
             mbar_init(&S.s_full[g], 1);
@@ -259,7 +277,7 @@ __global__ void __launch_bounds__(tree::kThreads, 1) attn_tree_kernel(const Tree
         const uint32_t lanes = (uint32_t)(quad * 32) << 16;
         uint32_t count = 0, copies = 0, part = 0;
         int last_b = -1;
-        at.begin(P, S.pre, from, units);
+        at.begin(P, W, S.pre, from, units);
         do {
             const TreeItem it = tree_item(at.item, at.s.row_tiles, T::kHalves);
             const int row0 = it.tile * kTreeRows, rows = min(kTreeRows, at.s.n * group - row0);
@@ -529,14 +547,14 @@ __global__ void __launch_bounds__(tree::kThreads, 1) attn_tree_kernel(const Tree
             count += at.cnt;
             copies += 2 * at.cnt;
             part++;
-        } while (at.next(P, S.pre));
+        } while (at.next(P, W, S.pre));
     } else if (warp < kCopies) {
         // ================================================================ sums: a thread has a row
         regs_up<184>();
         const int quad = warp % 4, r = quad * 32 + lane;
         const uint32_t lanes = (uint32_t)(quad * 32) << 16;
         uint32_t count = 0;
-        at.begin(P, S.pre, from, units);
+        at.begin(P, W, S.pre, from, units);
         do {
             const TreeItem it = tree_item(at.item, at.s.row_tiles, T::kHalves);
             const int row0 = it.tile * kTreeRows, rows = min(kTreeRows, at.s.n * group - row0);
@@ -635,7 +653,7 @@ __global__ void __launch_bounds__(tree::kThreads, 1) attn_tree_kernel(const Tree
                         P.lse[(int64_t)(at.s.row + node) * P.q_heads + head] = attn_lse(m == -INFINITY ? 0.f : m, l, T::kShift);
                 }
             }
-        } while (at.next(P, S.pre));
+        } while (at.next(P, W, S.pre));
     } else if (regs_down<88>(); warp < kProducts) {
         // ================================================================ copies
         constexpr int kBytes = T::kRaw ? 1 : 2;
@@ -656,6 +674,7 @@ __global__ void __launch_bounds__(tree::kThreads, 1) attn_tree_kernel(const Tree
             const char *src = pool + (in ? elem * kBytes : 0);
             const uint32_t slot = copy % kRing;
             if (!T::kRaw) wait_warp(&S.empty[slot], ((copy / T::kSlots) & 1) ^ 1);
+            kinds = kinds << 1 | (is_k.value ? 1 : 0);
             const uint32_t *offs = S.row_off[of_tile & 3], *seen = S.seen[of_tile & 15];
             bool all = in;
 #pragma unroll
@@ -682,20 +701,40 @@ __global__ void __launch_bounds__(tree::kThreads, 1) attn_tree_kernel(const Tree
             if (T::kRaw) copy_commit();
             else arrive_behind_copies(&S.full[slot]);
             copy++;
+        };
+        // the same as boxes of W.box places: a lane of the first warp has one, of page `page` from `from` on (page < 0: none)
+        auto issue_boxes = [&](auto is_k, const CUtensorMap *map, int page, int from, int head, int half) {
+            constexpr int kWide = is_k.value ? DP : NC, kBoxes = T::kRaw ? 1 : kWide / 64;
+            const uint32_t slot = copy % kRing;
+            uint64_t *bar = T::kRaw ? &S.raw_full[slot] : &S.full[slot];
+            if (T::kRaw) wait_warp(&S.raw_empty[slot], ((copy / kRing) & 1) ^ 1);
+            else wait_warp(&S.empty[slot], ((copy / T::kSlots) & 1) ^ 1);
             kinds = kinds << 1 | (is_k.value ? 1 : 0);
+            if (cw == 0) {
+                const uint32_t row = lane * W.box;
+                if (page >= 0) {
+                    expect_bytes(bar, W.box * (T::kRaw ? kWide : kBoxes * 128));
+                    const uint32_t to = T::kRaw ? raws_a + slot * T::kRawBytes + row * kWide : slots_a + slot * T::kSlotBytes + row * 128;
+#pragma unroll
+                    for (int i = 0; i < kBoxes; i++) copy_box(to + i * kSlab, map, half * NC + i * 64, from, head, page, bar);
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar);
+            }
+            copy++;
         };
         // e4m3 rows of copy c to f16 in their slot
-        auto widen_rows = [&](auto is_k, uint32_t c) {
+        auto widen_rows = [&](auto is_k, auto boxes, uint32_t c) {
             constexpr int CH = (is_k.value ? DP : NC) / 16, kRows = 32 / CH;
             const int ch = lane % CH, sub = lane / CH;
             unsigned char *slot = slots + (c % T::kSlots) * T::kSlotBytes + (ch / 4) * kSlab;
-            const unsigned char *raw = raws + (c % kRing) * T::kRawBytes + lane * 16;
-#pragma unroll 2
+            const unsigned char *raw = raws + (c % kRing) * T::kRawBytes + lane * 16;  // (rows lie one behind the other)
+#pragma unroll 3
             for (int block = cw; block < TN / kBlock; block += kCopiers / 32) {
 #pragma unroll
                 for (int i = 0; i < kBlock / kRows; i++) {
                     const int row = i * kRows + sub;  // of the block
-                    const uint4 v = *(const uint4 *)(raw + block * (kBlock * DP) + i * 512);
+                    const uint4 v = *(const uint4 *)(raw + block * (kBlock * (boxes.value ? CH * 16 : DP)) + i * 512);
                     uint4 a, b;
                     a.x = widen(v.x);
                     a.y = widen_hi(v.x);
@@ -715,22 +754,82 @@ __global__ void __launch_bounds__(tree::kThreads, 1) attn_tree_kernel(const Tree
         // 8-bit copy c has arrived (its group is waited for)
         auto hand_on = [&](uint32_t c) {
             wait_warp(&S.empty[c % T::kSlots], ((c / T::kSlots) & 1) ^ 1);
-            if (kinds >> (copy - 1 - c) & 1) widen_rows(std::true_type{}, c);
-            else widen_rows(std::false_type{}, c);
+            const bool k = kinds >> (copy - 1 - c) & 1;
+            if (W.box) {
+                wait_warp(&S.raw_full[c % kRing], (c / kRing) & 1);
+                if (k) widen_rows(std::true_type{}, std::true_type{}, c);
+                else widen_rows(std::false_type{}, std::true_type{}, c);
+                mbar_arrive(&S.raw_empty[c % kRing]);
+            } else {
+                if (k) widen_rows(std::true_type{}, std::false_type{}, c);
+                else widen_rows(std::false_type{}, std::false_type{}, c);
+            }
             mbar_arrive(&S.full[c % T::kSlots]);
         };
         auto advance = [&]() {
             if (T::kRaw && copy > (uint32_t)kAhead) {
-                copy_wait<kAhead>();
+                if (!W.box) copy_wait<kAhead>();
                 hand_on(copy - 1 - kAhead);
             }
         };
 
-        at.begin(P, S.pre, from, units);
-        do {
+        at.begin(P, W, S.pre, from, units);
+        if (!W.box || T::kRaw || cw == 0) do {
             const TreeItem it = tree_item(at.item, at.s.row_tiles, T::kHalves);
             const int32_t *pages = P.table + (int64_t)at.b * P.table_width;
             const int end = at.s.past + at.s.n;
+            if (W.box) {
+                // a lane looks its box up
+                const int boxes = TN / W.box;
+                int page = -1, slot = 0;
+                auto look_up = [&](int j) {
+                    int t;
+                    page = -1;
+                    if (j < at.cnt && lane < boxes && kv_unit_token(at.s.start, end, TN, at.u + j, lane * W.box, t)) {
+                        const int x = kv_quotient(W.divide, t);
+                        slot = t - x * P.cache.page_size;
+                        page = pages[x];
+                        if (page < 0) page = INT32_MAX;
+                    }
+                };
+                int v_page = -1, v_slot = 0;
+                if (cw == 0) look_up(0);
+                for (int j = 0; j <= at.cnt; j++) {
+                    int k_page = -1, k_slot = slot;
+                    if (j < at.cnt) {
+                        if (cw == 0) {
+                            k_page = page;
+                            if (k_page >= P.cache.pages) {
+                                k_page = -1;
+                                if (P.err) atomicOr(P.err, COLI_LAYER_BAD_PAGE);
+                            }
+                            // the places of boxes that come
+                            uint32_t good = __ballot_sync(0xffffffffu, k_page >= 0);
+                            if (lane < TN / 32) {
+                                const int log = __ffs(W.box) - 1;
+                                uint32_t w = 0;
+                                if (W.box >= 32) w = good >> (lane * 32 >> log) & 1 ? 0xffffffffu : 0u;
+                                else
+                                    for (int i = 0; i < 32 >> log; i++)
+                                        if (good >> ((lane * 32 >> log) + i) & 1) w |= ((1u << W.box) - 1) << (i << log);
+                                S.seen[tile & 15][lane] = w;
+                            }
+                            __syncwarp();
+                            look_up(j + 1);
+                        }
+                        issue_boxes(std::true_type{}, &k_map, k_page, k_slot, it.kh, 0);
+                        tile++;
+                        advance();
+                    }
+                    if (j >= 1) {
+                        issue_boxes(std::false_type{}, &v_map, v_page, v_slot, it.kh, it.half);
+                        advance();
+                    }
+                    v_page = k_page;
+                    v_slot = k_slot;
+                }
+                continue;
+            }
             // a thread looks rows ct and ct + 96 of a tile up; page numbers are not looked at before the copy
             int page[2], slot[2];
             bool ok[2];
@@ -776,7 +875,7 @@ __global__ void __launch_bounds__(tree::kThreads, 1) attn_tree_kernel(const Tree
                     advance();
                 }
             }
-        } while (at.next(P, S.pre));
+        } while (at.next(P, W, S.pre));
         copy_wait<0>();
         if (T::kRaw)
             for (uint32_t c = copy > (uint32_t)kAhead ? copy - kAhead : 0; c < copy; c++) hand_on(c);
@@ -785,7 +884,7 @@ __global__ void __launch_bounds__(tree::kThreads, 1) attn_tree_kernel(const Tree
         if (lane == 1) {
             // the border before this run, for the join
             TreeCut cut{-1, 0, 0, (int32_t)R.runs};
-            at.begin(P, S.pre, from, units);
+            at.begin(P, W, S.pre, from, units);
             if (at.u > 0 && run > 0 && from - (uint32_t)at.u >= R.start(run - 1)) {
                 cut.b = at.b;
                 cut.item = at.item;
@@ -802,7 +901,7 @@ __global__ void __launch_bounds__(tree::kThreads, 1) attn_tree_kernel(const Tree
             const uint64_t q_desc = sdesc_k_sw128(smem_u32(sm));
             const uint32_t slots_a = smem_u32(slots);
             uint32_t count = 0, copies = 0, part = 0;
-            at.begin(P, S.pre, from, units);
+            at.begin(P, W, S.pre, from, units);
             do {
                 wait_warp(&S.q_full, part & 1);
                 for (int j = 0; j <= at.cnt; j++) {
@@ -849,7 +948,7 @@ __global__ void __launch_bounds__(tree::kThreads, 1) attn_tree_kernel(const Tree
                 count += at.cnt;
                 copies += 2 * at.cnt;
                 part++;
-            } while (at.next(P, S.pre));
+            } while (at.next(P, W, S.pre));
             tc_commit(&S.done, lead);
             wait_warp(&S.done, 0);
         }
@@ -862,7 +961,7 @@ __global__ void __launch_bounds__(tree::kThreads, 1) attn_tree_kernel(const Tree
 }
 
 template <typename T>
-cudaError_t launch_tree_typed(const TreeParams &P, const TreeWork &W, int grid, cudaStream_t s) {
+cudaError_t launch_tree_typed(const TreeParams &P, const TreeWork &W, const TreeMaps &maps, int grid, cudaStream_t s) {
     // once per device
     static std::atomic<uint64_t> set{0};
     int dev = 0;
@@ -873,19 +972,19 @@ cudaError_t launch_tree_typed(const TreeParams &P, const TreeWork &W, int grid, 
         if (e != cudaSuccess) return e;
         if (dev < 64) set.fetch_or((uint64_t)1 << dev);
     }
-    return launch_overlapped(attn_tree_kernel<T>, dim3(grid), tree::kThreads, T::kSmem, s, P, W);
+    return launch_overlapped(attn_tree_kernel<T>, dim3(grid), tree::kThreads, T::kSmem, s, P, W, maps.k, maps.v);
 }
 
 template <int FMT, int DP>
-cudaError_t launch_tree_dim(const TreeParams &P, const TreeWork &W, int grid, cudaStream_t s) {
-    return W.wide ? launch_tree_typed<TreeTraits<FMT, DP, true>>(P, W, grid, s)
-                  : launch_tree_typed<TreeTraits<FMT, DP, false>>(P, W, grid, s);
+cudaError_t launch_tree_dim(const TreeParams &P, const TreeWork &W, const TreeMaps &maps, int grid, cudaStream_t s) {
+    return W.wide ? launch_tree_typed<TreeTraits<FMT, DP, true>>(P, W, maps, grid, s)
+                  : launch_tree_typed<TreeTraits<FMT, DP, false>>(P, W, maps, grid, s);
 }
 template <int FMT>
-cudaError_t launch_tree(const TreeParams &P, const TreeWork &W, int grid, cudaStream_t s) {
-    return W.dim == 64    ? launch_tree_dim<FMT, 64>(P, W, grid, s)
-           : W.dim == 128 ? launch_tree_dim<FMT, 128>(P, W, grid, s)
-                          : launch_tree_dim<FMT, 256>(P, W, grid, s);
+cudaError_t launch_tree(const TreeParams &P, const TreeWork &W, const TreeMaps &maps, int grid, cudaStream_t s) {
+    return W.dim == 64    ? launch_tree_dim<FMT, 64>(P, W, maps, grid, s)
+           : W.dim == 128 ? launch_tree_dim<FMT, 128>(P, W, maps, grid, s)
+                          : launch_tree_dim<FMT, 256>(P, W, maps, grid, s);
 }
 
 }  // namespace colimoe
