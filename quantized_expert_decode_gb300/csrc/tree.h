@@ -22,7 +22,7 @@ struct TreeTraits {
     static constexpr int kHalves = DP / kCols;
     static constexpr int kQParts = !WIDE ? 1 : FMT == COLI_KV_BF16 ? 3 : 2;
     static constexpr int kPParts = WIDE && FMT == COLI_KV_BF16 ? 3 : 2;
-    static constexpr int kTile = DP == 256 ? (WIDE ? 32 : 64) : (kPParts == 3 ? 64 : 128);  // tokens
+    static constexpr int kTile = DP == 256 ? (WIDE ? 32 : 64) : 128;  // tokens
     // p is kept times 2^kShift, so that the second f16 part of a small p is still above f16's smallest step
     static constexpr int kShift = FMT == COLI_KV_BF16 ? 0 : 14;
     static constexpr int kQBytes = kQParts * kTreeRows * DP * 2;
@@ -34,9 +34,13 @@ struct TreeTraits {
     static constexpr int kSlots = kRoom / kSlotBytes < 8 ? kRoom / kSlotBytes : 8;
     static_assert(kSlots >= 1, "shared memory of an SM");
     static constexpr int kSmem = kQBytes + kSlots * kSlotBytes + kRawSlots * kRawBytes + kMiscBytes;
-    // tensor memory: two buffers of scores, over which the parts of p are written, and two of a tile's sums
+    // tensor memory: two buffers of scores, over which the parts of p are written, and two of a tile's sums; one where
+    // two do not fit (beside three parts of p; the scores' products of 128 places then run while the sums are read. Tiles of
+    // 64 places with two buffers: products with 64 columns take as long as with 128, 32 sequences of up to 8192 tokens
+    // with 21 nodes 289 us)
     static constexpr int kScoreCols = kPParts == 3 ? (kTile + kTile / 2 + 31) / 32 * 32 : kTile;
-    static_assert(2 * kScoreCols + 2 * kCols <= 512, "tensor memory of an SM");
+    static constexpr int kSumBuffers = 2 * kScoreCols + 2 * kCols <= 512 ? 2 : 1;
+    static_assert(2 * kScoreCols + kSumBuffers * kCols <= 512, "tensor memory of an SM");
 };
 
 // The item whose units the border before a run cuts, told for its first cut only (b < 0: none)

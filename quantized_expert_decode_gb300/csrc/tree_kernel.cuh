@@ -24,7 +24,7 @@
 // where pages are multiples of 8 tokens as boxes through tensor maps, else by 16-byte asynchronous copies; e4m3 through
 // 8-bit staging that they widen. One warp issues the products.
 // What a thread of one role leaves for another lies in rings of four tiles: the products of a tile wait for the sums of
-// two tiles before, and its scores for the products of two tiles before, so that no role runs four tiles ahead.
+// two tiles before (or one), and its scores for the products of two tiles before, so that no role runs four tiles ahead.
 //
 // Places that some rows see and others do not (nodes, the window's edge) lie in `mixed` tiles. There a row's visible
 // places are bits, what is not seen has p = 0, and infinities and NaN of V are taken out of the tile (0 times infinity
@@ -81,7 +81,7 @@ struct Misc {
     uint32_t row_off[4][kTreeRows];  // of a tile's places in the pool, in steps
     uint32_t seen[16][4];  // places of a tile that lie on good pages
     uint32_t odd[4][4];    // places of a tile whose values' infinities and NaN are taken out
-    uint64_t full[8], empty[8], raw_full[4], raw_empty[4], s_full[2], m_ready[2], v_full[2], p_ready[2], o_full[2], o_free[2], q_full, done;
+    uint64_t full[8], empty[8], raw_full[4], raw_empty[4], s_full[2], m_ready[2], v_full[2], p_half[2], p_ready[2], o_full[2], o_free[2], q_full, done;
     uint32_t tmem;
     int32_t dead;
 };
@@ -228,6 +228,7 @@ __global__ void __launch_bounds__(tree::kThreads, 1) attn_tree_kernel(const Tree
             mbar_init(&S.s_full[g], 1);
             mbar_init(&S.m_ready[g], 128);
             mbar_init(&S.v_full[g], 1);
+            mbar_init(&S.p_half[g], 128);
             mbar_init(&S.p_ready[g], 128);
             mbar_init(&S.o_full[g], 1);
             mbar_init(&S.o_free[g], 128);
@@ -246,7 +247,7 @@ __global__ void __launch_bounds__(tree::kThreads, 1) attn_tree_kernel(const Tree
     tc_fence_after_sync();
     const uint32_t tmem = S.tmem;
     auto score_at = [&](int g) { return tmem + g * T::kScoreCols; };
-    auto sums_at = [&](int g) { return tmem + 2 * T::kScoreCols + g * NC; };
+    auto sums_at = [&](int g) { return tmem + 2 * T::kScoreCols + (T::kSumBuffers == 2 ? g * NC : 0); };
 
     // A wait that never ends is given up for good: the flag lets every other wait of the CTA pass, so that all threads
     // reach their ends (with wrong sums, and an error told).
@@ -452,6 +453,7 @@ __global__ void __launch_bounds__(tree::kThreads, 1) attn_tree_kernel(const Tree
                 S.m[k & 3][r] = mn;
                 mbar_arrive(&S.m_ready[g]);
                 // ---- the exponents and their parts
+                bool half_told = false;
                 if (active) {
                     const float ref = mn == -INFINITY ? 0.f : mn;
                     const float f = m == mn ? 1.f : exp2f(m - mn);
@@ -487,6 +489,13 @@ __global__ void __launch_bounds__(tree::kThreads, 1) attn_tree_kernel(const Tree
                         tmem_ld_x16(sc, s0);
 #pragma unroll 1
                         for (int c = 0; c < TN / 16; c += 2) {
+                            if (c == TN / 32 && c > 0) {
+                                // the first half's products may start
+                                tmem_st_wait();
+                                tc_fence_before_sync();
+                                mbar_arrive(&S.p_half[g]);
+                                half_told = true;
+                            }
                             tmem_ld_wait();
                             tmem_ld_x16(sc + 16 * (c + 1), s1);
                             parts(s0, c, std::false_type{}, 0u);
@@ -542,6 +551,7 @@ __global__ void __launch_bounds__(tree::kThreads, 1) attn_tree_kernel(const Tree
                 }
                 if (lane == 0) S.odd[k & 3][quad] = odds;
                 tc_fence_before_sync();
+                if (!half_told) mbar_arrive(&S.p_half[g]);
                 mbar_arrive(&S.p_ready[g]);
             }
             count += at.cnt;
@@ -929,18 +939,27 @@ __global__ void __launch_bounds__(tree::kThreads, 1) attn_tree_kernel(const Tree
                         // for those who look at the values. (They cannot wait for the slot: who waits for some phases of a barrier
                         // only must not be two behind, and here a phase ends with the products of two tiles before.)
                         if (lead) mbar_arrive(&S.v_full[g]);
-                        if (use) wait_warp(&S.o_free[g], (use - 1) & 1);
-                        wait_warp(&S.p_ready[g], use & 1);
+                        // the sums' place has been read: two tiles before, or one where there is one place
+                        const uint32_t was = T::kSumBuffers == 2 ? k - 2 : k - 1;
+                        if (k >= (uint32_t)T::kSumBuffers) wait_warp(&S.o_free[was & 1], (was >> 1) & 1);
+                        wait_warp(&S.p_half[g], use & 1);
                         fence_async_smem();
                         tc_fence_after_sync();
                         const uint64_t vd = sdesc_mn_sw128(slots_a + slot * T::kSlotBytes, kSlab);
 #pragma unroll
-                        for (int p = T::kPParts - 1; p >= 0; p--)
-#pragma unroll
-                            for (int s = 0; s < TN / 16; s++) {
-                                const uint32_t a = score_at(g) + (p < 2 ? 16 * s + 8 * p : TN + 8 * s);
-                                tc_mma_f16kind_ta(sums_at(g), a, vd + (s * 2048 >> 4), kPv, p < T::kPParts - 1 || s > 0, lead);
+                        for (int h = 0; h < 2; h++) {
+                            if (h) {
+                                wait_warp(&S.p_ready[g], use & 1);
+                                tc_fence_after_sync();
                             }
+#pragma unroll
+                            for (int p = T::kPParts - 1; p >= 0; p--)
+#pragma unroll
+                                for (int s = h * (TN / 32); s < (h + 1) * (TN / 32); s++) {
+                                    const uint32_t a = score_at(g) + (p < 2 ? 16 * s + 8 * p : TN + 8 * s);
+                                    tc_mma_f16kind_ta(sums_at(g), a, vd + (s * 2048 >> 4), kPv, h > 0 || p < T::kPParts - 1 || s > 0, lead);
+                                }
+                        }
                         tc_commit(&S.o_full[g], lead);
                         tc_commit(&S.empty[slot], lead);
                     }
