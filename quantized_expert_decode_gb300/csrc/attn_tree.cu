@@ -132,6 +132,7 @@ Layout layout_of(const TreeParams &P) {
     else if (P.fmt == COLI_KV_F16) take_format<COLI_KV_F16>(L.w);
     else take_format<COLI_KV_E4M3>(L.w);
     L.w.divide = kv_divide_by(P.cache.page_size);
+    L.w.group = kv_divide_by(group);
     const int size = P.fmt == COLI_KV_E4M3 ? 1 : 2;
     attn_steps(P.cache, P.kv_heads, size, L.w.off_shift);
     L.w.page_step = (uint32_t)(P.cache.page_stride * size >> L.w.off_shift);

@@ -52,7 +52,7 @@ struct TreeCut {
 struct TreeWork {
     int32_t dim, cols, tile, halves;
     int32_t wide, ctas;
-    KvDivide divide;  // by the page size
+    KvDivide divide, group;  // by the page size, by the query heads of a kv head
     // the cache's strides in steps of 2^off_shift bytes, which divides them all
     uint32_t page_step, token_step, head_step, off_shift;
     int32_t box;             // places of a box of the tensor maps: a power of two that divides the page size; 0: none

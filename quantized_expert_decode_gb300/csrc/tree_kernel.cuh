@@ -143,8 +143,7 @@ struct Walk {
     }
 };
 
-// The places of copies in the order K0, K1, V0, K2, V1, ... of a part of an item
-__device__ __forceinline__ int k_copy(int j) { return j ? 2 * j - 1 : 0; }
+// V's place in the order of copies K0, K1, V0, K2, V1, ... of a part of an item
 __device__ __forceinline__ int v_copy(int j, int cnt) { return j == cnt - 1 ? 2 * cnt - 1 : 2 * j + 2; }
 
 // Whether node i sees place t, from the parents themselves (for the rare places whose values are not finite)
@@ -298,7 +297,7 @@ __global__ void __launch_bounds__(tree::kThreads, 1) attn_tree_kernel(const Tree
                 sync_softmax();
             }
             if (g == 0 && real) {
-                const int node = (row0 + r) / group;
+                const int node = kv_quotient(W.group, row0 + r);
 #pragma unroll
                 for (int i = 0; i < kTreeMaxNodes / 32; i++) S.mask[r][i] = 0;
                 int depth = 0;
@@ -309,74 +308,117 @@ __global__ void __launch_bounds__(tree::kThreads, 1) attn_tree_kernel(const Tree
                 const int64_t low = P.window ? (int64_t)at.s.past + depth - P.window : 0;  // (depth counts the node itself)
                 S.low[r] = low < 0 ? 0 : (int32_t)low;
             }
-            // ---- queries: neighbouring lanes have neighbouring 8-element chunks of a row
+            // ---- queries: neighbouring lanes have neighbouring 8-element chunks of a row. Beside the streams of K and V a load
+            // takes some thousand cycles, so four rows' are on their way at a time, and the next item's lines are asked
+            // for an item ahead; cold instructions cost as much, so that is all that is unrolled.
             {
-                constexpr int kCh = DP / 8, kRows = 32 / kCh;
+                constexpr int kCh = DP / 8, kRows = 32 / kCh, kStep = 8 * kRows;
                 const float ks = P.scale * 1.4426950408889634f * (P.k_scale ? P.k_scale[it.kh] : 1.f);
-                const float sign = ks < 0.f ? -1.f : 1.f;
                 const int ch = lane % kCh, sub = lane / kCh;
-#pragma unroll 2
-                for (int i = warp * kRows + sub; i < (rows + kRows - 1) / kRows * kRows; i += 8 * kRows) {
-                    float x[8];
+                const int end = (rows + kRows - 1) / kRows * kRows;
+                struct Raw {
+                    uint4 a, b;  // 8 elements: 16 bytes, or 32 of fp32
+                };
+                auto load = [&](int i) {
+                    Raw v;
+                    v.a = v.b = make_uint4(0, 0, 0, 0);
+                    if (i >= rows || ch * 8 >= P.dim) return v;
+                    const int nd = kv_quotient(W.group, row0 + i), h = it.kh * group + (row0 + i - nd * group);
+                    const int64_t off = (int64_t)(at.s.row + nd) * P.q_stride + (int64_t)h * P.dim + ch * 8;
+                    const uint4 *src = reinterpret_cast<const uint4 *>((const char *)P.q + off * (P.act == COLI_ACT_F32 ? 4 : 2));
+                    if (W.q_vec) {
+                        v.a = src[0];
+                        if (P.act == COLI_ACT_F32) v.b = src[1];
+                    } else if (P.act == COLI_ACT_F32) {
+                        const uint32_t *w = reinterpret_cast<const uint32_t *>(src);
+                        v.a = make_uint4(w[0], w[1], w[2], w[3]);
+                        v.b = make_uint4(w[4], w[5], w[6], w[7]);
+                    } else {
+                        const uint16_t *w = reinterpret_cast<const uint16_t *>(src);
+                        v.a = make_uint4(w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16);
+                    }
+                    return v;
+                };
+                auto store = [&](int i, const Raw &now) {
+                    unsigned char *dst = sm + (ch / 8) * (kTreeRows * 128) + i * 128 + (((ch % 8) ^ (i & 7)) << 4);
+                    float down = 1.f;
+                    if (FMT == COLI_KV_BF16 && !T::kWide) {
+                        const uint32_t flip = ks < 0.f ? 0x80008000u : 0u;
+                        *(uint4 *)dst = make_uint4(now.a.x ^ flip, now.a.y ^ flip, now.a.z ^ flip, now.a.w ^ flip);
+                    } else {
+                        float x[8];
+                        if (P.act == COLI_ACT_F32) {
 #pragma unroll
-                    for (int e = 0; e < 8; e++) x[e] = 0.f;
-                    if (i < rows && ch * 8 < P.dim) {
-                        const int nd = (row0 + i) / group, h = it.kh * group + (row0 + i - nd * group);
-                        const int64_t off = (int64_t)(at.s.row + nd) * P.q_stride + (int64_t)h * P.dim + ch * 8;
-                        if (W.q_vec) {
-                            if (P.act == COLI_ACT_F32) {
-                                Run<float, 8> v;
-                                v.load((const float *)P.q + off);
-#pragma unroll
-                                for (int e = 0; e < 8; e++) x[e] = v.e[e];
-                            } else if (P.act == COLI_ACT_BF16) {
-                                Run<__nv_bfloat16, 8> v;
-                                v.load((const __nv_bfloat16 *)P.q + off);
-#pragma unroll
-                                for (int e = 0; e < 8; e++) x[e] = to_f32(v.e[e]);
-                            } else {
-                                Run<__half, 8> v;
-                                v.load((const __half *)P.q + off);
-#pragma unroll
-                                for (int e = 0; e < 8; e++) x[e] = to_f32(v.e[e]);
-                            }
+                            for (int e = 0; e < 8; e++) x[e] = __uint_as_float((&now.a.x)[e]);
                         } else {
 #pragma unroll
-                            for (int e = 0; e < 8; e++) x[e] = load_act(P.q, off + e, P.act);
+                            for (int e = 0; e < 4; e++) {
+                                const uint32_t w = (&now.a.x)[e];
+                                const float2 f = P.act == COLI_ACT_BF16
+                                                     ? make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u))
+                                                     : __half22float2(*reinterpret_cast<const __half2 *>(&w));
+                                x[2 * e] = f.x;
+                                x[2 * e + 1] = f.y;
+                            }
                         }
-                    }
-                    float up = 1.f, down = 1.f;
-                    if (FMT != COLI_KV_BF16) {
-                        // the row's largest element to [2^13, 2^14)
-                        float big = 0.f;
+                        float up = ks < 0.f ? -1.f : 1.f;
+                        if (FMT != COLI_KV_BF16) {
+                            // the row's largest element to [2^13, 2^14)
+                            float big = 0.f;
 #pragma unroll
-                        for (int e = 0; e < 8; e++) big = fmaxf(big, fabsf(x[e]));
+                            for (int e = 0; e < 8; e++) big = fmaxf(big, fabsf(x[e]));
 #pragma unroll
-                        for (int o = kCh / 2; o; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
-                        if (big > 0.f && big < INFINITY) {
-                            int e = 13 + 127 - (int)(__float_as_uint(big) >> 23);
-                            e = e > 126 ? 126 : e;
-                            up = __uint_as_float((uint32_t)(e + 127) << 23);
-                            down = __uint_as_float((uint32_t)(127 - e) << 23);
+                            for (int o = kCh / 2; o; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
+                            if (big > 0.f && big < INFINITY) {
+                                int e = 13 + 127 - (int)(__float_as_uint(big) >> 23);
+                                e = e > 126 ? 126 : e;
+                                up *= __uint_as_float((uint32_t)(e + 127) << 23);
+                                down = __uint_as_float((uint32_t)(127 - e) << 23);
+                            }
+                        }
+#pragma unroll
+                        for (int e = 0; e < 8; e++) x[e] *= up;
+#pragma unroll
+                        for (int p = 0; p < T::kQParts; p++) {
+                            uint4 v;
+                            v.x = take_part<FMT>(x[0], x[1]);
+                            v.y = take_part<FMT>(x[2], x[3]);
+                            v.z = take_part<FMT>(x[4], x[5]);
+                            v.w = take_part<FMT>(x[6], x[7]);
+                            *(uint4 *)(dst + p * (kTreeRows * DP * 2)) = v;
                         }
                     }
                     if (ch == 0) S.qs[i] = fabsf(ks) * down;
+                };
+#pragma unroll 1
+                for (int i = warp * kRows + sub; i < end; i += 4 * kStep) {
+                    Raw v[4];
 #pragma unroll
-                    for (int e = 0; e < 8; e++) x[e] *= up * sign;
-                    unsigned char *dst = sm + (ch / 8) * (kTreeRows * 128) + i * 128 + (((ch % 8) ^ (i & 7)) << 4);
+                    for (int e = 0; e < 4; e++) v[e] = load(i + e * kStep);
 #pragma unroll
-                    for (int p = 0; p < T::kQParts; p++) {
-                        uint4 v;
-                        v.x = take_part<FMT>(x[0], x[1]);
-                        v.y = take_part<FMT>(x[2], x[3]);
-                        v.z = take_part<FMT>(x[4], x[5]);
-                        v.w = take_part<FMT>(x[6], x[7]);
-                        *(uint4 *)(dst + p * (kTreeRows * DP * 2)) = v;
-                    }
+                    for (int e = 0; e < 4; e++)
+                        if (i + e * kStep < end) store(i + e * kStep, v[e]);
                 }
             }
             fence_async_smem();
             mbar_arrive(&S.q_full);
+            Walk<T> then = at;
+            const bool more = then.next(P, W, S.pre);
+            {
+                if (more) {
+                    if (P.parent && then.b != at.b && tid < (then.s.n + 31) / 32)
+                        asm volatile("prefetch.global.L2 [%0];" ::"l"(P.parent + then.s.row + tid * 32));
+                    const TreeItem ti = tree_item(then.item, then.s.row_tiles, T::kHalves);
+                    const int size = P.act == COLI_ACT_F32 ? 4 : 2, first = ti.tile * kTreeRows;
+                    const int last = min(kTreeRows, then.s.n * group - first), lines = (P.dim * size + 127) / 128;
+                    for (int i = tid; i < last * lines; i += 256) {
+                        const int row = first + i / lines, nd = kv_quotient(W.group, row);
+                        const char *at_q = (const char *)P.q + ((int64_t)(then.s.row + nd) * P.q_stride +
+                                                                (int64_t)(ti.kh * group + row - nd * group) * P.dim) * size;
+                        asm volatile("prefetch.global.L2 [%0];" ::"l"(at_q + min((i % lines) * 128, P.dim * size - 1)));
+                    }
+                }
+            }
             wait_warp(&S.q_full, part & 1);
             const float qs = real ? S.qs[r] : 0.f;
             const int low = real ? S.low[r] : 0;
@@ -517,11 +559,10 @@ __global__ void __launch_bounds__(tree::kThreads, 1) attn_tree_kernel(const Tree
                     tmem_st_wait();
                 }
                 S.l[k & 3][r] = l;
-                const int vc = copies + v_copy(j, at.cnt);
                 uint32_t odds = 0;
                 if (mixed) {
                     // ---- infinities and NaN among the values of this tile
-                    const int slot = vc % T::kSlots;
+                    const int slot = (copies + v_copy(j, at.cnt)) % T::kSlots;
                     wait_warp(&S.v_full[g], parity);
                     bool odd = false;
                     if (wt < TN) {
@@ -557,7 +598,9 @@ __global__ void __launch_bounds__(tree::kThreads, 1) attn_tree_kernel(const Tree
             count += at.cnt;
             copies += 2 * at.cnt;
             part++;
-        } while (at.next(P, W, S.pre));
+            if (!more) break;
+            at = then;
+        } while (true);
     } else if (warp < kCopies) {
         // ================================================================ sums: a thread has a row
         regs_up<184>();
@@ -569,7 +612,7 @@ __global__ void __launch_bounds__(tree::kThreads, 1) attn_tree_kernel(const Tree
             const TreeItem it = tree_item(at.item, at.s.row_tiles, T::kHalves);
             const int row0 = it.tile * kTreeRows, rows = min(kTreeRows, at.s.n * group - row0);
             const bool active = quad * 32 < rows, real = r < rows;
-            const int node = real ? (row0 + r) / group : 0;
+            const int node = real ? kv_quotient(W.group, row0 + r) : 0;
             float2 acc[NC / 2];
             float m = -INFINITY, l = 0.f;
 #pragma unroll
@@ -676,6 +719,7 @@ __global__ void __launch_bounds__(tree::kThreads, 1) attn_tree_kernel(const Tree
         const uint32_t step = 1u << W.off_shift;
 
         // K or V of a tile, in 16-byte chunks: CH of them in a row, the same one for every row of a thread
+        using OfV = std::bool_constant<DP == NC>;  // V's rows are as K's
         auto issue = [&](auto is_k, const char *pool, uint32_t of_tile, int half) {
             constexpr int CH = (is_k.value ? DP : NC) * kBytes / 16, kRows = 32 / CH;  // (of an instruction)
             const int ch = lane % CH, sub = lane / CH;
@@ -684,7 +728,7 @@ __global__ void __launch_bounds__(tree::kThreads, 1) attn_tree_kernel(const Tree
             const char *src = pool + (in ? elem * kBytes : 0);
             const uint32_t slot = copy % kRing;
             if (!T::kRaw) wait_warp(&S.empty[slot], ((copy / T::kSlots) & 1) ^ 1);
-            kinds = kinds << 1 | (is_k.value ? 1 : 0);
+            kinds = kinds << 1 | (is_k.value ? 1 : 0);  // (counts where the two differ only)
             const uint32_t *offs = S.row_off[of_tile & 3], *seen = S.seen[of_tile & 15];
             bool all = in;
 #pragma unroll
@@ -739,7 +783,7 @@ __global__ void __launch_bounds__(tree::kThreads, 1) attn_tree_kernel(const Tree
             const int ch = lane % CH, sub = lane / CH;
             unsigned char *slot = slots + (c % T::kSlots) * T::kSlotBytes + (ch / 4) * kSlab;
             const unsigned char *raw = raws + (c % kRing) * T::kRawBytes + lane * 16;  // (rows lie one behind the other)
-#pragma unroll 3
+#pragma unroll 6
             for (int block = cw; block < TN / kBlock; block += kCopiers / 32) {
 #pragma unroll
                 for (int i = 0; i < kBlock / kRows; i++) {
@@ -764,15 +808,15 @@ __global__ void __launch_bounds__(tree::kThreads, 1) attn_tree_kernel(const Tree
         // 8-bit copy c has arrived (its group is waited for)
         auto hand_on = [&](uint32_t c) {
             wait_warp(&S.empty[c % T::kSlots], ((c / T::kSlots) & 1) ^ 1);
-            const bool k = kinds >> (copy - 1 - c) & 1;
+            const bool k = DP == NC || (kinds >> (copy - 1 - c) & 1);
             if (W.box) {
                 wait_warp(&S.raw_full[c % kRing], (c / kRing) & 1);
                 if (k) widen_rows(std::true_type{}, std::true_type{}, c);
-                else widen_rows(std::false_type{}, std::true_type{}, c);
+                else widen_rows(OfV{}, std::true_type{}, c);
                 mbar_arrive(&S.raw_empty[c % kRing]);
             } else {
                 if (k) widen_rows(std::true_type{}, std::false_type{}, c);
-                else widen_rows(std::false_type{}, std::false_type{}, c);
+                else widen_rows(OfV{}, std::false_type{}, c);
             }
             mbar_arrive(&S.full[c % T::kSlots]);
         };
@@ -832,7 +876,7 @@ __global__ void __launch_bounds__(tree::kThreads, 1) attn_tree_kernel(const Tree
                         advance();
                     }
                     if (j >= 1) {
-                        issue_boxes(std::false_type{}, &v_map, v_page, v_slot, it.kh, it.half);
+                        issue_boxes(OfV{}, &v_map, v_page, v_slot, it.kh, it.half);
                         advance();
                     }
                     v_page = k_page;
@@ -881,7 +925,7 @@ __global__ void __launch_bounds__(tree::kThreads, 1) attn_tree_kernel(const Tree
                     advance();
                 }
                 if (j >= 1) {
-                    issue(std::false_type{}, (const char *)P.v_cache, tile - (j < at.cnt ? 2 : 1), it.half);
+                    issue(OfV{}, (const char *)P.v_cache, tile - (j < at.cnt ? 2 : 1), it.half);
                     advance();
                 }
             }
@@ -908,64 +952,79 @@ __global__ void __launch_bounds__(tree::kThreads, 1) attn_tree_kernel(const Tree
             const uint32_t lead = tc_elect();
             constexpr bool kBf = FMT == COLI_KV_BF16;
             constexpr uint32_t kQk = idesc_f32acc(kTreeRows, TN, kBf), kPv = idesc_f32acc(kTreeRows, NC, kBf) | kIdescBMnMajor;
+            // (loops are short, so that this warp's instructions stay near: it is waited for by all others)
             const uint64_t q_desc = sdesc_k_sw128(smem_u32(sm));
-            const uint32_t slots_a = smem_u32(slots);
-            uint32_t count = 0, copies = 0, part = 0;
+            uint64_t k_desc = sdesc_k_sw128(smem_u32(slots)), v_desc = sdesc_mn_sw128(smem_u32(slots), kSlab);
+            uint32_t k = 0, part = 0, slot = 0, lap = 0;  // slots are used up in the order of the copies
+            auto next_slot = [&]() {
+                if (++slot == T::kSlots) {
+                    slot = 0;
+                    lap ^= 1;
+                }
+            };
             at.begin(P, W, S.pre, from, units);
             do {
                 wait_warp(&S.q_full, part & 1);
-                for (int j = 0; j <= at.cnt; j++) {
+#pragma unroll 1
+                for (int j = 0; j <= at.cnt; j++, k++) {
                     if (j < at.cnt) {
-                        const uint32_t k = count + j, g = k & 1, use = k >> 1, c = copies + k_copy(j), slot = c % T::kSlots;
-                        wait_warp(&S.full[slot], (c / T::kSlots) & 1);
+                        const uint32_t g = k & 1;
+                        wait_warp(&S.full[slot], lap);
                         // the scores' place still holds the p of two tiles before until its products have ended
-                        if (use) wait_warp(&S.o_full[g], (use - 1) & 1);
+                        if (k >= 2) wait_warp(&S.o_full[g], ((k >> 1) - 1) & 1);
                         fence_async_smem();  // what the copies wrote is read by the tensor core
                         tc_fence_after_sync();
-                        const uint64_t kd = sdesc_k_sw128(slots_a + slot * T::kSlotBytes);
+                        uint32_t more = 0;
+#pragma unroll 1
+                        for (int p = T::kQParts - 1; p >= 0; p--) {
+#pragma unroll 1
+                            for (int b = 0; b < DP / 64; b++) {
+                                const uint64_t qd = q_desc + (p * (DP / 64) + b) * (kTreeRows * 128 >> 4);
+                                const uint64_t kd = k_desc + slot * (T::kSlotBytes >> 4) + b * (kSlab >> 4);
 #pragma unroll
-                        for (int p = T::kQParts - 1; p >= 0; p--)
-#pragma unroll
-                            for (int s = 0; s < DP / 16; s++)
-                                tc_mma_f16kind(score_at(g),
-                                               q_desc + ((p * (kTreeRows * DP * 2) + (s / 4) * (kTreeRows * 128) + (s % 4) * 32) >> 4),
-                                               kd + (((s / 4) * kSlab + (s % 4) * 32) >> 4), kQk, p < T::kQParts - 1 || s > 0, lead);
+                                for (int i = 0; i < 4; i++) {
+                                    tc_mma_f16kind(score_at(g), qd + 2 * i, kd + 2 * i, kQk, more, lead);
+                                    more = 1;
+                                }
+                            }
+                        }
                         tc_commit(&S.s_full[g], lead);
                         tc_commit(&S.empty[slot], lead);
+                        next_slot();
                     }
                     if (j >= 1) {
-                        const uint32_t k = count + j - 1, g = k & 1, use = k >> 1, c = copies + v_copy(j - 1, at.cnt), slot = c % T::kSlots;
-                        wait_warp(&S.full[slot], (c / T::kSlots) & 1);
+                        const uint32_t g = (k - 1) & 1, use = (k - 1) >> 1;
+                        wait_warp(&S.full[slot], lap);
                         // for those who look at the values. (They cannot wait for the slot: who waits for some phases of a barrier
                         // only must not be two behind, and here a phase ends with the products of two tiles before.)
                         if (lead) mbar_arrive(&S.v_full[g]);
                         // the sums' place has been read: two tiles before, or one where there is one place
-                        const uint32_t was = T::kSumBuffers == 2 ? k - 2 : k - 1;
-                        if (k >= (uint32_t)T::kSumBuffers) wait_warp(&S.o_free[was & 1], (was >> 1) & 1);
-                        wait_warp(&S.p_half[g], use & 1);
-                        fence_async_smem();
-                        tc_fence_after_sync();
-                        const uint64_t vd = sdesc_mn_sw128(slots_a + slot * T::kSlotBytes, kSlab);
-#pragma unroll
+                        const uint32_t was = k - 1 - T::kSumBuffers;
+                        if (k > (uint32_t)T::kSumBuffers) wait_warp(&S.o_free[was & 1], (was >> 1) & 1);
+                        uint32_t more = 0;
+#pragma unroll 1
                         for (int h = 0; h < 2; h++) {
-                            if (h) {
-                                wait_warp(&S.p_ready[g], use & 1);
-                                tc_fence_after_sync();
-                            }
+                            wait_warp(h ? &S.p_ready[g] : &S.p_half[g], use & 1);
+                            if (!h) fence_async_smem();
+                            tc_fence_after_sync();
+#pragma unroll 1
+                            for (int p = T::kPParts - 1; p >= 0; p--) {
+                                const uint32_t to = p < 2 ? 16 : 8;  // columns of 16 places
+                                const uint32_t a = score_at(g) + (p < 2 ? 8 * p : TN) + h * (TN / 32) * to;
+                                const uint64_t vd = v_desc + slot * (T::kSlotBytes >> 4) + h * (TN / 32) * (2048 >> 4);
 #pragma unroll
-                            for (int p = T::kPParts - 1; p >= 0; p--)
-#pragma unroll
-                                for (int s = h * (TN / 32); s < (h + 1) * (TN / 32); s++) {
-                                    const uint32_t a = score_at(g) + (p < 2 ? 16 * s + 8 * p : TN + 8 * s);
-                                    tc_mma_f16kind_ta(sums_at(g), a, vd + (s * 2048 >> 4), kPv, h > 0 || p < T::kPParts - 1 || s > 0, lead);
+                                for (int i = 0; i < TN / 32; i++) {
+                                    tc_mma_f16kind_ta(sums_at(g), a + i * to, vd + i * (2048 >> 4), kPv, more, lead);
+                                    more = 1;
                                 }
+                            }
                         }
                         tc_commit(&S.o_full[g], lead);
                         tc_commit(&S.empty[slot], lead);
+                        next_slot();
                     }
                 }
-                count += at.cnt;
-                copies += 2 * at.cnt;
+                k--;  // (the last round has no scores)
                 part++;
             } while (at.next(P, W, S.pre));
             tc_commit(&S.done, lead);
