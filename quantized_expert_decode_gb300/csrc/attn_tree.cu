@@ -9,6 +9,7 @@ namespace colimoe {
 namespace {
 
 constexpr int kPer = 2;  // float4 columns of a thread
+static_assert(kPer == 2, "8 columns are stored at once");
 
 // One block per (border between runs, kPer columns of four): the blocks of an item's first cut add up the partial sums
 // of all runs that hold units of the item, in their order. A thread has a row. Everything is scaled to the largest m, by
@@ -17,16 +18,9 @@ __global__ void __launch_bounds__(kTreeRows) attn_tree_join_kernel(const TreePar
     let_next_start();
     wait_for_previous();
     const int c = blockIdx.x + 1, runs = W.cuts[0].runs;
-    if (c >= runs) return;
-    const TreeCut cut = W.cuts[c];
-    if (cut.b < 0) return;
+    const TreeCut cut = W.cuts[c];  // written if c < runs
     const int group = P.q_heads / P.kv_heads, r = threadIdx.x;
-    int row, n, past, why;
-    draft_rows(P.first[cut.b], P.first[cut.b + 1], P.rows, P.nodes, row, n, why);
-    draft_places(P.past[cut.b], P.table_width, P.cache.page_size, past, n, why);
-    const TreeItem it = tree_item(cut.item, (n * group + kTreeRows - 1) / kTreeRows, W.halves);
-    const int at = it.tile * kTreeRows + r;
-    if (at >= n * group) return;
+    if (c >= runs || r >= cut.rows) return;
     const int c0 = c - 1, col = blockIdx.y * kPer;
     float4 o[kPer];
     float l = 0.f, m = -INFINITY;
@@ -51,20 +45,35 @@ __global__ void __launch_bounds__(kTreeRows) attn_tree_join_kernel(const TreePar
             o[j].w = fmaf(o[j].w, f0, v[j].w * f1);
         }
     }
-    const int node = at / group, head = it.kh * group + at - node * group;
-    const float norm = l == 0.f ? 0.f : (P.v_scale ? P.v_scale[it.kh] : 1.f) / l;
-    const int64_t out = (int64_t)(row + node) * P.out_stride + (int64_t)head * P.dim;
+    const int at = cut.first + r, node = kv_quotient(W.group, at), head = cut.kh * group + at - node * group;
+    const float norm = l == 0.f ? 0.f : (P.v_scale ? P.v_scale[cut.kh] : 1.f) / l;
+    const int64_t out = (int64_t)(cut.row + node) * P.out_stride + (int64_t)head * P.dim;
+    const int d = cut.half * W.cols + col * 4;  // 8 columns, which lie within the head or behind it
+    if (d < P.dim) {
+        const float x[8] = {o[0].x * norm, o[0].y * norm, o[0].z * norm, o[0].w * norm,
+                            o[1].x * norm, o[1].y * norm, o[1].z * norm, o[1].w * norm};
+        if (W.out_vec && P.act == COLI_ACT_F32) {
+            Run<float, 8> v;
 #pragma unroll
-    for (int j = 0; j < kPer; j++) {
-        const int d = it.half * W.cols + (col + j) * 4;
-        if (d >= P.dim) continue;  // (a multiple of 8)
-        store_act(P.out, out + d, o[j].x * norm, P.act);
-        store_act(P.out, out + d + 1, o[j].y * norm, P.act);
-        store_act(P.out, out + d + 2, o[j].z * norm, P.act);
-        store_act(P.out, out + d + 3, o[j].w * norm, P.act);
+            for (int e = 0; e < 8; e++) v.e[e] = x[e];
+            v.store((float *)P.out + out + d);
+        } else if (W.out_vec && P.act == COLI_ACT_BF16) {
+            Run<__nv_bfloat16, 8> v;
+#pragma unroll
+            for (int e = 0; e < 8; e++) v.e[e] = from_f32<__nv_bfloat16>(x[e]);
+            v.store((__nv_bfloat16 *)P.out + out + d);
+        } else if (W.out_vec) {
+            Run<__half, 8> v;
+#pragma unroll
+            for (int e = 0; e < 8; e++) v.e[e] = from_f32<__half>(x[e]);
+            v.store((__half *)P.out + out + d);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; e++) store_act(P.out, out + d + e, x[e], P.act);
+        }
     }
-    if (P.lse && it.half == 0 && col == 0)
-        P.lse[(int64_t)(row + node) * P.q_heads + head] = attn_lse(m == -INFINITY ? 0.f : m, l, shift);
+    if (P.lse && cut.half == 0 && col == 0)
+        P.lse[(int64_t)(cut.row + node) * P.q_heads + head] = attn_lse(m == -INFINITY ? 0.f : m, l, shift);
 }
 
 using Encode = decltype(&cuTensorMapEncodeTiled);

@@ -43,9 +43,10 @@ struct TreeTraits {
     static_assert(2 * kScoreCols + kSumBuffers * kCols <= 512, "tensor memory of an SM");
 };
 
-// The item whose units the border before a run cuts, told for its first cut only (b < 0: none)
-struct TreeCut {
-    int32_t b, item, last, runs;
+// The item whose units the border before a run cuts, told for its first cut only (else it has no rows): its rows are
+// [first, first + rows) of the (node, head) pairs of a sequence whose nodes begin at `row`
+struct alignas(16) TreeCut {
+    int32_t rows, last, row, runs, first, kh, half, reserved = 0;
 };
 
 // How the launch is laid out, and the workspace

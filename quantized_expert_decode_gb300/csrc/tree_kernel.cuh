@@ -937,12 +937,16 @@ __global__ void __launch_bounds__(tree::kThreads, 1) attn_tree_kernel(const Tree
         // ================================================================ products: one warp issues them
         if (lane == 1) {
             // the border before this run, for the join
-            TreeCut cut{-1, 0, 0, (int32_t)R.runs};
+            TreeCut cut{0, 0, 0, (int32_t)R.runs, 0, 0};
             at.begin(P, W, S.pre, from, units);
             if (at.u > 0 && run > 0 && from - (uint32_t)at.u >= R.start(run - 1)) {
-                cut.b = at.b;
-                cut.item = at.item;
+                const TreeItem it = tree_item(at.item, at.s.row_tiles, T::kHalves);
+                cut.rows = min(kTreeRows, at.s.n * group - it.tile * kTreeRows);
                 cut.last = R.of(from - (uint32_t)at.u + (uint32_t)at.s.tiles - 1);
+                cut.row = at.s.row;
+                cut.first = it.tile * kTreeRows;
+                cut.kh = it.kh;
+                cut.half = it.half;
             }
             W.cuts[run] = cut;
         }
