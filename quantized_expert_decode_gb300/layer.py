@@ -1,55 +1,161 @@
-"""A decoder layer's decode step around the MoE block: the paged cache, its page tables, and the
-calls in the order a layer makes them. Allocation, bookkeeping of pages and the two plain
-projections (library products); everything else runs in the library's kernels."""
+"""A decoder layer's decode step around the MoE block, for one new token of every sequence or for a tree of
+drafted tokens: the paged cache, its page tables, and the calls in the order a layer makes them. Allocation,
+bookkeeping of pages and the two plain projections (library products); everything else runs in the
+library's kernels."""
 from __future__ import annotations
 
 import torch
 
-from . import (COLI_ACT_F32, COLI_GATE_NONE, COLI_KV_BF16, COLI_KV_E4M3, COLI_KV_F16, coli_attn_decode,
-               coli_attn_workspace_bytes, coli_block_norms, coli_kv_append, coli_moe_check, coli_moe_forward,
-               make_append_desc, make_attn_desc, make_kv_cache, make_norms_desc)
+from . import (COLI_ACT_F32, COLI_GATE_NONE, COLI_KV_BF16, COLI_KV_E4M3, COLI_KV_F16, coli_attn_decode, coli_attn_tree,
+               coli_attn_workspace_bytes, coli_block_norms, coli_kv_append, coli_kv_compact, coli_kv_copy_pages,
+               coli_moe_check, coli_moe_desc, coli_moe_forward, coli_moe_workspace_bytes, coli_norm_append,
+               coli_tree_workspace_bytes, make_append_desc, make_attn_desc, make_compact_desc, make_kv_cache,
+               make_kv_caches, make_norm_append_desc, make_norms_desc, make_tree_desc)
 
 _TORCH = {COLI_KV_BF16: torch.bfloat16, COLI_KV_F16: torch.float16, COLI_KV_E4M3: torch.float8_e4m3fn}
 
 
 class PagedCache:
-    """Pools of `pages` pages for keys and values, and a page table for `seqs` sequences. Pages are handed
-    out as sequences grow and come back when a sequence ends; nothing is copied or cleared. The table is
-    written on torch's current stream."""
+    """Pools of `pages` pages for keys and values, for each of `layers` layers, and one page table for `seqs`
+    sequences. Pages are handed out as sequences grow and come back when the last sequence that holds them
+    ends. Sequences that were forked share pages; one that is about to be written is copied first. The table is
+    written and pages are copied on torch's current stream."""
 
     def __init__(self, seqs, pages, page_size, heads, dim, fmt=COLI_KV_BF16, max_tokens=None, k_scale=None,
-                 v_scale=None, device="cuda"):
+                 v_scale=None, device="cuda", layers=1):
         self.seqs, self.page_size, self.heads, self.dim, self.fmt = seqs, page_size, heads, dim, fmt
         self.device = torch.device(device)
         self.width = -(-(max_tokens or pages * page_size) // page_size)
         pool = (pages, heads, page_size, dim)
-        self.k = torch.empty(pool, dtype=_TORCH[fmt], device=self.device)
-        self.v = torch.empty(pool, dtype=_TORCH[fmt], device=self.device)
+        self.k_pools = [torch.empty(pool, dtype=_TORCH[fmt], device=self.device) for _ in range(layers)]
+        self.v_pools = [torch.empty(pool, dtype=_TORCH[fmt], device=self.device) for _ in range(layers)]
+        self.k, self.v = self.k_pools[0], self.v_pools[0]
         self.k_scale, self.v_scale = k_scale, v_scale
         self.table = torch.full((seqs, self.width), -1, dtype=torch.int32, device=self.device)
         self.free = list(range(pages - 1, -1, -1))
         self.held = [[] for _ in range(seqs)]
+        self.uses = [0] * pages  # sequences that hold a page
         self.tokens = [0] * seqs
-        self.desc = make_kv_cache(self.k, self.v, fmt, pages, page_size, heads, dim, k_scale=k_scale, v_scale=v_scale)
+        self.descs = [make_kv_cache(k, v, fmt, pages, page_size, heads, dim, k_scale=k_scale, v_scale=v_scale)
+                      for k, v in zip(self.k_pools, self.v_pools)]
+        self.desc = self.descs[0]
+        self.caches = make_kv_caches(self.descs)
+
+    def _take(self):
+        page = self.free.pop()
+        self.uses[page] = 1
+        return page
+
+    def _give(self, page):
+        self.uses[page] -= 1
+        if self.uses[page] == 0:
+            self.free.append(page)
+
+    def _write(self, seq, first, pages):
+        self.table[seq, first:first + len(pages)] = torch.tensor(pages, dtype=torch.int32, device=self.device)
+
+    def _copy(self, src, dst):
+        pair = torch.tensor([src, dst], dtype=torch.int32, device=self.device)
+        stream = torch.cuda.current_stream(self.device) if self.device.type == "cuda" else None
+        coli_kv_copy_pages(self.caches, len(self.descs), 1, pair[:1], pair[1:], None, stream)
 
     def grow(self, seq, n=1):
         """Makes room for n more tokens of a sequence; returns the position of the first."""
         at = self.tokens[seq]
+        held = self.held[seq]
         want = -(-(at + n) // self.page_size)
-        if want > self.width or want - len(self.held[seq]) > len(self.free):
+        # the page that the next token goes to, where another sequence holds it too
+        shared = n > 0 and at % self.page_size != 0 and self.uses[held[at // self.page_size]] > 1
+        if want > self.width or want - len(held) + shared > len(self.free):
             raise MemoryError("the cache has no page left")
-        new = [self.free.pop() for _ in range(want - len(self.held[seq]))]
+        if shared:
+            i, page = at // self.page_size, self._take()
+            self._copy(held[i], page)
+            self._give(held[i])
+            held[i] = page
+            self._write(seq, i, [page])
+        new = [self._take() for _ in range(want - len(held))]
         if new:
-            first = len(self.held[seq])
-            self.table[seq, first:want] = torch.tensor(new, dtype=torch.int32, device=self.device)
-            self.held[seq] += new
+            self._write(seq, len(held), new)
+            held += new
         self.tokens[seq] = at + n
         return at
 
+    def cut(self, seq, tokens):
+        """Keeps the first `tokens` tokens of a sequence; pages behind them are given back."""
+        if not 0 <= tokens <= self.tokens[seq]:
+            raise ValueError("a sequence is cut to a part of its tokens")
+        keep = -(-tokens // self.page_size)
+        held = self.held[seq]
+        for page in reversed(held[keep:]):
+            self._give(page)
+        if len(held) > keep:
+            self.table[seq, keep:len(held)].fill_(-1)
+        del held[keep:]
+        self.tokens[seq] = tokens
+
+    def fork(self, seq, to):
+        """Makes sequence `to`, which must be empty, a copy of `seq`: the pages are shared, but for a last one that is
+        not full, which is copied."""
+        if seq == to or self.held[to]:
+            raise ValueError("a sequence is forked to an empty one")
+        tokens, pages = self.tokens[seq], self.held[seq][: -(-self.tokens[seq] // self.page_size)]
+        last = tokens % self.page_size != 0
+        if last and not self.free:
+            raise MemoryError("the cache has no page left")
+        mine = list(pages)
+        for page in pages[: len(pages) - last]:
+            self.uses[page] += 1
+        if last:
+            mine[-1] = self._take()
+            self._copy(pages[-1], mine[-1])
+        if mine:
+            self._write(to, 0, mine)
+        self.held[to], self.tokens[to] = mine, tokens
+
+    def compact(self, past, path, count, err=None, stream=None):
+        """Moves the rows of accepted nodes up behind the committed tokens, in all layers (past, count [seqs] int32, path
+        [seqs][nodes] int32 as coli_draft_verify gives them, on the device). The page table stays; cut() gives
+        back what is behind."""
+        stream = torch.cuda.current_stream(self.device) if stream is None else stream
+        desc = make_compact_desc(self.seqs, path.shape[1], self.width, len(self.descs))
+        coli_kv_compact(desc, self.caches, past, path, count, self.table, err, stream)
+
     def end(self, seq):
-        self.free += reversed(self.held[seq])
+        for page in reversed(self.held[seq]):
+            self._give(page)
         self.held[seq], self.tokens[seq] = [], 0
         self.table[seq].fill_(-1)
+
+
+class Nodes:
+    """The drafted nodes of all sequences of a cache, one behind the other, as the calls take them: for each sequence
+    how many tokens are committed and the nodes' parents (a list, -1 for a node behind the last committed token;
+    empty: an idle slot). `rows` rows in all, at most `nodes` of a sequence; where `rows` is given, the rows behind the
+    last node are padding. The nodes' places (past + index) must have been made room for."""
+
+    def __init__(self, past, parents, rows=None, nodes=None, device="cuda"):
+        count = [len(p) for p in parents]
+        total = sum(count)
+        self.rows, self.nodes = rows or max(total, 1), nodes or max(max(count), 1)
+        if total > self.rows or max(count) > self.nodes:
+            raise ValueError("more nodes than rows")
+        first, seq, pos, place, parent = [0], [], [], [], []
+        for b, (at, tree) in enumerate(zip(past, parents)):
+            depth = []
+            for i, p in enumerate(tree):
+                if not -1 <= p < i:
+                    raise ValueError("a node's parent comes before it")
+                depth.append(depth[p] + 1 if p >= 0 else 0)
+            first.append(first[-1] + len(tree))
+            seq += [b] * len(tree)
+            pos += [at + d for d in depth]
+            place += range(at, at + len(tree))
+            parent += tree
+        pad = self.rows - total
+        ints = lambda x: torch.tensor(x, dtype=torch.int32, device=device)  # noqa: E731
+        self.first, self.past, self.seq = ints(first), ints(list(past)), ints(seq + [-1] * pad)
+        self.pos, self.place, self.parent = ints(pos + [0] * pad), ints(place + [0] * pad), ints(parent + [-1] * pad)
 
 
 class DecodeLayer:
@@ -59,11 +165,14 @@ class DecodeLayer:
 
       w_qkv [(q_heads + 2 kv_heads) * dim, H], w_o [H, q_heads * dim]; mid_w, next_w [H]: the norms in
       front of the block and of the next layer; attn_post_w, block_post_w [H] or None: norms of what
-      attention and block give back, before the residual takes it."""
+      attention and block give back, before the residual takes it; q_norm, k_norm [dim] fp32 or None: norms of
+      every head's query and key in front of the rotation; layer: which of the cache's layers this is."""
 
     def __init__(self, block, cache: PagedCache, w_qkv, w_o, mid_w, next_w, inv_freq, q_heads, eps=1e-5, window=0,
-                 interleaved=False, attn_post_w=None, block_post_w=None):
+                 interleaved=False, attn_post_w=None, block_post_w=None, q_norm=None, k_norm=None, layer=0):
         self.block, self.cache, self.q_heads, self.eps = block, cache, q_heads, eps
+        self.desc, self.window, self.interleaved = cache.descs[layer], window, interleaved
+        self.q_norm, self.k_norm = q_norm, k_norm
         self.w_qkv, self.w_o, self.inv_freq = w_qkv, w_o, inv_freq
         self.mid_w, self.next_w, self.attn_post_w, self.block_post_w = mid_w, next_w, attn_post_w, block_post_w
         n, h, d, kh = cache.seqs, w_o.shape[0], cache.dim, cache.heads
@@ -73,9 +182,12 @@ class DecodeLayer:
         # q, k and v are slices of one projection's rows; q is rotated where it lies
         self.append = make_append_desc(n, q_heads, n, cache.width, COLI_ACT_F32, 2 * inv_freq.numel(), interleaved,
                                        q_stride=row, k_stride=row, v_stride=row, q_out_stride=row)
+        if q_norm is not None or k_norm is not None:
+            self.append = make_norm_append_desc(n, q_heads, n, cache.width, COLI_ACT_F32, 2 * inv_freq.numel(), interleaved,
+                                                eps, row, row, row, row)
         self.attn = make_attn_desc(n, q_heads, cache.width, COLI_ACT_F32, d ** -0.5, window=window, q_stride=row)
         self.norms = make_norms_desc(n, h, COLI_ACT_F32, COLI_GATE_NONE, eps, eps)
-        ws_bytes = coli_attn_workspace_bytes(self.attn, cache.desc)
+        ws_bytes = coli_attn_workspace_bytes(self.attn, self.desc)
         if ws_bytes == 0:
             raise ValueError("the attention does not take this cache with these heads and sequences")
         self.ws = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
@@ -95,13 +207,16 @@ class DecodeLayer:
         given must be ready on the current stream, and the result is: another `stream` waits for the current one
         before the step, and the current one for it after. Can be captured into a graph (after one step outside
         it, which sets up the library products)."""
+        return self._on(stream, lambda s: self._run(xn, resid, pos, lens, seq, s))
+
+    def _on(self, stream, run):
         now, on = self._streams(stream)
         if on is None:
-            return self._run(xn, resid, pos, lens, seq, now)
+            return run(now)
         on.wait_stream(now)
         try:
             with torch.cuda.stream(on):
-                out = self._run(xn, resid, pos, lens, seq, on)
+                out = run(on)
         finally:  # what is under way still reads the arguments
             now.wait_stream(on)
         out.record_stream(now)  # it is on's memory
@@ -115,26 +230,92 @@ class DecodeLayer:
             stream = torch.cuda.ExternalStream(stream, dev) if stream else torch.cuda.default_stream(dev)
         return now, None if stream is None or stream.cuda_stream == now.cuda_stream else stream
 
-    def _run(self, xn, resid, pos, lens, seq, stream):
-        c, d, qd = self.cache, self.cache.dim, self.q_heads * self.cache.dim
-        kd = c.heads * d
+    def _project(self, xn):
+        qd, kd = self.q_heads * self.cache.dim, self.cache.heads * self.cache.dim
         qkv = xn @ self.w_qkv.T
-        q, k, v = qkv[:, :qd], qkv[:, qd:qd + kd], qkv[:, qd + kd:]
-        coli_kv_append(self.append, c.desc, q, k, v, self.inv_freq, seq, pos, c.table, q, self.err, stream)
-        coli_attn_decode(self.attn, c.desc, q, c.table, lens, self.heads_out, None, self.err, self.ws, self.ws.numel(),
+        return qkv[:, :qd], qkv[:, qd:qd + kd], qkv[:, qd + kd:]
+
+    def _run(self, xn, resid, pos, lens, seq, stream):
+        c = self.cache
+        q, k, v = self._project(xn)
+        if self.q_norm is None and self.k_norm is None:
+            coli_kv_append(self.append, self.desc, q, k, v, self.inv_freq, seq, pos, c.table, q, self.err, stream)
+        else:
+            coli_norm_append(self.append, self.desc, q, k, v, self.q_norm, self.k_norm, self.inv_freq, seq, pos, None, c.table,
+                             q, self.err, stream)
+        coli_attn_decode(self.attn, self.desc, q, c.table, lens, self.heads_out, None, self.err, self.ws, self.ws.numel(),
                          stream)
-        y = self.heads_out @ self.w_o.T
-        mid = torch.empty_like(y)
-        coli_block_norms(self.norms, y, resid, self.attn_post_w, None, self.mid_w, resid, mid, stream)
         b = self.block
-        coli_moe_forward(b.desc, mid, b.Wr, b.bias, b.table, b.shared, self.block_out, None, None, b.ws, b.ws_bytes,
-                         stream)
+        return self._rest(self.heads_out, resid, self.norms, b.desc, b.ws, b.ws_bytes, self.block_out, stream)
+
+    def _rest(self, heads_out, resid, norms, block_desc, block_ws, block_ws_bytes, block_out, stream):
+        """From the attention's heads to the next layer's input."""
+        y = heads_out @ self.w_o.T
+        mid = torch.empty_like(y)
+        coli_block_norms(norms, y, resid, self.attn_post_w, None, self.mid_w, resid, mid, stream)
+        b = self.block
+        coli_moe_forward(block_desc, mid, b.Wr, b.bias, b.table, b.shared, block_out, None, None, block_ws,
+                         block_ws_bytes, stream)
         out = torch.empty_like(y)
-        coli_block_norms(self.norms, self.block_out, resid, self.block_post_w, None, self.next_w, resid, out, stream)
+        coli_block_norms(norms, block_out, resid, self.block_post_w, None, self.next_w, resid, out, stream)
         return out
 
-    def check(self, stream=None):
-        """Raises if a kernel flagged an error since the last check (synchronises `stream`, or the current one)."""
+    def drafts(self, rows, nodes):
+        """What draft_step needs for `rows` rows of nodes, at most `nodes` of a sequence."""
+        return _Drafts(self, rows, nodes)
+
+    def draft_step(self, drafts, xn, resid, nodes, stream=None):
+        """The layer's step for drafted nodes: xn [rows, H] their normalised inputs, resid [rows, H] their residuals
+        (updated in place), nodes a Nodes of as many rows. Every node sees its sequence's committed tokens, its ancestors
+        and itself; its key and value are cached at its place. Returns the next layer's xn. Rows of padding go through
+        the block and mean nothing. Streams and capturing as in step()."""
+        if nodes.rows != drafts.rows or nodes.nodes > drafts.nodes or xn.shape[0] != drafts.rows:
+            raise ValueError("the step was made for other rows or nodes")
+        return self._on(stream, lambda s: self._run_drafts(drafts, xn, resid, nodes, s))
+
+    def _run_drafts(self, d, xn, resid, nodes, stream):
+        c = self.cache
+        q, k, v = self._project(xn)
+        coli_norm_append(d.append, self.desc, q, k, v, self.q_norm, self.k_norm, self.inv_freq, nodes.seq, nodes.pos,
+                         nodes.place, c.table, q, self.err, stream)
+        coli_attn_tree(d.attn, self.desc, q, nodes.first, nodes.past, nodes.parent, c.table, d.heads_out, None, self.err,
+                       d.ws, d.ws.numel(), stream)
+        return self._rest(d.heads_out, resid, d.norms, d.block, d.block_ws, d.block_ws.numel(), d.block_out, stream)
+
+    def check(self, stream=None, drafts=None):
+        """Raises if a kernel flagged an error since the last check (synchronises `stream`, or the current one); `drafts`:
+        in steps made with it, too."""
         now, on = self._streams(stream)
         coli_moe_check(self.err, on or now)
         coli_moe_check(self.block.ws, on or now)
+        if drafts is not None:
+            coli_moe_check(drafts.block_ws, on or now)
+
+
+class _Drafts:
+    """Descriptions and buffers of a layer's steps on drafted nodes."""
+
+    def __init__(self, layer, rows, nodes):
+        c, dev = layer.cache, layer.cache.device
+        h, qd = layer.w_o.shape
+        row = qd + 2 * c.heads * c.dim
+        self.rows, self.nodes = rows, nodes
+        # q, k and v are slices of one projection's rows; q is rotated where it lies
+        self.append = make_norm_append_desc(rows, layer.q_heads, c.seqs, c.width, COLI_ACT_F32, 2 * layer.inv_freq.numel(),
+                                            layer.interleaved, layer.eps, row, row, row, row)
+        self.attn = make_tree_desc(c.seqs, rows, nodes, layer.q_heads, c.width, COLI_ACT_F32, c.dim ** -0.5,
+                                   window=layer.window, q_stride=row)
+        self.norms = make_norms_desc(rows, h, COLI_ACT_F32, COLI_GATE_NONE, layer.eps, layer.eps)
+        ws_bytes = coli_tree_workspace_bytes(self.attn, layer.desc)
+        if ws_bytes == 0:
+            raise ValueError("the attention does not take this cache with these heads and nodes")
+        self.ws = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
+        self.block = coli_moe_desc.from_buffer_copy(layer.block.desc)
+        self.block.T = rows
+        block_bytes = coli_moe_workspace_bytes(self.block)
+        if block_bytes == 0:
+            raise ValueError("the block does not take as many rows")
+        self.block_ws = torch.zeros(block_bytes, dtype=torch.uint8, device=dev)
+        # rows that no sequence names stay 0
+        self.heads_out = torch.zeros(rows, qd, device=dev)
+        self.block_out = torch.empty(rows, h, device=dev)
