@@ -390,3 +390,15 @@ def test_steps_on_nodes_in_a_graph_and_on_a_stream(q):
             graph.replay()
     side.synchronize()
     near(y, want)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("args", [["--steps", "3"], ["--layers", "1", "--seqs", "3", "--past", "0", "--wide", "1", "--deep", "5", "--steps", "4"]])
+def test_the_example_runs(q, args):
+    import os
+    import subprocess
+    import sys
+    at = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "draft_layer.py")
+    r = subprocess.run([sys.executable, at, *args], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
+    assert "tokens of a sequence a step" in r.stdout
