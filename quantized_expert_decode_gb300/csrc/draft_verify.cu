@@ -6,14 +6,16 @@
 // numbers (a, m), and a child x with random number u is accepted iff (a + u m) q(x) < p(x). Without a draft r is p
 // without the rejected tokens.
 //
-// Sums over the vocabulary are kept as unevaluated pairs of floats (48 bits; 64-bit additions would take 30 times
-// an fp32 addition's time) and joined in 64 bits, so that a number falls on the wrong side of a border between two
-// tokens with a chance of some 2^-45 times the tokens, whatever the order of the sums.
+// Sums over the vocabulary are kept and joined as unevaluated pairs of floats (48 bits; 64-bit additions would take 30
+// times an fp32 addition's time), so that a number falls on the wrong side of a border between two tokens with a
+// chance of some 2^-45 times the tokens, whatever the order of the sums; the tests themselves are in 64 bits.
 //
 // What bounds it: for few sequences the latency of its steps: nodes, their entries, one or two rows of p and q
 // spread over the cluster's CTAs, and the exchange of the CTAs' sums through distributed shared memory. All CTAs of a
 // cluster walk the nodes alike; only sums are shared. Nodes that are accepted at their first test need no row at all:
-// the entries that the tests need are gathered at the start, all at once.
+// the entries that the tests need are gathered at the start, all at once. A rejection reads the node's rows of p and q, from
+// L2 if it is not the first there: of 32 sequences with 131072 tokens 33 MB a pass, 3 to 5 us, and the exchange 2 to 4; the
+// sequence with most rejections (six there) sets the time. (512 threads instead of 256: 82 us with 8 CTAs, 127 with 16.)
 #include <cooperative_groups.h>
 
 #include "act.cuh"
@@ -26,17 +28,31 @@ namespace cg = cooperative_groups;
 namespace colimoe {
 namespace {
 
-constexpr int kThreads = 512, kWarps = kThreads / 32;
-constexpr int kCluster = 8;
+constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kCluster = 16, kLeast = 8;  // CTAs of a cluster: where sequences are few, and else
+constexpr int kFewSeqs = 64, kLongRow = 65536;
 constexpr int kMaxNodes = 1024;
 constexpr int kMaxVocab = 1 << 20;
-constexpr int kChunk = 512;  // tokens of a warp's sum
+constexpr int kChunk = 256;  // tokens of a warp's sum
 constexpr int kPer = 4;      // tokens of a lane at once
-constexpr int kMaxChunks = (kMaxVocab / kCluster + kChunk - 1) / kChunk + 1;
+constexpr int kMaxChunks = (kMaxVocab / kLeast + kChunk - 1) / kChunk + 1;
 
 struct Two {
     float hi, lo;
 };
+// Two sums beside each other, by packed instructions
+struct Twos {
+    float2 hi, lo;
+};
+// a - b in one packed instruction
+__device__ __forceinline__ float2 minus(float2 a, float2 b) { return __ffma2_rn(b, make_float2(-1.f, -1.f), a); }
+// s + x, the rounding error kept
+__device__ __forceinline__ void add(Twos &s, float2 x, float2 rest) {
+    const float2 t = __fadd2_rn(s.hi, x), z = minus(t, s.hi);
+    const float2 e = __fadd2_rn(minus(s.hi, minus(t, z)), minus(x, z));
+    s.hi = t;
+    s.lo = __fadd2_rn(s.lo, __fadd2_rn(e, rest));
+}
 // s + x, the rounding error kept
 __device__ __forceinline__ void add(Two &s, float x, float rest) {
     const float t = __fadd_rn(s.hi, x), z = __fsub_rn(t, s.hi);
@@ -44,30 +60,36 @@ __device__ __forceinline__ void add(Two &s, float x, float rest) {
     s.hi = t;
     s.lo = __fadd_rn(s.lo, __fadd_rn(e, rest));
 }
-__device__ __forceinline__ double warp_total(Two s) {
+__device__ __forceinline__ double value(Two s) { return (double)s.hi + (double)s.lo; }
+// the sum of all lanes: every lane gets lane 0's, as the additions' roundings depend on their order and what is decided by
+// a sum has to be decided alike by all threads
+__device__ __forceinline__ Two warp_total(Two s) {
 #pragma unroll
     for (int o = 16; o; o >>= 1) {
         const float hi = __shfl_xor_sync(0xffffffffu, s.hi, o), lo = __shfl_xor_sync(0xffffffffu, s.lo, o);
         add(s, hi, lo);
     }
-    return (double)s.hi + (double)s.lo;
+    return {__shfl_sync(0xffffffffu, s.hi, 0), __shfl_sync(0xffffffffu, s.lo, 0)};
 }
 
-// max(p - a q, 0) with a = ah + al, as a pair
-__device__ __forceinline__ Two residual(float p, float q, float ah, float al) {
-    const float h = __fmul_rn(ah, q), e = fmaf(ah, q, -h);  // ah q = h + e
-    const float d = __fsub_rn(p, h), z = __fsub_rn(d, p);
-    const float f = __fsub_rn(__fsub_rn(p, __fsub_rn(d, z)), __fadd_rn(h, z));  // p - h = d + f
-    const float low = __fsub_rn(f, fmaf(al, q, e));
-    return __fadd_rn(d, low) > 0.f ? Two{d, low} : Two{0.f, 0.f};
+// max(p - a q, 0) with a = ah + al, as pairs
+__device__ __forceinline__ Twos residual(float2 p, float2 q, float ah, float al) {
+    const float2 a = make_float2(ah, ah), b = make_float2(al, al);
+    const float2 h = __fmul2_rn(a, q);
+    const float2 rest = __ffma2_rn(a, q, make_float2(-h.x, -h.y));  // a q = h + rest
+    const float2 d = minus(p, h), z = minus(d, p);
+    const float2 f = minus(minus(p, minus(d, z)), __fadd2_rn(h, z));  // p - h = d + f
+    const float2 low = minus(f, __ffma2_rn(b, q, rest));
+    const float2 all = __fadd2_rn(d, low);
+    const bool x = all.x > 0.f, y = all.y > 0.f;
+    return {make_float2(x ? d.x : 0.f, y ? d.y : 0.f), make_float2(x ? low.x : 0.f, y ? low.y : 0.f)};
 }
 
 struct Shared {
     float p[kMaxNodes], q[kMaxNodes];  // the parent's entries at the node's token
     int32_t parent[kMaxNodes], token[kMaxNodes];
-    double chunk[kMaxChunks];
-    double warp_sum[kWarps];
-    double part[2][kCluster];  // the CTAs' sums, in turn
+    Two chunk[kMaxChunks];
+    Two part[2][kCluster];  // the CTAs' sums, in turn
     float best[2][kCluster];
     int32_t best_at[2][kCluster];
     float warp_best[kWarps];
@@ -76,10 +98,10 @@ struct Shared {
 };
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads) draft_verify_kernel(const VerifyParams P, int slice, int vec) {
+__global__ void __launch_bounds__(kThreads, 4) draft_verify_kernel(const VerifyParams P, int slice, int vec, int ranks) {
     __shared__ Shared S;
     cg::cluster_group cl = cg::this_cluster();
-    const int rank = (int)cl.block_rank(), b = blockIdx.x / kCluster;
+    const int rank = (int)cl.block_rank(), b = blockIdx.x / ranks;
     const int tid = threadIdx.x, w = tid / 32, lane = tid % 32;
     wait_for_previous();
     let_next_start();
@@ -132,13 +154,14 @@ __global__ void __launch_bounds__(kThreads) draft_verify_kernel(const VerifyPara
         }
     };
     // r at tokens x .. x + kPer - 1 of the current node
-    auto left = [&](int x, int end, float ah, float al, bool whole, Two (&r)[kPer]) {
+    auto left = [&](int x, int end, float ah, float al, bool whole, Twos (&r)[kPer / 2]) {
         float p[kPer], q[kPer];
         entries(target + cur * P.target_stride, x, end, p);
         if (draft && !whole && ah > 0.f) {
             entries(draft + cur * P.draft_stride, x, end, q);
 #pragma unroll
-            for (int j = 0; j < kPer; j++) r[j] = residual(p[j], q[j], ah, al);
+            for (int j = 0; j < kPer / 2; j++)
+                r[j] = residual(make_float2(p[2 * j], p[2 * j + 1]), make_float2(q[2 * j], q[2 * j + 1]), ah, al);
         } else {
             if (!whole)
                 for (int k = 0; k < lost; k++)
@@ -146,40 +169,38 @@ __global__ void __launch_bounds__(kThreads) draft_verify_kernel(const VerifyPara
                     for (int j = 0; j < kPer; j++)
                         if (S.lost[k] == x + j) p[j] = 0.f;
 #pragma unroll
-            for (int j = 0; j < kPer; j++) r[j] = Two{p[j], 0.f};
+            for (int j = 0; j < kPer / 2; j++) r[j] = Twos{make_float2(p[2 * j], p[2 * j + 1]), make_float2(0.f, 0.f)};
         }
     };
     // sums of r over this CTA's chunks, and over the row: every thread of the cluster gets the same bits
-    double before = 0.0;  // of the CTAs before this one
     auto total = [&](bool whole) {
         const float ah = (float)a, al = (float)(a - (double)ah);
+#pragma unroll 2
         for (int c = w; c < chunks; c += kWarps) {
-            Two s{0.f, 0.f};
+            Twos s{make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
             for (int k = 0; k < kChunk / (32 * kPer); k++) {
-                Two r[kPer];
+                Twos r[kPer / 2];
                 left(v0 + c * kChunk + (k * 32 + lane) * kPer, v1, ah, al, whole, r);
 #pragma unroll
-                for (int j = 0; j < kPer; j++) add(s, r[j].hi, r[j].lo);
+                for (int j = 0; j < kPer / 2; j++) add(s, r[j].hi, r[j].lo);
             }
-            const double t = warp_total(s);
-            if (lane == 0) S.chunk[c] = t;
+            Two one{s.hi.x, s.lo.x};
+            add(one, s.hi.y, s.lo.y);
+            one = warp_total(one);
+            if (lane == 0) S.chunk[c] = one;
         }
         __syncthreads();
         if (w == 0) {
-            double t = 0.0;
-            for (int c = lane; c < chunks; c += 32) t += S.chunk[c];
-#pragma unroll
-            for (int o = 16; o; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-            if (lane < kCluster) *cl.map_shared_rank(&S.part[turn][rank], lane) = t;
+            Two t{0.f, 0.f};
+            for (int c = lane; c < chunks; c += 32) add(t, S.chunk[c].hi, S.chunk[c].lo);
+            t = warp_total(t);
+            if (lane < ranks) *cl.map_shared_rank(&S.part[turn][rank], lane) = t;
         }
         cl.sync();
-        double all = 0.0;
-        before = 0.0;
-        for (int k = 0; k < kCluster; k++) {
-            if (k == rank) before = all;
-            all += S.part[turn][k];
-        }
+        // sums by the same steps in every CTA
+        const Two mine = lane < ranks ? S.part[turn][lane] : Two{0.f, 0.f};
+        const double all = value(warp_total(mine));
         turn ^= 1;
         return all;
     };
@@ -212,7 +233,7 @@ __global__ void __launch_bounds__(kThreads) draft_verify_kernel(const VerifyPara
                 const float ob = __shfl_xor_sync(0xffffffffu, best, o);
                 better(ob, __shfl_xor_sync(0xffffffffu, at, o));
             }
-            if (lane < kCluster) {
+            if (lane < ranks) {
                 *cl.map_shared_rank(&S.best[turn][rank], lane) = best;
                 *cl.map_shared_rank(&S.best_at[turn][rank], lane) = at;
             }
@@ -220,7 +241,7 @@ __global__ void __launch_bounds__(kThreads) draft_verify_kernel(const VerifyPara
         cl.sync();
         best = -INFINITY;
         at = INT32_MAX;
-        for (int k = 0; k < kCluster; k++) better(S.best[turn][k], S.best_at[turn][k]);
+        for (int k = 0; k < ranks; k++) better(S.best[turn][k], S.best_at[turn][k]);
         turn ^= 1;
         return at == INT32_MAX ? 0 : at;  // nothing but NaN
     };
@@ -281,10 +302,11 @@ __global__ void __launch_bounds__(kThreads) draft_verify_kernel(const VerifyPara
     double border = (double)P.uniform[row] * all;
     if (!(border >= 0.0)) border = 0.0;  // no number in [0, 1)
     // the last CTA with anything takes what rounding leaves behind the sum
-    double mine = 0.0;
+    double before = 0.0, mine = 0.0;
     int last = 0;
-    for (int k = 0; k < kCluster; k++) {
-        const double t = S.part[turn ^ 1][k];
+    for (int k = 0; k < ranks; k++) {
+        const double t = value(S.part[turn ^ 1][k]);
+        if (k < rank) before += t;
         if (k == rank) mine = t;
         if (t > 0.0) last = k;
     }
@@ -295,7 +317,7 @@ __global__ void __launch_bounds__(kThreads) draft_verify_kernel(const VerifyPara
         int found = -1;
         double found_at = 0.0;
         for (int c = 0; c < chunks; c++) {
-            const double t = S.chunk[c];
+            const double t = value(S.chunk[c]);
             if (t > 0.0) {
                 found = c;
                 found_at = run;
@@ -308,14 +330,15 @@ __global__ void __launch_bounds__(kThreads) draft_verify_kernel(const VerifyPara
         run = found_at;
 #pragma unroll 1
         for (int k = 0; k < kChunk / (32 * kPer) && token < 0; k++) {
-            Two r[kPer];
+            Twos r[kPer / 2];
             const int x = v0 + found * kChunk + (k * 32 + lane) * kPer;
             left(x, v1, ah, al, whole, r);
             double s[kPer], t = 0.0;
             int positive = -1;
 #pragma unroll
             for (int j = 0; j < kPer; j++) {
-                const double e = (double)r[j].hi + (double)r[j].lo;
+                const Twos &t2 = r[j / 2];
+                const double e = j % 2 ? (double)t2.hi.y + (double)t2.lo.y : (double)t2.hi.x + (double)t2.lo.x;
                 if (e > 0.0) positive = x + j;
                 t += e;
                 s[j] = t;
@@ -345,23 +368,28 @@ __global__ void __launch_bounds__(kThreads) draft_verify_kernel(const VerifyPara
 
 template <typename T>
 cudaError_t launch_typed(const VerifyParams &P, cudaStream_t s) {
-    const int slice = ((P.vocab + kCluster - 1) / kCluster + kChunk - 1) / kChunk * kChunk;
+    // more CTAs of a sequence shorten a pass over its row, and lengthen the exchange of sums: 32 sequences of 131072 tokens
+    // with trees of 32 nodes 73 us with 16, 101 with 8; one of 32000 tokens 19.8 against 18.4
+    const int ranks = P.seqs <= kFewSeqs && P.vocab >= kLongRow ? kCluster : kLeast;
+    const int slice = ((P.vocab + ranks - 1) / ranks + kChunk - 1) / kChunk * kChunk;
     constexpr int kAlign = sizeof(T) * kPer;
     auto ok = [](const void *p, int64_t stride) {
         return reinterpret_cast<uintptr_t>(p) % kAlign == 0 && stride % kPer == 0;
     };
     const int vec = ok(P.target, P.target_stride) && ok(P.draft, P.draft ? P.draft_stride : 0);
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)P.seqs * kCluster);
+    cudaError_t e = cudaFuncSetAttribute(draft_verify_kernel<T>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
+    cfg.gridDim = dim3((unsigned)P.seqs * ranks);
     cfg.blockDim = dim3(kThreads);
     cfg.stream = s;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = kCluster;
+    at[0].val.clusterDim.x = ranks;
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, draft_verify_kernel<T>, P, slice, vec);
+    return cudaLaunchKernelEx(&cfg, draft_verify_kernel<T>, P, slice, vec, ranks);
 }
 
 }  // namespace
