@@ -88,7 +88,7 @@ size_t coli_tree_workspace_bytes(const coli_tree_desc *desc, const coli_kv_cache
  * sequence with more nodes than the table has places keeps those that fit. What the pages hold behind a sequence's
  * nodes, before its window, at nodes that a row does not see, or on pages that no table names does not reach a row,
  * whatever its bits. Precision is that of coli_attn_decode; keys and values that are seen should be finite.
- *   q [rows][q_heads][dim], out alike, lse [rows][q_heads] fp32 or NULL, first [seqs + 1], past [seqs], parent [rows] or
+ *   q [rows][q_heads][dim], out alike (and not q itself), lse [rows][q_heads] fp32 or NULL, first [seqs + 1], past [seqs], parent [rows] or
  *   NULL, table [seqs][table_width] int32 (entries behind a sequence's nodes are not read).
  * The same call gives the same bits. */
 int coli_attn_tree(const coli_tree_desc *desc, const coli_kv_cache *cache, const void *q, const int32_t *first,
@@ -113,7 +113,7 @@ typedef struct {
 /* Node 0 of every sequence is its last committed token (the root): it is not tested. target[row] is the target's
  * distribution behind that node (COLI_VERIFY_GREEDY: any scores, logits too), draft[row] the distribution that the
  * tokens of its children were drawn from, tokens[row] the node's own token. From the root, at each accepted node c, its
- * children x_1, x_2, ... are tested in the order of their rows:
+ * children x_1, x_2, ... are tested in the order of their rows (other nodes without a parent are not reached):
  *   with a draft, u_j = uniform[x_j's row] in [0, 1):
  *     r_1 = target[c];  x_j is accepted if u_j * draft[c][x_j] < r_j[x_j] / m_j, with m_1 = 1 and m_j = sum(r_j);
  *     otherwise r_{j+1} = max(r_j - m_j * draft[c], 0)

@@ -153,7 +153,7 @@ int coli_attn_tree(const coli_tree_desc *d, const coli_kv_cache *c, const void *
                    const int32_t *parent, const int32_t *table, void *out, float *lse, int32_t *err, void *ws,
                    size_t ws_bytes, coli_stream_t stream) {
     if (int rc = check_tree(d, c)) return rc;
-    if (!q || !first || !past || !table || !out) return COLI_MOE_EINVAL;
+    if (!q || !first || !past || !table || !out || q == out) return COLI_MOE_EINVAL;
     const int ab = act_bytes(d->act);
     if (!aligned(q, ab) || !aligned(out, ab) || !aligned(first, 4) || !aligned(past, 4) || !aligned(parent, 4) ||
         !aligned(table, 4) || !aligned(lse, 4) || !aligned(err, 4))

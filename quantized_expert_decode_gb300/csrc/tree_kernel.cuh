@@ -527,10 +527,8 @@ __global__ void __launch_bounds__(tree::kThreads, 1) attn_tree_kernel(const Tree
                         if (T::kPParts == 3) tmem_st_x8(sc + TN + 8 * c, w3);
                     };
                     if (!mixed && !__any_sync(0xffffffffu, fabsf(ref) >= 0x1p22f)) {
-                        uint32_t s0[16], s1[16];
-                        tmem_ld_x16(sc, s0);
 #pragma unroll 1
-                        for (int c = 0; c < TN / 16; c += 2) {
+                        for (int c = 0; c < TN / 16; c++) {
                             if (c == TN / 32 && c > 0) {
                                 // the first half's products may start
                                 tmem_st_wait();
@@ -538,12 +536,10 @@ __global__ void __launch_bounds__(tree::kThreads, 1) attn_tree_kernel(const Tree
                                 mbar_arrive(&S.p_half[g]);
                                 half_told = true;
                             }
+                            uint32_t s[16];
+                            tmem_ld_x16(sc + 16 * c, s);
                             tmem_ld_wait();
-                            tmem_ld_x16(sc + 16 * (c + 1), s1);
-                            parts(s0, c, std::false_type{}, 0u);
-                            tmem_ld_wait();
-                            if (c + 2 < TN / 16) tmem_ld_x16(sc + 16 * (c + 2), s0);
-                            parts(s1, c + 1, std::false_type{}, 0u);
+                            parts(s, c, std::false_type{}, 0u);
                         }
                     } else {
 #pragma unroll 1
@@ -783,7 +779,7 @@ __global__ void __launch_bounds__(tree::kThreads, 1) attn_tree_kernel(const Tree
             const int ch = lane % CH, sub = lane / CH;
             unsigned char *slot = slots + (c % T::kSlots) * T::kSlotBytes + (ch / 4) * kSlab;
             const unsigned char *raw = raws + (c % kRing) * T::kRawBytes + lane * 16;  // (rows lie one behind the other)
-#pragma unroll 6
+#pragma unroll 1
             for (int block = cw; block < TN / kBlock; block += kCopiers / 32) {
 #pragma unroll
                 for (int i = 0; i < kBlock / kRows; i++) {

@@ -31,7 +31,7 @@ def q():
 
 
 def ints(*x):
-    return torch.tensor(*x, dtype=torch.int32, device="cuda")
+    return torch.as_tensor(np.asarray(*x), dtype=torch.int32, device="cuda")
 
 
 # ------------------------------------------------------------------------------------ append
@@ -340,6 +340,24 @@ def test_tree_types(q, act, kv):
     check_tree(q, 20, [70, 0, 300], [9, 5, 31], act=act, kv=kv, dim=128)
 
 
+@pytest.mark.parametrize("act", ["f32", "bf16"])
+@pytest.mark.parametrize("kv", sorted(KV))
+@pytest.mark.parametrize("dim", [48, 128, 208])
+def test_tree_types_on_pages_of_odd_sizes(q, act, kv, dim):
+    check_tree(q, 20, [170, 0, 300], [30, 5, 91], act=act, kv=kv, dim=dim, page=5)
+    check_tree(q, 20, [170, 0, 300], [30, 5, 91], act=act, kv=kv, dim=dim, page=12, window=40, layout="nhd")
+
+
+@pytest.mark.parametrize("act,kv,dim,page", [("f32", "e4m3", 256, 16), ("bf16", "e4m3", 256, 16), ("bf16", "e4m3", 128, 5), ("f32", "bf16", 256, 16),
+                                             ("f32", "bf16", 128, 16), ("bf16", "bf16", 128, 7), ("f32", "f16", 64, 16)])
+def test_tree_repeats_bit_by_bit(q, act, kv, dim, page):
+    t = Trees(q, 35, [900, 2000, 0], [256, 3, 100], act=act, kv=kv, heads=(10, 2), dim=dim, page=page)
+    want = t.run()
+    for _ in range(15):
+        for a, b in zip(t.run(), want):
+            assert torch.equal(a, b)
+
+
 @pytest.mark.parametrize("heads", [(1, 1), (7, 1), (8, 8), (16, 1), (12, 4), (24, 1), (10, 2), (40, 1), (17, 1), (64, 2), (128, 1)])
 @pytest.mark.parametrize("kv", ["bf16", "e4m3"])
 def test_tree_heads(q, heads, kv):
@@ -619,6 +637,38 @@ def test_tree_behind_two_to_the_31_elements(q):
         q.coli_attn_tree(d, c, x, ints([0, 20]), ints([1880]), None, table, out, None, None, ws, n)
         got.append(out)
     assert torch.equal(*got) and bool(torch.isfinite(got[0]).all())
+
+
+def test_tree_at_the_longest_lengths(q):
+    # tables that name all but 2^31 tokens on few pages, the nodes at their end, the window before them
+    rng = np.random.default_rng(52)
+    for ps in (64, 1023):
+        width = (2 ** 31 - 1) // ps
+        c = Cache(q, rng, "bf16", 12, ps, 2, 64)
+        for which in (0, 1):
+            for slot in range(ps):
+                c.put(which, torch.arange(12, device="cuda"), torch.full((12,), slot, device="cuda"), randn(rng, 12, 2, 64))
+        table = (torch.arange(width, device="cuda") % 12).int().view(1, width)
+        n, window = 30, 200
+        past = width * ps - n
+        parent = random_tree(rng, n)
+        x = randn(rng, n, 8, 64)
+        d = q.make_tree_desc(1, n, n, 8, width, 0, 0.125, window)
+        ws_bytes = q.coli_tree_workspace_bytes(d, c.desc)
+        assert ws_bytes > 0
+        out, lse, err = torch.empty_like(x), torch.empty(n, 8, device="cuda"), err_word()
+        q.coli_attn_tree(d, c.desc, x, ints([0, n]), ints([past]), ints(parent), table, out, lse, err,
+                         torch.empty(ws_bytes, dtype=torch.uint8, device="cuda"), ws_bytes)
+        assert int(err.item()) == 0
+        for i, line in enumerate(lines_of(parent)):
+            t = torch.tensor(list(range(past + len(line) - window, past)) + [past + j for j in line], device="cuda")
+            page, slot = (t // ps) % 12, t % ps
+            k, v = c.rows(0, page, slot), c.rows(1, page, slot)
+            s = torch.einsum("hgd,thd->hgt", x[i].double().view(2, 4, 64), k) * 0.125
+            want = torch.einsum("hgt,thd->hgd", torch.softmax(s, -1), v).view(8, 64)
+            # scores of at most some 6, 230 tokens: far within 1e-5 of values of at most 5
+            close(out[i], want, torch.full_like(want, 2e-5))
+            close(lse[i], torch.logsumexp(s, -1).flatten(), torch.full((8,), 2e-5, dtype=torch.float64, device="cuda"))
 
 
 def test_tree_repeats_on_streams_and_in_graphs(q):

@@ -71,7 +71,7 @@ def append(lib, c=None, **over):
 
 def tree(lib, c=None, **over):
     desc = dict(seqs=2, rows=20, nodes=10, q_heads=8, table_width=5, act=0, scale=0.1, window=0, q_stride=0, out_stride=0)
-    args = dict(cache=c or cache(lib), q=FAKE, first=FAKE, past=FAKE, parent=FAKE, table=FAKE, out=FAKE, lse=FAKE, err=None, ws=FAKE,
+    args = dict(cache=c or cache(lib), q=FAKE, first=FAKE, past=FAKE, parent=FAKE, table=FAKE, out=2 * FAKE, lse=FAKE, err=None, ws=FAKE,
                 ws_bytes=1 << 40)
     return call(lib, lib.coli_attn_tree, lib.make_tree_desc, desc, args, over)
 
@@ -135,7 +135,7 @@ def test_append_refusals(q, over, code):
     (dict(table_width=0), "EINVAL"), (dict(table_width=1 << 27), "EINVAL"), (dict(act=-1), "EINVAL"), (dict(window=-1), "EINVAL"),
     (dict(scale=float("nan")), "EINVAL"), (dict(scale=float("inf")), "EINVAL"), (dict(q_stride=8), "EINVAL"),
     (dict(out_stride=-8), "EINVAL"), (dict(q=None), "EINVAL"), (dict(out=None), "EINVAL"), (dict(first=None), "EINVAL"),
-    (dict(past=None), "EINVAL"), (dict(table=None), "EINVAL"), (dict(q=FAKE + 1), "EALIGN"), (dict(first=FAKE + 2), "EALIGN"),
+    (dict(past=None), "EINVAL"), (dict(table=None), "EINVAL"), (dict(out=FAKE), "EINVAL"), (dict(q=FAKE + 1), "EALIGN"), (dict(first=FAKE + 2), "EALIGN"),
     (dict(parent=FAKE + 2), "EALIGN"), (dict(lse=FAKE + 2), "EALIGN"), (dict(ws=None), "EWORKSPACE"),
     (dict(ws=FAKE + 16), "EWORKSPACE"), (dict(ws_bytes=0), "EWORKSPACE")])
 def test_tree_refusals(q, over, code):
