@@ -21,13 +21,13 @@ __global__ void __launch_bounds__(kTreeRows) attn_tree_join_kernel(const TreePar
     const TreeCut cut = W.cuts[c];  // written if c < runs
     const int group = P.q_heads / P.kv_heads, r = threadIdx.x;
     if (c >= runs || r >= cut.rows) return;
-    const int c0 = c - 1, col = blockIdx.y * kPer;
+    const int c0 = c - cut.side, col = blockIdx.y * kPer;
     float4 o[kPer];
     float l = 0.f, m = -INFINITY;
 #pragma unroll
     for (int j = 0; j < kPer; j++) o[j] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
-    for (int k = c0; k <= cut.last; k++) {
+    for (int k = c0; k <= cut.last; k += cut.side) {
         const int64_t s = 2 * (int64_t)k + (k == c0 ? 1 : 0);
         const float2 e = W.part_ml[s * kTreeRows + r];
         float4 v[kPer];

@@ -29,7 +29,7 @@ struct TreeTraits {
     static constexpr int kSlotBytes = kTile * DP * 2;  // K or V of a tile, 16-bit
     static constexpr int kRawSlots = kRaw ? 4 : 0;     // K or V of a tile on its way in 8 bits
     static constexpr int kRawBytes = kTile * DP;
-    static constexpr int kMiscBytes = 16640;
+    static constexpr int kMiscBytes = 16896;
     static constexpr int kRoom = (227 << 10) - kMiscBytes - kQBytes - kRawSlots * kRawBytes;
     static constexpr int kSlots = kRoom / kSlotBytes < 8 ? kRoom / kSlotBytes : 8;
     static_assert(kSlots >= 1, "shared memory of an SM");
@@ -46,7 +46,8 @@ struct TreeTraits {
 // The item whose units the border before a run cuts, told for its first cut only (else it has no rows): its rows are
 // [first, first + rows) of the (node, head) pairs of a sequence whose nodes begin at `row`
 struct alignas(16) TreeCut {
-    int32_t rows, last, row, runs, first, kh, half, reserved = 0;
+    int32_t rows, last, row, runs, first, kh, half;
+    int32_t side;  // the runs of an item are so far apart
 };
 
 // How the launch is laid out, and the workspace

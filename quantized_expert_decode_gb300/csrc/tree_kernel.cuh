@@ -44,6 +44,7 @@ namespace tree {
 
 constexpr int kWarps = 16, kThreads = kWarps * 32;
 constexpr int kSums = 8, kCopies = 12, kProducts = 15;  // the roles' first warps
+constexpr int kMostSides = 8;
 constexpr int kCopiers = (kProducts - kCopies) * 32;
 // registers of a thread: 128 at the launch, 2 * 120 + 184 + 88 = 4 * 128 behind it
 constexpr uint64_t kWaitNs = 2000000000;  // of a wait that should take microseconds
@@ -77,7 +78,7 @@ struct Misc {
     float m[4][kTreeRows], l[4][kTreeRows];        // behind a tile: the maximum; its group's sum of p
     int16_t parent[kTreeMaxNodes];
     int32_t pre[kTreeMaxSeqs + 1];  // units before a sequence
-    int32_t scan[kWarps];
+    int32_t scan[kWarps], least[kWarps], most[kWarps];
     uint32_t row_off[4][kTreeRows];  // of a tile's places in the pool, in steps
     uint32_t seen[16][4];  // places of a tile that lie on good pages
     uint32_t odd[4][4];    // places of a tile whose values' infinities and NaN are taken out
@@ -108,10 +109,10 @@ __device__ __forceinline__ Seq seq_of(const TreeParams &P, const TreeWork &W, in
 // A run's walk over the parts of items: `cnt` tiles of an item from tile u on
 template <typename T>
 struct Walk {
-    Seq s;
+    Seq s;  // its items are groups of `side` row tiles
     int32_t b, item, u, cnt;
     uint32_t left;
-    __device__ __forceinline__ void begin(const TreeParams &P, const TreeWork &W, const int32_t *pre, uint32_t at, uint32_t units) {
+    __device__ __forceinline__ void begin(const TreeParams &P, const TreeWork &W, const int32_t *pre, uint32_t at, uint32_t units, int side) {
         int lo = 0, hi = P.seqs;  // pre[lo] <= at < pre[hi]
         while (hi - lo > 1) {
             const int mid = (lo + hi) / 2;
@@ -121,13 +122,14 @@ struct Walk {
         b = lo;
         int f;
         s = seq_of<T>(P, W, b, f);
+        s.items /= side;
         const int off = (int)(at - (uint32_t)pre[b]);
         item = off / s.tiles;
         u = off - item * s.tiles;
         left = units;
         cnt = min((int)left, s.tiles - u);
     }
-    __device__ __forceinline__ bool next(const TreeParams &P, const TreeWork &W, const int32_t *pre) {
+    __device__ __forceinline__ bool next(const TreeParams &P, const TreeWork &W, const int32_t *pre, int side) {
         left -= cnt;
         if (left == 0) return false;
         u = 0;
@@ -137,6 +139,7 @@ struct Walk {
             while (pre[b + 1] == pre[b]);
             int f;
             s = seq_of<T>(P, W, b, f);
+            s.items /= side;
         }
         cnt = min((int)left, s.tiles);
         return true;
@@ -182,34 +185,55 @@ __global__ void __launch_bounds__(tree::kThreads, 1) attn_tree_kernel(const Tree
     // ---- units before each sequence
     const int per = (P.seqs + kThreads - 1) / kThreads;
     const int b0 = min(tid * per, P.seqs), b1 = min(b0 + per, P.seqs);
-    int mine = 0;
+    int mine = 0, least = INT32_MAX, most = 0;  // row tiles of a sequence
     for (int b = b0; b < b1; b++) {
         int flags;
         const Seq s = seq_of<T>(P, W, b, flags);
         if (flags && blockIdx.x == 0 && P.err) atomicOr(P.err, flags);
         const int u = s.n ? s.items * s.tiles : 0;
+        if (s.n) {
+            least = min(least, s.row_tiles);
+            most = max(most, s.row_tiles);
+        }
         S.pre[b + 1] = u;
         mine += u;
     }
+    least = __reduce_min_sync(0xffffffffu, least);
+    most = __reduce_max_sync(0xffffffffu, most);
     int incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const int v = __shfl_up_sync(0xffffffffu, incl, o);
         if (lane >= o) incl += v;
     }
-    if (lane == 31) S.scan[warp] = incl;
+    if (lane == 31) {
+        S.scan[warp] = incl;
+        S.least[warp] = least;
+        S.most[warp] = most;
+    }
     __syncthreads();
     int before = incl - mine;
-    for (int i = 0; i < warp; i++) before += S.scan[i];
+    for (int i = 0; i < kWarps; i++) {
+        if (i < warp) before += S.scan[i];
+        least = min(least, S.least[i]);
+        most = max(most, S.most[i]);
+    }
+    // Row tiles that read the same K and V do it side by side, so that they find it in L2: where all sequences have as many
+    // row tiles, `side` CTAs take the same run, each of its own row tile.
+    int side = 1;
+    if (least == most)
+        for (int i = 2; i <= kMostSides && i <= W.ctas; i++)
+            if (most % i == 0) side = i;
     for (int b = b0; b < b1; b++) {
         before += S.pre[b + 1];
-        S.pre[b + 1] = before;
+        S.pre[b + 1] = before / side;  // (every sequence's items are a multiple)
     }
     if (tid == 0) S.pre[0] = 0;
     __syncthreads();
-    const AttnRuns R((uint32_t)S.pre[P.seqs], (uint32_t)W.ctas);
-    const uint32_t run = blockIdx.x;
-    if (R.runs == 0 && run == 0 && tid == 0) W.cuts[0].runs = 0;
+    const AttnRuns R((uint32_t)S.pre[P.seqs], (uint32_t)(W.ctas / side));
+    const uint32_t slot_run = blockIdx.x, run = slot_run / side;
+    const int rank = slot_run - run * side;
+    if (R.runs == 0 && slot_run == 0 && tid == 0) W.cuts[0].runs = 0;
     if (run >= R.runs) return;
     const uint32_t from = R.start(run), units = R.start(run + 1) - from;
 
@@ -277,9 +301,9 @@ __global__ void __launch_bounds__(tree::kThreads, 1) attn_tree_kernel(const Tree
         const uint32_t lanes = (uint32_t)(quad * 32) << 16;
         uint32_t count = 0, copies = 0, part = 0;
         int last_b = -1;
-        at.begin(P, W, S.pre, from, units);
+        at.begin(P, W, S.pre, from, units, side);
         do {
-            const TreeItem it = tree_item(at.item, at.s.row_tiles, T::kHalves);
+            const TreeItem it = tree_item(at.item * side + rank, at.s.row_tiles, T::kHalves);
             const int row0 = it.tile * kTreeRows, rows = min(kTreeRows, at.s.n * group - row0);
             const bool active = quad * 32 < rows, real = r < rows;
             if (part) sync_softmax();  // both groups are done with the queries and masks before
@@ -403,12 +427,12 @@ __global__ void __launch_bounds__(tree::kThreads, 1) attn_tree_kernel(const Tree
             fence_async_smem();
             mbar_arrive(&S.q_full);
             Walk<T> then = at;
-            const bool more = then.next(P, W, S.pre);
+            const bool more = then.next(P, W, S.pre, side);
             {
                 if (more) {
                     if (P.parent && then.b != at.b && tid < (then.s.n + 31) / 32)
                         asm volatile("prefetch.global.L2 [%0];" ::"l"(P.parent + then.s.row + tid * 32));
-                    const TreeItem ti = tree_item(then.item, then.s.row_tiles, T::kHalves);
+                    const TreeItem ti = tree_item(then.item * side + rank, then.s.row_tiles, T::kHalves);
                     const int size = P.act == COLI_ACT_F32 ? 4 : 2, first = ti.tile * kTreeRows;
                     const int last = min(kTreeRows, then.s.n * group - first), lines = (P.dim * size + 127) / 128;
                     for (int i = tid; i < last * lines; i += 256) {
@@ -603,9 +627,9 @@ __global__ void __launch_bounds__(tree::kThreads, 1) attn_tree_kernel(const Tree
         const int quad = warp % 4, r = quad * 32 + lane;
         const uint32_t lanes = (uint32_t)(quad * 32) << 16;
         uint32_t count = 0;
-        at.begin(P, W, S.pre, from, units);
+        at.begin(P, W, S.pre, from, units, side);
         do {
-            const TreeItem it = tree_item(at.item, at.s.row_tiles, T::kHalves);
+            const TreeItem it = tree_item(at.item * side + rank, at.s.row_tiles, T::kHalves);
             const int row0 = it.tile * kTreeRows, rows = min(kTreeRows, at.s.n * group - row0);
             const bool active = quad * 32 < rows, real = r < rows;
             const int node = real ? kv_quotient(W.group, row0 + r) : 0;
@@ -660,7 +684,7 @@ __global__ void __launch_bounds__(tree::kThreads, 1) attn_tree_kernel(const Tree
             count += at.cnt;
             if (real) {
                 const bool whole = at.cnt == at.s.tiles;
-                const int64_t slot = 2 * (int64_t)run + (at.u == 0 ? 1 : 0);
+                const int64_t slot = 2 * (int64_t)slot_run + (at.u == 0 ? 1 : 0);
                 const int head = it.kh * group + (row0 + r - node * group);
                 if (!whole) {
 #pragma unroll
@@ -702,7 +726,7 @@ __global__ void __launch_bounds__(tree::kThreads, 1) attn_tree_kernel(const Tree
                         P.lse[(int64_t)(at.s.row + node) * P.q_heads + head] = attn_lse(m == -INFINITY ? 0.f : m, l, T::kShift);
                 }
             }
-        } while (at.next(P, W, S.pre));
+        } while (at.next(P, W, S.pre, side));
     } else if (regs_down<88>(); warp < kProducts) {
         // ================================================================ copies
         constexpr int kBytes = T::kRaw ? 1 : 2;
@@ -823,9 +847,9 @@ __global__ void __launch_bounds__(tree::kThreads, 1) attn_tree_kernel(const Tree
             }
         };
 
-        at.begin(P, W, S.pre, from, units);
+        at.begin(P, W, S.pre, from, units, side);
         if (!W.box || T::kRaw || cw == 0) do {
-            const TreeItem it = tree_item(at.item, at.s.row_tiles, T::kHalves);
+            const TreeItem it = tree_item(at.item * side + rank, at.s.row_tiles, T::kHalves);
             const int32_t *pages = P.table + (int64_t)at.b * P.table_width;
             const int end = at.s.past + at.s.n;
             if (W.box) {
@@ -925,7 +949,7 @@ __global__ void __launch_bounds__(tree::kThreads, 1) attn_tree_kernel(const Tree
                     advance();
                 }
             }
-        } while (at.next(P, W, S.pre));
+        } while (at.next(P, W, S.pre, side));
         copy_wait<0>();
         if (T::kRaw)
             for (uint32_t c = copy > (uint32_t)kAhead ? copy - kAhead : 0; c < copy; c++) hand_on(c);
@@ -933,18 +957,18 @@ __global__ void __launch_bounds__(tree::kThreads, 1) attn_tree_kernel(const Tree
         // ================================================================ products: one warp issues them
         if (lane == 1) {
             // the border before this run, for the join
-            TreeCut cut{0, 0, 0, (int32_t)R.runs, 0, 0};
-            at.begin(P, W, S.pre, from, units);
+            TreeCut cut{0, 0, 0, (int32_t)R.runs * side, 0, 0, 0, side};
+            at.begin(P, W, S.pre, from, units, side);
             if (at.u > 0 && run > 0 && from - (uint32_t)at.u >= R.start(run - 1)) {
-                const TreeItem it = tree_item(at.item, at.s.row_tiles, T::kHalves);
+                const TreeItem it = tree_item(at.item * side + rank, at.s.row_tiles, T::kHalves);
                 cut.rows = min(kTreeRows, at.s.n * group - it.tile * kTreeRows);
-                cut.last = R.of(from - (uint32_t)at.u + (uint32_t)at.s.tiles - 1);
+                cut.last = R.of(from - (uint32_t)at.u + (uint32_t)at.s.tiles - 1) * side + rank;
                 cut.row = at.s.row;
                 cut.first = it.tile * kTreeRows;
                 cut.kh = it.kh;
                 cut.half = it.half;
             }
-            W.cuts[run] = cut;
+            W.cuts[slot_run] = cut;
         }
         __syncwarp();
         {
@@ -962,7 +986,7 @@ __global__ void __launch_bounds__(tree::kThreads, 1) attn_tree_kernel(const Tree
                     lap ^= 1;
                 }
             };
-            at.begin(P, W, S.pre, from, units);
+            at.begin(P, W, S.pre, from, units, side);
             do {
                 wait_warp(&S.q_full, part & 1);
 #pragma unroll 1
@@ -1026,7 +1050,7 @@ __global__ void __launch_bounds__(tree::kThreads, 1) attn_tree_kernel(const Tree
                 }
                 k--;  // (the last round has no scores)
                 part++;
-            } while (at.next(P, W, S.pre));
+            } while (at.next(P, W, S.pre, side));
             tc_commit(&S.done, lead);
             wait_warp(&S.done, 0);
         }
