@@ -250,7 +250,7 @@ __global__ void __launch_bounds__(kThreads, 4) draft_verify_kernel(const VerifyP
     if (P.mode == COLI_VERIFY_GREEDY) top = largest();
     // Nodes come behind their parents: one look at each in turn walks down the tree.
     for (int i0 = 0; i0 < n; i0 += 32) {
-        int done = i0 == 0 ? 0 : -1;  // nodes of this round up to here are dealt with
+        int done = i0 == 0 ? 0 : -1;  // nodes of these 32 up to here are dealt with
         while (true) {
             const int i = i0 + lane;
             const unsigned is = __ballot_sync(0xffffffffu, lane > done && i < n && S.parent[i] == cur);

@@ -26,6 +26,17 @@
 // What a thread of one role leaves for another lies in rings of four tiles: the products of a tile wait for the sums of
 // two tiles before (or one), and its scores for the products of two tiles before, so that no role runs four tiles ahead.
 //
+// What bounds it. Up to 128 rows on a kv head the bytes of K and V would (128 rows do 128 operations a byte, the matrix
+// units could do 290); measured is the chain of one tile's steps: scores 460 cycles to issue and as many to end, their
+// maximum 520, the other group's maximum 200, exponents and parts 1900 to 2000, sums 700 behind the second half of p, and
+// 100 to 250 for each of the eight waits between. Two buffers of scores overlap two such chains: 2700 cycles for a
+// tile of 128 places and 128 bf16 elements, 4200 beside fp32 queries, 4700 on e4m3, whose widening takes 1300 for K
+// and V each. One sequence of 131007 tokens with 64 nodes (384 rows on a kv head: three row tiles) 240 us, 860
+// TFLOP/s and 44 % of the measured rate; 32 sequences of up to 8192 tokens with 21 nodes, fp32 queries, 192 us,
+// 44 % of the copy rate; 48 of 16384 e4m3 tokens with 16 nodes 770 us, 31 %. Instructions take 46 % of the issue slots,
+// the matrix units are busy 56 % of the time. What did not help: a warp of its own for the scores' products (238 us and
+// 200), a load from tensor memory on its way behind each piece, waiting by spinning, no proxy fences (all within 2 %).
+//
 // Places that some rows see and others do not (nodes, the window's edge) lie in `mixed` tiles. There a row's visible
 // places are bits, what is not seen has p = 0, and infinities and NaN of V are taken out of the tile (0 times infinity
 // would reach every row) and added to the sums of the rows that do see them.
