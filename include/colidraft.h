@@ -75,7 +75,8 @@ typedef struct {
     int64_t q_stride, out_stride; /* elements from one row to the next; 0: q_heads * dim */
 } coli_tree_desc;
 
-/* Bytes of device workspace (256-byte aligned) coli_attn_tree needs; 0 if a description is invalid. The workspace needs
+/* Bytes of device workspace (256-byte aligned) coli_attn_tree needs; 0 if a description is invalid, or if its tables and
+ * nodes name more than 2^31 tiles of work (coli_attn_tree answers COLI_MOE_ENOTSUP). The workspace needs
  * no preparation and may be shared with other calls on one stream. */
 size_t coli_tree_workspace_bytes(const coli_tree_desc *desc, const coli_kv_cache *cache);
 

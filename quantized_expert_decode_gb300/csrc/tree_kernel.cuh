@@ -59,6 +59,7 @@ constexpr int kMostSides = 8;
 constexpr int kCopiers = (kProducts - kCopies) * 32;
 // registers of a thread: 128 at the launch, 2 * 120 + 184 + 88 = 4 * 128 behind it
 constexpr uint64_t kWaitNs = 2000000000;  // of a wait that should take microseconds
+constexpr uint64_t kSettleNs = 100000000;
 constexpr uint32_t kNapNs = 1000000;      // a thread sleeps at most so long before it looks at the clock
 
 __device__ __forceinline__ void sync_softmax() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
@@ -298,6 +299,12 @@ __global__ void __launch_bounds__(tree::kThreads, 1) attn_tree_kernel(const Tree
                 return;
             }
         }
+    };
+    // what is under way has to have ended before the CTA does, given up or not
+    auto settle = [&](uint64_t *bar, uint32_t parity) {
+        const uint64_t since = globaltimer_ns();
+        while (!mbar_try_wait_for(bar, parity, kNapNs) && globaltimer_ns() - since < kSettleNs) {}
+        __syncwarp();
     };
     auto wait_warp = [&](uint64_t *bar, uint32_t parity) {  // and the warp is together again
         wait(bar, parity);
@@ -962,6 +969,9 @@ __global__ void __launch_bounds__(tree::kThreads, 1) attn_tree_kernel(const Tree
             }
         } while (at.next(P, W, S.pre, side));
         copy_wait<0>();
+        if (W.box && cw == 0 && *(volatile int32_t *)&S.dead)
+            for (uint32_t c = copy > (uint32_t)kRing ? copy - kRing : 0; c < copy; c++)
+                settle(T::kRaw ? &S.raw_full[c % kRing] : &S.full[c % T::kSlots], (c / kRing) & 1);
         if (T::kRaw)
             for (uint32_t c = copy > (uint32_t)kAhead ? copy - kAhead : 0; c < copy; c++) hand_on(c);
     } else {
@@ -1063,7 +1073,7 @@ __global__ void __launch_bounds__(tree::kThreads, 1) attn_tree_kernel(const Tree
                 part++;
             } while (at.next(P, W, S.pre, side));
             tc_commit(&S.done, lead);
-            wait_warp(&S.done, 0);
+            settle(&S.done, 0);
         }
         __syncwarp();
     }

@@ -461,6 +461,55 @@ def test_tree_peaked_and_flat_scores(q):
     check_tree(q, 39, [1000, 100], [10, 20], boost=0.0)
 
 
+@pytest.mark.parametrize("act,kv", [("f32", "bf16"), ("bf16", "bf16"), ("f32", "f16"), ("bf16", "e4m3")])
+@pytest.mark.parametrize("boost", [3e6, 3e7])
+def test_tree_scores_beyond_two_to_the_23(q, act, kv, boost):
+    # products whose rounding steps are 1 and more: one key has all the weight, and it is the largest one's
+    t = Trees(q, 53, [300, 40], [12, 30], act=act, kv=kv, boost=boost, dim=128)
+    out, lse = t.run()
+    assert bool(torch.isfinite(out).all()) and bool(torch.isfinite(lse).all())
+    t.compare((out, lse))
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.125, 2.0, 1e-30])
+@pytest.mark.parametrize("kv", sorted(KV))
+def test_tree_scales_of_any_sign(q, scale, kv):
+    t = Trees(q, 54, [300, 0, 40], [12, 3, 30], kv=kv, dim=64)
+    t.scale = scale
+    t.compare(t.run())
+
+
+def test_tree_queries_that_are_not_finite_reach_their_rows_only(q):
+    for kv in sorted(KV):
+        t = Trees(q, 55, [300, 40], [12, 30], kv=kv, dim=64)
+        want = t.run()
+        t.x[5, 3, 7], t.x[20, 0, 0] = math.nan, math.inf
+        got = t.run()
+        hit = torch.zeros(t.x.shape[:2], dtype=torch.bool, device="cuda")
+        hit[5, 3], hit[20, 0] = True, True
+        for a, b in zip(got, want):
+            assert torch.equal(a[~hit], b[~hit])
+        assert bool(torch.isnan(got[0][5, 3]).all())
+
+
+def test_tree_calls_beside_each_other(q):
+    # two streams with workspaces of their own, the device shared out between them as it likes
+    ts = [Trees(q, 56 + i, [3000, 700], [64, 20], heads=(16, 2), dim=128, act="bf16") for i in range(2)]
+    want = [t.run() for t in ts]
+    streams = [torch.cuda.Stream() for _ in ts]
+    ws = [torch.empty(q.coli_tree_workspace_bytes(t.desc(), t.c.desc), dtype=torch.uint8, device="cuda") for t in ts]
+    torch.cuda.synchronize()
+    got = [None, None]
+    for _ in range(10):
+        for i, (t, s) in enumerate(zip(ts, streams)):
+            with torch.cuda.stream(s):
+                got[i] = t.run(stream=s, ws=ws[i])
+    torch.cuda.synchronize()
+    for g, w in zip(got, want):
+        for a, b in zip(g, w):
+            assert torch.equal(a, b)
+
+
 def test_tree_large_and_small_values(q):
     for kv, f in (("bf16", 2.0 ** 60), ("bf16", 2.0 ** -60), ("f16", 2.0 ** 10), ("f16", 2.0 ** -12)):
         t = Trees(q, 40, [200, 31], [10, 20], kv=kv)
