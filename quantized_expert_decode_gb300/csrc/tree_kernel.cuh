@@ -30,12 +30,12 @@
 // units could do 290); measured is the chain of one tile's steps: scores 460 cycles to issue and as many to end, their
 // maximum 520, the other group's maximum 200, exponents and parts 1900 to 2000, sums 700 behind the second half of p, and
 // 100 to 250 for each of the eight waits between. Two buffers of scores overlap two such chains: 2700 cycles for a
-// tile of 128 places and 128 bf16 elements, 4200 beside fp32 queries, 4700 on e4m3, whose widening takes 1300 for K
-// and V each. One sequence of 131007 tokens with 64 nodes (384 rows on a kv head: three row tiles) 240 us, 860
+// tile of 128 places and 128 bf16 elements, 4200 beside fp32 queries, 3900 on e4m3 (3000 without the widening). One sequence of 131007 tokens with 64 nodes (384 rows on a kv head: three row tiles) 240 us, 860
 // TFLOP/s and 44 % of the measured rate; 32 sequences of up to 8192 tokens with 21 nodes, fp32 queries, 192 us,
-// 44 % of the copy rate; 48 of 16384 e4m3 tokens with 16 nodes 770 us, 31 %. Instructions take 46 % of the issue slots,
+// 44 % of the copy rate; 48 of 16384 e4m3 tokens with 16 nodes 650 us, 36 %. Instructions take 46 % of the issue slots,
 // the matrix units are busy 56 % of the time. What did not help: a warp of its own for the scores' products (238 us and
-// 200), a load from tensor memory on its way behind each piece, waiting by spinning, no proxy fences (all within 2 %).
+// 200), a load from tensor memory on its way behind each piece, waiting by spinning, no proxy fences (all within 2 %); three
+// buffers of scores beside one of sums (269 us instead of 240).
 //
 // Places that some rows see and others do not (nodes, the window's edge) lie in `mixed` tiles. There a row's visible
 // places are bits, what is not seen has p = 0, and infinities and NaN of V are taken out of the tile (0 times infinity
@@ -57,7 +57,7 @@ constexpr int kWarps = 16, kThreads = kWarps * 32;
 constexpr int kSums = 8, kCopies = 12, kProducts = 15;  // the roles' first warps
 constexpr int kMostSides = 8;
 constexpr int kCopiers = (kProducts - kCopies) * 32;
-// registers of a thread: 128 at the launch, 2 * 120 + 184 + 88 = 4 * 128 behind it
+// registers of a thread: 128 at the launch, behind it 2 * 120 + 184 + 88 = 4 * 128, or 2 * 112 + 184 + 104 where e4m3 is widened
 constexpr uint64_t kWaitNs = 2000000000;  // of a wait that should take microseconds
 constexpr uint64_t kSettleNs = 100000000;
 constexpr uint32_t kNapNs = 1000000;      // a thread sleeps at most so long before it looks at the clock
@@ -314,7 +314,7 @@ __global__ void __launch_bounds__(tree::kThreads, 1) attn_tree_kernel(const Tree
     Walk<T> at;
     if (warp < 8) {
         // ================================================================ softmax: a thread has a row
-        regs_down<120>();
+        regs_down<T::kRaw ? 112 : 120>();
         const int g = warp / 4, quad = warp % 4, r = quad * 32 + lane, wt = tid % 128;
         const uint32_t lanes = (uint32_t)(quad * 32) << 16;
         uint32_t count = 0, copies = 0, part = 0;
@@ -745,7 +745,7 @@ __global__ void __launch_bounds__(tree::kThreads, 1) attn_tree_kernel(const Tree
                 }
             }
         } while (at.next(P, W, S.pre, side));
-    } else if (regs_down<88>(); warp < kProducts) {
+    } else if (regs_down<T::kRaw ? 104 : 88>(); warp < kProducts) {
         // ================================================================ copies
         constexpr int kBytes = T::kRaw ? 1 : 2;
         constexpr int kAhead = T::kRaw ? T::kRawSlots - 1 : 0;  // 8-bit copies on their way behind the newest
@@ -821,25 +821,28 @@ __global__ void __launch_bounds__(tree::kThreads, 1) attn_tree_kernel(const Tree
             const int ch = lane % CH, sub = lane / CH;
             unsigned char *slot = slots + (c % T::kSlots) * T::kSlotBytes + (ch / 4) * kSlab;
             const unsigned char *raw = raws + (c % kRing) * T::kRawBytes + lane * 16;  // (rows lie one behind the other)
+            auto load = [&](int block, uint4 *v) {
+#pragma unroll
+                for (int i = 0; i < kBlock / kRows; i++)
+                    v[i] = *(const uint4 *)(raw + block * (kBlock * (boxes.value ? CH * 16 : DP)) + i * 512);
+            };
+            // a block's loads are on their way while the one before is widened: 48 sequences of 16384 tokens 650 us, 770 without
+            // (without conversions at all 767, without stores 760: it is the latency of one behind the other)
+            uint4 v[kBlock / kRows];
+            load(cw, v);
 #pragma unroll 1
             for (int block = cw; block < TN / kBlock; block += kCopiers / 32) {
+                uint4 then[kBlock / kRows];
+                load(block + kCopiers / 32 < TN / kBlock ? block + kCopiers / 32 : block, then);
 #pragma unroll
                 for (int i = 0; i < kBlock / kRows; i++) {
                     const int row = i * kRows + sub;  // of the block
-                    const uint4 v = *(const uint4 *)(raw + block * (kBlock * (boxes.value ? CH * 16 : DP)) + i * 512);
-                    uint4 a, b;
-                    a.x = widen(v.x);
-                    a.y = widen_hi(v.x);
-                    a.z = widen(v.y);
-                    a.w = widen_hi(v.y);
-                    b.x = widen(v.z);
-                    b.y = widen_hi(v.z);
-                    b.z = widen(v.w);
-                    b.w = widen_hi(v.w);
                     unsigned char *to = slot + block * (kBlock * 128) + row * 128;
-                    *(uint4 *)(to + (((2 * ch) % 8 ^ row) << 4)) = a;
-                    *(uint4 *)(to + (((2 * ch + 1) % 8 ^ row) << 4)) = b;
+                    *(uint4 *)(to + (((2 * ch) % 8 ^ row) << 4)) = make_uint4(widen(v[i].x), widen_hi(v[i].x), widen(v[i].y), widen_hi(v[i].y));
+                    *(uint4 *)(to + (((2 * ch + 1) % 8 ^ row) << 4)) = make_uint4(widen(v[i].z), widen_hi(v[i].z), widen(v[i].w), widen_hi(v[i].w));
                 }
+#pragma unroll
+                for (int i = 0; i < kBlock / kRows; i++) v[i] = then[i];
             }
             fence_async_smem();
         };
